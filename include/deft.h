@@ -475,6 +475,181 @@ int deft_pages_release(deft_pages_t *pool, int32_t n, const int32_t *page_ids);
 int32_t deft_pages_free_count(const deft_pages_t *pool);
 int32_t deft_pages_refcount(const deft_pages_t *pool, int32_t page);
 
+/*
+ * deft_page_table -- page table and slot map of a tree, built on the GPU from
+ * its node lengths (DeFT Guide, "Production Engineering", paged KV-cache
+ * compatibility: the arrays every step reads, which a caller otherwise
+ * builds on the host and copies).  For every node n, of node_len[n] tokens
+ * of which prev_len[n] are in the cache already:
+ *   pages(n) = ceil(node_len[n] / page_size); the first min(pages(n),
+ *   ceil(prev_len[n] / page_size)) of them are the node's pages in the
+ *   earlier table, in order; the others are taken from free_pages, in node
+ *   order, from its beginning;
+ *   new tokens: prev_len[n] .. node_len[n] - 1 (none when the node shrank).
+ * Inputs (device int32): node_len [num_nodes]; the earlier table prev_len,
+ * prev_page_off [num_prev_nodes] (its num_prev_nodes + 1st entry is not
+ * read) and prev_page_id [num_prev_ids], for the first num_prev_nodes <=
+ * num_nodes nodes (the others are new; num_prev_nodes 0: no earlier table);
+ * free_pages [num_free], distinct pages below 2^27 (deft_pages_alloc's).
+ * Outputs (device int32), none of which may overlap an input:
+ *   node_page_off [num_nodes + 1], page_id [max_pages]: the page table;
+ *   entries of page_id past the last page are left as they were;
+ *   tok_off [num_nodes + 1]: where each node's new tokens begin among all
+ *   new tokens, packed in node order;
+ *   slot [max_tokens]: page * page_size + place in the page of every new
+ *   token, -1 past the last (a padded batch: deft_kv_write skips them);
+ *   counts [4]: pages, pages taken from free_pages, new tokens, and 0 or an
+ *   OR of DEFT_TABLE_*.
+ * No pages or tokens are written past max_pages / max_tokens; a page that
+ * free_pages or the earlier table does not hold becomes -1, and so do its
+ * tokens' slots.  A negative length counts as 0.  A table whose counts[3] is
+ * not 0 must not be given to a step.
+ * At most 1,048,576 nodes, page_size 16 (DEFT_EUNSUPPORTED).  Above 2048
+ * nodes a workspace of deft_page_table_workspace_bytes(num_nodes) bytes,
+ * 256-byte aligned (DEFT_EWORKSPACE), whose contents need not be initialised
+ * and which one call at a time may use; below, none (NULL).  Never
+ * allocates, never synchronises; stream-ordered on `stream`.
+ */
+enum {
+    DEFT_TABLE_BAD_LENGTH = 1,    /* a node_len or prev_len is negative                    */
+    DEFT_TABLE_BAD_PREV = 2,      /* an earlier page lies outside prev_page_id             */
+    DEFT_TABLE_NO_FREE_PAGE = 4,  /* more pages are needed than num_free                   */
+    DEFT_TABLE_PAGE_CAP = 8,      /* more pages than max_pages                             */
+    DEFT_TABLE_TOKEN_CAP = 16     /* more new tokens than max_tokens                       */
+};
+size_t deft_page_table_workspace_bytes(int32_t num_nodes);
+int deft_page_table(const int32_t *node_len, int32_t num_nodes, const int32_t *prev_len,
+                    const int32_t *prev_page_off, const int32_t *prev_page_id, int32_t num_prev_nodes,
+                    int64_t num_prev_ids, const int32_t *free_pages, int32_t num_free, int32_t page_size,
+                    int32_t *node_page_off, int32_t *page_id, int32_t max_pages, int32_t *tok_off,
+                    int32_t *slot, int32_t max_tokens, int32_t *counts, void *workspace,
+                    size_t workspace_bytes, void *stream);
+
+/*
+ * deft_kv_write -- K and V rows of new tokens into the paged cache (device;
+ * the write that fills what every step reads).  Row t of k and v,
+ * [num_kv_heads][head_dim] contiguous, k_stride / v_stride elements after the
+ * row before (views of a fused projection's output need no copy), is written
+ * to slot[t] = page * page_size + place in k_pages / v_pages, rounded to
+ * bf16 to nearest even when in_dtype is DEFT_OUT_F32 (DEFT_OUT_BF16: copied
+ * as it is).  A row whose slot is outside [0, num_pages * page_size)
+ * (deft_page_table's -1 among them) is not written anywhere.  Slots are
+ * distinct: of two rows with one slot, either's 8-element pieces may land.
+ * k, v, k_pages and v_pages 16-byte aligned, strides multiples of 16 bytes
+ * and at least a row (DEFT_EINVAL); head_dim in {64, 128}, page_size 16,
+ * fewer than 2^27 pages (DEFT_EUNSUPPORTED).  Never allocates, never
+ * synchronises; stream-ordered on `stream`.
+ */
+int deft_kv_write(const void *k, const void *v, int32_t in_dtype, int64_t k_stride, int64_t v_stride,
+                  const int32_t *slot, int32_t num_tokens, void *k_pages, void *v_pages, int32_t num_pages,
+                  int32_t num_kv_heads, int32_t head_dim, int32_t page_size, void *stream);
+
+/*
+ * Prompts: causal attention of many tokens of a node at once, over the paged
+ * cache (prefill; the DeFT Guide's causal tree mask, "Deep Dive", for whole
+ * nodes: deft_plan_at gives single tokens of a node to the tree step, whose
+ * work items hold 64 rows; here a tile holds 128 rows and a prompt any
+ * number).  Prompt p is the last prompt_len[p] tokens of node
+ * prompt_node[p]: the token at position t of its node attends, with one
+ * softmax, to every token of the nodes above and to tokens 0..t of the node,
+ * all of which are in the cache already.  Its rows are packed: q and out
+ * hold prompt 0's tokens, then prompt 1's, and so on.  A forest of roots is
+ * a packed batch of ordinary prompts; prompt_len below the node's length is
+ * the next chunk of a longer prompt, or one token of a decode step.
+ *
+ * deft_prompt_plan -- the plan of one batch of prompts (host only, no CUDA
+ * call).
+ *   - parent [num_nodes] as for deft_plan, or NULL: every node a root;
+ *     node_len [num_nodes]: tokens in the cache, the prompts' included.
+ *   - prompt_node, prompt_len [num_prompts]; prompt_len NULL or -1: the whole
+ *     node; 0: no rows.  A node may carry several prompts.  num_prompts may
+ *     be 0.
+ *   - num_kv_heads >= 1 and gqa_group in 1..64 of the layer it will run.
+ * DEFT_EINVAL: a null array, a negative length, a bad count; DEFT_ERANGE: a
+ * parent, prompt_node or prompt_len out of range; DEFT_ECYCLE;
+ * DEFT_EUNSUPPORTED: a path of 2^25 pages or more, or more work than 32-bit
+ * counts hold.  On success *out owns the plan (deft_prompt_plan_free); the
+ * arrays are not retained.
+ *
+ * deft_prompt_plan_rebuild -- another batch into an existing plan, which
+ * keeps its device allocation and staging buffer; upload again before the
+ * next step.  On an error the plan is unchanged.  A CUDA graph that captured
+ * a step of this plan is captured again after a rebuild.
+ *
+ * deft_prompt_plan_upload -- the device copy, exactly as deft_plan_upload.
+ */
+typedef struct deft_prompt_plan_t deft_prompt_plan_t;
+
+typedef struct deft_prompt_stats {
+    int32_t num_nodes;
+    int32_t num_prompts;
+    int32_t num_rows;         /* tokens of all prompts: rows of q and out             */
+    int32_t num_items;        /* (one or two query tiles) x (range of KV pages)       */
+    int32_t num_units;        /* items x num_kv_heads                                 */
+    int32_t num_split_items;  /* items whose range was cut: merged by a second launch */
+    int32_t ctas;             /* CTAs of the attention launch                         */
+    int32_t reserved0;
+    int64_t pair_tokens;      /* sum over rows of the tokens they attend              */
+    int64_t partial_slots;    /* partial rows of the pieces, all query heads          */
+    int64_t device_bytes;     /* size of the device copy                              */
+} deft_prompt_stats;
+
+/* Arrays of a prompt plan (deft_prompt_plan_get; int32, for tests and tools). */
+enum {
+    DEFT_P_NODES = 0,     /* [num_nodes * 2]       nearest ancestor with tokens, tokens          */
+    DEFT_P_ITEMS = 1,     /* [num_items * 12]      first row, tokens of tile A and B, position   */
+                          /*   of the first token, node, pages, KV tiles of A and B, first page  */
+                          /*   (node, page of it), first partial slot (-1: none), 0              */
+    DEFT_P_CTA_OFF = 2,   /* [153]                 range of each CTA in CTA_UNIT                 */
+    DEFT_P_CTA_UNIT = 3,  /* [num_units]           item * num_kv_heads + KV head                 */
+    DEFT_P_MERGES = 4     /* [num_split_items * 4] first row, tokens, first partial slot, pieces */
+};
+
+int deft_prompt_plan(const int32_t *parent, const int32_t *node_len, int32_t num_nodes,
+                     const int32_t *prompt_node, const int32_t *prompt_len, int32_t num_prompts,
+                     int32_t num_kv_heads, int32_t gqa_group, deft_prompt_plan_t **out);
+int deft_prompt_plan_rebuild(deft_prompt_plan_t *plan, const int32_t *parent, const int32_t *node_len,
+                             int32_t num_nodes, const int32_t *prompt_node, const int32_t *prompt_len,
+                             int32_t num_prompts, int32_t num_kv_heads, int32_t gqa_group);
+int deft_prompt_plan_upload(deft_prompt_plan_t *plan, void *stream);
+int deft_prompt_plan_stats_get(const deft_prompt_plan_t *plan, deft_prompt_stats *out);
+int deft_prompt_plan_get(const deft_prompt_plan_t *plan, int32_t which, void *dst, size_t bytes);
+void deft_prompt_plan_free(deft_prompt_plan_t *plan);
+
+/* Bytes of device workspace deft_prompt_attn needs for this plan (the
+ * partial rows of cut ranges; at least 512).  0 on bad arguments. */
+size_t deft_prompt_workspace_bytes(const deft_prompt_plan_t *plan, int32_t num_q_heads, int32_t head_dim);
+
+/*
+ * deft_prompt_attn -- one layer's attention of the plan's prompts.
+ *   q: bf16, num_rows rows (at least the plan's num_rows, else DEFT_EINVAL)
+ *     of [num_q_heads][head_dim], q_stride elements apart (a multiple of 8;
+ *     a view of a fused projection's output needs no copy); 16-byte aligned.
+ *   k_pages, v_pages, node_page_off, page_id, num_pages, head geometry,
+ *     scale, out_dtype, workspace: as for deft_tree_attn, with
+ *     num_kv_heads and num_q_heads / num_kv_heads the plan's (DEFT_ESTATE)
+ *     and head_dim in {64, 128}; out 16-byte aligned.
+ *   out: [rows][num_q_heads][head_dim], lse: fp32 [rows][num_q_heads],
+ *     natural log; rows past the plan's are left as they were.
+ * Cache slots past a node's last token, and pages past those its length
+ * needs, never affect a result, whatever they hold.  The values of tokens in
+ * the cache must be finite (a NaN or infinity in V reaches every row of the
+ * tiles it is read in, attended or not).  page_id and node_page_off are
+ * trusted, as in deft_tree_attn; a page outside [0, num_pages) reads as
+ * zeros.  Steps of one plan may run at the same time on several streams,
+ * each with its own outputs and workspace.  Never allocates, never
+ * synchronises; stream-ordered on `stream`; may be captured into a CUDA
+ * graph.
+ *
+ * deft_prompt_status -- as deft_step_status, for the steps of this plan.
+ */
+int deft_prompt_attn(const void *q, int64_t q_stride, int32_t num_rows, const void *k_pages,
+                     const void *v_pages, const int32_t *node_page_off, const int32_t *page_id,
+                     int32_t num_pages, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                     int32_t page_size, float scale, const deft_prompt_plan_t *plan, void *out,
+                     int32_t out_dtype, float *lse, void *workspace, size_t workspace_bytes, void *stream);
+int deft_prompt_status(deft_prompt_plan_t *plan, void *stream, int32_t *code);
+
 /* Free a plan and its device copy (the caller must ensure no kernel using it
  * is still running).  NULL is a no-op. */
 void deft_plan_free(deft_plan_t *plan);

@@ -44,11 +44,21 @@ EXPORTS = ["deft_plan", "deft_plan_at", "deft_plan_ex", "deft_plan_rebuild", "de
            "deft_plan_update", "deft_pages_create", "deft_pages_free", "deft_pages_alloc",
            "deft_pages_retain", "deft_pages_release", "deft_pages_free_count", "deft_pages_refcount",
            "deft_plan_free", "deft_status_str", "deft_version", "deft_trace_enable",
-           "deft_trace_read", "deft_tree_attn_noalloc", "deft_tree_attn_host"]
+           "deft_trace_read", "deft_tree_attn_noalloc", "deft_tree_attn_host",
+           "deft_page_table_workspace_bytes", "deft_page_table", "deft_kv_write", "deft_prompt_plan",
+           "deft_prompt_plan_rebuild", "deft_prompt_plan_upload", "deft_prompt_plan_stats_get",
+           "deft_prompt_plan_get", "deft_prompt_plan_free", "deft_prompt_workspace_bytes",
+           "deft_prompt_attn", "deft_prompt_status"]
 
 KERNEL_NAMES = {0: "phase1_fma", 1: "phase1_mma", 2: "phase2_merge"}
 PLAN_TREE_ONLY = 1   # deft_plan_ex flags
 PLAN_TENSOR_PACK = 2
+# deft_page_table's counts[3]
+TABLE_BAD_LENGTH = 1
+TABLE_BAD_PREV = 2
+TABLE_NO_FREE_PAGE = 4
+TABLE_PAGE_CAP = 8
+TABLE_TOKEN_CAP = 16
 # deft_tree_attn_ex flags
 STEP_NAIVE = 1
 STEP_CUDA_CORES = 2
@@ -74,6 +84,15 @@ class PlanStats(ctypes.Structure):
         "max_chunk_tokens", "max_slots_per_query", "naive_num_chunks", "naive_num_slots",
         "naive_num_segments", "num_merge_queries", "reserved0")] + [(n, ctypes.c_int64) for n in (
         "unique_tokens", "naive_tokens", "planned_tokens", "pair_tokens", "device_bytes")]
+
+    def as_dict(self):
+        return {n: getattr(self, n) for n, _ in self._fields_}
+
+
+class PromptStats(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "num_nodes", "num_prompts", "num_rows", "num_items", "num_units", "num_split_items", "ctas",
+        "reserved0")] + [(n, ctypes.c_int64) for n in ("pair_tokens", "partial_slots", "device_bytes")]
 
     def as_dict(self):
         return {n: getattr(self, n) for n, _ in self._fields_}
@@ -125,12 +144,31 @@ def load(path: str = LIB_PATH):
     lib.deft_version.argtypes = []
     lib.deft_trace_enable.argtypes = [i32]
     lib.deft_trace_read.argtypes = [ctypes.POINTER(TraceRecord), i32, ctypes.POINTER(i32)]
+    i64 = ctypes.c_int64
+    lib.deft_page_table_workspace_bytes.argtypes = [i32]
+    lib.deft_page_table_workspace_bytes.restype = sz
+    lib.deft_page_table.argtypes = [P, i32, P, P, P, i32, i64, P, i32, i32, P, P, i32, P, P, i32, P, P, sz, P]
+    lib.deft_kv_write.argtypes = [P, P, i32, i64, i64, P, i32, P, P, i32, i32, i32, i32, P]
+    prompt = [P, P, i32, P, P, i32, i32, i32]
+    lib.deft_prompt_plan.argtypes = prompt + [ctypes.POINTER(P)]
+    lib.deft_prompt_plan_rebuild.argtypes = [P] + prompt
+    lib.deft_prompt_plan_upload.argtypes = [P, P]
+    lib.deft_prompt_plan_stats_get.argtypes = [P, ctypes.POINTER(PromptStats)]
+    lib.deft_prompt_plan_get.argtypes = [P, i32, P, sz]
+    lib.deft_prompt_plan_free.argtypes = [P]
+    lib.deft_prompt_plan_free.restype = None
+    lib.deft_prompt_workspace_bytes.argtypes = [P, i32, i32]
+    lib.deft_prompt_workspace_bytes.restype = sz
+    lib.deft_prompt_attn.argtypes = [P, i64, i32, P, P, P, P, i32, i32, i32, i32, i32, f32, P, P, i32, P, P, sz, P]
+    lib.deft_prompt_status.argtypes = [P, P, ctypes.POINTER(i32)]
     for fn in ("deft_plan", "deft_plan_at", "deft_plan_ex", "deft_plan_rebuild", "deft_plan_stats_get",
                "deft_plan_get", "deft_plan_upload", "deft_tree_attn", "deft_naive_attn", "deft_version",
                "deft_trace_enable", "deft_trace_read", "deft_tree_attn_noalloc", "deft_tree_attn_ex",
                "deft_step_status", "deft_check_pages", "deft_plan_update", "deft_pages_create",
                "deft_pages_alloc", "deft_pages_retain", "deft_pages_release", "deft_pages_free_count",
-               "deft_pages_refcount"):
+               "deft_pages_refcount", "deft_page_table", "deft_kv_write", "deft_prompt_plan",
+               "deft_prompt_plan_rebuild", "deft_prompt_plan_upload", "deft_prompt_plan_stats_get",
+               "deft_prompt_plan_get", "deft_prompt_attn", "deft_prompt_status"):
         getattr(lib, fn).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -449,6 +487,236 @@ class PagePool:
 
     def refcount(self, page: int) -> int:
         return int(load().deft_pages_refcount(self.handle, int(page)))
+
+
+def _on_device(*tensors):
+    """Raises unless every tensor is a CUDA tensor of the current device (the
+    library launches there)."""
+    import torch
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if not t.is_cuda or t.device.index != cur:
+            raise ValueError("tensors must be on the current CUDA device")
+
+
+def _heads_packed(x) -> bool:
+    """Whether x [tokens, heads, head_dim] holds each token's heads
+    contiguously (the stride of a dimension of one element says nothing)."""
+    return x.shape[0] == 0 or (x.stride(2) == 1 and (x.shape[1] == 1 or x.stride(1) == x.shape[2]))
+
+
+def _index_tensor(t, name: str, ndim: int = 1):
+    import torch
+    if t.dtype != torch.int32 or t.dim() != ndim or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous one-dimensional int32 tensor")
+    return t
+
+
+@dataclass
+class PageTable:
+    """Outputs of deft_page_table (int32 CUDA tensors): node_page_off and
+    page_id as the steps take them, tok_off / slot of the new tokens, counts =
+    (pages, pages taken from the free list, new tokens, 0 or TABLE_*).
+    workspace: page_table_workspace(num_nodes)."""
+    page_off: "object"
+    page_id: "object"
+    tok_off: "object"
+    slot: "object"
+    counts: "object"
+    workspace: "object" = None
+
+
+def page_table_workspace(num_nodes: int, device="cuda"):
+    """Device workspace deft_page_table needs for so many nodes (None: none)."""
+    import torch
+    n = int(load().deft_page_table_workspace_bytes(int(num_nodes)))
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def alloc_page_table(num_nodes: int, max_pages: int, max_tokens: int, device="cuda") -> PageTable:
+    """Tensors for a table of at most max_pages pages and max_tokens new tokens."""
+    import torch
+
+    def new(n):
+        return torch.empty(int(n), dtype=torch.int32, device=device)
+    return PageTable(new(num_nodes + 1), new(max_pages), new(num_nodes + 1), new(max_tokens), new(4),
+                     page_table_workspace(num_nodes, device))
+
+
+def deft_page_table(node_len, free_pages, prev=None, table: Optional[PageTable] = None, max_pages: Optional[int] = None,
+                    max_tokens: Optional[int] = None, page_size: int = 16, stream=None) -> PageTable:
+    """deft_page_table: page table and slot map of the nodes' new tokens.
+    prev: (prev_len, prev_page_off, prev_page_id) of the earlier table, None:
+    every node starts empty.  table: the tensors to write (reused between
+    steps); None: allocated for max_pages and max_tokens."""
+    nl, free = _index_tensor(node_len, "node_len"), _index_tensor(free_pages, "free_pages")
+    n = int(nl.shape[0])
+    if table is None:
+        if max_pages is None or max_tokens is None:
+            raise ValueError("max_pages and max_tokens are needed to allocate a table")
+        table = alloc_page_table(n, max_pages, max_tokens, nl.device)
+    t = table
+    for name in ("page_off", "page_id", "tok_off", "slot", "counts"):
+        _index_tensor(getattr(t, name), name)
+    if t.page_off.shape[0] < n + 1 or t.tok_off.shape[0] < n + 1 or t.counts.shape[0] < 4:
+        raise ValueError("page_off and tok_off need num_nodes + 1 entries, counts 4")
+    used = [nl, free, t.page_off, t.page_id, t.tok_off, t.slot, t.counts]
+    pl = po = pi = None
+    n_prev = n_ids = 0
+    if prev is not None:
+        pl, po, pi = (_index_tensor(x, "prev") for x in prev)
+        n_prev, n_ids = int(pl.shape[0]), int(pi.shape[0])
+        if po.shape[0] < n_prev:
+            raise ValueError("prev_page_off is shorter than prev_len")
+        used += [pl, po, pi]
+    if t.workspace is not None:
+        used.append(t.workspace)
+    _on_device(*used)
+    _check("deft_page_table", load().deft_page_table(
+        nl.data_ptr(), n, pl.data_ptr() if n_prev else None, po.data_ptr() if n_prev else None,
+        pi.data_ptr() if n_prev else None, n_prev, n_ids, free.data_ptr(), int(free.shape[0]), int(page_size),
+        t.page_off.data_ptr(), t.page_id.data_ptr(), int(t.page_id.shape[0]), t.tok_off.data_ptr(),
+        t.slot.data_ptr(), int(t.slot.shape[0]), t.counts.data_ptr(),
+        None if t.workspace is None else t.workspace.data_ptr(), 0 if t.workspace is None else int(t.workspace.numel()),
+        _stream(stream)))
+    return table
+
+
+def deft_kv_write(k, v, slot, k_pages, v_pages, stream=None):
+    """deft_kv_write: rows of k and v ([tokens, num_kv_heads, head_dim], bf16
+    or fp32, views with any token stride) into the pages at their slots; rows
+    with a slot outside the pool (-1) are skipped."""
+    import torch
+    T, Hkv, d = k.shape
+    if v.shape != k.shape or v.dtype != k.dtype or k.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("k and v must be alike: [tokens, heads, head_dim], bf16 or fp32")
+    if not _heads_packed(k) or not _heads_packed(v):
+        raise ValueError("the heads of a token must be contiguous")
+    for p in (k_pages, v_pages):
+        if p.dtype != torch.bfloat16 or not p.is_contiguous() or p.dim() != 4 or p.shape[1] != Hkv or p.shape[3] != d:
+            raise ValueError("k_pages and v_pages must be contiguous bf16 [pages, heads, page_size, head_dim]")
+    if k_pages.shape != v_pages.shape:
+        raise ValueError("k_pages and v_pages differ in shape")
+    _index_tensor(slot, "slot")
+    if slot.shape[0] != T:
+        raise ValueError("slot must have one entry per token")
+    _on_device(k, v, slot, k_pages, v_pages)
+    _check("deft_kv_write", load().deft_kv_write(
+        k.data_ptr(), v.data_ptr(), DEFT_OUT_BF16 if k.dtype == torch.bfloat16 else DEFT_OUT_F32, int(k.stride(0)),
+        int(v.stride(0)), slot.data_ptr(), int(T), k_pages.data_ptr(), v_pages.data_ptr(), int(k_pages.shape[0]),
+        int(Hkv), int(d), int(k_pages.shape[2]), _stream(stream)))
+
+
+PROMPT_ARRAYS = {"nodes": (0, 2), "items": (1, 12), "cta_off": (2, 1), "cta_unit": (3, 1), "merges": (4, 4)}
+
+
+class PromptPlan:
+    """Owner of a deft_prompt_plan_t handle.  parent None: every node a root;
+    prompt_len None: every prompt its whole node (an entry -1: the same)."""
+
+    def __init__(self, parent, node_len, prompt_node, num_kv_heads: int, gqa_group: int = 1, prompt_len=None):
+        h = ctypes.c_void_p()
+        args = self._args(parent, node_len, prompt_node, num_kv_heads, gqa_group, prompt_len)
+        _check("deft_prompt_plan", load().deft_prompt_plan(*args[0], ctypes.byref(h)))
+        self.handle = h
+        self._stats = None
+
+    @staticmethod
+    def _args(parent, node_len, prompt_node, num_kv_heads, gqa_group, prompt_len):
+        ln, pn = _i32(node_len), _i32(prompt_node)
+        par = None if parent is None else _i32(parent)
+        pl = None if prompt_len is None else _i32(prompt_len)
+        if par is not None and par.shape != ln.shape:
+            raise ValueError("parent and node_len differ in length")
+        if pl is not None and pl.shape != pn.shape:
+            raise ValueError("prompt_node and prompt_len differ in length")
+        # The arrays are held until the call has returned.
+        return (None if par is None else _ptr(par), _ptr(ln), int(ln.shape[0]), _ptr(pn),
+                None if pl is None else _ptr(pl), int(pn.shape[0]), int(num_kv_heads), int(gqa_group)), (par, ln, pn, pl)
+
+    def rebuild(self, parent, node_len, prompt_node, num_kv_heads: int, gqa_group: int = 1, prompt_len=None):
+        """deft_prompt_plan_rebuild; upload() again before the next step."""
+        args = self._args(parent, node_len, prompt_node, num_kv_heads, gqa_group, prompt_len)
+        _check("deft_prompt_plan_rebuild", load().deft_prompt_plan_rebuild(self.handle, *args[0]))
+        self._stats = None
+
+    def __del__(self):
+        h = getattr(self, "handle", None)
+        if h and _lib is not None:
+            _lib.deft_prompt_plan_free(h)
+            self.handle = None
+
+    @property
+    def stats(self) -> dict:
+        """deft_prompt_plan_stats_get, read once per build."""
+        if self._stats is None:
+            st = PromptStats()
+            _check("deft_prompt_plan_stats_get", load().deft_prompt_plan_stats_get(self.handle, ctypes.byref(st)))
+            self._stats = st.as_dict()
+        return self._stats
+
+    def get(self, name: str) -> np.ndarray:
+        """Host copy of one plan array (deft_prompt_plan_get), a row per record."""
+        which, width = PROMPT_ARRAYS[name]
+        s = self.stats
+        n = {"nodes": s["num_nodes"], "items": s["num_items"], "cta_off": 153, "cta_unit": s["num_units"],
+             "merges": s["num_split_items"]}[name]
+        out = np.zeros(max(n * width, 1), dtype=np.int32)
+        _check("deft_prompt_plan_get", load().deft_prompt_plan_get(self.handle, which, _ptr(out), out.nbytes))
+        return out[: n * width].reshape(n, width) if width > 1 else out[:n]
+
+    def upload(self, stream=None):
+        _check("deft_prompt_plan_upload", load().deft_prompt_plan_upload(self.handle, _stream(stream)))
+
+    def workspace_bytes(self, num_q_heads: int, head_dim: int) -> int:
+        return int(load().deft_prompt_workspace_bytes(self.handle, int(num_q_heads), int(head_dim)))
+
+    def step_status(self, stream=None) -> int:
+        """deft_prompt_status: 0, or the code of a kernel wait that ran out."""
+        code = ctypes.c_int32()
+        rc = load().deft_prompt_status(self.handle, _stream(stream), ctypes.byref(code))
+        if rc not in (0, -9):
+            _check("deft_prompt_status", rc)
+        return int(code.value)
+
+
+def deft_prompt_attn(q, k_pages, v_pages, node_page_off, page_id, plan: PromptPlan, bufs: Optional[StepBuffers] = None,
+                     scale: Optional[float] = None, out_dtype: int = DEFT_OUT_BF16, stream=None):
+    """Causal attention of the plan's prompts: q [rows, num_q_heads,
+    head_dim] bf16 (any token stride), rows packed prompt by prompt; returns
+    (out, lse).  bufs: alloc_buffers(plan, rows, num_q_heads, head_dim)."""
+    import torch
+    T, Hq, d = q.shape
+    if bufs is None:
+        bufs = alloc_buffers(plan, T, Hq, d, q.device, out_dtype)
+    if q.dtype != torch.bfloat16 or not _heads_packed(q):
+        raise ValueError("q must be bf16 with the heads of a token contiguous")
+    for t in (k_pages, v_pages):
+        if t.dtype != torch.bfloat16 or not t.is_contiguous() or t.dim() != 4 or t.shape[3] != d:
+            raise ValueError("k_pages and v_pages must be contiguous bf16 [pages, heads, page_size, head_dim]")
+    if k_pages.shape != v_pages.shape:
+        raise ValueError("k_pages and v_pages differ in shape")
+    _index_tensor(node_page_off, "node_page_off")
+    _index_tensor(page_id, "page_id")
+    if node_page_off.shape[0] < plan.stats["num_nodes"]:
+        raise ValueError("node_page_off is shorter than the plan's nodes")
+    if bufs.out.dtype not in (torch.bfloat16, torch.float32) or not bufs.out.is_contiguous() or \
+            tuple(bufs.out.shape[1:]) != (Hq, d) or bufs.out.shape[0] < plan.stats["num_rows"]:
+        raise ValueError("out must be contiguous bf16 or fp32 [rows, num_q_heads, head_dim]")
+    if bufs.lse.dtype != torch.float32 or not bufs.lse.is_contiguous() or tuple(bufs.lse.shape[1:]) != (Hq,) or \
+            bufs.lse.shape[0] < plan.stats["num_rows"]:
+        raise ValueError("lse must be contiguous fp32 [rows, num_q_heads]")
+    _on_device(q, k_pages, v_pages, node_page_off, page_id, bufs.out, bufs.lse, bufs.workspace)
+    if T == 0 and plan.stats["num_rows"] == 0:
+        return bufs.out, bufs.lse
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    odt = DEFT_OUT_BF16 if bufs.out.dtype == torch.bfloat16 else DEFT_OUT_F32
+    _check("deft_prompt_attn", load().deft_prompt_attn(
+        q.data_ptr(), int(q.stride(0)) if T > 1 else int(Hq * d), int(T), k_pages.data_ptr(), v_pages.data_ptr(),
+        node_page_off.data_ptr(), page_id.data_ptr(), int(k_pages.shape[0]), int(Hq), int(k_pages.shape[1]), int(d),
+        int(k_pages.shape[2]), float(scale), plan.handle, bufs.out.data_ptr(), odt, bufs.lse.data_ptr(),
+        bufs.workspace.data_ptr(), int(bufs.workspace.numel()), _stream(stream)))
+    return bufs.out, bufs.lse
 
 
 def deft_check_pages(node_len, node_page_off, page_id, num_pages: int, page_size: int = 16) -> int:

@@ -1,0 +1,471 @@
+// kvcache.cu -- filling the paged KV cache: page tables and slot maps built
+// on the GPU from node lengths (deft_page_table), and K / V rows written into
+// the pages by slot (deft_kv_write).
+//
+// Page tables.  With P = 16 tokens a page, node n of `len` tokens, `prev` of
+// them in the cache already, needs ceil(len / P) pages, keeps the first
+// min(ceil(prev / P), pages) of its earlier ones and brings max(0, len -
+// prev) new tokens.  Three exclusive sums over the nodes (pages, new tokens,
+// pages taken) give node_page_off, tok_off and each node's place in the free
+// list; the rest is a copy.  Sums saturate at 2^31 - 1 (saturating addition
+// of non-negative numbers is associative, so the scan may), which no
+// capacity reaches, so an overflow shows as a capacity exceeded.
+//
+// The work is a few bytes a page and a token, so a call costs its launch and
+// a chain of dependent loads, not bandwidth.  Up to kBlockNodes nodes it is
+// one launch: every CTA scans all lengths into shared memory itself (8 KB
+// from L2) and fills its share of the page ids and slots, found by binary
+// search in the scanned offsets, so a single long node is spread over all
+// CTAs as well.  Above that a first launch writes the sums of every block of
+// kBlockNodes nodes to the workspace, and each CTA of the second scans the
+// block sums and then only the blocks its share touches.
+//
+// KV write.  One thread moves 16 bytes of a page row (8 elements of one head
+// of one token), several in flight; reads are coalesced over a token's row
+// (all heads), writes over one head's row of 128 or 256 bytes.  Bound by
+// DRAM bandwidth for prompts, by latency for a decode step.
+#include <cstdint>
+
+#include "common.cuh"
+#include "deft_internal.h"
+
+namespace deft {
+namespace {
+
+constexpr int kTableThreads = 512;
+constexpr int kPerThread = 4;
+constexpr int kBlockNodes = kTableThreads * kPerThread;   // nodes scanned at once
+constexpr int kMaxBlocks = 512;                           // blocks of one call
+constexpr uint32_t kSat = 0x7fffffffu;
+
+// counts[3]
+constexpr int32_t kBadLength = DEFT_TABLE_BAD_LENGTH, kBadPrev = DEFT_TABLE_BAD_PREV, kNoPages = DEFT_TABLE_NO_FREE_PAGE,
+                  kPageCap = DEFT_TABLE_PAGE_CAP, kTokenCap = DEFT_TABLE_TOKEN_CAP;
+
+struct TableArgs {
+    const int32_t *node_len, *prev_len, *prev_off, *prev_id, *free_pages;
+    int32_t num_nodes, num_prev, num_free;
+    int64_t num_prev_ids;
+    int32_t *page_off, *page_id, *tok_off, *slot, *counts;
+    int32_t max_pages, max_tokens;
+    uint32_t *block_sums;   // [4][kMaxBlocks]: pages, tokens, taken, flags (null: one block)
+};
+
+struct Sum3 {
+    uint32_t pages, toks, taken;
+};
+
+__device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b)
+{
+    return min(a + b, kSat);
+}
+__device__ __forceinline__ Sum3 add(const Sum3 &a, const Sum3 &b)
+{
+    return Sum3{sat_add(a.pages, b.pages), sat_add(a.toks, b.toks), sat_add(a.taken, b.taken)};
+}
+
+// One node's pages, new tokens and pages taken from the free list.
+__device__ __forceinline__ Sum3 node_sum(const TableArgs &a, int n, int32_t &bad)
+{
+    int32_t len = a.node_len[n];
+    int32_t prev = n < a.num_prev ? a.prev_len[n] : 0;
+    if (len < 0 || prev < 0) {
+        bad |= kBadLength;
+        len = max(len, 0);
+        prev = max(prev, 0);
+    }
+    const uint32_t pages = ((uint32_t)len + kPageSize - 1) / kPageSize;
+    const uint32_t had = ((uint32_t)prev + kPageSize - 1) / kPageSize;
+    const uint32_t kept = min(had, pages);
+    if (kept > 0) {
+        const int64_t at = a.prev_off[n];
+        if (at < 0 || at + kept > a.num_prev_ids)
+            bad |= kBadPrev;
+    }
+    return Sum3{pages, (uint32_t)max(len - prev, 0), pages - kept};
+}
+
+// Exclusive scan over the CTA's threads; `total` is every thread's.
+__device__ __forceinline__ Sum3 cta_scan(Sum3 v, Sum3 *warp_sum, Sum3 &total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Sum3 inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const Sum3 u{__shfl_up_sync(0xffffffffu, inc.pages, o), __shfl_up_sync(0xffffffffu, inc.toks, o),
+                     __shfl_up_sync(0xffffffffu, inc.taken, o)};
+        if (lane >= o)
+            inc = add(inc, u);
+    }
+    __syncthreads();   // an earlier scan's readers are done
+    if (lane == 31)
+        warp_sum[warp] = inc;
+    __syncthreads();
+    Sum3 before{0, 0, 0};
+    total = Sum3{0, 0, 0};
+    for (int w = 0; w < kTableThreads / 32; ++w) {
+        if (w == warp)
+            before = total;
+        total = add(total, warp_sum[w]);
+    }
+    Sum3 exc{__shfl_up_sync(0xffffffffu, inc.pages, 1), __shfl_up_sync(0xffffffffu, inc.toks, 1),
+             __shfl_up_sync(0xffffffffu, inc.taken, 1)};
+    if (lane == 0)
+        exc = Sum3{0, 0, 0};
+    return add(before, exc);
+}
+
+// Sums of every block of nodes (more than one block only).
+__global__ void __launch_bounds__(kTableThreads) table_sums_kernel(TableArgs a)
+{
+    __shared__ Sum3 warp_sum[kTableThreads / 32];
+    grid_dep_launch();
+    int32_t bad = 0;
+    Sum3 v{0, 0, 0}, total;
+    const int first = blockIdx.x * kBlockNodes + threadIdx.x * kPerThread;
+    for (int i = 0; i < kPerThread; ++i)
+        if (first + i < a.num_nodes)
+            v = add(v, node_sum(a, first + i, bad));
+    cta_scan(v, warp_sum, total);
+    const int neg = __syncthreads_or(bad & kBadLength), prev = __syncthreads_or(bad & kBadPrev);
+    if (threadIdx.x == 0) {
+        a.block_sums[blockIdx.x] = total.pages;
+        a.block_sums[kMaxBlocks + blockIdx.x] = total.toks;
+        a.block_sums[2 * kMaxBlocks + blockIdx.x] = total.taken;
+        a.block_sums[3 * kMaxBlocks + blockIdx.x] = (neg ? kBadLength : 0) | (prev ? kBadPrev : 0);
+    }
+}
+
+struct TableSmem {
+    uint32_t blk[3][kMaxBlocks + 1];    // exclusive sums before each block
+    uint32_t off[3][kBlockNodes + 1];   // ... before each node of the block in hand
+    Sum3 warp_sum[kTableThreads / 32];
+};
+
+// Largest i in [lo, hi) with off[i] <= x (off[lo] <= x < off[hi]).
+__device__ __forceinline__ int find(const uint32_t *off, int lo, int hi, uint32_t x)
+{
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (off[mid] <= x)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kTableThreads) table_fill_kernel(TableArgs a, int32_t num_blocks)
+{
+    __shared__ TableSmem s;
+    const int tid = threadIdx.x;
+    int32_t bad = 0;
+    int in_hand = -1;
+    Sum3 total;
+    if (num_blocks > 1) {
+        grid_dep_wait();
+        Sum3 v{0, 0, 0};
+        if (tid < num_blocks) {
+            v = Sum3{a.block_sums[tid], a.block_sums[kMaxBlocks + tid], a.block_sums[2 * kMaxBlocks + tid]};
+            bad = (int32_t)a.block_sums[3 * kMaxBlocks + tid];
+        }
+        const Sum3 e = cta_scan(v, s.warp_sum, total);
+        if (tid <= num_blocks) {
+            s.blk[0][tid] = e.pages;
+            s.blk[1][tid] = e.toks;
+            s.blk[2][tid] = e.taken;
+        }
+        // num_blocks can equal the thread count: the end by thread 0.
+        if (tid == 0) {
+            s.blk[0][num_blocks] = total.pages;
+            s.blk[1][num_blocks] = total.toks;
+            s.blk[2][num_blocks] = total.taken;
+        }
+        __syncthreads();
+    }
+    // Scans block b's nodes into s.off (absolute offsets).
+    auto take_block = [&](int b) {
+        if (b == in_hand)
+            return;
+        __syncthreads();
+        in_hand = b;
+        const int first = b * kBlockNodes + tid * kPerThread;
+        Sum3 node[kPerThread], sum{0, 0, 0}, all;
+#pragma unroll
+        for (int i = 0; i < kPerThread; ++i) {
+            node[i] = first + i < a.num_nodes ? node_sum(a, first + i, bad) : Sum3{0, 0, 0};
+            sum = add(sum, node[i]);
+        }
+        Sum3 e = cta_scan(sum, s.warp_sum, all);
+        if (num_blocks > 1)
+            e = add(e, Sum3{s.blk[0][b], s.blk[1][b], s.blk[2][b]});
+#pragma unroll
+        for (int i = 0; i < kPerThread; ++i) {
+            s.off[0][tid * kPerThread + i] = e.pages;
+            s.off[1][tid * kPerThread + i] = e.toks;
+            s.off[2][tid * kPerThread + i] = e.taken;
+            e = add(e, node[i]);
+        }
+        if (tid == kTableThreads - 1) {
+            s.off[0][kBlockNodes] = e.pages;
+            s.off[1][kBlockNodes] = e.toks;
+            s.off[2][kBlockNodes] = e.taken;
+        }
+        __syncthreads();
+        if (num_blocks == 1)
+            total = all;
+    };
+    if (num_blocks == 1)
+        take_block(0);
+    const int grid = gridDim.x, cta = blockIdx.x;
+
+    // Page j of the node at index i of the block in hand (node n), or -1.
+    auto page_of = [&](int i, int n, uint32_t j) -> int32_t {
+        const uint32_t first_taken = s.off[2][i];
+        const uint32_t pages = s.off[0][i + 1] - s.off[0][i], kept = pages - (s.off[2][i + 1] - first_taken);
+        if (j < kept) {
+            const int64_t at = (int64_t)a.prev_off[n] + j;
+            return at >= 0 && at < a.num_prev_ids ? a.prev_id[at] : -1;
+        }
+        const uint32_t at = first_taken + (j - kept);
+        return at < (uint32_t)a.num_free ? a.free_pages[at] : -1;
+    };
+
+    // Offsets: block b by CTA b (and b + grid ...).
+    for (int b = cta; b < num_blocks; b += grid) {
+        take_block(b);
+        for (int i = tid; i < kBlockNodes && b * kBlockNodes + i < a.num_nodes; i += kTableThreads) {
+            a.page_off[b * kBlockNodes + i] = (int32_t)s.off[0][i];
+            a.tok_off[b * kBlockNodes + i] = (int32_t)s.off[1][i];
+        }
+    }
+    // Page ids: CTA's share of [0, max_pages), node blocks in turn.
+    {
+        const int64_t share = ((int64_t)a.max_pages + grid - 1) / grid;
+        const uint32_t lo = (uint32_t)min(share * cta, (int64_t)total.pages);
+        const uint32_t hi = (uint32_t)min(min(share * (cta + 1), (int64_t)a.max_pages), (int64_t)total.pages);
+        uint32_t at = lo;
+        while (at < hi) {
+            const int b = num_blocks > 1 ? find(s.blk[0], 0, num_blocks, at) : 0;
+            take_block(b);
+            const uint32_t end = min(hi, s.off[0][kBlockNodes]);
+            for (uint32_t x = at + tid; x < end; x += kTableThreads) {
+                const int i = find(s.off[0], 0, kBlockNodes, x);
+                a.page_id[x] = page_of(i, b * kBlockNodes + i, x - s.off[0][i]);
+            }
+            at = end;
+        }
+    }
+    // Slots: CTA's share of [0, max_tokens); past the last token, -1.
+    {
+        const int64_t share = ((int64_t)a.max_tokens + grid - 1) / grid;
+        const int64_t lo = min(share * cta, (int64_t)a.max_tokens), hi = min(lo + share, (int64_t)a.max_tokens);
+        const uint32_t held = (uint32_t)min(hi, (int64_t)total.toks);
+        uint32_t at = (uint32_t)min(lo, (int64_t)total.toks);
+        for (int64_t x = max(lo, (int64_t)total.toks) + tid; x < hi; x += kTableThreads)
+            a.slot[x] = -1;
+        while (at < held) {
+            const int b = num_blocks > 1 ? find(s.blk[1], 0, num_blocks, at) : 0;
+            take_block(b);
+            const uint32_t end = min(held, s.off[1][kBlockNodes]);
+            for (uint32_t x = at + tid; x < end; x += kTableThreads) {
+                const int i = find(s.off[1], 0, kBlockNodes, x);
+                const int n = b * kBlockNodes + i;
+                const uint32_t prev = n < a.num_prev ? (uint32_t)max(a.prev_len[n], 0) : 0u;
+                const uint32_t t = prev + (x - s.off[1][i]);
+                const int32_t page = page_of(i, n, t / kPageSize);
+                a.slot[x] = page < 0 || page >= INT32_MAX / kPageSize ? -1 : page * kPageSize + (int32_t)(t % kPageSize);
+            }
+            at = end;
+        }
+    }
+    // The ends of both offset arrays and the counts, by CTA 0: every CTA has
+    // the totals, and the flags of all nodes (scanned, or of the sums).
+    if (cta == 0) {
+        const int neg = __syncthreads_or(bad & kBadLength), prev = __syncthreads_or(bad & kBadPrev);
+        if (tid == 0) {
+            a.page_off[a.num_nodes] = (int32_t)total.pages;
+            a.tok_off[a.num_nodes] = (int32_t)total.toks;
+            a.counts[0] = (int32_t)total.pages;
+            a.counts[1] = (int32_t)total.taken;
+            a.counts[2] = (int32_t)total.toks;
+            int32_t st = (neg ? kBadLength : 0) | (prev ? kBadPrev : 0);
+            st |= total.taken > (uint32_t)a.num_free ? kNoPages : 0;
+            st |= total.pages > (uint32_t)a.max_pages ? kPageCap : 0;
+            st |= total.toks > (uint32_t)a.max_tokens ? kTokenCap : 0;
+            a.counts[3] = st;
+        }
+    }
+}
+
+// 8 elements from `src` as bf16.
+template <bool kF32>
+struct Row8 {
+    uint4 v[kF32 ? 2 : 1];
+    __device__ __forceinline__ void load(const void *src, int64_t elem)
+    {
+        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const char *>(src) + elem * (kF32 ? 4 : 2));
+        v[0] = __ldcs(p);
+        if constexpr (kF32)
+            v[1] = __ldcs(p + 1);
+    }
+    __device__ __forceinline__ uint4 bf16() const
+    {
+        if constexpr (!kF32) {
+            return v[0];
+        } else {
+            auto two = [](uint32_t x, uint32_t y) {
+                const __nv_bfloat162 r = __floats2bfloat162_rn(__uint_as_float(x), __uint_as_float(y));
+                return *reinterpret_cast<const uint32_t *>(&r);
+            };
+            return make_uint4(two(v[0].x, v[0].y), two(v[0].z, v[0].w), two(v[1].x, v[1].y), two(v[1].z, v[1].w));
+        }
+    }
+};
+
+struct WriteArgs {
+    const void *k, *v;
+    int64_t k_stride, v_stride;   // elements between tokens
+    const int32_t *slot;
+    uint4 *k_pages, *v_pages;
+    int32_t num_tokens, num_pages, num_kv_heads, head_dim;
+};
+
+constexpr int kWriteThreads = 256;
+
+// U 16-byte pieces a thread, kWriteThreads apart; a token's pieces are its K
+// row's, then its V row's (c8 = heads * head_dim / 8 each).
+template <bool kF32, int U>
+__global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(WriteArgs a, uint32_t c8, int64_t pieces)
+{
+    const uint32_t per_tok = 2 * c8, d8 = (uint32_t)a.head_dim / 8;
+    const int64_t x0 = (int64_t)blockIdx.x * (kWriteThreads * U) + threadIdx.x;
+    const int64_t num_slots = (int64_t)a.num_pages * kPageSize;
+    Row8<kF32> row[U];
+    int64_t dst[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t x = x0 + u * kWriteThreads;
+        dst[u] = -1;
+        if (x < pieces) {
+            const int64_t tok = x / per_tok;
+            const uint32_t j = (uint32_t)(x - tok * per_tok);
+            const bool is_v = j >= c8;
+            const uint32_t e = is_v ? j - c8 : j;
+            const int32_t slot = a.slot[tok];
+            if (slot >= 0 && slot < num_slots) {
+                const uint32_t h = e / d8, part = e - h * d8;
+                dst[u] = (((int64_t)(slot / kPageSize) * a.num_kv_heads + h) * kPageSize + slot % kPageSize) * d8 + part;
+                if (is_v)
+                    row[u].load(a.v, tok * a.v_stride + (int64_t)e * 8);
+                else
+                    row[u].load(a.k, tok * a.k_stride + (int64_t)e * 8);
+            }
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (dst[u] >= 0) {
+            const int64_t x = x0 + u * kWriteThreads;
+            const uint32_t j = (uint32_t)(x % per_tok);
+            (j >= c8 ? a.v_pages : a.k_pages)[dst[u]] = row[u].bf16();
+        }
+    }
+}
+
+template <bool kF32>
+int launch_write(const WriteArgs &a, cudaStream_t st)
+{
+    constexpr int U = 4;
+    const uint32_t c8 = (uint32_t)a.num_kv_heads * a.head_dim / 8;
+    const int64_t pieces = (int64_t)a.num_tokens * 2 * c8;
+    const int64_t blocks = (pieces + kWriteThreads * U - 1) / (kWriteThreads * U);
+    if (blocks > INT32_MAX)
+        return DEFT_EUNSUPPORTED;
+    kv_write_kernel<kF32, U><<<(unsigned)blocks, kWriteThreads, 0, st>>>(a, c8, pieces);
+    return cudaGetLastError() == cudaSuccess ? DEFT_OK : DEFT_ECUDA;
+}
+
+}  // namespace
+}  // namespace deft
+
+extern "C" {
+
+size_t deft_page_table_workspace_bytes(int32_t num_nodes)
+{
+    if (num_nodes < 1)
+        return 0;
+    return num_nodes <= deft::kBlockNodes ? 0 : (size_t)4 * deft::kMaxBlocks * sizeof(uint32_t);
+}
+
+int deft_page_table(const int32_t *node_len, int32_t num_nodes, const int32_t *prev_len, const int32_t *prev_page_off,
+                    const int32_t *prev_page_id, int32_t num_prev_nodes, int64_t num_prev_ids,
+                    const int32_t *free_pages, int32_t num_free, int32_t page_size, int32_t *node_page_off,
+                    int32_t *page_id, int32_t max_pages, int32_t *tok_off, int32_t *slot, int32_t max_tokens,
+                    int32_t *counts, void *workspace, size_t workspace_bytes, void *stream)
+{
+    using namespace deft;
+    if (!node_len || num_nodes < 1 || !node_page_off || !tok_off || !counts || num_free < 0 || max_pages < 0 ||
+        max_tokens < 0 || num_prev_nodes < 0 || num_prev_ids < 0 || num_prev_nodes > num_nodes)
+        return DEFT_EINVAL;
+    if ((num_free > 0 && !free_pages) || (max_pages > 0 && !page_id) || (max_tokens > 0 && !slot) ||
+        (num_prev_nodes > 0 && (!prev_len || !prev_page_off)) || (num_prev_ids > 0 && !prev_page_id))
+        return DEFT_EINVAL;
+    // The earlier table is read while the new one is written.
+    if (num_prev_nodes > 0 && (prev_page_off == node_page_off || prev_len == node_page_off || prev_len == tok_off ||
+                               (num_prev_ids > 0 && prev_page_id == page_id)))
+        return DEFT_EINVAL;
+    if (page_size != kPageSize || num_nodes > kMaxBlocks * kBlockNodes)
+        return DEFT_EUNSUPPORTED;
+    const size_t need = deft_page_table_workspace_bytes(num_nodes);
+    if (need && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < need))
+        return DEFT_EWORKSPACE;
+    TableArgs a{node_len, prev_len, prev_page_off, prev_page_id, free_pages, num_nodes, num_prev_nodes, num_free,
+                num_prev_ids, node_page_off, page_id, tok_off, slot, counts, max_pages, max_tokens,
+                need ? static_cast<uint32_t *>(workspace) : nullptr};
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const int blocks = (num_nodes + kBlockNodes - 1) / kBlockNodes;
+    // One CTA for every 2048 outputs, two an SM at most.
+    const int64_t outputs = (int64_t)max_pages + max_tokens;
+    const int64_t want = (outputs + 2047) / 2048;
+    const int grid = (int)(want < 1 ? 1 : want > 2 * num_sms() ? 2 * num_sms() : want);
+    if (blocks > 1) {
+        table_sums_kernel<<<blocks, kTableThreads, 0, st>>>(a);
+        if (cudaGetLastError() != cudaSuccess)
+            return DEFT_ECUDA;
+        return launch_dependent(table_fill_kernel, dim3(grid), dim3(kTableThreads), 0, st, a, blocks) == cudaSuccess
+                   ? DEFT_OK
+                   : DEFT_ECUDA;
+    }
+    table_fill_kernel<<<grid, kTableThreads, 0, st>>>(a, 1);
+    return cudaGetLastError() == cudaSuccess ? DEFT_OK : DEFT_ECUDA;
+}
+
+int deft_kv_write(const void *k, const void *v, int32_t in_dtype, int64_t k_stride, int64_t v_stride,
+                  const int32_t *slot, int32_t num_tokens, void *k_pages, void *v_pages, int32_t num_pages,
+                  int32_t num_kv_heads, int32_t head_dim, int32_t page_size, void *stream)
+{
+    using namespace deft;
+    if (num_tokens < 0 || num_pages < 1 || num_kv_heads < 1 || !k_pages || !v_pages || k_pages == v_pages ||
+        (in_dtype != DEFT_OUT_BF16 && in_dtype != DEFT_OUT_F32))
+        return DEFT_EINVAL;
+    if ((head_dim != 64 && head_dim != 128) || page_size != kPageSize || num_pages > INT32_MAX / kPageSize)
+        return DEFT_EUNSUPPORTED;
+    if (num_tokens == 0)
+        return DEFT_OK;
+    const int64_t row = (int64_t)num_kv_heads * head_dim;
+    const int64_t es = in_dtype == DEFT_OUT_F32 ? 4 : 2;
+    if (!k || !v || !slot || row > (1 << 24))
+        return DEFT_EINVAL;
+    // Rows are read in 16-byte pieces and do not overlap.
+    if (((uintptr_t)k | (uintptr_t)v | (uintptr_t)k_pages | (uintptr_t)v_pages) & 15u)
+        return DEFT_EINVAL;
+    if ((num_tokens > 1) && (k_stride < row || v_stride < row || (k_stride * es) % 16 || (v_stride * es) % 16))
+        return DEFT_EINVAL;
+    WriteArgs a{k, v, k_stride, v_stride, slot, static_cast<uint4 *>(k_pages), static_cast<uint4 *>(v_pages),
+                num_tokens, num_pages, num_kv_heads, head_dim};
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return in_dtype == DEFT_OUT_F32 ? launch_write<true>(a, st) : launch_write<false>(a, st);
+}
+
+}  // extern "C"

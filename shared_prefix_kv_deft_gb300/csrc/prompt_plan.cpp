@@ -1,0 +1,289 @@
+// prompt_plan.cpp -- host planner of the prompt step: query tiles, splits of
+// long key ranges, and the units each CTA runs.
+//
+// A prompt is the last m tokens of a node; its rows (m tokens x GQA group,
+// token-major, so that the heads of a group share every K and V tile) are
+// cut into tiles of floor(128 / group) tokens, and neighbouring tiles are
+// paired (tensor-core work of one hides under the softmax of the other).  A
+// tile reads the pages of the path in one order: the ancestors' from the
+// node's parent up to its root, then the node's own up to its last row's
+// token (causal), so the masked pages come last.
+//
+// Units (item x KV head) are dealt to kPromptCtas CTAs by list scheduling
+// on an estimated cost: in order, each to the CTA that is free first.  The
+// order is head-major, costliest item first: the CTAs running at a time read
+// few heads' K and V, which then stay in L2, and the last head's smallest
+// items fill the gaps at the end.  A dealt list needs no work queue, so
+// steps of one plan may run at the same time.
+//
+// When a few units would leave SMs idle or one unit would outlast the rest,
+// the page ranges of the items are cut into pieces whose partial results a
+// second launch merges by log-sum-exp.  The cut is chosen by simulating the
+// deal for a few piece sizes and taking the shortest, the merge counted.
+#include <algorithm>
+#include <cstring>
+#include <queue>
+
+#include "prompt_internal.h"
+
+namespace deft {
+namespace {
+
+// Estimated costs in KV tiles of a pair of query tiles.
+constexpr double kCostSingle = 0.75;  // a KV tile against one query tile
+constexpr double kCostUnit = 2.0;     // a unit's start and end
+constexpr double kCostMerge = 3.0;    // the merge launch
+constexpr int32_t kMinPieceTiles = 4; // shortest piece
+constexpr int64_t kMaxSimUnits = 8 * kPromptCtas;   // above, no split is looked for: many units balance by themselves
+
+int32_t pages_of(int64_t tokens) { return (int32_t)((tokens + kPageSize - 1) / kPageSize); }
+int32_t tiles_of(int32_t pages) { return (pages + kPromptTilePages - 1) / kPromptTilePages; }
+
+// An item before its page range is cut.
+struct Proto {
+    PromptItem it;
+    int32_t pages_a, pages_b;   // pages tile A / B reads from the path's first page on
+    int32_t prompt_above;       // pages of the ancestors
+    int32_t tiles() const { return tiles_of(std::max(pages_a, pages_b)); }
+    double tile_cost() const { return it.tok_b > 0 ? 1.0 : kCostSingle; }
+};
+
+int32_t pieces_of(const Proto &p, int32_t cap) { return 1 + (p.tiles() - 1) / cap; }
+
+using Slot = std::pair<double, int32_t>;   // (time a CTA is free, CTA)
+using Heap = std::priority_queue<Slot, std::vector<Slot>, std::greater<Slot>>;
+
+Heap idle_ctas()
+{
+    std::vector<Slot> v;
+    for (int32_t c = 0; c < kPromptCtas; ++c)
+        v.emplace_back(0.0, c);
+    return Heap(std::greater<Slot>(), std::move(v));
+}
+
+// Length of the deal when ranges are cut into pieces of at most `cap` tiles.
+double simulate(const std::vector<Proto> &protos, int32_t heads, int32_t cap)
+{
+    std::vector<double> cost;
+    bool split = false;
+    for (const Proto &p : protos) {
+        const int32_t n = pieces_of(p, cap), t = (p.tiles() + n - 1) / n;
+        split |= n > 1;
+        for (int32_t i = 0; i < n; ++i)
+            cost.push_back(kCostUnit + t * p.tile_cost());
+    }
+    std::sort(cost.begin(), cost.end(), std::greater<double>());
+    Heap heap = idle_ctas();
+    double end = 0;
+    for (int32_t h = 0; h < heads; ++h)
+        for (const double c : cost) {
+            Slot s = heap.top();
+            heap.pop();
+            s.first += c;
+            end = std::max(end, s.first);
+            heap.push(s);
+        }
+    return end + (split ? kCostMerge : 0.0);
+}
+
+}  // namespace
+
+int build_prompt_plan(const int32_t *parent, const int32_t *node_len, int32_t num_nodes, const int32_t *prompt_node,
+                      const int32_t *prompt_len, int32_t num_prompts, int32_t num_kv_heads, int32_t gqa_group,
+                      deft_prompt_plan_t *p)
+{
+    if (!node_len || num_nodes < 1 || num_prompts < 0 || (num_prompts > 0 && !prompt_node) || num_kv_heads < 1 ||
+        num_kv_heads > 65535 || gqa_group < 1 || gqa_group > kMmaMaxRows)
+        return DEFT_EINVAL;
+    for (int32_t n = 0; n < num_nodes; ++n) {
+        if (node_len[n] < 0)
+            return DEFT_EINVAL;
+        if (parent && (parent[n] < -1 || parent[n] >= num_nodes))
+            return DEFT_ERANGE;
+    }
+    // Nearest ancestor with tokens and the pages above each node, parents
+    // first; a node met again on the way up belongs to a cycle.
+    p->nodes.assign(2 * (size_t)num_nodes, -1);
+    std::vector<int64_t> above(num_nodes, -1);
+    std::vector<int32_t> way;
+    std::vector<uint8_t> seen(num_nodes, 0);   // 1: on the way, 2: done
+    for (int32_t n = 0; n < num_nodes; ++n) {
+        way.clear();
+        int32_t a = n;
+        while (a >= 0 && seen[a] == 0) {
+            seen[a] = 1;
+            way.push_back(a);
+            a = parent ? parent[a] : -1;
+        }
+        if (a >= 0 && seen[a] == 1)
+            return DEFT_ECYCLE;
+        for (auto it = way.rbegin(); it != way.rend(); ++it) {
+            const int32_t x = *it, up = parent ? parent[x] : -1;
+            const int32_t from = up < 0 ? -1 : node_len[up] > 0 ? up : p->nodes[2 * (size_t)up];
+            p->nodes[2 * (size_t)x] = from;
+            p->nodes[2 * (size_t)x + 1] = node_len[x];
+            above[x] = from < 0 ? 0 : above[from] + pages_of(node_len[from]);
+            if (above[x] + pages_of(node_len[x]) > (1 << 25) - 1)
+                return DEFT_EUNSUPPORTED;
+            seen[x] = 2;
+        }
+    }
+    p->num_nodes = num_nodes;
+    p->num_prompts = num_prompts;
+    p->num_kv_heads = num_kv_heads;
+    p->gqa_group = gqa_group;
+    p->items.clear();
+    p->cta_unit.clear();
+    p->merges.clear();
+    p->part_slots = 0;
+    deft_prompt_stats st{};
+
+    const int32_t tile_tok = kPromptRows / gqa_group;
+    std::vector<Proto> protos;
+    int64_t rows = 0, pair_tokens = 0;
+    for (int32_t i = 0; i < num_prompts; ++i) {
+        const int32_t n = prompt_node[i];
+        if (n < 0 || n >= num_nodes)
+            return DEFT_ERANGE;
+        const int32_t L = node_len[n];
+        const int32_t m = !prompt_len || prompt_len[i] == -1 ? L : prompt_len[i];
+        if (m < 0 || m > L)
+            return DEFT_ERANGE;
+        for (int32_t t = 0; t < m; t += 2 * tile_tok) {
+            Proto q{};
+            q.it.row0 = (int32_t)(rows + t);
+            q.it.tok_a = std::min(tile_tok, m - t);
+            q.it.tok_b = std::min(tile_tok, m - t - q.it.tok_a);
+            q.it.pos0 = L - m + t;
+            q.it.node = n;
+            q.it.part0 = -1;
+            q.prompt_above = (int32_t)above[n];
+            q.pages_a = (int32_t)above[n] + pages_of((int64_t)q.it.pos0 + q.it.tok_a);
+            q.pages_b = q.it.tok_b ? (int32_t)above[n] + pages_of((int64_t)q.it.pos0 + q.it.tok_a + q.it.tok_b) : 0;
+            protos.push_back(q);
+        }
+        rows += m;
+        if (rows > INT32_MAX)
+            return DEFT_EUNSUPPORTED;
+        // Tokens seen: those above (exactly, not in pages), then 1 .. m of
+        // the node's last m and all before them.
+        int64_t up = 0;
+        for (int32_t a = p->nodes[2 * (size_t)n]; m > 0 && a >= 0; a = p->nodes[2 * (size_t)a])
+            up += node_len[a];
+        pair_tokens += (int64_t)m * (up + L - m) + (int64_t)m * (m + 1) / 2;
+    }
+    if ((int64_t)protos.size() * num_kv_heads > INT32_MAX / 8)
+        return DEFT_EUNSUPPORTED;
+    p->num_rows = (int32_t)rows;
+
+    // Where to cut.
+    int32_t cap = INT32_MAX;
+    if ((int64_t)protos.size() * num_kv_heads <= kMaxSimUnits && !protos.empty()) {
+        double total = 0;
+        int32_t longest = 0;
+        for (const Proto &q : protos) {
+            total += q.tiles() * q.tile_cost();
+            longest = std::max(longest, q.tiles());
+        }
+        const double even = total * num_kv_heads / kPromptCtas;
+        double best = simulate(protos, num_kv_heads, cap);
+        for (const double part : {1.0, 0.7, 0.5, 0.35, 0.25}) {
+            const int32_t c = std::max(kMinPieceTiles, (int32_t)(even * part + 0.999));
+            if (c >= longest)
+                continue;
+            const double t = simulate(protos, num_kv_heads, c);
+            if (t < best) {
+                best = t;
+                cap = c;
+            }
+        }
+    }
+
+    // The items: pieces of equal length, whole KV tiles.
+    std::vector<std::pair<double, PromptItem>> cut;
+    for (Proto &q : protos) {
+        const int32_t n = pieces_of(q, cap), t = (q.tiles() + n - 1) / n;
+        const int32_t all = std::max(q.pages_a, q.pages_b);
+        const int32_t item_rows = (q.it.tok_a + q.it.tok_b) * gqa_group;
+        const int64_t piece_slots = (int64_t)item_rows * num_kv_heads;
+        int32_t made = 0;
+        const int64_t part0 = p->part_slots;
+        // The page the next piece starts at, walked along the path.
+        int32_t node = q.prompt_above > 0 ? p->nodes[2 * (size_t)q.it.node] : q.it.node, first = 0;
+        for (int32_t begin = 0; begin < all; begin += t * kPromptTilePages) {
+            const int32_t end = std::min(all, begin + t * kPromptTilePages);
+            PromptItem it = q.it;
+            it.pages = end - begin;
+            it.tiles_a = tiles_of(std::max(0, std::min(end, q.pages_a) - begin));
+            it.tiles_b = tiles_of(std::max(0, std::min(end, q.pages_b) - begin));
+            it.start_node = node;
+            it.start_page = first;
+            if (n > 1) {
+                if (part0 + (made + 1) * piece_slots > INT32_MAX)
+                    return DEFT_EUNSUPPORTED;
+                it.part0 = (int32_t)(part0 + made * piece_slots);
+            }
+            ++made;
+            cut.emplace_back(kCostUnit + std::max(it.tiles_a, it.tiles_b) * q.tile_cost(), it);
+            for (int32_t left = end - begin; left > 0 && end < all;) {
+                const int32_t here = node == q.it.node ? INT32_MAX : pages_of(node_len[node]) - first;
+                const int32_t step = std::min(left, here);
+                first += step;
+                left -= step;
+                if (step == here) {
+                    node = p->nodes[2 * (size_t)node];
+                    if (node < 0)
+                        node = q.it.node;
+                    first = 0;
+                }
+            }
+        }
+        if (n > 1) {
+            p->part_slots = part0 + made * piece_slots;
+            p->merges.push_back(PromptMerge{q.it.row0, q.it.tok_a + q.it.tok_b, (int32_t)part0, made});
+        }
+    }
+    std::stable_sort(cut.begin(), cut.end(), [](const auto &a, const auto &b) { return a.first > b.first; });
+    if ((int64_t)cut.size() * num_kv_heads > INT32_MAX)
+        return DEFT_EUNSUPPORTED;
+
+    // The deal.
+    std::vector<int32_t> owner((size_t)cut.size() * num_kv_heads);
+    p->cta_off.assign(kPromptCtas + 1, 0);
+    Heap heap = idle_ctas();
+    size_t u = 0;
+    for (int32_t h = 0; h < num_kv_heads; ++h)
+        for (size_t i = 0; i < cut.size(); ++i) {
+            Slot s = heap.top();
+            heap.pop();
+            s.first += cut[i].first;
+            owner[u++] = s.second;
+            ++p->cta_off[s.second + 1];
+            heap.push(s);
+        }
+    for (int32_t c = 0; c < kPromptCtas; ++c)
+        p->cta_off[c + 1] += p->cta_off[c];
+    std::vector<int32_t> at(p->cta_off.begin(), p->cta_off.end() - 1);
+    p->cta_unit.resize(u);
+    u = 0;
+    for (int32_t h = 0; h < num_kv_heads; ++h)
+        for (size_t i = 0; i < cut.size(); ++i)
+            p->cta_unit[at[owner[u++]]++] = (int32_t)i * num_kv_heads + h;
+    p->items.reserve(cut.size());
+    for (const auto &c : cut)
+        p->items.push_back(c.second);
+
+    st.num_nodes = num_nodes;
+    st.num_prompts = num_prompts;
+    st.num_rows = (int32_t)rows;
+    st.num_items = (int32_t)p->items.size();
+    st.num_units = (int32_t)p->cta_unit.size();
+    st.num_split_items = (int32_t)p->merges.size();
+    st.ctas = (int32_t)std::min<size_t>(kPromptCtas, p->cta_unit.size());
+    st.pair_tokens = pair_tokens;
+    st.partial_slots = p->part_slots;
+    p->stats = st;
+    return DEFT_OK;
+}
+
+}  // namespace deft

@@ -1,0 +1,514 @@
+"""GPU parity of the prompt path: deft_page_table, deft_kv_write and
+deft_prompt_attn against plain numpy / torch forms in 64 bits, and a run of
+them together with the tree step.
+
+Tolerances.  A bf16 rounding is off by at most 2^-8 of the value.  The
+attention kernel rounds each probability p_j to bf16 before the product with
+V, so its output is off by at most 2^-8 sum p_j |v_j| / sum p_j (`mean_abs`
+below, from the reference), and a bf16 output by another 2^-8 |out|.  Logits
+are fp32 sums of d exact products: off by at most d 2^-24 scale sum |q||k|;
+the sum of n probabilities in fp32 by n 2^-24 of itself, ex2 by 2^-22.
+"""
+from __future__ import annotations
+
+import math
+import random
+
+import numpy as np
+import pytest
+import torch
+
+import shared_prefix_kv_deft_gb300 as deft
+import workloads as W
+
+pytestmark = pytest.mark.gpu
+PAGE = 16
+NAN = float("nan")
+
+
+# ---------------------------------------------------------------------------
+# Reference
+# ---------------------------------------------------------------------------
+
+class Case:
+    """A tree whose nodes' K and V are kept per token (CPU, bf16) and
+    scattered into pages; slots that hold no token are NaN."""
+
+    def __init__(self, parent, node_len, prompt_node, prompt_len, hkv, group, d, seed=0, shuffle=True, q_pad=0, k_scale=1.0, fused=False):
+        rng = np.random.default_rng(seed)
+        g = torch.Generator().manual_seed(seed)
+        self.parent, self.node_len, self.prompt_node = list(parent), list(node_len), list(prompt_node)
+        self.new = [node_len[n] if prompt_len is None or prompt_len[i] < 0 else prompt_len[i] for i, n in enumerate(prompt_node)]
+        self.prompt_len, self.hkv, self.group, self.d = prompt_len, hkv, group, d
+        rows, hq = sum(self.new), hkv * group
+        self.k = [(torch.randn((n, hkv, d), generator=g) * k_scale).bfloat16() for n in node_len]
+        self.v = [torch.randn((n, hkv, d), generator=g).bfloat16() for n in node_len]
+        q = torch.randn((rows + q_pad, hq + 3 if fused else hq, d), generator=g).bfloat16()
+        self.q = q[:, 2:2 + hq] if fused else q
+        counts = [-(-n // PAGE) for n in node_len]
+        total = sum(counts)
+        self.num_pages = total + 5
+        ids = rng.permutation(self.num_pages)[:total] if shuffle else np.arange(total)
+        self.off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+        self.ids = ids.astype(np.int32)
+        kp = torch.full((self.num_pages, hkv, PAGE, d), NAN, dtype=torch.bfloat16)
+        vp = kp.clone()
+        for n, m in enumerate(node_len):
+            for j in range(counts[n]):
+                c = min(PAGE, m - j * PAGE)
+                pg = int(ids[self.off[n] + j])
+                kp[pg, :, :c] = self.k[n][j * PAGE:j * PAGE + c].transpose(0, 1)
+                vp[pg, :, :c] = self.v[n][j * PAGE:j * PAGE + c].transpose(0, 1)
+        self.kp, self.vp = kp.cuda(), vp.cuda()
+        self.qd = q.cuda()[:, 2:2 + hq] if fused else q.cuda()
+        self.npo = torch.from_numpy(self.off).cuda()
+        # an empty table still needs an address
+        self.pid = torch.from_numpy(self.ids if total else np.zeros(1, np.int32)).cuda()
+
+    def plan(self):
+        p = deft.PromptPlan(self.parent, self.node_len, self.prompt_node, self.hkv, self.group, prompt_len=self.prompt_len)
+        p.upload()
+        return p
+
+    def run(self, out_dtype=deft.DEFT_OUT_BF16, plan=None, scale=None, bufs=None):
+        plan = plan or self.plan()
+        out, lse = deft.deft_prompt_attn(self.qd, self.kp, self.vp, self.npo, self.pid, plan, bufs, scale=scale, out_dtype=out_dtype)
+        torch.cuda.synchronize()
+        assert plan.step_status() == 0
+        return out.cpu(), lse.cpu()
+
+    def reference(self, scale=None):
+        """(out, lse, sum p |v| / sum p, lse tolerance), 64 bits, row by row block."""
+        scale = 1 / math.sqrt(self.d) if scale is None else scale
+        dev = "cuda"
+        outs, lses, means, tols = [], [], [], []
+        row = 0
+        for p, n in enumerate(self.prompt_node):
+            way, a = [n], self.parent[n]
+            while a >= 0:
+                way.insert(0, a)
+                a = self.parent[a]
+            K = torch.cat([self.k[x] for x in way]).to(dev).double()
+            V = torch.cat([self.v[x] for x in way]).to(dev).double()
+            m, T = self.new[p], K.shape[0]
+            if m == 0:
+                continue
+            q = self.q[row:row + m].to(dev).double()
+            K, V = (x.repeat_interleave(self.group, 1) for x in (K, V))
+            s = torch.einsum("ihd,jhd->hij", q, K) * scale
+            hidden = torch.arange(T, device=dev)[None, :] > T - m + torch.arange(m, device=dev)[:, None]
+            big = torch.einsum("ihd,jhd->hij", q.abs(), K.abs()).masked_fill(hidden, 0).amax(-1) * scale
+            s.masked_fill_(hidden, -math.inf)
+            lse = torch.logsumexp(s, -1)
+            w = torch.exp(s - lse[..., None])
+            outs.append(torch.einsum("hij,jhd->ihd", w, V))
+            means.append(torch.einsum("hij,jhd->ihd", w, V.abs()))
+            lses.append(lse.T)
+            # the logits' error (and that of the shift by the maximum and of
+            # the sum's logarithm, each a rounding of the lse), the sum's
+            tols.append((big * (self.d + 4) * 2 ** -24 + (T + 8) * 2 ** -24 + lse.abs() * 2 ** -22 + 2 ** -20).T)
+            row += m
+        cat = lambda x, *s: torch.cat(x).cpu() if x else torch.zeros(0, *s)  # noqa: E731
+        hq = self.hkv * self.group
+        return cat(outs, hq, self.d), cat(lses, hq), cat(means, hq, self.d), cat(tols, hq)
+
+    def check(self, out_dtype=deft.DEFT_OUT_BF16, scale=None, plan=None):
+        out, lse = self.run(out_dtype, scale=scale, plan=plan)
+        self.compare(out, lse, scale)
+        return out, lse
+
+    def compare(self, out, lse, scale=None):
+        ref, rlse, mean, tol = self.reference(scale)
+        rows = sum(self.new)
+        f32 = out.dtype == torch.float32
+        # a probability's relative error besides its rounding is the logits'
+        # absolute error, twice (once through the sum)
+        bound = (2 ** -8 + 2 * tol[..., None]) * mean + (0 if f32 else 2 ** -8) * (ref.abs() + 2 ** -8 * mean) + 2 ** -24
+        err = (out[:rows].double() - ref).abs()
+        assert torch.isfinite(out[:rows]).all()
+        assert (err <= bound).all(), f"out: {(err / bound).max():.3f} of the bound"
+        lerr = (lse[:rows].double() - rlse).abs()
+        assert (lerr <= tol).all(), f"lse: {(lerr / tol).max():.3f} of the bound"
+
+
+def forest(lens, new=None, **kw):
+    return dict(parent=[-1] * len(lens), node_len=lens, prompt_node=list(range(len(lens))), prompt_len=new, **kw)
+
+
+# ---------------------------------------------------------------------------
+# deft_prompt_attn
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 255, 256, 257, 300])
+def test_one_prompt(n, d):
+    Case(**forest([n]), hkv=2, group=1, d=d, seed=n).check()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("group", [1, 2, 3, 4, 5, 7, 8, 16, 33, 64])
+def test_groups(group, d):
+    Case(**forest([150, 1, 37]), hkv=2, group=group, d=d, seed=group).check()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("seed", range(10))
+def test_random_trees(seed, d):
+    rng = random.Random(100 + seed)
+    n = rng.randint(2, 12)
+    parent = [-1 if i == 0 or rng.random() < 0.15 else rng.randrange(i) for i in range(n)]
+    lens = [0 if rng.random() < 0.15 else rng.choice([1, 16, rng.randint(1, 40), rng.randint(1, 500)]) for _ in range(n)]
+    nodes = [rng.randrange(n) for _ in range(rng.randint(1, 8))]
+    new = None if seed % 2 else [rng.choice([-1, 0, rng.randint(0, lens[x])]) for x in nodes]
+    Case(parent, lens, nodes, new, hkv=rng.choice([1, 2, 3]), group=rng.choice([1, 2, 4, 6]), d=d, seed=seed, shuffle=seed % 3 != 0,
+         q_pad=seed % 4).check()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens,new,hkv,group", [
+    ([4096], [1], 1, 8), ([4099], [3], 2, 4), ([5000, 31, 700], [40, 31, 1], 2, 3), ([2047, 1, 129], [64, 1, 129], 1, 1),
+    ([3000], [200], 1, 4), ([2500, 2500], [1, 1], 4, 64)])
+def test_split_ranges(lens, new, hkv, group, d):
+    c = Case(**forest(lens, new), hkv=hkv, group=group, d=d, seed=7)
+    plan = c.plan()
+    assert plan.stats["num_split_items"] > 0
+    c.check(plan=plan)
+    c.check(out_dtype=deft.DEFT_OUT_F32)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_chain_of_one_token_nodes(d):
+    n = 40      # every page of the path holds one token
+    Case([-1] + list(range(n - 1)), [1] * n, [n - 1, 17, 0], None, hkv=1, group=2, d=d).check()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_growing_logits(d):
+    """Keys scaled up along the node: later tiles exceed earlier maxima by far
+    more than the rescale threshold."""
+    c = Case(**forest([700]), hkv=1, group=2, d=d, seed=3)
+    ramp = (1 + torch.arange(700) * 0.1)[:, None, None]
+    c.k[0] = (c.k[0].float() * ramp).bfloat16()
+    for j in range(44):
+        m = min(16, 700 - 16 * j)
+        c.kp[int(c.ids[j]), :, :m] = c.k[0][16 * j:16 * j + m].transpose(0, 1).cuda()
+    c.check()
+    c.check(out_dtype=deft.DEFT_OUT_F32)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_fused_projection_view_and_padding(d):
+    """q as a view of a wider row, more q rows than the plan's: rows past the
+    plan's are left as they were."""
+    c = Case(**forest([90, 33]), hkv=2, group=2, d=d, q_pad=50, fused=True)
+    assert not c.qd.is_contiguous()
+    plan = c.plan()
+    bufs = deft.alloc_buffers(plan, 173, 4, d)
+    bufs.out.fill_(7)
+    bufs.lse.fill_(9)
+    out, lse = c.run(plan=plan, bufs=bufs)
+    c.compare(out, lse)
+    assert (out[123:] == 7).all() and (lse[123:] == 9).all()
+
+
+def test_closed_forms():
+    """q = 0: the mean of the values seen and ln of their number."""
+    c = Case(parent=[-1, 0], node_len=[100, 60], prompt_node=[1], prompt_len=None, hkv=1, group=1, d=128)
+    c.qd.zero_()
+    out, lse = c.run(out_dtype=deft.DEFT_OUT_F32)
+    seen = torch.arange(101, 161).double()
+    assert ((lse[:, 0].double() - seen.log()).abs() < 2 ** -20).all()
+    mean = torch.cat([c.v[0], c.v[1]]).double()[:, 0].cumsum(0)[100:] / seen[:, None]
+    # every probability is 1: no rounding but the fp32 sums
+    assert ((out[:, 0].double() - mean).abs() < 160 * 2 ** -24 * 4).all()
+
+
+def test_scale_and_types():
+    c = Case(**forest([200]), hkv=1, group=4, d=64)
+    for scale in (0.01, 1.0):
+        c.check(scale=scale)
+    a, la = c.run(out_dtype=deft.DEFT_OUT_F32)
+    b, lb = c.run()
+    assert torch.equal(a.bfloat16(), b) and torch.equal(la, lb)
+
+
+def test_repeatable_and_streams():
+    """Bitwise repeatable; one plan on two streams at once, each with its own
+    outputs and workspace."""
+    c = Case(**forest([3000, 500], [100, 500]), hkv=2, group=4, d=128)
+    plan = c.plan()
+    ref = c.run(plan=plan)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    bufs = [deft.alloc_buffers(plan, 600, 8, 128) for _ in streams]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, b in zip(streams, bufs):
+            deft.deft_prompt_attn(c.qd, c.kp, c.vp, c.npo, c.pid, plan, b, stream=s)
+    torch.cuda.synchronize()
+    for b in bufs:
+        assert torch.equal(b.out.cpu(), ref[0]) and torch.equal(b.lse.cpu(), ref[1])
+    assert plan.step_status() == 0
+
+
+def test_captured_and_replayed():
+    c = Case(**forest([2000, 77], [60, 77]), hkv=2, group=4, d=128)
+    plan = c.plan()
+    bufs = deft.alloc_buffers(plan, 137, 8, 128)
+    ref = c.run(plan=plan)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        deft.deft_prompt_attn(c.qd, c.kp, c.vp, c.npo, c.pid, plan, bufs)
+    s.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        deft.deft_prompt_attn(c.qd, c.kp, c.vp, c.npo, c.pid, plan, bufs)
+    bufs.out.zero_()
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(bufs.out.cpu(), ref[0]) and torch.equal(bufs.lse.cpu(), ref[1])
+
+
+def test_no_rows_and_refusals():
+    c = Case(**forest([40], [0]), hkv=1, group=1, d=64)
+    out, lse = c.run()
+    assert out.shape[0] == 0
+    c = Case(**forest([40]), hkv=1, group=1, d=64)
+    plan = c.plan()
+    with pytest.raises((ValueError, deft.DeftError)):     # fewer q rows than the plan's
+        deft.deft_prompt_attn(c.qd[:39], c.kp, c.vp, c.npo, c.pid, plan)
+    with pytest.raises(ValueError):
+        deft.deft_prompt_attn(c.qd.float(), c.kp, c.vp, c.npo, c.pid, plan)
+    with pytest.raises(ValueError):
+        deft.deft_prompt_attn(c.qd.cpu(), c.kp, c.vp, c.npo, c.pid, plan)
+    with pytest.raises(ValueError):
+        deft.deft_prompt_attn(c.qd, c.kp, c.vp, c.npo.long(), c.pid, plan)
+    small = deft.alloc_buffers(plan, 40, 1, 64)
+    small.workspace = small.workspace[:0]
+    with pytest.raises(deft.DeftError):
+        deft.deft_prompt_attn(c.qd, c.kp, c.vp, c.npo, c.pid, plan, small)
+
+
+def test_long_prompt_against_the_definition():
+    """One 6001-token prompt with grouped heads: 47 query tiles a head."""
+    Case(**forest([6001]), hkv=1, group=4, d=128, seed=11).check()
+
+
+def test_wide_batch():
+    """More units than CTAs, so every CTA runs several in turn."""
+    rng = random.Random(5)
+    lens = [rng.randint(1, 400) for _ in range(120)]
+    Case(**forest(lens), hkv=4, group=2, d=128, seed=12).check()
+    Case(**forest(lens), hkv=4, group=3, d=64, seed=12).check()
+
+
+# ---------------------------------------------------------------------------
+# deft_page_table
+# ---------------------------------------------------------------------------
+
+def table_reference(lens, prev, prev_off, prev_id, free):
+    off, ids, tok, slot, took = [0], [], [0], [], 0
+    for n, x in enumerate(lens):
+        p = prev[n] if n < len(prev) else 0
+        pages = -(-x // PAGE)
+        kept = min(-(-p // PAGE), pages)
+        own = [int(prev_id[prev_off[n] + j]) for j in range(kept)] + [int(free[took + j]) for j in range(pages - kept)]
+        took += pages - kept
+        ids += own
+        off.append(len(ids))
+        slot += [own[t // PAGE] * PAGE + t % PAGE for t in range(p, x)]
+        tok.append(len(slot))
+    return off, ids, tok, slot, took
+
+
+def cu(a):
+    return torch.from_numpy(np.ascontiguousarray(np.asarray(a, dtype=np.int32))).cuda()
+
+
+@pytest.mark.parametrize("nodes", [1, 2, 31, 257, 2047, 2048, 2049, 5000, 70000])
+@pytest.mark.parametrize("with_prev", [False, True])
+def test_page_table(nodes, with_prev):
+    rng = np.random.default_rng(nodes)
+    hi = 40 if nodes > 10000 else 200
+    lens = rng.integers(0, hi, nodes)
+    if nodes > 2:
+        lens[nodes // 2] = 30000       # one node over several CTAs' shares
+    n_prev = nodes - nodes // 3 if with_prev else 0
+    # grown, unchanged and shrunken nodes
+    prev = np.maximum(0, lens[:n_prev] + rng.integers(-40, 20, n_prev)) if n_prev else np.zeros(0, int)
+    prev_pages = -(-prev // PAGE)
+    prev_off = np.concatenate([[0], np.cumsum(prev_pages)])
+    pool = rng.permutation(int(prev_off[-1]) + int((-(-lens // PAGE)).sum()) + 5)
+    prev_id, free = pool[:prev_off[-1]], pool[prev_off[-1]:]
+    off, ids, tok, slot, took = table_reference(lens, prev, prev_off, prev_id, free)
+    t = deft.deft_page_table(cu(lens), cu(free), prev=(cu(prev), cu(prev_off), cu(prev_id)) if n_prev else None, max_pages=len(ids) + 3,
+                             max_tokens=len(slot) + 37)
+    assert t.counts.tolist() == [len(ids), took, len(slot), 0]
+    assert t.page_off.tolist() == off and t.page_id[:len(ids)].tolist() == ids
+    assert t.tok_off.tolist() == tok and t.slot.tolist() == slot + [-1] * 37
+
+
+def test_page_table_leaves_the_rest_and_reuses_tensors():
+    t = deft.alloc_page_table(3, 10, 40)
+    t.page_id.fill_(-7)
+    for lens in ([20, 0, 5], [1, 1, 1]):
+        deft.deft_page_table(cu(lens), cu(range(9)), table=t)
+        used = sum(-(-x // PAGE) for x in lens)
+        assert t.counts.tolist() == [used, used, sum(lens), 0]
+        assert t.slot.tolist()[sum(lens):] == [-1] * (40 - sum(lens))
+    assert t.page_id.tolist()[3:] == [-7] * 7
+
+
+@pytest.mark.parametrize("nodes", [3, 3000])
+def test_page_table_reports(nodes):
+    """Every shortage is reported, nothing is written past a capacity, tokens
+    without a page get -1."""
+    lens = [33] + [1] * (nodes - 1)
+    need, toks = nodes + 2, nodes + 32
+    t = deft.deft_page_table(cu(lens), cu(range(2)), max_pages=need, max_tokens=toks)
+    assert t.counts.tolist() == [need, need, toks, deft.TABLE_NO_FREE_PAGE]
+    assert t.page_id.tolist() == [0, 1] + [-1] * (need - 2) and t.slot.tolist() == list(range(32)) + [-1] * (toks - 32)
+    big = deft.alloc_page_table(nodes, need, toks)
+    big.page_id.fill_(-7)
+    big.slot.fill_(-7)
+    full_p, full_s = big.page_id, big.slot
+    big.page_id, big.slot = full_p[:2], full_s[:5]
+    deft.deft_page_table(cu(lens), cu(range(need)), table=big)
+    assert big.counts.tolist() == [need, need, toks, deft.TABLE_PAGE_CAP | deft.TABLE_TOKEN_CAP]
+    assert full_p.tolist() == [0, 1] + [-7] * (need - 2) and full_s.tolist() == list(range(5)) + [-7] * (toks - 5)
+    bad = list(lens)
+    bad[-1] = -5
+    t = deft.deft_page_table(cu(bad), cu(range(need)), max_pages=need, max_tokens=toks)
+    assert t.counts.tolist() == [need - 1, need - 1, toks - 1, deft.TABLE_BAD_LENGTH]
+    # earlier pages outside the earlier table
+    t = deft.deft_page_table(cu(lens), cu(range(need)), prev=(cu([16]), cu([5]), cu([3, 4])), max_pages=need, max_tokens=toks)
+    assert t.counts.tolist()[3] == deft.TABLE_BAD_PREV and t.page_id.tolist()[0] == -1
+    # sums past 31 bits
+    t = deft.deft_page_table(cu([2 ** 31 - 1] * nodes), cu(range(4)), max_pages=4, max_tokens=8)
+    assert t.counts.tolist()[2:] == [2 ** 31 - 1, deft.TABLE_NO_FREE_PAGE | deft.TABLE_PAGE_CAP | deft.TABLE_TOKEN_CAP]
+    assert t.page_id.tolist() == [0, 1, 2, 3] and t.slot.tolist() == list(range(8))
+
+
+def test_page_table_captured():
+    lens, free = cu([40, 3]), cu(range(10, 20))
+    t = deft.alloc_page_table(2, 8, 64)
+    deft.deft_page_table(lens, free, table=t)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        deft.deft_page_table(lens, free, table=t)
+    lens.copy_(cu([1, 17]))
+    g.replay()
+    assert t.counts.tolist() == [3, 3, 18, 0] and t.page_id.tolist()[:3] == [10, 11, 12]
+    assert t.slot.tolist()[:18] == [160] + list(range(176, 193))
+
+
+# ---------------------------------------------------------------------------
+# deft_kv_write
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("tokens,hkv", [(1, 1), (5, 3), (33, 8), (1000, 2), (4097, 1)])
+def test_kv_write(tokens, hkv, d, dtype):
+    g = torch.Generator().manual_seed(tokens)
+    rng = np.random.default_rng(tokens)
+    qkv = torch.randn((tokens, 3 * hkv, d), generator=g).to(dtype).cuda()
+    k, v = qkv[:, hkv:2 * hkv], qkv[:, 2 * hkv:]
+    pages = -(-tokens // PAGE) + 3
+    slot = rng.permutation(pages * PAGE)[:tokens]
+    slot[rng.random(tokens) < 0.1] = -1
+    if tokens > 2:
+        slot[1] = pages * PAGE          # behind the pool: skipped as well
+    kp = torch.full((pages, hkv, PAGE, d), 3.0, dtype=torch.bfloat16, device="cuda")
+    vp = torch.full_like(kp, 4.0)
+    wk, wv = kp.cpu(), vp.cpu()
+    for t, s in enumerate(slot):
+        if 0 <= s < pages * PAGE:
+            wk[s // PAGE, :, s % PAGE] = k[t].cpu().bfloat16()
+            wv[s // PAGE, :, s % PAGE] = v[t].cpu().bfloat16()
+    deft.deft_kv_write(k, v, cu(slot), kp, vp)
+    assert torch.equal(kp.cpu(), wk) and torch.equal(vp.cpu(), wv)
+
+
+def test_kv_write_specials_and_refusals():
+    k = torch.tensor([NAN, math.inf, -math.inf, 1e-40, 3.4e38, 1 + 2 ** -8, 1 + 3 * 2 ** -8, -0.0] * 8).view(1, 1, 64).cuda()
+    kp = torch.zeros((1, 1, PAGE, 64), dtype=torch.bfloat16, device="cuda")
+    vp = torch.zeros_like(kp)
+    deft.deft_kv_write(k, -k, cu([3]), kp, vp)
+    assert torch.equal(kp[0, 0, 3].isnan(), k[0, 0].bfloat16().isnan())
+    assert torch.equal(kp[0, 0, 3].nan_to_num(1).view(torch.int16), k[0, 0].bfloat16().nan_to_num(1).view(torch.int16))
+    deft.deft_kv_write(k[:0], k[:0], cu([]), kp, vp)
+    with pytest.raises(ValueError):
+        deft.deft_kv_write(k, k.bfloat16(), cu([0]), kp, vp)
+    with pytest.raises(ValueError):
+        deft.deft_kv_write(k.half(), k.half(), cu([0]), kp, vp)
+    with pytest.raises(ValueError):
+        deft.deft_kv_write(k, k, cu([0, 1]), kp, vp)
+    with pytest.raises(ValueError):
+        deft.deft_kv_write(k, k, cu([0]).cpu(), kp, vp)
+    with pytest.raises(deft.DeftError):     # rows that are not 16-byte aligned
+        deft.deft_kv_write(*(torch.zeros(65, device="cuda")[1:].view(1, 1, 64) for _ in "kv"), cu([0]), kp, vp)
+
+
+# ---------------------------------------------------------------------------
+# Together: prefill of a prefix, prefill of branches under it, a decode step
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("hkv,group,d", [(2, 4, 128), (4, 1, 64)])
+def test_prefill_then_tree_decode(hkv, group, d):
+    """A 300-token prefix and 20 branches of 45 tokens under it enter the
+    cache through deft_page_table and deft_kv_write, attend through
+    deft_prompt_attn, then grow by a token each and take a tree step."""
+    hq, pool = hkv * group, deft.PagePool(200)
+    parent = [-1] + [0] * 20
+    lens_at = [[300] + [0] * 20, [300] + [45] * 20, [300] + [46] * 20]
+    c = Case(parent, lens_at[2], list(range(21)), None, hkv, group, d, seed=21)      # every token's K and V, and q rows
+    kp = torch.full((200, hkv, PAGE, d), NAN, dtype=torch.bfloat16, device="cuda")
+    vp = kp.clone()
+    prev, spec = None, None
+    qrow = dict(zip(range(21), np.concatenate([[0], np.cumsum(lens_at[2])[:-1]])))
+    ref, rlse, mean, tol = c.reference()
+    before = [0] * 21
+    for lens in lens_at[:2]:
+        free = pool.alloc(sum(-(-x // PAGE) for x in lens) - sum(-(-x // PAGE) for x in before))
+        t = deft.deft_page_table(cu(lens), cu(free), prev=prev, max_pages=200, max_tokens=1500)
+        total = sum(lens) - sum(before)
+        assert t.counts.tolist() == [sum(-(-x // PAGE) for x in lens), len(free), total, 0]
+        pad = torch.zeros((1500 - total, hkv, d), dtype=torch.bfloat16)
+        k, v = (torch.cat([x[n][before[n]:lens[n]] for n in range(21)] + [pad]).cuda() for x in (c.k, c.v))
+        deft.deft_kv_write(k, v, t.slot, kp, vp)
+        nodes = [n for n in range(21) if lens[n] > before[n]]
+        plan = deft.PromptPlan(parent, lens, nodes, hkv, group, prompt_len=[lens[n] - before[n] for n in nodes])
+        plan.upload()
+        rows = np.concatenate([qrow[n] + np.arange(before[n], lens[n]) for n in nodes])
+        out, lse = deft.deft_prompt_attn(c.q[rows].cuda(), kp, vp, t.page_off, t.page_id, plan)
+        err = (out.cpu().double() - ref[rows]).abs()
+        bound = (2 ** -8 + 2 * tol[rows][..., None]) * mean[rows] + 2 ** -8 * (ref[rows].abs() + 2 ** -8 * mean[rows]) + 2 ** -24
+        assert (err <= bound).all() and ((lse.cpu().double() - rlse[rows]).abs() <= tol[rows]).all()
+        prev, before = (cu(lens), t.page_off, t.page_id), lens
+    lens = lens_at[2]
+    free = pool.alloc(sum(-(-x // PAGE) for x in lens) - sum(-(-x // PAGE) for x in before))
+    t = deft.deft_page_table(cu(lens), cu(free), prev=prev, max_pages=200, max_tokens=20)
+    assert t.counts.tolist()[3] == 0
+    k, v = (torch.cat([x[n][45:46] for n in range(1, 21)]).cuda() for x in (c.k, c.v))
+    deft.deft_kv_write(k, v, t.slot, kp, vp)
+    assert deft.deft_check_pages(lens, t.page_off.cpu().numpy(), t.page_id.cpu().numpy(), 200) == 0
+    plan = deft.Plan(parent, lens, list(range(1, 21)), 256, group)
+    plan.upload()
+    rows = [qrow[n] + 45 for n in range(1, 21)]
+    out, lse = deft.deft_tree_attn(c.q[rows].cuda(), kp, vp, t.page_off, t.page_id, plan)
+    # the tree step's own tolerances
+    assert (out.cpu().double() - ref[rows]).abs().max() <= 1e-2 and (lse.cpu().double() - rlse[rows]).abs().max() <= 1e-3
+    # and the prompt step on the same single tokens
+    plan = deft.PromptPlan(parent, lens, list(range(1, 21)), hkv, group, prompt_len=[1] * 20)
+    plan.upload()
+    out, lse = deft.deft_prompt_attn(c.q[rows].cuda(), kp, vp, t.page_off, t.page_id, plan)
+    err = (out.cpu().double() - ref[rows]).abs()
+    assert (err <= (2 ** -8 + 2 * tol[rows][..., None]) * mean[rows] + 2 ** -8 * (ref[rows].abs() + 2 ** -8 * mean[rows]) + 2 ** -24).all()
+
+
+@pytest.mark.parametrize("i", [1, 4])
+def test_workload_prefill(i):
+    """Every node of a benchmark tree as a prompt."""
+    s = W.config(i)
+    Case(s.parent.tolist(), s.node_len.tolist(), list(range(s.num_nodes)), None, min(s.num_kv_heads, 2), s.gqa_group, s.head_dim, seed=i).check()
