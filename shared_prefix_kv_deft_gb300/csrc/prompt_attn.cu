@@ -1,85 +1,719 @@
-// prompt_attn.cu -- attention of whole prompts over the paged cache: a
-// simple form, one warp per row and head, tokens one after another.
+// prompt_attn.cu -- attention of whole prompts over the paged cache on
+// tcgen05 tensor cores (deft_prompt_attn), head_dim 64 and 128.
+//
+// Formulation: query rows on the MMA's M dimension, KV tokens on N in tiles
+// of 128 (eight pages of the path, whichever nodes they belong to):
+//     S[128 rows x 128 tok]  = Q . K_tile^T          (TMEM, fp32)
+//     O[128 rows x d]       += P . V_tile            (TMEM, fp32; P bf16 in TMEM)
+// A row is a (token, head of the group) pair, token-major, so the heads that
+// share a KV head share its tiles.  A CTA works on two row tiles, A and B:
+// while the softmax of one runs on its warpgroup, the tensor core works for
+// the other.  S of a tile and its P share 128 TMEM columns (P replaces the
+// S it came from), and PV(t) is issued before S(t + 1), so the tensor core's
+// program order protects both: 2 x 128 columns of S / P and 2 x d of O fill
+// the 512 TMEM columns at d = 128.
+//
+// A softmax thread owns one row: no exchange between threads.  The running
+// maximum is stale: it is raised, and O and the sum rescaled, only when a
+// logit exceeds it by 2^8 (base 2), decided per warp; the sum is fp32 over
+// the unrounded probabilities.  P is rounded to bf16, the type of V (one MMA
+// has one operand type): half a step of 2^-8 on each probability, of the
+// size of the bf16 output's own rounding.
+//
+// Masks.  Only the tiles that hold a partial page, a page past the range or
+// own tokens past a row's position are masked; a tile's description (page
+// counts and positions) travels with its K and V.  V rows of slots past a
+// node's last token are zeroed in shared memory before the product (their P
+// is 0, which must not meet a NaN), K's need not be: their logits are
+// replaced.
+//
+// Bound: at 256 rows a KV tile costs 2 x 2 x 256 x 128 x d flop against 256 x
+// 128 exponentials; the tensor core's time is the longer one.
+//
+// Roles (12 warps): warps 0-3 and 4-7 softmax and output of tiles A and B (216 registers
+// a thread), warp 8 the TMA producer (a lane a page), warp 9 the MMA issuer;
+// the last warpgroup runs with 72 registers.  Every hand-off is an mbarrier,
+// every wait is bounded; a CTA whose wait runs out fills its rows with NaN,
+// records the code, waits for its copies and MMAs, frees TMEM and returns.
+#include <atomic>
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "common.cuh"
 #include "prompt_internal.h"
+#include "tcgen05.cuh"
 
 namespace deft {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 384;
+constexpr uint32_t kRegsSoftmax = 216, kRegsOther = 72;
+static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsOther == kThreads * 168, "register split");
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kHalf = 128 * 128;   // 128 rows x 64 dims, bf16, 128-byte swizzled
+constexpr int kMetaSlots = 8;
+constexpr int kMetaInts = 12;           // 8 pages, flags
+constexpr float kRescale = 8.f;         // base-2 logits a row may exceed its running maximum by
+
+// flags of a tile's description
+constexpr int32_t kMaskA = 1, kMaskB = 2;   // tile A / B needs its mask
+constexpr int kFixShift = 8;                // pages whose V rows past the count are zeroed
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) prompt_kernel(PromptArgs a)
+struct Smem {
+    static constexpr uint32_t tile = (D / 64) * kHalf;       // one 128 x D operand
+    static constexpr int stages = D == 128 ? 5 : 10;         // K and V tiles in turn
+    static constexpr uint32_t group = D * 16;                // 8 tokens x D dims
+    static constexpr uint32_t q_off = 0;                     // [2]: [d half][128 rows][128 B]
+    static constexpr uint32_t kv_off = 2 * tile;             // [stages]: [16 groups of 8 tokens][d half][8 tokens][128 B]
+    static constexpr uint32_t meta_off = kv_off + stages * tile;
+    static constexpr uint32_t bar_off = meta_off + kMetaSlots * kMetaInts * 4;
+    static constexpr int num_bars = 2 * stages + 11;
+    static constexpr uint32_t misc_off = bar_off + num_bars * 8;   // TMEM base, error
+    static constexpr uint32_t total = misc_off + 16;
+    static constexpr uint32_t alloc = total + 1024;
+    static_assert(alloc <= 227 * 1024, "shared memory of one CTA");
+};
+
+struct PromptMaps {
+    CUtensorMap q, k1, v1, k8, v8;
+};
+
+// D[tmem] (+)= A[tmem] . B[smem]
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate)
 {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    asm volatile(
+        "{\n.reg .pred p;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// 32 columns of this thread's lane, not yet waited for.
+__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+// Waits for this thread's TMEM loads; the operands tie the loaded registers
+// to the wait.
+__device__ __forceinline__ void tmem_ld_wait(uint32_t *r)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+// 16 columns of this thread's lane, not waited for.
+__device__ __forceinline__ void tmem_st16_issue(uint32_t taddr, const uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait()
+{
+    asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, int c0, int c1, int c2, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ PromptItem load_item(const PromptItem *p)
+{
+    union {
+        int4 v[3];
+        PromptItem it;
+    } u;
+    const int4 *s = reinterpret_cast<const int4 *>(p);
+    u.v[0] = __ldg(s);
+    u.v[1] = __ldg(s + 1);
+    u.v[2] = __ldg(s + 2);
+    return u.it;
+}
+
+// Tokens of page entry `e` (count, own flag, page of the node) that a row at
+// position `pos` of its node attends: 0..16.
+__device__ __forceinline__ int attended(int32_t e, int pos)
+{
+    const int cnt = e & 31;
+    return (e & 32) ? min(cnt, max(0, pos + 1 - (e >> 6) * kPageSize)) : cnt;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const __grid_constant__ PromptMaps maps)
+{
+    using L = Smem<D>;
+    constexpr int NST = L::stages;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *smem = smem_raw + (base - raw);
+    volatile int32_t *meta = reinterpret_cast<volatile int32_t *>(smem + L::meta_off);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::misc_off);
+    volatile int *err = reinterpret_cast<volatile int *>(smem + L::misc_off + 4);
+    auto bar = [&](int i) { return base + L::bar_off + 8u * (uint32_t)i; };
+    constexpr int kFull = 0, kEmpty = NST, kQFull = 2 * NST, kQEmpty = kQFull + 2, kSFull = kQFull + 4,
+                  kPFull = kQFull + 6, kOFull = kQFull + 8, kDrain = kQFull + 10;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = a.gqa_group, Hkv = a.num_kv_heads;
-    const __nv_bfloat16 *K = static_cast<const __nv_bfloat16 *>(a.k_pages), *V = static_cast<const __nv_bfloat16 *>(a.v_pages);
-    for (int u = a.plan.cta_off[blockIdx.x]; u < a.plan.cta_off[blockIdx.x + 1]; ++u) {
-        const int unit = a.plan.cta_unit[u], h = unit % Hkv;
-        const PromptItem it = a.plan.items[unit / Hkv];
-        const int rows = (it.tok_a + it.tok_b) * G;
-        for (int r = warp; r < rows; r += kThreads / 32) {
-            const int tok = r / G, head = h * G + r % G, pos = it.pos0 + tok;
-            const __nv_bfloat16 *qp = static_cast<const __nv_bfloat16 *>(a.q) + (it.row0 + tok) * a.q_stride + (size_t)head * D + lane * E;
-            float q[E], o[E] = {}, m = -INFINITY, l = 0.f;
-            for (int e = 0; e < E; ++e)
-                q[e] = __bfloat162float(qp[e]) * a.scale_log2;
-            int node = it.start_node, pg = it.start_page;
-            for (int k = 0; k < it.pages; ++k) {
-                const int2 rec = a.plan.nodes[node];
-                const bool own = node == it.node;
-                const int cnt = min(kPageSize, (own ? pos + 1 : rec.y) - pg * kPageSize);
-                const size_t page = a.page_id[a.node_page_off[node] + pg];
-                for (int i = 0; i < cnt; ++i) {
-                    const size_t at = ((page * Hkv + h) * kPageSize + i) * D + lane * E;
-                    float s = 0.f;
-                    for (int e = 0; e < E; ++e)
-                        s += q[e] * __bfloat162float(K[at + e]);
-                    s = warp_sum(s);
-                    const float mn = fmaxf(m, s), f = exp2f(m - mn), p = exp2f(s - mn);
-                    m = mn;
-                    l = l * f + p;
-                    for (int e = 0; e < E; ++e)
-                        o[e] = o[e] * f + p * __bfloat162float(V[at + e]);
-                }
-                if (++pg * kPageSize >= rec.y && !own) {
-                    node = rec.x < 0 ? it.node : rec.x;
-                    pg = 0;
+    const int tile_tok = kPromptRows / G;
+
+    // ---------------- set-up ----------------
+    if (tid == 0) {
+        grid_dep_launch();
+        for (int i = 0; i < NST; ++i) {
+            tc::mbar_init(bar(kFull + i), 1);
+            tc::mbar_init(bar(kEmpty + i), 1);
+        }
+        for (int w = 0; w < 2; ++w) {
+            tc::mbar_init(bar(kQFull + w), 1);
+            tc::mbar_init(bar(kQEmpty + w), 1);
+            tc::mbar_init(bar(kSFull + w), 1);
+            tc::mbar_init(bar(kPFull + w), 4);   // one arrival a softmax warp
+            tc::mbar_init(bar(kOFull + w), 1);
+        }
+        tc::mbar_init(bar(kDrain), 1);
+        *err = 0;
+        tc::fence_mbar_init();
+    }
+    if (warp == 8) {
+        if (lane == 0) {
+            tc::prefetch_tmap(&maps.q);
+            tc::prefetch_tmap(&maps.k1);
+            tc::prefetch_tmap(&maps.v1);
+            tc::prefetch_tmap(&maps.k8);
+            tc::prefetch_tmap(&maps.v8);
+        }
+    }
+    if (warp == 9) {
+        tc::tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    const int u0 = a.plan.cta_off[blockIdx.x], u1 = a.plan.cta_off[blockIdx.x + 1];
+    // A bounded wait of a whole warp; the first one that runs out leaves its
+    // code.  A warpgroup may sit out many units (tile B of units that have
+    // none): its first wait of a unit goes on for 64 limits, unless another
+    // role has failed.
+    auto wait = [&](int b, uint32_t parity, int code, bool idle = false) -> bool {
+        for (int i = 0; i < (idle ? 64 : 1); ++i) {
+            if (__all_sync(0xffffffffu, tc::mbar_wait(bar(b), parity)))
+                return true;
+            if (__any_sync(0xffffffffu, *err != 0))
+                return false;
+        }
+        *err = code;
+        return false;
+    };
+
+    if (warp >= 8) {
+        tc::setmaxnreg_dec<kRegsOther>();
+        if (warp == 8) {
+            // ---------------- TMA producer ----------------
+            const uint64_t pol = tc::l2_kv_policy(false);
+            uint32_t g = 0, gt = 0;       // operand tiles, KV tiles so far
+            uint32_t nq[2] = {0, 0};      // Q tiles so far
+            bool ok = true;
+            for (int u = u0; u < u1 && ok; ++u) {
+                const int unit = a.plan.cta_unit[u], h = unit % Hkv;
+                const PromptItem it = load_item(a.plan.items + unit / Hkv);
+                const int n = max(it.tiles_a, it.tiles_b);
+                // Lane i < 8 follows page i of every tile: its node, page of
+                // the node and the node's record.
+                int node = it.start_node, pg = it.start_page + (lane & 7);
+                int2 rec = a.plan.nodes[node];
+                auto settle = [&]() {
+                    while (node != it.node) {
+                        const int pages = (rec.y + kPageSize - 1) / kPageSize;
+                        if (pg < pages)
+                            break;
+                        pg -= pages;
+                        node = rec.x < 0 ? it.node : rec.x;
+                        rec = a.plan.nodes[node];
+                    }
+                };
+                settle();
+                const int min_a = it.pos0, min_b = it.pos0 + it.tok_a;
+                for (int t = 0; t < n && ok; ++t, ++gt) {
+                    // This tile's pages.
+                    const bool held = t * kPromptTilePages + (lane & 7) < it.pages;
+                    int cnt = 0, page = a.num_pages;   // past the range: a box out of the pool reads zeros
+                    int32_t entry = 0;
+                    bool mask_a = true, mask_b = true;
+                    if (held) {
+                        const bool own = node == it.node;
+                        cnt = min(kPageSize, rec.y - pg * kPageSize);
+                        page = a.page_id[a.node_page_off[node] + pg];
+                        entry = cnt | (own ? 32 : 0) | (pg << 6);
+                        const int last = pg * kPageSize + kPageSize - 1;
+                        mask_a = cnt < kPageSize || (own && last > min_a);
+                        mask_b = cnt < kPageSize || (own && last > min_b);
+                    }
+                    const int page0 = __shfl_sync(0xffffffffu, page, 0);
+                    const bool run8 = __all_sync(0xffffffffu, held && page == page0 + (lane & 7));
+                    const int32_t flags = (__any_sync(0xffffffffu, mask_a) ? kMaskA : 0) |
+                                          (__any_sync(0xffffffffu, mask_b) ? kMaskB : 0) |
+                                          (int32_t)((__ballot_sync(0xffffffffu, cnt > 0 && cnt < kPageSize) & 255u)
+                                                    << kFixShift);
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv, ++g) {
+                        const int s = (int)(g % NST);
+                        if (g >= NST)
+                            ok = ok && wait(kEmpty + s, (g / NST - 1) & 1, 301);
+                        if (!ok)
+                            break;
+                        if (kv == 0) {
+                            // The slot's last reader is done: its tile's P,
+                            // which the stage just freed came after.
+                            const int ms = (int)(gt % kMetaSlots) * kMetaInts;
+                            if (lane < 8)
+                                meta[ms + lane] = entry;
+                            if (lane == 0)
+                                meta[ms + 8] = flags;
+                            __syncwarp();
+                        }
+                        const uint32_t dst = base + L::kv_off + (uint32_t)s * L::tile;
+                        if (lane == 0)
+                            tc::mbar_arrive_expect_tx(bar(kFull + s), L::tile);
+                        __syncwarp();
+                        const CUtensorMap *one = kv ? &maps.v1 : &maps.k1, *eight = kv ? &maps.v8 : &maps.k8;
+                        if (run8) {
+                            if (lane == 0)
+                                tc::tma_load_5d(dst, eight, 0, 0, 0, 2 * h, page, bar(kFull + s), pol);
+                        } else if (lane < 8) {
+                            tc::tma_load_5d(dst + (uint32_t)lane * 2 * L::group, one, 0, 0, 0, 2 * h, page,
+                                            bar(kFull + s), pol);
+                        }
+                        if (t == 0 && kv == 0) {
+                            // The unit's rows, once the unit before has made
+                            // its last S from the buffer.
+                            for (int w = 0; w < 2 && ok; ++w) {
+                                if ((w ? it.tiles_b : it.tiles_a) == 0)
+                                    continue;
+                                if (nq[w])
+                                    ok = wait(kQEmpty + w, (nq[w] - 1) & 1, 302);
+                                if (!ok)
+                                    break;
+                                ++nq[w];
+                                if (lane == 0) {
+                                    tc::mbar_arrive_expect_tx(bar(kQFull + w), (uint32_t)(tile_tok * G) * D * 2);
+                                    for (int x = 0; x < D / 64; ++x)
+                                        tma_load_3d(base + L::q_off + (uint32_t)w * L::tile + x * kHalf, &maps.q,
+                                                    64 * x, h * G, it.row0 + (w ? it.tok_a : 0), bar(kQFull + w));
+                                }
+                            }
+                        }
+                    }
+                    pg += kPromptTilePages;
+                    settle();
                 }
             }
-            const float inv = l > 0.f ? 1.f / l : 0.f;
-            if (it.part0 >= 0) {
-                const size_t slot = (size_t)it.part0 + (size_t)h * rows + r;
-                for (int e = 0; e < E; ++e)
-                    a.o_part[slot * D + lane * E + e] = o[e] * inv;
-                if (lane == 0)
-                    a.lse_part[slot] = m + log2f(l);
-            } else {
-                const size_t row = (size_t)(it.row0 + tok) * a.num_q_heads + head;
-                for (int e = 0; e < E; ++e) {
-                    if (a.out_dtype == DEFT_OUT_F32)
-                        static_cast<float *>(a.out)[row * D + lane * E + e] = o[e] * inv;
-                    else
-                        static_cast<__nv_bfloat16 *>(a.out)[row * D + lane * E + e] = __float2bfloat16_rn(o[e] * inv);
+            if (!ok) {
+                // Every copy that went out lands before the CTA ends.
+                const uint32_t first = g > (uint32_t)NST ? g - NST : 0;
+                for (uint32_t i = first; i < g; ++i)
+                    tc::mbar_wait(bar(kFull + (int)(i % NST)), (i / NST) & 1);
+                for (int w = 0; w < 2; ++w)
+                    if (nq[w])
+                        tc::mbar_wait(bar(kQFull + w), (nq[w] - 1) & 1);
+            }
+        } else if (warp == 9) {
+            // ---------------- MMA issue ----------------
+            constexpr uint32_t idesc_s = tc::idesc_bf16(128, 128, 0, 0);
+            constexpr uint32_t idesc_o = tc::idesc_bf16(128, D, 0, 1);
+            const uint64_t dq0 = tc::smem_desc(base + L::q_off, 16, 1024);
+            // K: K-major, 8-token groups L::group apart; V: MN-major, its d
+            // halves 1 KB apart and its 8-token groups L::group apart.
+            const uint64_t dk0 = tc::smem_desc(base + L::kv_off, 16, L::group);
+            const uint64_t dv0 = tc::smem_desc(base + L::kv_off, 1024, L::group);
+            uint32_t g = 0, gt = 0, nq[2] = {0, 0}, np[2] = {0, 0};
+            bool ok = true;
+            auto issue_s = [&](int w, int stage) {
+                if (lane == 0) {
+#pragma unroll
+                    for (int s = 0; s < D / 16; ++s) {
+                        const uint64_t qo = (uint64_t)((w * L::tile + (s >> 2) * kHalf + (s & 3) * 32) >> 4);
+                        const uint64_t ko = (uint64_t)((stage * L::tile + (s >> 2) * 1024 + (s & 3) * 32) >> 4);
+                        tc::mma_bf16(tmem + w * 128, dq0 + qo, dk0 + ko, idesc_s, s > 0 ? 1u : 0u);
+                    }
+                    tc::mma_commit(bar(kSFull + w));
                 }
+            };
+            auto issue_pv = [&](int w, int stage, bool first) {
+                if (lane == 0) {
+#pragma unroll
+                    for (int s = 0; s < 8; ++s) {
+                        const uint64_t vo = (uint64_t)((stage * L::tile + s * 2 * L::group) >> 4);
+                        mma_ts(tmem + 256 + w * 128, tmem + w * 128 + s * 8, dv0 + vo, idesc_o, (!first || s > 0) ? 1u : 0u);
+                    }
+                }
+            };
+            for (int u = u0; u < u1 && ok; ++u) {
+                const PromptItem it = load_item(a.plan.items + a.plan.cta_unit[u] / Hkv);
+                const int nt[2] = {it.tiles_a, it.tiles_b};
+                const int n = max(nt[0], nt[1]);
+                ok = wait(kFull + (int)(g % NST), (g / NST) & 1, 311);
+                for (int w = 0; w < 2 && ok; ++w) {
+                    if (nt[w] == 0)
+                        continue;
+                    ok = wait(kQFull + w, nq[w] & 1, 312);
+                    ++nq[w];
+                    if (!ok)
+                        break;
+                    tc::fence_after_sync();
+                    issue_s(w, (int)(g % NST));
+                    if (nt[w] == 1 && lane == 0)
+                        tc::mma_commit(bar(kQEmpty + w));
+                }
+                if (!ok)
+                    break;
                 if (lane == 0)
-                    a.lse[row] = (m + log2f(l)) * kLn2;
+                    tc::mma_commit(bar(kEmpty + (int)(g % NST)));
+                ++g;
+                for (int t = 0; t < n && ok; ++t, ++gt) {
+                    const int sv = (int)(g % NST);
+                    ok = wait(kFull + sv, (g / NST) & 1, 313);
+                    if (!ok)
+                        break;
+                    const int ms = (int)(gt % kMetaSlots) * kMetaInts;
+                    uint32_t fix = ((uint32_t)meta[ms + 8] >> kFixShift) & 255u;
+                    if (fix) {
+                        // Rows past the token count of partial pages: zeros.
+                        for (; fix; fix &= fix - 1) {
+                            const int j = __ffs((int)fix) - 1, cnt = meta[ms + j] & 31;
+                            uint8_t *pg = smem + L::kv_off + (uint32_t)sv * L::tile + (uint32_t)j * 2 * L::group;
+                            // 16 rows x D / 64 halves of 128 B, 8 16-byte pieces each
+                            for (int x = lane; x < (kPageSize - cnt) * (D / 64) * 8; x += 32) {
+                                const int row = cnt + x / ((D / 64) * 8), rest = x % ((D / 64) * 8);
+                                *reinterpret_cast<uint4 *>(pg + (row >> 3) * L::group + (rest >> 3) * 1024 +
+                                                           (row & 7) * 128 + (rest & 7) * 16) = make_uint4(0, 0, 0, 0);
+                            }
+                        }
+                        tc::fence_proxy_async();
+                        __syncwarp();
+                    }
+                    const int sk = (int)((g + 1) % NST);
+                    for (int w = 0; w < 2 && ok; ++w) {
+                        if (t >= nt[w])
+                            continue;
+                        ok = wait(kPFull + w, np[w] & 1, 314);
+                        ++np[w];
+                        if (!ok)
+                            break;
+                        tc::fence_after_sync();
+                        issue_pv(w, sv, t == 0);
+                        if (lane == 0) {
+                            if (t + 1 == nt[w])
+                                tc::mma_commit(bar(kOFull + w));
+                            if (w == 1 || t >= nt[1])
+                                tc::mma_commit(bar(kEmpty + sv));
+                        }
+                        if (t + 1 < nt[w]) {
+                            ok = wait(kFull + sk, ((g + 1) / NST) & 1, 315);
+                            if (!ok)
+                                break;
+                            tc::fence_after_sync();
+                            issue_s(w, sk);
+                            if (lane == 0) {
+                                if (t + 2 == nt[w])
+                                    tc::mma_commit(bar(kQEmpty + w));
+                                if (w == 1 || t + 1 >= nt[1])
+                                    tc::mma_commit(bar(kEmpty + sk));
+                            }
+                        }
+                    }
+                    ++g;
+                    if (t + 1 < n)
+                        ++g;
+                }
+            }
+            // Every MMA and its arrivals end before the CTA does.
+            if (lane == 0)
+                tc::mma_commit(bar(kDrain));
+            wait(kDrain, 0, 316);
+        }
+    } else {
+        tc::setmaxnreg_inc<kRegsSoftmax>();
+        // ---------------- softmax and output: one row a thread ----------------
+        const int w = warp >> 2, r = tid & 127;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // this warp's TMEM lanes
+        const uint32_t ts = tmem + lanes + w * 128, to = tmem + lanes + 256 + w * 128;
+        const int tok = r / G, head = r - tok * G;
+        const float scale = a.scale_log2;
+        const f32x2 scale2 = f2_pack(scale, scale);
+        uint32_t gt = 0, ns = 0, no = 0;
+        bool ok = true;
+        for (int u = u0; u < u1 && ok; ++u) {
+            const int unit = a.plan.cta_unit[u], h = unit % Hkv;
+            const PromptItem it = load_item(a.plan.items + unit / Hkv);
+            const int nt = w ? it.tiles_b : it.tiles_a, before = w ? it.tok_a : 0;
+            const bool held = tok < (w ? it.tok_b : it.tok_a);
+            const int pos = it.pos0 + before + tok;
+            float m = -INFINITY, l = 0.f;
+            for (int t = 0; t < nt; ++t) {
+                if (!wait(kSFull + w, ns & 1, 321 + w, t == 0)) {
+                    ok = false;
+                    break;
+                }
+                ++ns;
+                tc::fence_after_sync();
+                uint32_t sr[128];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    tmem_ld32_issue(ts + 32 * c, sr + 32 * c);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    tmem_ld_wait(sr + 32 * c);
+                const int ms = (int)((gt + t) % kMetaSlots) * kMetaInts;
+                if (meta[ms + 8] & (w ? kMaskB : kMaskA)) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int seen = attended(meta[ms + j], pos);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            sr[16 * j + i] = i < seen ? sr[16 * j + i] : 0xff800000u;   // -inf
+                    }
+                }
+                float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 128; i += 8) {
+                    mx0 = fmaxf(mx0, fmaxf(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])));
+                    mx1 = fmaxf(mx1, fmaxf(__uint_as_float(sr[i + 2]), __uint_as_float(sr[i + 3])));
+                    mx2 = fmaxf(mx2, fmaxf(__uint_as_float(sr[i + 4]), __uint_as_float(sr[i + 5])));
+                    mx3 = fmaxf(mx3, fmaxf(__uint_as_float(sr[i + 6]), __uint_as_float(sr[i + 7])));
+                }
+                const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * scale;
+                if (t == 0) {
+                    m = mx;
+                } else if (__any_sync(0xffffffffu, mx > m + kRescale)) {
+                    // PV(t - 1) has ended (S(t) came after it): O may be rescaled here.
+                    const float mn = fmaxf(m, mx);
+                    const float f = mn == -INFINITY ? 1.f : tc::ex2(m - mn);
+                    m = mn;
+                    l *= f;
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32_issue(to + 32 * c, o);
+                        tmem_ld_wait(o);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        tmem_st16_issue(to + 32 * c, o);
+                        tmem_st16_issue(to + 32 * c + 16, o + 16);
+                    }
+                }
+                const float neg = m == -INFINITY ? 0.f : -m;
+                const f32x2 neg2 = f2_pack(neg, neg);
+                f32x2 sum0 = f2_pack(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const f32x2 x = f2_fma(f2_pack(__uint_as_float(sr[32 * c + 2 * i]), __uint_as_float(sr[32 * c + 2 * i + 1])),
+                                               scale2, neg2);
+                        float2 y = f2_unpack(x);
+                        y.x = tc::ex2(y.x);
+                        y.y = tc::ex2(y.y);
+                        if (i & 1)
+                            sum1 = f2_add(sum1, f2_pack(y.x, y.y));
+                        else
+                            sum0 = f2_add(sum0, f2_pack(y.x, y.y));
+                        pk[i] = tc::pack_bf16x2(y.x, y.y);
+                    }
+                    tmem_st16_issue(ts + 16 * c, pk);
+                }
+                const float2 s2 = f2_unpack(f2_add(sum0, sum1));
+                l += s2.x + s2.y;
+                tmem_st_wait();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0)
+                    tc::mbar_arrive(bar(kPFull + w));
+            }
+            gt += (uint32_t)max(it.tiles_a, it.tiles_b);
+            if (!ok)
+                break;
+            const int rows = (it.tok_a + it.tok_b) * G;
+            const size_t orow = (size_t)(it.row0 + before + tok) * a.num_q_heads + h * G + head;
+            const size_t slot = (size_t)it.part0 + (size_t)h * rows + before * G + r;
+            if (nt > 0) {
+                if (!wait(kOFull + w, no & 1, 323 + w)) {
+                    ok = false;
+                    break;
+                }
+                ++no;
+                tc::fence_after_sync();
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32_issue(to + 32 * c, o);
+                    tmem_ld_wait(o);
+                    if (!held)
+                        continue;
+                    if (it.part0 >= 0 || a.out_dtype == DEFT_OUT_F32) {
+                        float4 *dst = reinterpret_cast<float4 *>(it.part0 >= 0 ? a.o_part + slot * D
+                                                                               : static_cast<float *>(a.out) + orow * D) + 8 * c;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            dst[i] = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
+                                                 __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
+                    } else {
+                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * D) + 4 * c;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t x[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                x[k] = tc::pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * inv,
+                                                       __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
+                            dst[i] = make_uint4(x[0], x[1], x[2], x[3]);
+                        }
+                    }
+                }
+            }
+            if (held) {
+                const float lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
+                if (it.part0 >= 0)
+                    a.lse_part[slot] = lse2;
+                else
+                    a.lse[orow] = lse2 * kLn2;
             }
         }
     }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (*err) {
+        // A wait ran out: every row of the CTA's units is marked.
+        if (tid == 0)
+            atomicCAS(a.plan.status, 0u, (uint32_t)*err);
+        const float nan = __int_as_float(0x7fc00000);
+        for (int u = u0; u < u1; ++u) {
+            const int unit = a.plan.cta_unit[u], h = unit % Hkv;
+            const PromptItem it = load_item(a.plan.items + unit / Hkv);
+            const int rows = (it.tok_a + it.tok_b) * G;
+            for (int x = tid; x < rows; x += kThreads) {
+                if (it.part0 >= 0) {
+                    a.lse_part[(size_t)it.part0 + (size_t)h * rows + x] = nan;
+                    continue;
+                }
+                const size_t orow = (size_t)(it.row0 + x / G) * a.num_q_heads + h * G + x % G;
+                a.lse[orow] = nan;
+                for (int e = 0; e < D; ++e) {
+                    if (a.out_dtype == DEFT_OUT_F32)
+                        static_cast<float *>(a.out)[orow * D + e] = nan;
+                    else
+                        static_cast<__nv_bfloat16 *>(a.out)[orow * D + e] = __float2bfloat16_rn(nan);
+                }
+            }
+        }
+    }
+    if (warp == 9)
+        tc::tmem_dealloc(tmem, kTmemCols);
+}
+
+// ---- host ----
+PFN_cuTensorMapEncodeTiled_v12000 encoder()
+{
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            ptr = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    }();
+    return fn;
+}
+
+// A view of the pool [pages][Hkv][16][D], innermost first: 64 dims (one
+// 128-byte swizzle row), 8 tokens, the D / 64 parts of a row, 2 Hkv groups of
+// 8 tokens and pages; a box holds one page (or eight) of one head and lands
+// as [8-token group][part][8 tokens][128 B].
+bool pool_map(const void *ptr, const PromptArgs &a, bool run8, CUtensorMap *m)
+{
+    const cuuint64_t row = (cuuint64_t)a.head_dim * 2;
+    const cuuint32_t parts = (cuuint32_t)a.head_dim / 64;
+    const cuuint64_t dims[5] = {64, 8, parts, 2 * (cuuint64_t)a.num_kv_heads, (cuuint64_t)a.num_pages};
+    const cuuint64_t strides[4] = {row, 128, 8 * row, row * kPageSize * a.num_kv_heads};
+    const cuuint32_t box[5] = {64, 8, parts, 2, run8 ? 8u : 1u};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(ptr), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// q as [tokens][Hq][D]; a box is a tile's tokens of one group, 64 dims.
+bool q_map(const PromptArgs &a, CUtensorMap *m)
+{
+    const cuuint64_t dims[3] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.num_q_heads, (cuuint64_t)a.num_rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)a.head_dim * 2, (cuuint64_t)a.q_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)a.gqa_group, (cuuint32_t)(kPromptRows / a.gqa_group)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.q), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+int launch_dim(const PromptArgs &a, const PromptMaps &maps, int32_t ctas, cudaStream_t st)
+{
+    // The shared-memory size is set once a device.
+    static std::atomic<uint64_t> set{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return (int)e;
+    if (dev >= 64 || !(set.load(std::memory_order_acquire) >> dev & 1)) {
+        e = cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Smem<D>::alloc);
+        if (e != cudaSuccess)
+            return (int)e;
+        if (dev < 64)
+            set.fetch_or(1ull << dev, std::memory_order_release);
+    }
+    prompt_kernel<D><<<ctas, kThreads, Smem<D>::alloc, st>>>(a, maps);
+    return (int)cudaGetLastError();
 }
 
 }  // namespace
 
 int launch_prompt(const PromptArgs &a, int32_t ctas, void *stream)
 {
+    PromptMaps maps;
+    if (!encoder() || !q_map(a, &maps.q) || !pool_map(a.k_pages, a, false, &maps.k1) ||
+        !pool_map(a.v_pages, a, false, &maps.v1) || !pool_map(a.k_pages, a, true, &maps.k8) ||
+        !pool_map(a.v_pages, a, true, &maps.v8))
+        return (int)cudaErrorInvalidValue;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (a.head_dim == 128)
-        prompt_kernel<128><<<ctas, kThreads, 0, st>>>(a);
-    else
-        prompt_kernel<64><<<ctas, kThreads, 0, st>>>(a);
-    return (int)cudaGetLastError();
+    return a.head_dim == 128 ? launch_dim<128>(a, maps, ctas, st) : launch_dim<64>(a, maps, ctas, st);
 }
 
 }  // namespace deft
