@@ -69,7 +69,7 @@ struct Smem {
     static constexpr uint32_t kv_off = 2 * tile;             // [stages]: [16 groups of 8 tokens][d half][8 tokens][128 B]
     static constexpr uint32_t meta_off = kv_off + stages * tile;
     static constexpr uint32_t bar_off = meta_off + kMetaSlots * kMetaInts * 4;
-    static constexpr int num_bars = 2 * stages + 11;
+    static constexpr int num_bars = 3 * stages + 11;
     static constexpr uint32_t misc_off = bar_off + num_bars * 8;   // TMEM base, error
     static constexpr uint32_t total = misc_off + 16;
     static constexpr uint32_t alloc = total + 1024;
@@ -140,6 +140,18 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, int 
         : "memory");
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile(
+        "{\n.reg .pred p;\n"
+        "elect.sync _|p, 0xffffffff;\n"
+        "selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(p));
+    return p != 0;
+}
+
 __device__ __forceinline__ PromptItem load_item(const PromptItem *p)
 {
     union {
@@ -175,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
     volatile int *err = reinterpret_cast<volatile int *>(smem + L::misc_off + 4);
     auto bar = [&](int i) { return base + L::bar_off + 8u * (uint32_t)i; };
     constexpr int kFull = 0, kEmpty = NST, kQFull = 2 * NST, kQEmpty = kQFull + 2, kSFull = kQFull + 4,
-                  kPFull = kQFull + 6, kOFull = kQFull + 8, kDrain = kQFull + 10;
+                  kPFull = kQFull + 6, kOFull = kQFull + 8, kDrain = kQFull + 10, kFixed = kQFull + 11;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = a.gqa_group, Hkv = a.num_kv_heads;
     const int tile_tok = kPromptRows / G;
@@ -195,6 +207,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
             tc::mbar_init(bar(kOFull + w), 1);
         }
         tc::mbar_init(bar(kDrain), 1);
+        for (int i = 0; i < NST; ++i)
+            tc::mbar_init(bar(kFixed + i), 1);
         *err = 0;
         tc::fence_mbar_init();
     }
@@ -329,6 +343,30 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                             }
                         }
                     }
+                    uint32_t fix = ((uint32_t)flags >> kFixShift) & 255u;
+                    if (ok && fix) {
+                        // V rows past a node's last token: the page holds
+                        // anything there, and their P of 0 must not meet a
+                        // NaN.  V has to land first; the ring covers the
+                        // wait, as the tile is used two tiles later.
+                        const uint32_t gv = g - 1;
+                        const int sv = (int)(gv % NST);
+                        ok = wait(kFull + sv, (gv / NST) & 1, 303);
+                        for (; fix; fix &= fix - 1) {
+                            const int j = __ffs((int)fix) - 1, used = __shfl_sync(0xffffffffu, cnt, j);
+                            uint8_t *at = smem + L::kv_off + (uint32_t)sv * L::tile + (uint32_t)j * 2 * L::group;
+                            // 16 rows of D / 64 x 128 B, in 16-byte pieces
+                            for (int x = lane; x < (kPageSize - used) * (D / 64) * 8; x += 32) {
+                                const int row = used + x / ((D / 64) * 8), rest = x % ((D / 64) * 8);
+                                *reinterpret_cast<uint4 *>(at + (row >> 3) * L::group + (rest >> 3) * 1024 +
+                                                           (row & 7) * 128 + (rest & 7) * 16) = make_uint4(0, 0, 0, 0);
+                            }
+                        }
+                        tc::fence_proxy_async();
+                        __syncwarp();
+                        if (lane == 0)
+                            tc::mbar_arrive(bar(kFixed + sv));
+                    }
                     pg += kPromptTilePages;
                     settle();
                 }
@@ -344,118 +382,125 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
             }
         } else if (warp == 9) {
             // ---------------- MMA issue ----------------
-            constexpr uint32_t idesc_s = tc::idesc_bf16(128, 128, 0, 0);
-            constexpr uint32_t idesc_o = tc::idesc_bf16(128, D, 0, 1);
-            const uint64_t dq0 = tc::smem_desc(base + L::q_off, 16, 1024);
-            // K: K-major, 8-token groups L::group apart; V: MN-major, its d
-            // halves 1 KB apart and its 8-token groups L::group apart.
-            const uint64_t dk0 = tc::smem_desc(base + L::kv_off, 16, L::group);
-            const uint64_t dv0 = tc::smem_desc(base + L::kv_off, 1024, L::group);
-            uint32_t g = 0, gt = 0, nq[2] = {0, 0}, np[2] = {0, 0};
-            bool ok = true;
-            auto issue_s = [&](int w, int stage) {
-                if (lane == 0) {
-#pragma unroll
-                    for (int s = 0; s < D / 16; ++s) {
-                        const uint64_t qo = (uint64_t)((w * L::tile + (s >> 2) * kHalf + (s & 3) * 32) >> 4);
-                        const uint64_t ko = (uint64_t)((stage * L::tile + (s >> 2) * 1024 + (s & 3) * 32) >> 4);
-                        tc::mma_bf16(tmem + w * 128, dq0 + qo, dk0 + ko, idesc_s, s > 0 ? 1u : 0u);
+            // One thread runs the whole loop: the tensor core idles while
+            // its issuer does anything else, so there is no vote, no
+            // reconvergence and no shared work in it.
+            if (elect_one()) {
+                constexpr uint32_t idesc_s = tc::idesc_bf16(128, 128, 0, 0);
+                constexpr uint32_t idesc_o = tc::idesc_bf16(128, D, 0, 1);
+                const uint64_t dq0 = tc::smem_desc(base + L::q_off, 16, 1024);
+                // K: K-major, 8-token groups L::group apart; V: MN-major, its
+                // d halves 1 KB apart and its 8-token groups L::group apart.
+                const uint64_t dk0 = tc::smem_desc(base + L::kv_off, 16, L::group);
+                const uint64_t dv0 = tc::smem_desc(base + L::kv_off, 1024, L::group);
+                uint32_t gt = 0, nq[2] = {0, 0}, np[2] = {0, 0}, nf = 0;
+                uint32_t st = 0, ph = 0;   // next operand stage and its parity
+                bool ok = true;
+                auto wait1 = [&](int b, uint32_t parity, int code) {
+                    if (!tc::mbar_wait(bar(b), parity)) {
+                        if (!*err)
+                            *err = code;
+                        ok = false;
                     }
+                    return ok;
+                };
+                auto issue_s = [&](int w, uint32_t stage) {
+                    const uint64_t dq = dq0 + (uint64_t)((w * L::tile) >> 4), dk = dk0 + (uint64_t)((stage * L::tile) >> 4);
+#pragma unroll
+                    for (int s = 0; s < D / 16; ++s)
+                        tc::mma_bf16(tmem + w * 128, dq + (uint64_t)(((s >> 2) * kHalf + (s & 3) * 32) >> 4),
+                                     dk + (uint64_t)(((s >> 2) * 1024 + (s & 3) * 32) >> 4), idesc_s, s > 0 ? 1u : 0u);
                     tc::mma_commit(bar(kSFull + w));
-                }
-            };
-            auto issue_pv = [&](int w, int stage, bool first) {
-                if (lane == 0) {
+                };
+                auto issue_pv = [&](int w, uint32_t stage, bool first) {
+                    const uint64_t dv = dv0 + (uint64_t)((stage * L::tile) >> 4);
 #pragma unroll
-                    for (int s = 0; s < 8; ++s) {
-                        const uint64_t vo = (uint64_t)((stage * L::tile + s * 2 * L::group) >> 4);
-                        mma_ts(tmem + 256 + w * 128, tmem + w * 128 + s * 8, dv0 + vo, idesc_o, (!first || s > 0) ? 1u : 0u);
+                    for (int s = 0; s < 8; ++s)
+                        mma_ts(tmem + 256 + w * 128, tmem + w * 128 + s * 8, dv + (uint64_t)((s * 2 * L::group) >> 4),
+                               idesc_o, (!first || s > 0) ? 1u : 0u);
+                };
+                int next_a = 0, next_b = 0;
+                auto look = [&](int u) {
+                    if (u < u1) {
+                        const PromptItem *it = a.plan.items + a.plan.cta_unit[u] / Hkv;
+                        next_a = it->tiles_a;
+                        next_b = it->tiles_b;
                     }
-                }
-            };
-            for (int u = u0; u < u1 && ok; ++u) {
-                const PromptItem it = load_item(a.plan.items + a.plan.cta_unit[u] / Hkv);
-                const int nt[2] = {it.tiles_a, it.tiles_b};
-                const int n = max(nt[0], nt[1]);
-                ok = wait(kFull + (int)(g % NST), (g / NST) & 1, 311);
-                for (int w = 0; w < 2 && ok; ++w) {
-                    if (nt[w] == 0)
-                        continue;
-                    ok = wait(kQFull + w, nq[w] & 1, 312);
-                    ++nq[w];
-                    if (!ok)
+                };
+                look(u0);
+                for (int u = u0; u < u1 && ok; ++u) {
+                    const int nt[2] = {next_a, next_b};
+                    const int n = max(nt[0], nt[1]);
+                    look(u + 1);
+                    if (!wait1(kFull + st, ph, 311))
                         break;
-                    tc::fence_after_sync();
-                    issue_s(w, (int)(g % NST));
-                    if (nt[w] == 1 && lane == 0)
-                        tc::mma_commit(bar(kQEmpty + w));
-                }
-                if (!ok)
-                    break;
-                if (lane == 0)
-                    tc::mma_commit(bar(kEmpty + (int)(g % NST)));
-                ++g;
-                for (int t = 0; t < n && ok; ++t, ++gt) {
-                    const int sv = (int)(g % NST);
-                    ok = wait(kFull + sv, (g / NST) & 1, 313);
-                    if (!ok)
-                        break;
-                    const int ms = (int)(gt % kMetaSlots) * kMetaInts;
-                    uint32_t fix = ((uint32_t)meta[ms + 8] >> kFixShift) & 255u;
-                    if (fix) {
-                        // Rows past the token count of partial pages: zeros.
-                        for (; fix; fix &= fix - 1) {
-                            const int j = __ffs((int)fix) - 1, cnt = meta[ms + j] & 31;
-                            uint8_t *pg = smem + L::kv_off + (uint32_t)sv * L::tile + (uint32_t)j * 2 * L::group;
-                            // 16 rows x D / 64 halves of 128 B, 8 16-byte pieces each
-                            for (int x = lane; x < (kPageSize - cnt) * (D / 64) * 8; x += 32) {
-                                const int row = cnt + x / ((D / 64) * 8), rest = x % ((D / 64) * 8);
-                                *reinterpret_cast<uint4 *>(pg + (row >> 3) * L::group + (rest >> 3) * 1024 +
-                                                           (row & 7) * 128 + (rest & 7) * 16) = make_uint4(0, 0, 0, 0);
-                            }
-                        }
-                        tc::fence_proxy_async();
-                        __syncwarp();
-                    }
-                    const int sk = (int)((g + 1) % NST);
-                    for (int w = 0; w < 2 && ok; ++w) {
-                        if (t >= nt[w])
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        if (nt[w] == 0)
                             continue;
-                        ok = wait(kPFull + w, np[w] & 1, 314);
-                        ++np[w];
-                        if (!ok)
+                        if (!wait1(kQFull + w, nq[w] & 1, 312))
                             break;
+                        ++nq[w];
                         tc::fence_after_sync();
-                        issue_pv(w, sv, t == 0);
-                        if (lane == 0) {
-                            if (t + 1 == nt[w])
-                                tc::mma_commit(bar(kOFull + w));
-                            if (w == 1 || t >= nt[1])
-                                tc::mma_commit(bar(kEmpty + sv));
-                        }
-                        if (t + 1 < nt[w]) {
-                            ok = wait(kFull + sk, ((g + 1) / NST) & 1, 315);
-                            if (!ok)
+                        issue_s(w, st);
+                        if (nt[w] == 1)
+                            tc::mma_commit(bar(kQEmpty + w));
+                    }
+                    if (!ok)
+                        break;
+                    tc::mma_commit(bar(kEmpty + st));
+                    for (int t = 0; t < n; ++t, ++gt) {
+                        st = st + 1 == NST ? 0 : st + 1;
+                        ph ^= st == 0;
+                        const uint32_t sv = st, pv = ph;
+                        if (!wait1(kFull + sv, pv, 313))
+                            break;
+                        // V of a tile with partial pages, once its empty rows are zeros.
+                        if (meta[(gt % kMetaSlots) * kMetaInts + 8] >> kFixShift) {
+                            if (!wait1(kFixed + sv, (nf >> sv) & 1, 317))
                                 break;
+                            nf ^= 1u << sv;
+                        }
+                        uint32_t sk = 0;
+                        if (t + 1 < n) {
+                            st = st + 1 == NST ? 0 : st + 1;
+                            ph ^= st == 0;
+                            sk = st;
+                            if (!wait1(kFull + sk, ph, 315))
+                                break;
+                        }
+#pragma unroll
+                        for (int w = 0; w < 2; ++w) {
+                            if (t >= nt[w])
+                                continue;
+                            if (!wait1(kPFull + w, np[w] & 1, 314))
+                                break;
+                            ++np[w];
                             tc::fence_after_sync();
-                            issue_s(w, sk);
-                            if (lane == 0) {
+                            issue_pv(w, sv, t == 0);
+                            if (t + 1 < nt[w]) {
+                                issue_s(w, sk);
                                 if (t + 2 == nt[w])
                                     tc::mma_commit(bar(kQEmpty + w));
-                                if (w == 1 || t + 1 >= nt[1])
-                                    tc::mma_commit(bar(kEmpty + sk));
+                            } else {
+                                tc::mma_commit(bar(kOFull + w));
                             }
                         }
+                        if (!ok)
+                            break;
+                        tc::mma_commit(bar(kEmpty + sv));
+                        if (t + 1 < n)
+                            tc::mma_commit(bar(kEmpty + sk));
                     }
-                    ++g;
-                    if (t + 1 < n)
-                        ++g;
+                    // the next unit's first K
+                    st = st + 1 == NST ? 0 : st + 1;
+                    ph ^= st == 0;
                 }
-            }
-            // Every MMA and its arrivals end before the CTA does.
-            if (lane == 0)
+                // Every MMA and its arrivals end before the CTA does.
                 tc::mma_commit(bar(kDrain));
-            wait(kDrain, 0, 316);
+                wait1(kDrain, 0, 316);
+            }
+            __syncwarp();
         }
     } else {
         tc::setmaxnreg_inc<kRegsSoftmax>();
