@@ -628,7 +628,7 @@ size_t deft_prompt_workspace_bytes(const deft_prompt_plan_t *plan, int32_t num_q
  *   k_pages, v_pages, node_page_off, page_id, num_pages, head geometry,
  *     scale, out_dtype, workspace: as for deft_tree_attn, with
  *     num_kv_heads and num_q_heads / num_kv_heads the plan's (DEFT_ESTATE)
- *     and head_dim in {64, 128}; out 16-byte aligned.
+ *     and head_dim in {64, 128}; out 32-byte aligned (else DEFT_EINVAL).
  *   out: [rows][num_q_heads][head_dim], lse: fp32 [rows][num_q_heads],
  *     natural log; rows past the plan's are left as they were.
  * Cache slots past a node's last token, and pages past those its length

@@ -290,7 +290,7 @@ int deft_prompt_attn(const void *q, int64_t q_stride, int32_t num_rows, const vo
         return DEFT_EINVAL;
     if (num_kv_heads < 1 || num_q_heads < 1 || num_q_heads % num_kv_heads != 0)
         return DEFT_EINVAL;
-    if (((uintptr_t)q | (uintptr_t)k_pages | (uintptr_t)v_pages | (uintptr_t)out) & 15u)
+    if ((((uintptr_t)q | (uintptr_t)k_pages | (uintptr_t)v_pages) & 15u) || ((uintptr_t)out & 31u))
         return DEFT_EINVAL;
     if ((head_dim != 64 && head_dim != 128) || page_size != kPageSize)
         return DEFT_EUNSUPPORTED;

@@ -63,7 +63,7 @@ constexpr int kFixShift = 8;                // pages whose V rows past the count
 template <int D>
 struct Smem {
     static constexpr uint32_t tile = (D / 64) * kHalf;       // one 128 x D operand
-    static constexpr int stages = D == 128 ? 5 : 10;         // K and V tiles in turn
+    static constexpr int stages = D == 128 ? 4 : 8;         // K and V tiles in turn
     static constexpr uint32_t group = D * 16;                // 8 tokens x D dims
     static constexpr uint32_t q_off = 0;                     // [2]: [d half][128 rows][128 B]
     static constexpr uint32_t kv_off = 2 * tile;             // [stages]: [16 groups of 8 tokens][d half][8 tokens][128 B]
@@ -138,6 +138,14 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, int 
         " [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
         : "memory");
+}
+
+// 32 bytes to global memory, a whole sector a lane.
+__device__ __forceinline__ void store32(void *dst, const uint32_t *r)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(dst), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 
 // One lane of a converged warp.
@@ -253,47 +261,70 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
             uint32_t g = 0, gt = 0;       // operand tiles, KV tiles so far
             uint32_t nq[2] = {0, 0};      // Q tiles so far
             bool ok = true;
-            for (int u = u0; u < u1 && ok; ++u) {
-                const int unit = a.plan.cta_unit[u], h = unit % Hkv;
-                const PromptItem it = load_item(a.plan.items + unit / Hkv);
-                const int n = max(it.tiles_a, it.tiles_b);
-                // Lane i < 8 follows page i of every tile: its node, page of
-                // the node and the node's record.
-                int node = it.start_node, pg = it.start_page + (lane & 7);
-                int2 rec = a.plan.nodes[node];
-                auto settle = [&]() {
-                    while (node != it.node) {
-                        const int pages = (rec.y + kPageSize - 1) / kPageSize;
-                        if (pg < pages)
-                            break;
-                        pg -= pages;
-                        node = rec.x < 0 ? it.node : rec.x;
-                        rec = a.plan.nodes[node];
-                    }
-                };
-                settle();
-                const int min_a = it.pos0, min_b = it.pos0 + it.tok_a;
-                for (int t = 0; t < n && ok; ++t, ++gt) {
-                    // This tile's pages.
-                    const bool held = t * kPromptTilePages + (lane & 7) < it.pages;
-                    int cnt = 0, page = a.num_pages;   // past the range: a box out of the pool reads zeros
-                    int32_t entry = 0;
-                    bool mask_a = true, mask_b = true;
-                    if (held) {
-                        const bool own = node == it.node;
-                        cnt = min(kPageSize, rec.y - pg * kPageSize);
-                        page = a.page_id[a.node_page_off[node] + pg];
-                        entry = cnt | (own ? 32 : 0) | (pg << 6);
-                        const int last = pg * kPageSize + kPageSize - 1;
-                        mask_a = cnt < kPageSize || (own && last > min_a);
-                        mask_b = cnt < kPageSize || (own && last > min_b);
-                    }
-                    const int page0 = __shfl_sync(0xffffffffu, page, 0);
-                    const bool run8 = __all_sync(0xffffffffu, held && page == page0 + (lane & 7));
-                    const int32_t flags = (__any_sync(0xffffffffu, mask_a) ? kMaskA : 0) |
-                                          (__any_sync(0xffffffffu, mask_b) ? kMaskB : 0) |
-                                          (int32_t)((__ballot_sync(0xffffffffu, cnt > 0 && cnt < kPageSize) & 255u)
-                                                    << kFixShift);
+            // The unit ahead: lane i < 8 follows page i of every tile: its
+            // node, that node's record and first page, the page of the node.
+            int unit = u0 < u1 ? a.plan.cta_unit[u0] : 0, after = 0, h = 0, node = 0, pg = 0, first = 0, n = 0, tn = 0;
+            int2 rec = make_int2(-1, 0);
+            PromptItem it{};
+            auto enter = [&]() {
+                while (node != it.node) {
+                    const int pages = (rec.y + kPageSize - 1) / kPageSize;
+                    if (pg < pages)
+                        break;
+                    pg -= pages;
+                    node = rec.x < 0 ? it.node : rec.x;
+                    rec = a.plan.nodes[node];
+                    first = a.node_page_off[node];
+                }
+            };
+            // This tile's pages, resolved one tile ahead (across units too),
+            // so that the page table's latency is off the ring's path.
+            int cnt = 0, page = 0;
+            int32_t entry = 0, flags = 0;
+            bool run8 = false;
+            auto resolve = [&]() {
+                const bool held = tn * kPromptTilePages + (lane & 7) < it.pages;
+                bool mask_a = true, mask_b = true;
+                cnt = 0;
+                entry = 0;
+                page = a.num_pages;   // past the range: a box out of the pool reads zeros
+                if (held) {
+                    const bool own = node == it.node;
+                    page = __ldg(a.page_id + first + pg);
+                    cnt = min(kPageSize, rec.y - pg * kPageSize);
+                    entry = cnt | (own ? 32 : 0) | (pg << 6);
+                    const int last = pg * kPageSize + kPageSize - 1;
+                    mask_a = cnt < kPageSize || (own && last > it.pos0);
+                    mask_b = cnt < kPageSize || (own && last > it.pos0 + it.tok_a);
+                }
+                flags = (__any_sync(0xffffffffu, mask_a) ? kMaskA : 0) | (__any_sync(0xffffffffu, mask_b) ? kMaskB : 0) |
+                        (int32_t)((__ballot_sync(0xffffffffu, cnt > 0 && cnt < kPageSize) & 255u) << kFixShift);
+                const int page0 = __shfl_sync(0xffffffffu, page, 0);
+                run8 = __all_sync(0xffffffffu, held && page == page0 + (lane & 7));
+                pg += kPromptTilePages;
+                enter();
+                ++tn;
+            };
+            auto open_unit = [&](int u) {
+                it = load_item(a.plan.items + unit / Hkv);
+                h = unit % Hkv;
+                after = u + 1 < u1 ? __ldg(a.plan.cta_unit + u + 1) : 0;
+                n = max(it.tiles_a, it.tiles_b);
+                tn = 0;
+                node = it.start_node;
+                pg = it.start_page + (lane & 7);
+                rec = a.plan.nodes[node];
+                first = a.node_page_off[node];
+                enter();
+                resolve();
+            };
+            if (u0 < u1)
+                open_unit(u0);
+            for (int u = u0; u < u1 && ok;) {
+                const int t = tn - 1;
+                {
+                    const int cnt_now = cnt;
+                    const int32_t flags_now = flags;
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv, ++g) {
                         const int s = (int)(g % NST);
@@ -308,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                             if (lane < 8)
                                 meta[ms + lane] = entry;
                             if (lane == 0)
-                                meta[ms + 8] = flags;
+                                meta[ms + 8] = flags_now;
                             __syncwarp();
                         }
                         const uint32_t dst = base + L::kv_off + (uint32_t)s * L::tile;
@@ -343,7 +374,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                             }
                         }
                     }
-                    uint32_t fix = ((uint32_t)flags >> kFixShift) & 255u;
+                    ++gt;
+                    // The next tile, while this one's copies are in flight.
+                    if (tn < n) {
+                        resolve();
+                    } else if (++u < u1) {
+                        unit = after;
+                        open_unit(u);
+                    }
+                    uint32_t fix = ((uint32_t)flags_now >> kFixShift) & 255u;
                     if (ok && fix) {
                         // V rows past a node's last token: the page holds
                         // anything there, and their P of 0 must not meet a
@@ -353,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                         const int sv = (int)(gv % NST);
                         ok = wait(kFull + sv, (gv / NST) & 1, 303);
                         for (; fix; fix &= fix - 1) {
-                            const int j = __ffs((int)fix) - 1, used = __shfl_sync(0xffffffffu, cnt, j);
+                            const int j = __ffs((int)fix) - 1, used = __shfl_sync(0xffffffffu, cnt_now, j);
                             uint8_t *at = smem + L::kv_off + (uint32_t)sv * L::tile + (uint32_t)j * 2 * L::group;
                             // 16 rows of D / 64 x 128 B, in 16-byte pieces
                             for (int x = lane; x < (kPageSize - used) * (D / 64) * 8; x += 32) {
@@ -367,8 +406,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                         if (lane == 0)
                             tc::mbar_arrive(bar(kFixed + sv));
                     }
-                    pg += kPromptTilePages;
-                    settle();
                 }
             }
             if (!ok) {
@@ -393,8 +430,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                 // d halves 1 KB apart and its 8-token groups L::group apart.
                 const uint64_t dk0 = tc::smem_desc(base + L::kv_off, 16, L::group);
                 const uint64_t dv0 = tc::smem_desc(base + L::kv_off, 1024, L::group);
-                uint32_t gt = 0, nq[2] = {0, 0}, np[2] = {0, 0}, nf = 0;
-                uint32_t st = 0, ph = 0;   // next operand stage and its parity
                 bool ok = true;
                 auto wait1 = [&](int b, uint32_t parity, int code) {
                     if (!tc::mbar_wait(bar(b), parity)) {
@@ -404,97 +439,111 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                     }
                     return ok;
                 };
-                auto issue_s = [&](int w, uint32_t stage) {
-                    const uint64_t dq = dq0 + (uint64_t)((w * L::tile) >> 4), dk = dk0 + (uint64_t)((stage * L::tile) >> 4);
-#pragma unroll
-                    for (int s = 0; s < D / 16; ++s)
-                        tc::mma_bf16(tmem + w * 128, dq + (uint64_t)(((s >> 2) * kHalf + (s & 3) * 32) >> 4),
-                                     dk + (uint64_t)(((s >> 2) * 1024 + (s & 3) * 32) >> 4), idesc_s, s > 0 ? 1u : 0u);
-                    tc::mma_commit(bar(kSFull + w));
+                // The CTA's KV tiles are one sequence, across units: a step
+                // makes PV of the tile in hand and S of the one after, for A,
+                // then for B.  One copy of the code serves both and the units'
+                // ends, which would otherwise run from a cold instruction cache.
+                uint32_t gt = 0;             // tile in hand
+                uint32_t bits = 0;           // parities: Q full of A, B (0, 1), P full (2, 3)
+                uint32_t fixed = 0;          // V fixed, by stage
+                uint32_t st = 0, ph = 0;     // next operand stage and its parity
+                int u = u0, t = 0, cur[2] = {0, 0}, nxt[2];
+                bool have = false;
+                // The next unit is read in two steps a tile apart: nothing
+                // here waits for a load just issued.
+                int next_unit = u0 < u1 ? __ldg(a.plan.cta_unit + u0) : 0, next_a = 0, next_b = 0;
+                auto look = [&]() {
+                    const PromptItem *it = a.plan.items + next_unit / Hkv;
+                    next_a = __ldg(&it->tiles_a);
+                    next_b = __ldg(&it->tiles_b);
                 };
-                auto issue_pv = [&](int w, uint32_t stage, bool first) {
-                    const uint64_t dv = dv0 + (uint64_t)((stage * L::tile) >> 4);
-#pragma unroll
-                    for (int s = 0; s < 8; ++s)
-                        mma_ts(tmem + 256 + w * 128, tmem + w * 128 + s * 8, dv + (uint64_t)((s * 2 * L::group) >> 4),
-                               idesc_o, (!first || s > 0) ? 1u : 0u);
-                };
-                int next_a = 0, next_b = 0;
-                auto look = [&](int u) {
-                    if (u < u1) {
-                        const PromptItem *it = a.plan.items + a.plan.cta_unit[u] / Hkv;
-                        next_a = it->tiles_a;
-                        next_b = it->tiles_b;
-                    }
-                };
-                look(u0);
-                for (int u = u0; u < u1 && ok; ++u) {
-                    const int nt[2] = {next_a, next_b};
-                    const int n = max(nt[0], nt[1]);
-                    look(u + 1);
-                    if (!wait1(kFull + st, ph, 311))
-                        break;
-#pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        if (nt[w] == 0)
-                            continue;
-                        if (!wait1(kQFull + w, nq[w] & 1, 312))
+                look();
+                while (ok) {
+                    const bool same = have && t + 1 < max(cur[0], cur[1]);
+                    const bool more = same || u < u1;
+                    const int tx = same ? t + 1 : 0;
+                    nxt[0] = same ? cur[0] : next_a;
+                    nxt[1] = same ? cur[1] : next_b;
+                    uint32_t sv = 0, sk = 0, pk = 0;
+                    if (have) {
+                        sv = st;
+                        if (!wait1(kFull + st, ph, 313))
                             break;
-                        ++nq[w];
-                        tc::fence_after_sync();
-                        issue_s(w, st);
-                        if (nt[w] == 1)
-                            tc::mma_commit(bar(kQEmpty + w));
-                    }
-                    if (!ok)
-                        break;
-                    tc::mma_commit(bar(kEmpty + st));
-                    for (int t = 0; t < n; ++t, ++gt) {
                         st = st + 1 == NST ? 0 : st + 1;
                         ph ^= st == 0;
-                        const uint32_t sv = st, pv = ph;
-                        if (!wait1(kFull + sv, pv, 313))
-                            break;
                         // V of a tile with partial pages, once its empty rows are zeros.
                         if (meta[(gt % kMetaSlots) * kMetaInts + 8] >> kFixShift) {
-                            if (!wait1(kFixed + sv, (nf >> sv) & 1, 317))
+                            if (!wait1(kFixed + sv, (fixed >> sv) & 1, 317))
                                 break;
-                            nf ^= 1u << sv;
+                            fixed ^= 1u << sv;
                         }
-                        uint32_t sk = 0;
-                        if (t + 1 < n) {
-                            st = st + 1 == NST ? 0 : st + 1;
-                            ph ^= st == 0;
-                            sk = st;
-                            if (!wait1(kFull + sk, ph, 315))
-                                break;
-                        }
-#pragma unroll
-                        for (int w = 0; w < 2; ++w) {
-                            if (t >= nt[w])
-                                continue;
-                            if (!wait1(kPFull + w, np[w] & 1, 314))
-                                break;
-                            ++np[w];
-                            tc::fence_after_sync();
-                            issue_pv(w, sv, t == 0);
-                            if (t + 1 < nt[w]) {
-                                issue_s(w, sk);
-                                if (t + 2 == nt[w])
-                                    tc::mma_commit(bar(kQEmpty + w));
-                            } else {
-                                tc::mma_commit(bar(kOFull + w));
-                            }
-                        }
-                        if (!ok)
-                            break;
-                        tc::mma_commit(bar(kEmpty + sv));
-                        if (t + 1 < n)
-                            tc::mma_commit(bar(kEmpty + sk));
+                        ++gt;
                     }
-                    // the next unit's first K
-                    st = st + 1 == NST ? 0 : st + 1;
-                    ph ^= st == 0;
+                    bool k_ready = false;
+                    if (more) {
+                        sk = st;
+                        pk = ph;
+                        st = st + 1 == NST ? 0 : st + 1;
+                        ph ^= st == 0;
+                    }
+#pragma unroll 1
+                    for (int w = 0; w < 2; ++w) {
+                        const uint32_t ts = tmem + w * 128;
+                        if (have && t < (w ? cur[1] : cur[0])) {
+                            if (!wait1(kPFull + w, (bits >> (2 + w)) & 1, 314))
+                                break;
+                            bits ^= 4u << w;
+                            tc::fence_after_sync();
+                            const uint64_t dv = dv0 + (uint64_t)((sv * L::tile) >> 4);
+#pragma unroll
+                            for (int s = 0; s < 8; ++s)
+                                mma_ts(ts + 256, ts + s * 8, dv + (uint64_t)((s * 2 * L::group) >> 4), idesc_o,
+                                       (t > 0 || s > 0) ? 1u : 0u);
+                            if (t + 1 == (w ? cur[1] : cur[0]))
+                                tc::mma_commit(bar(kOFull + w));
+                        }
+                        const int nw = w ? nxt[1] : nxt[0];
+                        if (more && tx < nw) {
+                            if (!k_ready && !wait1(kFull + sk, pk, 315))
+                                break;
+                            k_ready = true;
+                            if (tx == 0) {
+                                if (!wait1(kQFull + w, (bits >> w) & 1, 312))
+                                    break;
+                                bits ^= 1u << w;
+                            }
+                            tc::fence_after_sync();
+                            const uint64_t dq = dq0 + (uint64_t)((w * L::tile) >> 4), dk = dk0 + (uint64_t)((sk * L::tile) >> 4);
+#pragma unroll
+                            for (int s = 0; s < D / 16; ++s)
+                                tc::mma_bf16(ts, dq + (uint64_t)(((s >> 2) * kHalf + (s & 3) * 32) >> 4),
+                                             dk + (uint64_t)(((s >> 2) * 1024 + (s & 3) * 32) >> 4), idesc_s, s > 0 ? 1u : 0u);
+                            tc::mma_commit(bar(kSFull + w));
+                            if (tx + 1 == nw)
+                                tc::mma_commit(bar(kQEmpty + w));
+                        }
+                    }
+                    if (!ok || !more) {
+                        if (have)
+                            tc::mma_commit(bar(kEmpty + sv));
+                        break;
+                    }
+                    if (have)
+                        tc::mma_commit(bar(kEmpty + sv));
+                    tc::mma_commit(bar(kEmpty + sk));
+                    if (!same) {
+                        ++u;
+                        if (u < u1)
+                            next_unit = __ldg(a.plan.cta_unit + u);
+                        cur[0] = nxt[0];
+                        cur[1] = nxt[1];
+                    } else if (tx == 1) {
+                        look();
+                    }
+                    if (!same && max(cur[0], cur[1]) == 1)
+                        look();   // no second tile to do it in
+                    t = tx;
+                    have = true;
                 }
                 // Every MMA and its arrivals end before the CTA does.
                 tc::mma_commit(bar(kDrain));
@@ -513,9 +562,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
         const f32x2 scale2 = f2_pack(scale, scale);
         uint32_t gt = 0, ns = 0, no = 0;
         bool ok = true;
+        // The next unit's record is loaded a unit ahead, its number two.
+        int unit = u0 < u1 ? __ldg(a.plan.cta_unit + u0) : 0;
+        int next_unit = u0 + 1 < u1 ? __ldg(a.plan.cta_unit + u0 + 1) : unit;
+        PromptItem next = load_item(a.plan.items + unit / Hkv);
         for (int u = u0; u < u1 && ok; ++u) {
-            const int unit = a.plan.cta_unit[u], h = unit % Hkv;
-            const PromptItem it = load_item(a.plan.items + unit / Hkv);
+            const PromptItem it = next;
+            const int h = unit % Hkv;
+            next = load_item(a.plan.items + next_unit / Hkv);
+            unit = next_unit;
+            if (u + 2 < u1)
+                next_unit = __ldg(a.plan.cta_unit + u + 2);
             const int nt = w ? it.tiles_b : it.tiles_a, before = w ? it.tok_a : 0;
             const bool held = tok < (w ? it.tok_b : it.tok_a);
             const int pos = it.pos0 + before + tok;
@@ -561,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                     const float f = mn == -INFINITY ? 1.f : tc::ex2(m - mn);
                     m = mn;
                     l *= f;
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t o[32];
                         tmem_ld32_issue(to + 32 * c, o);
@@ -615,37 +672,38 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                 }
                 ++no;
                 tc::fence_after_sync();
-                const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
+                const float inv = l > 0.f ? __fdividef(1.f, l) : 0.f;
+                const bool f32 = it.part0 >= 0 || a.out_dtype == DEFT_OUT_F32;
+                uint8_t *dst = it.part0 >= 0 ? reinterpret_cast<uint8_t *>(a.o_part + slot * D)
+                                             : static_cast<uint8_t *>(a.out) + orow * D * (f32 ? 4 : 2);
+                // One copy of the code for the parts of a row: it runs once
+                // a unit, from a cold instruction cache.
+#pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t o[32];
                     tmem_ld32_issue(to + 32 * c, o);
                     tmem_ld_wait(o);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
                     if (!held)
                         continue;
-                    if (it.part0 >= 0 || a.out_dtype == DEFT_OUT_F32) {
-                        float4 *dst = reinterpret_cast<float4 *>(it.part0 >= 0 ? a.o_part + slot * D
-                                                                               : static_cast<float *>(a.out) + orow * D) + 8 * c;
+                    if (f32) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            dst[i] = make_float4(__uint_as_float(o[4 * i]) * inv, __uint_as_float(o[4 * i + 1]) * inv,
-                                                 __uint_as_float(o[4 * i + 2]) * inv, __uint_as_float(o[4 * i + 3]) * inv);
+                        for (int i = 0; i < 4; ++i)
+                            store32(dst + 128 * c + 32 * i, o + 8 * i);
                     } else {
-                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * D) + 4 * c;
+                        uint32_t x[16];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t x[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                x[k] = tc::pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * inv,
-                                                       __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
-                            dst[i] = make_uint4(x[0], x[1], x[2], x[3]);
-                        }
+                        for (int i = 0; i < 16; ++i)
+                            x[i] = tc::pack_bf16x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+                        store32(dst + 64 * c, x);
+                        store32(dst + 64 * c + 32, x + 8);
                     }
                 }
             }
             if (held) {
-                const float lse2 = l > 0.f ? m + log2f(l) : -INFINITY;
+                const float lse2 = l > 0.f ? m + __log2f(l) : -INFINITY;
                 if (it.part0 >= 0)
                     a.lse_part[slot] = lse2;
                 else
