@@ -63,11 +63,11 @@ constexpr int kFixShift = 8;                // pages whose V rows past the count
 template <int D>
 struct Smem {
     static constexpr uint32_t tile = (D / 64) * kHalf;       // one 128 x D operand
-    static constexpr int stages = D == 128 ? 4 : 8;         // K and V tiles in turn
+    static constexpr int stages = D == 128 ? 2 : 4;          // pairs: K of a tile and V of the tile before
     static constexpr uint32_t group = D * 16;                // 8 tokens x D dims
     static constexpr uint32_t q_off = 0;                     // [2]: [d half][128 rows][128 B]
-    static constexpr uint32_t kv_off = 2 * tile;             // [stages]: [16 groups of 8 tokens][d half][8 tokens][128 B]
-    static constexpr uint32_t meta_off = kv_off + stages * tile;
+    static constexpr uint32_t kv_off = 2 * tile;             // [stages][K, V]: [16 groups of 8 tokens][d half][8 tokens][128 B]
+    static constexpr uint32_t meta_off = kv_off + stages * 2 * tile;
     static constexpr uint32_t bar_off = meta_off + kMetaSlots * kMetaInts * 4;
     static constexpr int num_bars = 3 * stages + 11;
     static constexpr uint32_t misc_off = bar_off + num_bars * 8;   // TMEM base, error
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
     volatile int *err = reinterpret_cast<volatile int *>(smem + L::misc_off + 4);
     auto bar = [&](int i) { return base + L::bar_off + 8u * (uint32_t)i; };
     constexpr int kFull = 0, kEmpty = NST, kQFull = 2 * NST, kQEmpty = kQFull + 2, kSFull = kQFull + 4,
-                  kPFull = kQFull + 6, kOFull = kQFull + 8, kDrain = kQFull + 10, kFixed = kQFull + 11;
+                  kPFull = kQFull + 6, kOFull = kQFull + 8, kDrain = kQFull + 10, kVLand = kQFull + 11;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = a.gqa_group, Hkv = a.num_kv_heads;
     const int tile_tok = kPromptRows / G;
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
     if (tid == 0) {
         grid_dep_launch();
         for (int i = 0; i < NST; ++i) {
-            tc::mbar_init(bar(kFull + i), 1);
+            tc::mbar_init(bar(kFull + i), 2);   // the copies' bytes, and V's empty rows are zeros
             tc::mbar_init(bar(kEmpty + i), 1);
         }
         for (int w = 0; w < 2; ++w) {
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
         }
         tc::mbar_init(bar(kDrain), 1);
         for (int i = 0; i < NST; ++i)
-            tc::mbar_init(bar(kFixed + i), 1);
+            tc::mbar_init(bar(kVLand + i), 1);
         *err = 0;
         tc::fence_mbar_init();
     }
@@ -258,7 +258,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
         if (warp == 8) {
             // ---------------- TMA producer ----------------
             const uint64_t pol = tc::l2_kv_policy(false);
-            uint32_t g = 0, gt = 0;       // operand tiles, KV tiles so far
             uint32_t nq[2] = {0, 0};      // Q tiles so far
             bool ok = true;
             // The unit ahead: lane i < 8 follows page i of every tile: its
@@ -320,98 +319,111 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
             };
             if (u0 < u1)
                 open_unit(u0);
-            for (int u = u0; u < u1 && ok;) {
+            // A step loads K of the next tile and, beside it, V of the tile
+            // before: what the MMA issuer needs of one step.
+            bool v_run8 = false;
+            int v_page = 0, v_cnt = 0, v_h = 0;
+            uint32_t v_fix = 0, step = 0, land = 0;   // land: parity of V's own barriers, by stage
+            auto copy = [&](uint32_t dst, const CUtensorMap *one, const CUtensorMap *eight, bool whole, int pg0, int head, int b) {
+                if (whole) {
+                    if (lane == 0)
+                        tc::tma_load_5d(dst, eight, 0, 0, 0, 2 * head, pg0, bar(b), pol);
+                } else if (lane < 8) {
+                    tc::tma_load_5d(dst + (uint32_t)lane * 2 * L::group, one, 0, 0, 0, 2 * head, pg0, bar(b), pol);
+                }
+            };
+            for (int u = u0; ok; ++step) {
+                const bool more = u < u1;
                 const int t = tn - 1;
-                {
-                    const int cnt_now = cnt;
-                    const int32_t flags_now = flags;
-#pragma unroll
-                    for (int kv = 0; kv < 2; ++kv, ++g) {
-                        const int s = (int)(g % NST);
-                        if (g >= NST)
-                            ok = ok && wait(kEmpty + s, (g / NST - 1) & 1, 301);
-                        if (!ok)
+                const int s = (int)(step % NST);
+                if (step >= NST && !(ok = wait(kEmpty + s, (step / NST - 1) & 1, 301)))
+                    break;
+                const uint32_t dst = base + L::kv_off + (uint32_t)s * 2 * L::tile;
+                if (more) {
+                    // The slot's last reader is done: its tile's P, which
+                    // the stage just freed came after.
+                    const int ms = (int)(step % kMetaSlots) * kMetaInts;
+                    if (lane < 8)
+                        meta[ms + lane] = entry;
+                    if (lane == 0)
+                        meta[ms + 8] = flags;
+                    __syncwarp();
+                }
+                // V with partial pages lands on a barrier of its own: its
+                // empty rows are zeroed before the step is handed over.
+                if (lane == 0) {
+                    tc::mbar_arrive_expect_tx(bar(kFull + s), (more ? L::tile : 0) + (step > 0 && !v_fix ? L::tile : 0));
+                    if (v_fix)
+                        tc::mbar_arrive_expect_tx(bar(kVLand + s), L::tile);
+                    else
+                        tc::mbar_arrive(bar(kFull + s));
+                }
+                __syncwarp();
+                if (more)
+                    copy(dst, &maps.k1, &maps.k8, run8, page, h, kFull + s);
+                if (step > 0)
+                    copy(dst + L::tile, &maps.v1, &maps.v8, v_run8, v_page, v_h, (v_fix ? kVLand : kFull) + s);
+                if (more && t == 0) {
+                    // The unit's rows, once the unit before has made its last
+                    // S from the buffer.
+                    for (int w = 0; w < 2 && ok; ++w) {
+                        if ((w ? it.tiles_b : it.tiles_a) == 0)
+                            continue;
+                        if (nq[w] && !(ok = wait(kQEmpty + w, (nq[w] - 1) & 1, 302)))
                             break;
-                        if (kv == 0) {
-                            // The slot's last reader is done: its tile's P,
-                            // which the stage just freed came after.
-                            const int ms = (int)(gt % kMetaSlots) * kMetaInts;
-                            if (lane < 8)
-                                meta[ms + lane] = entry;
-                            if (lane == 0)
-                                meta[ms + 8] = flags_now;
-                            __syncwarp();
-                        }
-                        const uint32_t dst = base + L::kv_off + (uint32_t)s * L::tile;
-                        if (lane == 0)
-                            tc::mbar_arrive_expect_tx(bar(kFull + s), L::tile);
-                        __syncwarp();
-                        const CUtensorMap *one = kv ? &maps.v1 : &maps.k1, *eight = kv ? &maps.v8 : &maps.k8;
-                        if (run8) {
-                            if (lane == 0)
-                                tc::tma_load_5d(dst, eight, 0, 0, 0, 2 * h, page, bar(kFull + s), pol);
-                        } else if (lane < 8) {
-                            tc::tma_load_5d(dst + (uint32_t)lane * 2 * L::group, one, 0, 0, 0, 2 * h, page,
-                                            bar(kFull + s), pol);
-                        }
-                        if (t == 0 && kv == 0) {
-                            // The unit's rows, once the unit before has made
-                            // its last S from the buffer.
-                            for (int w = 0; w < 2 && ok; ++w) {
-                                if ((w ? it.tiles_b : it.tiles_a) == 0)
-                                    continue;
-                                if (nq[w])
-                                    ok = wait(kQEmpty + w, (nq[w] - 1) & 1, 302);
-                                if (!ok)
-                                    break;
-                                ++nq[w];
-                                if (lane == 0) {
-                                    tc::mbar_arrive_expect_tx(bar(kQFull + w), (uint32_t)(tile_tok * G) * D * 2);
-                                    for (int x = 0; x < D / 64; ++x)
-                                        tma_load_3d(base + L::q_off + (uint32_t)w * L::tile + x * kHalf, &maps.q,
-                                                    64 * x, h * G, it.row0 + (w ? it.tok_a : 0), bar(kQFull + w));
-                                }
-                            }
+                        ++nq[w];
+                        if (lane == 0) {
+                            tc::mbar_arrive_expect_tx(bar(kQFull + w), (uint32_t)(tile_tok * G) * D * 2);
+                            for (int x = 0; x < D / 64; ++x)
+                                tma_load_3d(base + L::q_off + (uint32_t)w * L::tile + x * kHalf, &maps.q, 64 * x, h * G,
+                                            it.row0 + (w ? it.tok_a : 0), bar(kQFull + w));
                         }
                     }
-                    ++gt;
-                    // The next tile, while this one's copies are in flight.
-                    if (tn < n) {
-                        resolve();
-                    } else if (++u < u1) {
-                        unit = after;
-                        open_unit(u);
+                    if (!ok) {
+                        ++step;
+                        break;
                     }
-                    uint32_t fix = ((uint32_t)flags_now >> kFixShift) & 255u;
-                    if (ok && fix) {
-                        // V rows past a node's last token: the page holds
-                        // anything there, and their P of 0 must not meet a
-                        // NaN.  V has to land first; the ring covers the
-                        // wait, as the tile is used two tiles later.
-                        const uint32_t gv = g - 1;
-                        const int sv = (int)(gv % NST);
-                        ok = wait(kFull + sv, (gv / NST) & 1, 303);
-                        for (; fix; fix &= fix - 1) {
-                            const int j = __ffs((int)fix) - 1, used = __shfl_sync(0xffffffffu, cnt_now, j);
-                            uint8_t *at = smem + L::kv_off + (uint32_t)sv * L::tile + (uint32_t)j * 2 * L::group;
-                            // 16 rows of D / 64 x 128 B, in 16-byte pieces
-                            for (int x = lane; x < (kPageSize - used) * (D / 64) * 8; x += 32) {
-                                const int row = used + x / ((D / 64) * 8), rest = x % ((D / 64) * 8);
-                                *reinterpret_cast<uint4 *>(at + (row >> 3) * L::group + (rest >> 3) * 1024 +
-                                                           (row & 7) * 128 + (rest & 7) * 16) = make_uint4(0, 0, 0, 0);
-                            }
+                }
+                if (v_fix) {
+                    // V rows past a node's last token: the page holds anything
+                    // there, and their P of 0 must not meet a NaN.
+                    ok = wait(kVLand + s, (land >> s) & 1, 303);
+                    land ^= 1u << s;
+                    for (; v_fix; v_fix &= v_fix - 1) {
+                        const int j = __ffs((int)v_fix) - 1, used = __shfl_sync(0xffffffffu, v_cnt, j);
+                        uint8_t *at = smem + L::kv_off + (uint32_t)s * 2 * L::tile + L::tile + (uint32_t)j * 2 * L::group;
+                        // 16 rows of D / 64 x 128 B, in 16-byte pieces
+                        for (int x = lane; x < (kPageSize - used) * (D / 64) * 8; x += 32) {
+                            const int row = used + x / ((D / 64) * 8), rest = x % ((D / 64) * 8);
+                            *reinterpret_cast<uint4 *>(at + (row >> 3) * L::group + (rest >> 3) * 1024 + (row & 7) * 128 +
+                                                       (rest & 7) * 16) = make_uint4(0, 0, 0, 0);
                         }
-                        tc::fence_proxy_async();
-                        __syncwarp();
-                        if (lane == 0)
-                            tc::mbar_arrive(bar(kFixed + sv));
                     }
+                    tc::fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0)
+                        tc::mbar_arrive(bar(kFull + s));
+                }
+                if (!more) {
+                    ++step;
+                    break;
+                }
+                // The next tile, while this one's copies are in flight.
+                v_run8 = run8;
+                v_page = page;
+                v_cnt = cnt;
+                v_h = h;
+                v_fix = ((uint32_t)flags >> kFixShift) & 255u;
+                if (tn < n) {
+                    resolve();
+                } else if (++u < u1) {
+                    unit = after;
+                    open_unit(u);
                 }
             }
             if (!ok) {
                 // Every copy that went out lands before the CTA ends.
-                const uint32_t first = g > (uint32_t)NST ? g - NST : 0;
-                for (uint32_t i = first; i < g; ++i)
+                for (uint32_t i = step > (uint32_t)NST ? step - NST : 0; i < step; ++i)
                     tc::mbar_wait(bar(kFull + (int)(i % NST)), (i / NST) & 1);
                 for (int w = 0; w < 2; ++w)
                     if (nq[w])
@@ -429,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                 // K: K-major, 8-token groups L::group apart; V: MN-major, its
                 // d halves 1 KB apart and its 8-token groups L::group apart.
                 const uint64_t dk0 = tc::smem_desc(base + L::kv_off, 16, L::group);
-                const uint64_t dv0 = tc::smem_desc(base + L::kv_off, 1024, L::group);
+                const uint64_t dv0 = tc::smem_desc(base + L::kv_off + L::tile, 1024, L::group);
                 bool ok = true;
                 auto wait1 = [&](int b, uint32_t parity, int code) {
                     if (!tc::mbar_wait(bar(b), parity)) {
@@ -443,12 +455,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                 // makes PV of the tile in hand and S of the one after, for A,
                 // then for B.  One copy of the code serves both and the units'
                 // ends, which would otherwise run from a cold instruction cache.
-                uint32_t gt = 0;             // tile in hand
-                uint32_t bits = 0;           // parities: Q full of A, B (0, 1), P full (2, 3)
-                uint32_t fixed = 0;          // V fixed, by stage
-                uint32_t st = 0, ph = 0;     // next operand stage and its parity
-                int u = u0, t = 0, cur[2] = {0, 0}, nxt[2];
-                bool have = false;
+                uint32_t qp = 0, pp = 0;           // parities of Q full and P full, bit w
+                uint32_t st = 0, ph = 0;           // the step's stage and its parity
+                int u = u0, t = 0, n = 0, na = 0, nb = 0;   // tile t of n; A has na of them, B nb
                 // The next unit is read in two steps a tile apart: nothing
                 // here waits for a load just issued.
                 int next_unit = u0 < u1 ? __ldg(a.plan.cta_unit + u0) : 0, next_a = 0, next_b = 0;
@@ -459,91 +468,72 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                 };
                 look();
                 while (ok) {
-                    const bool same = have && t + 1 < max(cur[0], cur[1]);
-                    const bool more = same || u < u1;
-                    const int tx = same ? t + 1 : 0;
-                    nxt[0] = same ? cur[0] : next_a;
-                    nxt[1] = same ? cur[1] : next_b;
-                    uint32_t sv = 0, sk = 0, pk = 0;
-                    if (have) {
-                        sv = st;
-                        if (!wait1(kFull + st, ph, 313))
-                            break;
-                        st = st + 1 == NST ? 0 : st + 1;
-                        ph ^= st == 0;
-                        // V of a tile with partial pages, once its empty rows are zeros.
-                        if (meta[(gt % kMetaSlots) * kMetaInts + 8] >> kFixShift) {
-                            if (!wait1(kFixed + sv, (fixed >> sv) & 1, 317))
-                                break;
-                            fixed ^= 1u << sv;
-                        }
-                        ++gt;
+                    // the tile after
+                    int tx = t + 1, xa = na, xb = nb;
+                    const bool same = tx < n;
+                    if (!same) {
+                        tx = 0;
+                        xa = u < u1 ? next_a : 0;
+                        xb = u < u1 ? next_b : 0;
                     }
-                    bool k_ready = false;
-                    if (more) {
-                        sk = st;
-                        pk = ph;
-                        st = st + 1 == NST ? 0 : st + 1;
-                        ph ^= st == 0;
-                    }
+                    if (!wait1(kFull + st, ph, 313))
+                        break;
+                    const uint32_t at = (st * 2 * L::tile) >> 4;
 #pragma unroll 1
                     for (int w = 0; w < 2; ++w) {
                         const uint32_t ts = tmem + w * 128;
-                        if (have && t < (w ? cur[1] : cur[0])) {
-                            if (!wait1(kPFull + w, (bits >> (2 + w)) & 1, 314))
+                        const int now = w ? nb : na, nxt = w ? xb : xa;
+                        if (t < now) {
+                            if (!wait1(kPFull + w, (pp >> w) & 1, 314))
                                 break;
-                            bits ^= 4u << w;
+                            pp ^= 1u << w;
                             tc::fence_after_sync();
-                            const uint64_t dv = dv0 + (uint64_t)((sv * L::tile) >> 4);
 #pragma unroll
                             for (int s = 0; s < 8; ++s)
-                                mma_ts(ts + 256, ts + s * 8, dv + (uint64_t)((s * 2 * L::group) >> 4), idesc_o,
+                                mma_ts(ts + 256, ts + s * 8, dv0 + (uint64_t)(at + ((s * 2 * L::group) >> 4)), idesc_o,
                                        (t > 0 || s > 0) ? 1u : 0u);
-                            if (t + 1 == (w ? cur[1] : cur[0]))
+                            if (t + 1 == now)
                                 tc::mma_commit(bar(kOFull + w));
                         }
-                        const int nw = w ? nxt[1] : nxt[0];
-                        if (more && tx < nw) {
-                            if (!k_ready && !wait1(kFull + sk, pk, 315))
-                                break;
-                            k_ready = true;
+                        if (tx < nxt) {
                             if (tx == 0) {
-                                if (!wait1(kQFull + w, (bits >> w) & 1, 312))
+                                if (!wait1(kQFull + w, (qp >> w) & 1, 312))
                                     break;
-                                bits ^= 1u << w;
+                                qp ^= 1u << w;
                             }
                             tc::fence_after_sync();
-                            const uint64_t dq = dq0 + (uint64_t)((w * L::tile) >> 4), dk = dk0 + (uint64_t)((sk * L::tile) >> 4);
+                            const uint64_t dq = dq0 + (uint64_t)((w * L::tile) >> 4);
 #pragma unroll
                             for (int s = 0; s < D / 16; ++s)
                                 tc::mma_bf16(ts, dq + (uint64_t)(((s >> 2) * kHalf + (s & 3) * 32) >> 4),
-                                             dk + (uint64_t)(((s >> 2) * 1024 + (s & 3) * 32) >> 4), idesc_s, s > 0 ? 1u : 0u);
+                                             dk0 + (uint64_t)(at + (((s >> 2) * 1024 + (s & 3) * 32) >> 4)), idesc_s,
+                                             s > 0 ? 1u : 0u);
                             tc::mma_commit(bar(kSFull + w));
-                            if (tx + 1 == nw)
+                            if (tx + 1 == nxt)
                                 tc::mma_commit(bar(kQEmpty + w));
                         }
                     }
-                    if (!ok || !more) {
-                        if (have)
-                            tc::mma_commit(bar(kEmpty + sv));
+                    if (!ok)
                         break;
-                    }
-                    if (have)
-                        tc::mma_commit(bar(kEmpty + sv));
-                    tc::mma_commit(bar(kEmpty + sk));
+                    // A unit's first step frees its stage here; the others'
+                    // are freed by the softmax of the step's last S.
                     if (!same) {
+                        tc::mma_commit(bar(kEmpty + st));
+                        if (u == u1)
+                            break;
+                        na = xa;
+                        nb = xb;
+                        n = max(na, nb);
                         ++u;
                         if (u < u1)
                             next_unit = __ldg(a.plan.cta_unit + u);
-                        cur[0] = nxt[0];
-                        cur[1] = nxt[1];
-                    } else if (tx == 1) {
-                        look();
                     }
-                    if (!same && max(cur[0], cur[1]) == 1)
-                        look();   // no second tile to do it in
+                    // (a unit of one tile has no later step to do it in)
+                    if (tx == 1 || (tx == 0 && n == 1))
+                        look();
                     t = tx;
-                    have = true;
+                    st = st + 1 == NST ? 0 : st + 1;
+                    ph ^= st == 0;
                 }
                 // Every MMA and its arrivals end before the CTA does.
                 tc::mma_commit(bar(kDrain));
@@ -576,6 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
             const int nt = w ? it.tiles_b : it.tiles_a, before = w ? it.tok_a : 0;
             const bool held = tok < (w ? it.tok_b : it.tok_a);
             const int pos = it.pos0 + before + tok;
+            const bool frees = w == (it.tiles_b > 0);
             float m = -INFINITY, l = 0.f;
             for (int t = 0; t < nt; ++t) {
                 if (!wait(kSFull + w, ns & 1, 321 + w, t == 0)) {
@@ -583,6 +574,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                     break;
                 }
                 ++ns;
+                // S of this tile is made, and what came before it: both
+                // operands of the step are free (of its last S, B's if the
+                // unit has a B; a unit's first step is freed by the issuer).
+                if (frees && t > 0 && r == 0)
+                    tc::mbar_arrive(bar(kEmpty + (int)((gt + t) % NST)));
                 tc::fence_after_sync();
                 uint32_t sr[128];
 #pragma unroll
