@@ -67,17 +67,17 @@ struct Smem {
     static constexpr uint32_t group = D * 16;                // 8 tokens x D dims
     static constexpr uint32_t q_off = 0;                     // [2]: [d half][128 rows][128 B]
     static constexpr uint32_t kv_off = 2 * tile;             // [stages][K, V]: [16 groups of 8 tokens][d half][8 tokens][128 B]
-    static constexpr uint32_t meta_off = kv_off + stages * 2 * tile;
+    static constexpr uint32_t out_off = kv_off + stages * 2 * tile;   // [2]: [128 rows][128 B] of output, swizzled
+    static constexpr uint32_t meta_off = out_off + 2 * kHalf;
     static constexpr uint32_t bar_off = meta_off + kMetaSlots * kMetaInts * 4;
     static constexpr int num_bars = 3 * stages + 11;
     static constexpr uint32_t misc_off = bar_off + num_bars * 8;   // TMEM base, error
     static constexpr uint32_t total = misc_off + 16;
-    static constexpr uint32_t alloc = total + 1024;
-    static_assert(alloc <= 227 * 1024, "shared memory of one CTA");
+    static_assert(total <= 227 * 1024, "shared memory of one CTA");
 };
 
 struct PromptMaps {
-    CUtensorMap q, k1, v1, k8, v8;
+    CUtensorMap q, k1, v1, k8, v8, out;
 };
 
 // D[tmem] (+)= A[tmem] . B[smem]
@@ -140,6 +140,30 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, int 
         : "memory");
 }
 
+__device__ __forceinline__ void st_shared16(uint32_t dst, const uint32_t *r)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(dst), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+// 3-D box shared -> global of this thread, and the waits for its source to
+// have been read / for everything to be written.
+__device__ __forceinline__ void tma_store_3d(const void *tmap, uint32_t src, int c0, int c1, int c2)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];\n"
+        "cp.async.bulk.commit_group;\n" ::"l"(reinterpret_cast<uint64_t>(tmap)),
+        "r"(src), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+__device__ __forceinline__ void bulk_wait_read()
+{
+    asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait_all()
+{
+    asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
+}
+
 // 32 bytes to global memory, a whole sector a lane.
 __device__ __forceinline__ void store32(void *dst, const uint32_t *r)
 {
@@ -186,10 +210,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
 {
     using L = Smem<D>;
     constexpr int NST = L::stages;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = smem_u32(smem_raw);
-    const uint32_t base = (raw + 1023u) & ~1023u;
-    uint8_t *smem = smem_raw + (base - raw);
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t base = smem_u32(smem);
     volatile int32_t *meta = reinterpret_cast<volatile int32_t *>(smem + L::meta_off);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::misc_off);
     volatile int *err = reinterpret_cast<volatile int *>(smem + L::misc_off + 4);
@@ -237,6 +259,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
+    if (tid == 0 && (base & 1023u) != 0)
+        *err = 300;   // the swizzled operands need their atoms aligned
     const int u0 = a.plan.cta_off[blockIdx.x], u1 = a.plan.cta_off[blockIdx.x + 1];
     // A bounded wait of a whole warp; the first one that runs out leaves its
     // code.  A warpgroup may sit out many units (tile B of units that have
@@ -564,7 +588,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
             if (u + 2 < u1)
                 next_unit = __ldg(a.plan.cta_unit + u + 2);
             const int nt = w ? it.tiles_b : it.tiles_a, before = w ? it.tok_a : 0;
-            const bool held = tok < (w ? it.tok_b : it.tok_a);
+            const int toks = w ? it.tok_b : it.tok_a;
+            const bool held = tok < toks;
             const int pos = it.pos0 + before + tok;
             const bool frees = w == (it.tiles_b > 0);
             float m = -INFINITY, l = 0.f;
@@ -590,11 +615,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                 const int ms = (int)((gt + t) % kMetaSlots) * kMetaInts;
                 if (meta[ms + 8] & (w ? kMaskB : kMaskA)) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int seen = attended(meta[ms + j], pos);
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t bits = ((1u << attended(meta[ms + 2 * c], pos)) - 1) |
+                                              (((1u << attended(meta[ms + 2 * c + 1], pos)) - 1) << 16);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            sr[16 * j + i] = i < seen ? sr[16 * j + i] : 0xff800000u;   // -inf
+                        for (int i = 0; i < 32; ++i)
+                            sr[32 * c + i] = (bits >> i) & 1 ? sr[32 * c + i] : 0xff800000u;   // -inf
                     }
                 }
                 float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
@@ -656,13 +682,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                     tc::mbar_arrive(bar(kPFull + w));
             }
             gt += (uint32_t)max(it.tiles_a, it.tiles_b);
-            if (!ok)
-                break;
             const int rows = (it.tok_a + it.tok_b) * G;
             const size_t orow = (size_t)(it.row0 + before + tok) * a.num_q_heads + h * G + head;
             const size_t slot = (size_t)it.part0 + (size_t)h * rows + before * G + r;
             if (nt > 0) {
-                if (!wait(kOFull + w, no & 1, 323 + w)) {
+                ok = ok && wait(kOFull + w, no & 1, 323 + w);
+                // The four warps go on, or end, together; the staging rows
+                // are free behind this barrier.
+                if (r == 0)
+                    bulk_wait_read();
+                if (tc::named_sync_or(1 + w, 128, !ok)) {
                     ok = false;
                     break;
                 }
@@ -670,6 +699,40 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                 tc::fence_after_sync();
                 const float inv = l > 0.f ? __fdividef(1.f, l) : 0.f;
                 const bool f32 = it.part0 >= 0 || a.out_dtype == DEFT_OUT_F32;
+                if (!f32 && toks == tile_tok) {
+                    // A whole tile in bf16: 64 dims of its rows to shared
+                    // memory, and out as one box.  (Written from here, 32
+                    // bytes of 32 rows a store, the rows cost the load/store
+                    // unit eight times as much: 275 us for the reasoning
+                    // tree's prefill against XXX.)
+                    const uint32_t row_s = base + L::out_off + w * kHalf + (uint32_t)r * 128;
+#pragma unroll 1
+                    for (int c = 0; c < D / 64; ++c) {
+                        uint32_t o[64];
+                        tmem_ld32_issue(to + 64 * c, o);
+                        tmem_ld32_issue(to + 64 * c + 32, o + 32);
+                        tmem_ld_wait(o);
+                        tmem_ld_wait(o + 32);
+                        if (c > 0) {
+                            if (r == 0)
+                                bulk_wait_read();   // the box before has been read
+                            tc::named_sync(1 + w, 128);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            uint32_t x[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                x[k] = tc::pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * inv,
+                                                       __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
+                            st_shared16(row_s + ((uint32_t)(i ^ (r & 7)) << 4), x);
+                        }
+                        tc::fence_proxy_async();
+                        tc::named_sync(1 + w, 128);
+                        if (r == 0)
+                            tma_store_3d(&maps.out, base + L::out_off + w * kHalf, 64 * c, h * G, it.row0 + before);
+                    }
+                } else {
                 uint8_t *dst = it.part0 >= 0 ? reinterpret_cast<uint8_t *>(a.o_part + slot * D)
                                              : static_cast<uint8_t *>(a.out) + orow * D * (f32 ? 4 : 2);
                 // One copy of the code for the parts of a row: it runs once
@@ -697,6 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                         store32(dst + 64 * c + 32, x + 8);
                     }
                 }
+                }
             }
             if (held) {
                 const float lse2 = l > 0.f ? m + __log2f(l) : -INFINITY;
@@ -707,6 +771,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
             }
         }
     }
+    if (tid == 0 || tid == 128)
+        bulk_wait_all();
     tc::fence_before_sync();
     __syncthreads();
     if (*err) {
@@ -770,14 +836,14 @@ bool pool_map(const void *ptr, const PromptArgs &a, bool run8, CUtensorMap *m)
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// q as [tokens][Hq][D]; a box is a tile's tokens of one group, 64 dims.
-bool q_map(const PromptArgs &a, CUtensorMap *m)
+// q (or out) as [tokens][Hq][D]; a box is a tile's tokens of one group, 64 dims.
+bool rows_map(const PromptArgs &a, const void *ptr, int64_t stride, CUtensorMap *m)
 {
     const cuuint64_t dims[3] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.num_q_heads, (cuuint64_t)a.num_rows};
-    const cuuint64_t strides[2] = {(cuuint64_t)a.head_dim * 2, (cuuint64_t)a.q_stride * 2};
+    const cuuint64_t strides[2] = {(cuuint64_t)a.head_dim * 2, (cuuint64_t)stride * 2};
     const cuuint32_t box[3] = {64, (cuuint32_t)a.gqa_group, (cuuint32_t)(kPromptRows / a.gqa_group)};
     const cuuint32_t estr[3] = {1, 1, 1};
-    return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.q), dims, strides, box, estr,
+    return encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, estr,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -792,13 +858,13 @@ int launch_dim(const PromptArgs &a, const PromptMaps &maps, int32_t ctas, cudaSt
     if (e != cudaSuccess)
         return (int)e;
     if (dev >= 64 || !(set.load(std::memory_order_acquire) >> dev & 1)) {
-        e = cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Smem<D>::alloc);
+        e = cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Smem<D>::total);
         if (e != cudaSuccess)
             return (int)e;
         if (dev < 64)
             set.fetch_or(1ull << dev, std::memory_order_release);
     }
-    prompt_kernel<D><<<ctas, kThreads, Smem<D>::alloc, st>>>(a, maps);
+    prompt_kernel<D><<<ctas, kThreads, Smem<D>::total, st>>>(a, maps);
     return (int)cudaGetLastError();
 }
 
@@ -807,7 +873,8 @@ int launch_dim(const PromptArgs &a, const PromptMaps &maps, int32_t ctas, cudaSt
 int launch_prompt(const PromptArgs &a, int32_t ctas, void *stream)
 {
     PromptMaps maps;
-    if (!encoder() || !q_map(a, &maps.q) || !pool_map(a.k_pages, a, false, &maps.k1) ||
+    if (!encoder() || !rows_map(a, a.q, a.q_stride, &maps.q) ||
+        !rows_map(a, a.out, (int64_t)a.num_q_heads * a.head_dim, &maps.out) || !pool_map(a.k_pages, a, false, &maps.k1) ||
         !pool_map(a.v_pages, a, false, &maps.v1) || !pool_map(a.k_pages, a, true, &maps.k8) ||
         !pool_map(a.v_pages, a, true, &maps.v8))
         return (int)cudaErrorInvalidValue;
