@@ -12,6 +12,7 @@
 #include <cstdint>
 #include <cstring>
 #include <new>
+#include <type_traits>
 #include <utility>
 
 #include <cuda_runtime.h>
@@ -25,12 +26,15 @@ namespace {
 constexpr int kMergeThreads = 256;
 
 // One warp per (split item, KV head, row): lane i owns D / 32 consecutive
-// elements, pieces in order.  Latency bound: the partials were written
-// moments earlier and come from L2.
+// elements.  The lse of all pieces first (one a lane), then the pieces' rows
+// four at a time, so that a row costs about two L2 latencies; pieces none of
+// whose tokens the row sees (lse -inf, their rows never written) are not
+// read.  The sum runs over the pieces in order.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) prompt_merge_kernel(PromptArgs a)
 {
     constexpr int E = D / 32;
+    using Vec = typename std::conditional<E == 4, float4, float2>::type;
     grid_dep_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int G = a.gqa_group, Hkv = a.num_kv_heads;
@@ -39,32 +43,54 @@ __global__ void __launch_bounds__(kMergeThreads) prompt_merge_kernel(PromptArgs 
     const int r = blockIdx.y * (kMergeThreads / 32) + warp;
     if (r >= rows)
         return;
-    grid_dep_wait();
     const size_t first = (size_t)m.part0 + (size_t)h * rows + r, step = (size_t)Hkv * rows;
+    grid_dep_wait();
     float M = -INFINITY;
     for (int j = lane; j < m.pieces; j += 32)
         M = fmaxf(M, a.lse_part[first + j * step]);
     M = warp_max(M);
     float acc[E] = {}, sum = 0.f;
-    for (int j = 0; j < m.pieces; ++j) {
-        const float w = exp2f(a.lse_part[first + j * step] - M);
+    for (int j0 = 0; j0 < m.pieces; j0 += 32) {
+        const float w = j0 + lane < m.pieces ? exp2f(a.lse_part[first + (j0 + lane) * step] - M) : 0.f;
         sum += w;
-        if (w == 0.f)
-            continue;   // a piece none of whose tokens the row sees
-        const float *o = a.o_part + (first + j * step) * D + lane * E;
+        const int n = min(32, m.pieces - j0);
+        for (int j = 0; j < n; j += 4) {
+            Vec v[4];
+            float wj[4];
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            acc[e] = fmaf(w, o[e], acc[e]);
+            for (int i = 0; i < 4; ++i) {
+                wj[i] = __shfl_sync(0xffffffffu, w, (j + i) & 31);
+                if (j + i >= n)
+                    wj[i] = 0.f;
+                if (wj[i] != 0.f)
+                    v[i] = *reinterpret_cast<const Vec *>(a.o_part + (first + (j0 + j + i) * step) * D + lane * E);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (wj[i] == 0.f)
+                    continue;
+                const float *o = reinterpret_cast<const float *>(&v[i]);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    acc[e] = fmaf(wj[i], o[e], acc[e]);
+            }
+        }
     }
+    sum = warp_sum(sum);
     const float inv = 1.f / sum;
     const size_t row = (size_t)(m.row0 + r / G) * a.num_q_heads + h * G + r % G;
+    if (a.out_dtype == DEFT_OUT_F32) {
+        Vec v;
+        float *o = reinterpret_cast<float *>(&v);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const size_t at = row * D + lane * E + e;
-        if (a.out_dtype == DEFT_OUT_F32)
-            static_cast<float *>(a.out)[at] = acc[e] * inv;
-        else
-            static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(acc[e] * inv);
+        for (int e = 0; e < E; ++e)
+            o[e] = acc[e] * inv;
+        *reinterpret_cast<Vec *>(static_cast<float *>(a.out) + row * D + lane * E) = v;
+    } else {
+        __nv_bfloat162 *o = reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.out) + row * D + lane * E);
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+            o[e / 2] = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
     }
     if (lane == 0)
         a.lse[row] = (M + log2f(sum)) * kLn2;

@@ -10,16 +10,20 @@
 // token (causal), so the masked pages come last.
 //
 // Units (item x KV head) are dealt to kPromptCtas CTAs by list scheduling
-// on an estimated cost: in order, each to the CTA that is free first.  The
-// order is head-major, costliest item first: the CTAs running at a time read
-// few heads' K and V, which then stay in L2, and the last head's smallest
-// items fill the gaps at the end.  A dealt list needs no work queue, so
-// steps of one plan may run at the same time.
+// on an estimated cost: in order, each to the CTA that is free first.  A
+// dealt list needs no work queue, so steps of one plan may run at the same
+// time.  With few units a CTA the order is costliest item first over all
+// heads, which balances best; with many it is head by head (each costliest
+// item first): the CTAs running at a time then read few heads' K and V,
+// which stay in L2, and the last head's smallest items fill the gaps.
 //
 // When a few units would leave SMs idle or one unit would outlast the rest,
 // the page ranges of the items are cut into pieces whose partial results a
 // second launch merges by log-sum-exp.  The cut is chosen by simulating the
-// deal for a few piece sizes and taking the shortest, the merge counted.
+// deal for a few piece sizes and taking the shortest, the pieces' fp32 rows
+// and the merge counted: cutting a 4096-token prompt of 16 heads into 640
+// units instead of 256 moved 75 MB of partials and cost more than it gained
+// (95 us against 55 us).
 #include <algorithm>
 #include <cstring>
 #include <queue>
@@ -29,12 +33,15 @@
 namespace deft {
 namespace {
 
-// Estimated costs in KV tiles of a pair of query tiles.
+// Estimated costs in KV tiles of a pair of query tiles (1.33 us each).
 constexpr double kCostSingle = 0.75;  // a KV tile against one query tile
-constexpr double kCostUnit = 2.0;     // a unit's start and end
+constexpr double kCostUnit = 3.0;     // a unit's start and end
+constexpr double kCostPiece = 1.5;    // a piece's fp32 rows (twice a bf16 tile's bytes, row by row)
 constexpr double kCostMerge = 3.0;    // the merge launch
+constexpr double kCostSlot = 1e-4;    // a partial row, written and read once through L2
 constexpr int32_t kMinPieceTiles = 4; // shortest piece
 constexpr int64_t kMaxSimUnits = 8 * kPromptCtas;   // above, no split is looked for: many units balance by themselves
+constexpr int64_t kMaxCostOrder = 16 * kPromptCtas; // above, units go head by head (few-shot prefill, 10 units a CTA: 442 us by cost, 449 by head)
 
 int32_t pages_of(int64_t tokens) { return (int32_t)((tokens + kPageSize - 1) / kPageSize); }
 int32_t tiles_of(int32_t pages) { return (pages + kPromptTilePages - 1) / kPromptTilePages; }
@@ -61,29 +68,33 @@ Heap idle_ctas()
     return Heap(std::greater<Slot>(), std::move(v));
 }
 
-// Length of the deal when ranges are cut into pieces of at most `cap` tiles.
-double simulate(const std::vector<Proto> &protos, int32_t heads, int32_t cap)
+bool head_major(size_t items, int32_t heads) { return (int64_t)items * heads > kMaxCostOrder; }
+
+// Length of the deal (costliest item first) when ranges are cut into pieces
+// of at most `cap` tiles.
+double simulate(const std::vector<Proto> &protos, int32_t heads, int32_t group, int32_t cap)
 {
     std::vector<double> cost;
-    bool split = false;
+    double slots = 0;
     for (const Proto &p : protos) {
         const int32_t n = pieces_of(p, cap), t = (p.tiles() + n - 1) / n;
-        split |= n > 1;
+        if (n > 1)
+            slots += (double)n * (p.it.tok_a + p.it.tok_b) * group * heads;
         for (int32_t i = 0; i < n; ++i)
-            cost.push_back(kCostUnit + t * p.tile_cost());
+            cost.push_back(kCostUnit + (n > 1 ? kCostPiece : 0.0) + t * p.tile_cost());
     }
     std::sort(cost.begin(), cost.end(), std::greater<double>());
     Heap heap = idle_ctas();
     double end = 0;
-    for (int32_t h = 0; h < heads; ++h)
-        for (const double c : cost) {
+    for (const double c : cost)
+        for (int32_t h = 0; h < heads; ++h) {
             Slot s = heap.top();
             heap.pop();
             s.first += c;
             end = std::max(end, s.first);
             heap.push(s);
         }
-    return end + (split ? kCostMerge : 0.0);
+    return end + (slots > 0 ? kCostMerge + kCostSlot * slots : 0.0);
 }
 
 }  // namespace
@@ -186,12 +197,12 @@ int build_prompt_plan(const int32_t *parent, const int32_t *node_len, int32_t nu
             longest = std::max(longest, q.tiles());
         }
         const double even = total * num_kv_heads / kPromptCtas;
-        double best = simulate(protos, num_kv_heads, cap);
-        for (const double part : {1.0, 0.7, 0.5, 0.35, 0.25}) {
+        double best = simulate(protos, num_kv_heads, gqa_group, cap);
+        for (const double part : {1.0, 0.6, 0.35, 0.2}) {
             const int32_t c = std::max(kMinPieceTiles, (int32_t)(even * part + 0.999));
             if (c >= longest)
                 continue;
-            const double t = simulate(protos, num_kv_heads, c);
+            const double t = simulate(protos, num_kv_heads, gqa_group, c);
             if (t < best) {
                 best = t;
                 cap = c;
@@ -224,7 +235,7 @@ int build_prompt_plan(const int32_t *parent, const int32_t *node_len, int32_t nu
                 it.part0 = (int32_t)(part0 + made * piece_slots);
             }
             ++made;
-            cut.emplace_back(kCostUnit + std::max(it.tiles_a, it.tiles_b) * q.tile_cost(), it);
+            cut.emplace_back(kCostUnit + (n > 1 ? kCostPiece : 0.0) + std::max(it.tiles_a, it.tiles_b) * q.tile_cost(), it);
             for (int32_t left = end - begin; left > 0 && end < all;) {
                 const int32_t here = node == q.it.node ? INT32_MAX : pages_of(node_len[node]) - first;
                 const int32_t step = std::min(left, here);
@@ -248,27 +259,27 @@ int build_prompt_plan(const int32_t *parent, const int32_t *node_len, int32_t nu
         return DEFT_EUNSUPPORTED;
 
     // The deal.
-    std::vector<int32_t> owner((size_t)cut.size() * num_kv_heads);
+    const size_t units = cut.size() * num_kv_heads;
+    const bool by_head = head_major(cut.size(), num_kv_heads);
+    auto item_of = [&](size_t u) { return by_head ? u % cut.size() : u / num_kv_heads; };
+    auto head_of = [&](size_t u) { return (int32_t)(by_head ? u / cut.size() : u % num_kv_heads); };
+    std::vector<int32_t> owner(units);
     p->cta_off.assign(kPromptCtas + 1, 0);
     Heap heap = idle_ctas();
-    size_t u = 0;
-    for (int32_t h = 0; h < num_kv_heads; ++h)
-        for (size_t i = 0; i < cut.size(); ++i) {
-            Slot s = heap.top();
-            heap.pop();
-            s.first += cut[i].first;
-            owner[u++] = s.second;
-            ++p->cta_off[s.second + 1];
-            heap.push(s);
-        }
+    for (size_t u = 0; u < units; ++u) {
+        Slot s = heap.top();
+        heap.pop();
+        s.first += cut[item_of(u)].first;
+        owner[u] = s.second;
+        ++p->cta_off[s.second + 1];
+        heap.push(s);
+    }
     for (int32_t c = 0; c < kPromptCtas; ++c)
         p->cta_off[c + 1] += p->cta_off[c];
     std::vector<int32_t> at(p->cta_off.begin(), p->cta_off.end() - 1);
-    p->cta_unit.resize(u);
-    u = 0;
-    for (int32_t h = 0; h < num_kv_heads; ++h)
-        for (size_t i = 0; i < cut.size(); ++i)
-            p->cta_unit[at[owner[u++]]++] = (int32_t)i * num_kv_heads + h;
+    p->cta_unit.resize(units);
+    for (size_t u = 0; u < units; ++u)
+        p->cta_unit[at[owner[u]]++] = (int32_t)item_of(u) * num_kv_heads + head_of(u);
     p->items.reserve(cut.size());
     for (const auto &c : cut)
         p->items.push_back(c.second);
