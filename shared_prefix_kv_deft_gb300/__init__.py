@@ -489,27 +489,44 @@ class PagePool:
         return int(load().deft_pages_refcount(self.handle, int(page)))
 
 
-def _on_device(*tensors):
-    """Raises unless every tensor is a CUDA tensor of the current device (the
-    library launches there)."""
-    import torch
-    cur = torch.cuda.current_device()
+def _launch_stream(stream, *tensors) -> int:
+    """The raw stream to launch on.  Raises unless every tensor is on the
+    current CUDA device (the library launches there)."""
+    dev = _torch.cuda.current_device()
     for t in tensors:
-        if not t.is_cuda or t.device.index != cur:
+        if t.get_device() != dev:      # -1: not on a GPU
             raise ValueError("tensors must be on the current CUDA device")
+    if stream is None:
+        raw = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            return raw(dev)
+    return _stream(stream)
 
 
-def _heads_packed(x) -> bool:
-    """Whether x [tokens, heads, head_dim] holds each token's heads
+_torch = None
+
+
+def _need_torch():
+    """torch, imported at the first call that takes tensors."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _heads_packed(shape, stride) -> bool:
+    """Whether [tokens, heads, head_dim] holds each token's heads
     contiguously (the stride of a dimension of one element says nothing)."""
-    return x.shape[0] == 0 or (x.stride(2) == 1 and (x.shape[1] == 1 or x.stride(1) == x.shape[2]))
+    return shape[0] == 0 or (stride[2] == 1 and (shape[1] == 1 or stride[1] == shape[2]))
 
 
-def _index_tensor(t, name: str, ndim: int = 1):
-    import torch
-    if t.dtype != torch.int32 or t.dim() != ndim or not t.is_contiguous():
+def _index_tensor(t, name: str) -> int:
+    """The length of a contiguous one-dimensional int32 tensor."""
+    n, = t.shape if t.dim() == 1 else (-1,)
+    if n < 0 or t.dtype != _torch.int32 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous one-dimensional int32 tensor")
-    return t
+    return n
 
 
 @dataclass
@@ -549,36 +566,38 @@ def deft_page_table(node_len, free_pages, prev=None, table: Optional[PageTable] 
     prev: (prev_len, prev_page_off, prev_page_id) of the earlier table, None:
     every node starts empty.  table: the tensors to write (reused between
     steps); None: allocated for max_pages and max_tokens."""
-    nl, free = _index_tensor(node_len, "node_len"), _index_tensor(free_pages, "free_pages")
-    n = int(nl.shape[0])
+    _need_torch()
+    n, n_free = _index_tensor(node_len, "node_len"), _index_tensor(free_pages, "free_pages")
     if table is None:
         if max_pages is None or max_tokens is None:
             raise ValueError("max_pages and max_tokens are needed to allocate a table")
-        table = alloc_page_table(n, max_pages, max_tokens, nl.device)
-    t = table
-    for name in ("page_off", "page_id", "tok_off", "slot", "counts"):
-        _index_tensor(getattr(t, name), name)
-    if t.page_off.shape[0] < n + 1 or t.tok_off.shape[0] < n + 1 or t.counts.shape[0] < 4:
+        table = alloc_page_table(n, max_pages, max_tokens, node_len.device)
+    off, ids, tok, slot, counts, ws = (table.page_off, table.page_id, table.tok_off, table.slot, table.counts,
+                                       table.workspace)
+    n_ids, n_slots = _index_tensor(ids, "page_id"), _index_tensor(slot, "slot")
+    if _index_tensor(off, "page_off") <= n or _index_tensor(tok, "tok_off") <= n or _index_tensor(counts, "counts") < 4:
         raise ValueError("page_off and tok_off need num_nodes + 1 entries, counts 4")
-    used = [nl, free, t.page_off, t.page_id, t.tok_off, t.slot, t.counts]
+    used = [node_len, free_pages, off, ids, tok, slot, counts]
     pl = po = pi = None
-    n_prev = n_ids = 0
+    n_prev = n_prev_ids = 0
     if prev is not None:
-        pl, po, pi = (_index_tensor(x, "prev") for x in prev)
-        n_prev, n_ids = int(pl.shape[0]), int(pi.shape[0])
-        if po.shape[0] < n_prev:
+        t_len, t_off, t_id = prev
+        n_prev, n_prev_ids = _index_tensor(t_len, "prev_len"), _index_tensor(t_id, "prev_page_id")
+        if _index_tensor(t_off, "prev_page_off") < n_prev:
             raise ValueError("prev_page_off is shorter than prev_len")
-        used += [pl, po, pi]
-    if t.workspace is not None:
-        used.append(t.workspace)
-    _on_device(*used)
-    _check("deft_page_table", load().deft_page_table(
-        nl.data_ptr(), n, pl.data_ptr() if n_prev else None, po.data_ptr() if n_prev else None,
-        pi.data_ptr() if n_prev else None, n_prev, n_ids, free.data_ptr(), int(free.shape[0]), int(page_size),
-        t.page_off.data_ptr(), t.page_id.data_ptr(), int(t.page_id.shape[0]), t.tok_off.data_ptr(),
-        t.slot.data_ptr(), int(t.slot.shape[0]), t.counts.data_ptr(),
-        None if t.workspace is None else t.workspace.data_ptr(), 0 if t.workspace is None else int(t.workspace.numel()),
-        _stream(stream)))
+        used += prev
+        if n_prev:
+            pl, po, pi = t_len.data_ptr(), t_off.data_ptr(), t_id.data_ptr()
+    ws_ptr, ws_bytes = None, 0
+    if ws is not None:
+        used.append(ws)
+        ws_ptr, ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    st = _launch_stream(stream, *used)
+    rc = load().deft_page_table(node_len.data_ptr(), n, pl, po, pi, n_prev, n_prev_ids, free_pages.data_ptr(), n_free,
+                                int(page_size), off.data_ptr(), ids.data_ptr(), n_ids, tok.data_ptr(), slot.data_ptr(),
+                                n_slots, counts.data_ptr(), ws_ptr, ws_bytes, st)
+    if rc:
+        _check("deft_page_table", rc)
     return table
 
 
@@ -586,25 +605,33 @@ def deft_kv_write(k, v, slot, k_pages, v_pages, stream=None):
     """deft_kv_write: rows of k and v ([tokens, num_kv_heads, head_dim], bf16
     or fp32, views with any token stride) into the pages at their slots; rows
     with a slot outside the pool (-1) are skipped."""
-    import torch
-    T, Hkv, d = k.shape
-    if v.shape != k.shape or v.dtype != k.dtype or k.dtype not in (torch.bfloat16, torch.float32):
+    torch = _need_torch()
+    shape, ks, vs, dt = k.shape, k.stride(), v.stride(), k.dtype
+    if len(shape) != 3 or v.shape != shape or v.dtype != dt or dt not in (torch.bfloat16, torch.float32):
         raise ValueError("k and v must be alike: [tokens, heads, head_dim], bf16 or fp32")
-    if not _heads_packed(k) or not _heads_packed(v):
+    T, Hkv, d = shape
+    if not _heads_packed(shape, ks) or not _heads_packed(shape, vs):
         raise ValueError("the heads of a token must be contiguous")
-    for p in (k_pages, v_pages):
-        if p.dtype != torch.bfloat16 or not p.is_contiguous() or p.dim() != 4 or p.shape[1] != Hkv or p.shape[3] != d:
-            raise ValueError("k_pages and v_pages must be contiguous bf16 [pages, heads, page_size, head_dim]")
-    if k_pages.shape != v_pages.shape:
-        raise ValueError("k_pages and v_pages differ in shape")
-    _index_tensor(slot, "slot")
-    if slot.shape[0] != T:
+    pool = _check_pools(k_pages, v_pages, d)
+    if pool[1] != Hkv:
+        raise ValueError("k_pages and v_pages have another number of heads")
+    if _index_tensor(slot, "slot") != T:
         raise ValueError("slot must have one entry per token")
-    _on_device(k, v, slot, k_pages, v_pages)
-    _check("deft_kv_write", load().deft_kv_write(
-        k.data_ptr(), v.data_ptr(), DEFT_OUT_BF16 if k.dtype == torch.bfloat16 else DEFT_OUT_F32, int(k.stride(0)),
-        int(v.stride(0)), slot.data_ptr(), int(T), k_pages.data_ptr(), v_pages.data_ptr(), int(k_pages.shape[0]),
-        int(Hkv), int(d), int(k_pages.shape[2]), _stream(stream)))
+    st = _launch_stream(stream, k, v, slot, k_pages, v_pages)
+    rc = load().deft_kv_write(k.data_ptr(), v.data_ptr(), DEFT_OUT_BF16 if dt == torch.bfloat16 else DEFT_OUT_F32, ks[0],
+                              vs[0], slot.data_ptr(), T, k_pages.data_ptr(), v_pages.data_ptr(), pool[0], Hkv, d,
+                              pool[2], st)
+    if rc:
+        _check("deft_kv_write", rc)
+
+
+def _check_pools(k_pages, v_pages, head_dim):
+    """The shape of the page pools, after their checks."""
+    shape, bf16 = k_pages.shape, _torch.bfloat16
+    if len(shape) != 4 or v_pages.shape != shape or shape[3] != head_dim or k_pages.dtype != bf16 or \
+            v_pages.dtype != bf16 or not k_pages.is_contiguous() or not v_pages.is_contiguous():
+        raise ValueError("k_pages and v_pages must be contiguous bf16 [pages, heads, page_size, head_dim], alike")
+    return shape
 
 
 PROMPT_ARRAYS = {"nodes": (0, 2), "items": (1, 12), "cta_off": (2, 1), "cta_unit": (3, 1), "merges": (4, 4)}
@@ -685,38 +712,37 @@ def deft_prompt_attn(q, k_pages, v_pages, node_page_off, page_id, plan: PromptPl
     """Causal attention of the plan's prompts: q [rows, num_q_heads,
     head_dim] bf16 (any token stride), rows packed prompt by prompt; returns
     (out, lse).  bufs: alloc_buffers(plan, rows, num_q_heads, head_dim)."""
-    import torch
-    T, Hq, d = q.shape
+    torch = _need_torch()
+    shape, qs = q.shape, q.stride()
+    if len(shape) != 3 or q.dtype != torch.bfloat16 or not _heads_packed(shape, qs):
+        raise ValueError("q must be bf16 [rows, num_q_heads, head_dim] with the heads of a token contiguous")
+    T, Hq, d = shape
     if bufs is None:
         bufs = alloc_buffers(plan, T, Hq, d, q.device, out_dtype)
-    if q.dtype != torch.bfloat16 or not _heads_packed(q):
-        raise ValueError("q must be bf16 with the heads of a token contiguous")
-    for t in (k_pages, v_pages):
-        if t.dtype != torch.bfloat16 or not t.is_contiguous() or t.dim() != 4 or t.shape[3] != d:
-            raise ValueError("k_pages and v_pages must be contiguous bf16 [pages, heads, page_size, head_dim]")
-    if k_pages.shape != v_pages.shape:
-        raise ValueError("k_pages and v_pages differ in shape")
-    _index_tensor(node_page_off, "node_page_off")
-    _index_tensor(page_id, "page_id")
-    if node_page_off.shape[0] < plan.stats["num_nodes"]:
+    out, lse, ws = bufs.out, bufs.lse, bufs.workspace
+    pool = _check_pools(k_pages, v_pages, d)
+    stats = plan.stats
+    rows = stats["num_rows"]
+    if _index_tensor(node_page_off, "node_page_off") < stats["num_nodes"]:
         raise ValueError("node_page_off is shorter than the plan's nodes")
-    if bufs.out.dtype not in (torch.bfloat16, torch.float32) or not bufs.out.is_contiguous() or \
-            tuple(bufs.out.shape[1:]) != (Hq, d) or bufs.out.shape[0] < plan.stats["num_rows"]:
+    _index_tensor(page_id, "page_id")
+    os, ls, odt = out.shape, lse.shape, out.dtype
+    if len(os) != 3 or os[1] != Hq or os[2] != d or os[0] < rows or odt not in (torch.bfloat16, torch.float32) or \
+            not out.is_contiguous():
         raise ValueError("out must be contiguous bf16 or fp32 [rows, num_q_heads, head_dim]")
-    if bufs.lse.dtype != torch.float32 or not bufs.lse.is_contiguous() or tuple(bufs.lse.shape[1:]) != (Hq,) or \
-            bufs.lse.shape[0] < plan.stats["num_rows"]:
+    if len(ls) != 2 or ls[1] != Hq or ls[0] < rows or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be contiguous fp32 [rows, num_q_heads]")
-    _on_device(q, k_pages, v_pages, node_page_off, page_id, bufs.out, bufs.lse, bufs.workspace)
-    if T == 0 and plan.stats["num_rows"] == 0:
-        return bufs.out, bufs.lse
-    scale = 1.0 / math.sqrt(d) if scale is None else scale
-    odt = DEFT_OUT_BF16 if bufs.out.dtype == torch.bfloat16 else DEFT_OUT_F32
-    _check("deft_prompt_attn", load().deft_prompt_attn(
-        q.data_ptr(), int(q.stride(0)) if T > 1 else int(Hq * d), int(T), k_pages.data_ptr(), v_pages.data_ptr(),
-        node_page_off.data_ptr(), page_id.data_ptr(), int(k_pages.shape[0]), int(Hq), int(k_pages.shape[1]), int(d),
-        int(k_pages.shape[2]), float(scale), plan.handle, bufs.out.data_ptr(), odt, bufs.lse.data_ptr(),
-        bufs.workspace.data_ptr(), int(bufs.workspace.numel()), _stream(stream)))
-    return bufs.out, bufs.lse
+    st = _launch_stream(stream, q, k_pages, v_pages, node_page_off, page_id, out, lse, ws)
+    if T == 0 and rows == 0:
+        return out, lse
+    rc = load().deft_prompt_attn(
+        q.data_ptr(), qs[0] if T > 1 else Hq * d, T, k_pages.data_ptr(), v_pages.data_ptr(), node_page_off.data_ptr(),
+        page_id.data_ptr(), pool[0], Hq, pool[1], d, pool[2], 1.0 / math.sqrt(d) if scale is None else float(scale),
+        plan.handle, out.data_ptr(), DEFT_OUT_BF16 if odt == torch.bfloat16 else DEFT_OUT_F32, lse.data_ptr(),
+        ws.data_ptr(), ws.numel() * ws.element_size(), st)
+    if rc:
+        _check("deft_prompt_attn", rc)
+    return out, lse
 
 
 def deft_check_pages(node_len, node_page_off, page_id, num_pages: int, page_size: int = 16) -> int:

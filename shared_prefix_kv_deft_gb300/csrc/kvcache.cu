@@ -64,11 +64,13 @@ __device__ __forceinline__ Sum3 add(const Sum3 &a, const Sum3 &b)
     return Sum3{sat_add(a.pages, b.pages), sat_add(a.toks, b.toks), sat_add(a.taken, b.taken)};
 }
 
-// One node's pages, new tokens and pages taken from the free list.
-__device__ __forceinline__ Sum3 node_sum(const TableArgs &a, int n, int32_t &bad)
+// One node's pages, new tokens and pages taken from the free list; `prev`
+// and `first` are its earlier length and first page.
+__device__ __forceinline__ Sum3 node_sum(const TableArgs &a, int n, int32_t &bad, int32_t &prev, int32_t &first)
 {
     int32_t len = a.node_len[n];
-    int32_t prev = n < a.num_prev ? a.prev_len[n] : 0;
+    prev = n < a.num_prev ? a.prev_len[n] : 0;
+    first = n < a.num_prev ? a.prev_off[n] : 0;
     if (len < 0 || prev < 0) {
         bad |= kBadLength;
         len = max(len, 0);
@@ -78,8 +80,7 @@ __device__ __forceinline__ Sum3 node_sum(const TableArgs &a, int n, int32_t &bad
     const uint32_t had = ((uint32_t)prev + kPageSize - 1) / kPageSize;
     const uint32_t kept = min(had, pages);
     if (kept > 0) {
-        const int64_t at = a.prev_off[n];
-        if (at < 0 || at + kept > a.num_prev_ids)
+        if (first < 0 || first + (int64_t)kept > a.num_prev_ids)
             bad |= kBadPrev;
     }
     return Sum3{pages, (uint32_t)max(len - prev, 0), pages - kept};
@@ -120,25 +121,26 @@ __global__ void __launch_bounds__(kTableThreads) table_sums_kernel(TableArgs a)
 {
     __shared__ Sum3 warp_sum[kTableThreads / 32];
     grid_dep_launch();
-    int32_t bad = 0;
+    int32_t bad = 0, prev, off;
     Sum3 v{0, 0, 0}, total;
     const int first = blockIdx.x * kBlockNodes + threadIdx.x * kPerThread;
     for (int i = 0; i < kPerThread; ++i)
         if (first + i < a.num_nodes)
-            v = add(v, node_sum(a, first + i, bad));
+            v = add(v, node_sum(a, first + i, bad, prev, off));
     cta_scan(v, warp_sum, total);
-    const int neg = __syncthreads_or(bad & kBadLength), prev = __syncthreads_or(bad & kBadPrev);
+    const int neg = __syncthreads_or(bad & kBadLength), outside = __syncthreads_or(bad & kBadPrev);
     if (threadIdx.x == 0) {
         a.block_sums[blockIdx.x] = total.pages;
         a.block_sums[kMaxBlocks + blockIdx.x] = total.toks;
         a.block_sums[2 * kMaxBlocks + blockIdx.x] = total.taken;
-        a.block_sums[3 * kMaxBlocks + blockIdx.x] = (neg ? kBadLength : 0) | (prev ? kBadPrev : 0);
+        a.block_sums[3 * kMaxBlocks + blockIdx.x] = (neg ? kBadLength : 0) | (outside ? kBadPrev : 0);
     }
 }
 
 struct TableSmem {
     uint32_t blk[3][kMaxBlocks + 1];    // exclusive sums before each block
     uint32_t off[3][kBlockNodes + 1];   // ... before each node of the block in hand
+    int32_t prev[kBlockNodes], first[kBlockNodes];   // those nodes' earlier lengths and first pages
     Sum3 warp_sum[kTableThreads / 32];
 };
 
@@ -193,7 +195,8 @@ __global__ void __launch_bounds__(kTableThreads) table_fill_kernel(TableArgs a, 
         Sum3 node[kPerThread], sum{0, 0, 0}, all;
 #pragma unroll
         for (int i = 0; i < kPerThread; ++i) {
-            node[i] = first + i < a.num_nodes ? node_sum(a, first + i, bad) : Sum3{0, 0, 0};
+            const int x = tid * kPerThread + i;
+            node[i] = first + i < a.num_nodes ? node_sum(a, first + i, bad, s.prev[x], s.first[x]) : Sum3{0, 0, 0};
             sum = add(sum, node[i]);
         }
         Sum3 e = cta_scan(sum, s.warp_sum, all);
@@ -219,16 +222,20 @@ __global__ void __launch_bounds__(kTableThreads) table_fill_kernel(TableArgs a, 
         take_block(0);
     const int grid = gridDim.x, cta = blockIdx.x;
 
-    // Page j of the node at index i of the block in hand (node n), or -1.
-    auto page_of = [&](int i, int n, uint32_t j) -> int32_t {
+    // Where page j of the node at index i of the block in hand is listed
+    // (null: nowhere).
+    auto page_at = [&](int i, uint32_t j) -> const int32_t * {
         const uint32_t first_taken = s.off[2][i];
         const uint32_t pages = s.off[0][i + 1] - s.off[0][i], kept = pages - (s.off[2][i + 1] - first_taken);
         if (j < kept) {
-            const int64_t at = (int64_t)a.prev_off[n] + j;
-            return at >= 0 && at < a.num_prev_ids ? a.prev_id[at] : -1;
+            const int64_t at = (int64_t)s.first[i] + j;
+            return at >= 0 && at < a.num_prev_ids ? a.prev_id + at : nullptr;
         }
         const uint32_t at = first_taken + (j - kept);
-        return at < (uint32_t)a.num_free ? a.free_pages[at] : -1;
+        return at < (uint32_t)a.num_free ? a.free_pages + at : nullptr;
+    };
+    auto slot_of = [](int32_t page, uint32_t t) {
+        return page < 0 || page >= INT32_MAX / kPageSize ? -1 : page * kPageSize + (int32_t)(t % kPageSize);
     };
 
     // Offsets: block b by CTA b (and b + grid ...).
@@ -249,16 +256,34 @@ __global__ void __launch_bounds__(kTableThreads) table_fill_kernel(TableArgs a, 
             const int b = num_blocks > 1 ? find(s.blk[0], 0, num_blocks, at) : 0;
             take_block(b);
             const uint32_t end = min(hi, s.off[0][kBlockNodes]);
-            for (uint32_t x = at + tid; x < end; x += kTableThreads) {
-                const int i = find(s.off[0], 0, kBlockNodes, x);
-                a.page_id[x] = page_of(i, b * kBlockNodes + i, x - s.off[0][i]);
+            // Four pages a thread at a time: their loads overlap.
+            for (uint32_t x = at + tid; x < end; x += 4 * kTableThreads) {
+                const int32_t *from[4];
+                int32_t page[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t y = x + k * kTableThreads;
+                    from[k] = nullptr;
+                    if (y < end) {
+                        const int i = find(s.off[0], 0, kBlockNodes, y);
+                        from[k] = page_at(i, y - s.off[0][i]);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    page[k] = from[k] ? *from[k] : -1;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (x + k * kTableThreads < end)
+                        a.page_id[x + k * kTableThreads] = page[k];
             }
             at = end;
         }
     }
     // Slots: CTA's share of [0, max_tokens); past the last token, -1.
     {
-        const int64_t share = ((int64_t)a.max_tokens + grid - 1) / grid;
+        const int64_t share = (((int64_t)a.max_tokens + grid - 1) / grid + 3) & ~(int64_t)3;
+        const bool wide = (reinterpret_cast<uintptr_t>(a.slot) & 15u) == 0;
         const int64_t lo = min(share * cta, (int64_t)a.max_tokens), hi = min(lo + share, (int64_t)a.max_tokens);
         const uint32_t held = (uint32_t)min(hi, (int64_t)total.toks);
         uint32_t at = (uint32_t)min(lo, (int64_t)total.toks);
@@ -268,13 +293,37 @@ __global__ void __launch_bounds__(kTableThreads) table_fill_kernel(TableArgs a, 
             const int b = num_blocks > 1 ? find(s.blk[1], 0, num_blocks, at) : 0;
             take_block(b);
             const uint32_t end = min(held, s.off[1][kBlockNodes]);
-            for (uint32_t x = at + tid; x < end; x += kTableThreads) {
-                const int i = find(s.off[1], 0, kBlockNodes, x);
-                const int n = b * kBlockNodes + i;
-                const uint32_t prev = n < a.num_prev ? (uint32_t)max(a.prev_len[n], 0) : 0u;
-                const uint32_t t = prev + (x - s.off[1][i]);
-                const int32_t page = page_of(i, n, t / kPageSize);
-                a.slot[x] = page < 0 || page >= INT32_MAX / kPageSize ? -1 : page * kPageSize + (int32_t)(t % kPageSize);
+            // Four slots in a row a thread: one search, and mostly one page.
+            for (uint32_t x = at + 4 * tid; x < end; x += 4 * kTableThreads) {
+                int i = find(s.off[1], 0, kBlockNodes, x);
+                const int32_t *from[4];
+                uint32_t t[4];
+                int32_t page[4], slot[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    from[k] = nullptr;
+                    t[k] = 0;
+                    if (x + k < end) {
+                        while (s.off[1][i + 1] <= x + k)
+                            ++i;
+                        t[k] = (uint32_t)max(s.prev[i], 0) + (x + k - s.off[1][i]);
+                        from[k] = page_at(i, t[k] / kPageSize);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    page[k] = !from[k] ? -1 : k > 0 && from[k] == from[k - 1] ? page[k - 1] : *from[k];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    slot[k] = slot_of(page[k], t[k]);
+                if (wide && x + 4 <= end && x % 4 == 0) {
+                    *reinterpret_cast<int4 *>(a.slot + x) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (x + k < end)
+                            a.slot[x + k] = slot[k];
+                }
             }
             at = end;
         }
@@ -333,50 +382,50 @@ struct WriteArgs {
 
 constexpr int kWriteThreads = 256;
 
+#ifndef WU
+#define WU 4
+#endif
 // U 16-byte pieces a thread, kWriteThreads apart; a token's pieces are its K
-// row's, then its V row's (c8 = heads * head_dim / 8 each).
+// row's, then its V row's (c8 = heads * head_dim / 8 each).  All loads go
+// out before the first store.
 template <bool kF32, int U>
 __global__ void __launch_bounds__(kWriteThreads) kv_write_kernel(WriteArgs a, uint32_t c8, int64_t pieces)
 {
-    const uint32_t per_tok = 2 * c8, d8 = (uint32_t)a.head_dim / 8;
+    const uint32_t per_tok = 2 * c8;
+    const int d8_log2 = a.head_dim == 128 ? 4 : 3;   // pieces of a head's row
     const int64_t x0 = (int64_t)blockIdx.x * (kWriteThreads * U) + threadIdx.x;
     const int64_t num_slots = (int64_t)a.num_pages * kPageSize;
+    int64_t tok = x0 / per_tok;
+    uint32_t j = (uint32_t)(x0 - tok * per_tok);
     Row8<kF32> row[U];
-    int64_t dst[U];
+    uint4 *dst[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int64_t x = x0 + u * kWriteThreads;
-        dst[u] = -1;
-        if (x < pieces) {
-            const int64_t tok = x / per_tok;
-            const uint32_t j = (uint32_t)(x - tok * per_tok);
+        dst[u] = nullptr;
+        if (x0 + u * kWriteThreads < pieces) {
             const bool is_v = j >= c8;
             const uint32_t e = is_v ? j - c8 : j;
             const int32_t slot = a.slot[tok];
             if (slot >= 0 && slot < num_slots) {
-                const uint32_t h = e / d8, part = e - h * d8;
-                dst[u] = (((int64_t)(slot / kPageSize) * a.num_kv_heads + h) * kPageSize + slot % kPageSize) * d8 + part;
-                if (is_v)
-                    row[u].load(a.v, tok * a.v_stride + (int64_t)e * 8);
-                else
-                    row[u].load(a.k, tok * a.k_stride + (int64_t)e * 8);
+                const uint32_t h = e >> d8_log2, part = e & ((1u << d8_log2) - 1);
+                const int64_t line = ((int64_t)(slot / kPageSize) * a.num_kv_heads + h) * kPageSize + slot % kPageSize;
+                dst[u] = (is_v ? a.v_pages : a.k_pages) + (line << d8_log2) + part;
+                row[u].load(is_v ? a.v : a.k, tok * (is_v ? a.v_stride : a.k_stride) + (int64_t)e * 8);
             }
+            for (j += kWriteThreads; j >= per_tok; j -= per_tok)
+                ++tok;
         }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        if (dst[u] >= 0) {
-            const int64_t x = x0 + u * kWriteThreads;
-            const uint32_t j = (uint32_t)(x % per_tok);
-            (j >= c8 ? a.v_pages : a.k_pages)[dst[u]] = row[u].bf16();
-        }
-    }
+    for (int u = 0; u < U; ++u)
+        if (dst[u])
+            *dst[u] = row[u].bf16();
 }
 
 template <bool kF32>
 int launch_write(const WriteArgs &a, cudaStream_t st)
 {
-    constexpr int U = 4;
+    constexpr int U = WU;
     const uint32_t c8 = (uint32_t)a.num_kv_heads * a.head_dim / 8;
     const int64_t pieces = (int64_t)a.num_tokens * 2 * c8;
     const int64_t blocks = (pieces + kWriteThreads * U - 1) / (kWriteThreads * U);
@@ -425,9 +474,9 @@ int deft_page_table(const int32_t *node_len, int32_t num_nodes, const int32_t *p
                 need ? static_cast<uint32_t *>(workspace) : nullptr};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const int blocks = (num_nodes + kBlockNodes - 1) / kBlockNodes;
-    // One CTA for every 2048 outputs, two an SM at most.
+    // One CTA for every 1024 outputs, two an SM at most.
     const int64_t outputs = (int64_t)max_pages + max_tokens;
-    const int64_t want = (outputs + 2047) / 2048;
+    const int64_t want = (outputs + 1023) / 1024;
     const int grid = (int)(want < 1 ? 1 : want > 2 * num_sms() ? 2 * num_sms() : want);
     if (blocks > 1) {
         table_sums_kernel<<<blocks, kTableThreads, 0, st>>>(a);
