@@ -14,7 +14,7 @@
 // The work is a few bytes a page and a token, so a call costs its launch and
 // a chain of dependent loads, not bandwidth.  Up to kBlockNodes nodes it is
 // one launch: every CTA scans all lengths into shared memory itself (8 KB
-// from L2) and fills its share of the page ids and slots, found by binary
+// from L2) and fills its share of the pages and their slots, found by binary
 // search in the scanned offsets, so a single long node is spread over all
 // CTAs as well.  Above that a first launch writes the sums of every block of
 // kBlockNodes nodes to the workspace, and each CTA of the second scans the
@@ -86,34 +86,50 @@ __device__ __forceinline__ Sum3 node_sum(const TableArgs &a, int n, int32_t &bad
     return Sum3{pages, (uint32_t)max(len - prev, 0), pages - kept};
 }
 
+__device__ __forceinline__ Sum3 shfl_up(const Sum3 &v, int o)
+{
+    return Sum3{__shfl_up_sync(0xffffffffu, v.pages, o), __shfl_up_sync(0xffffffffu, v.toks, o),
+                __shfl_up_sync(0xffffffffu, v.taken, o)};
+}
+__device__ __forceinline__ Sum3 shfl(const Sum3 &v, int l)
+{
+    return Sum3{__shfl_sync(0xffffffffu, v.pages, l), __shfl_sync(0xffffffffu, v.toks, l),
+                __shfl_sync(0xffffffffu, v.taken, l)};
+}
+// Inclusive scan over the first N lanes of a warp.
+template <int N>
+__device__ __forceinline__ Sum3 warp_scan(Sum3 v)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < N; o <<= 1) {
+        const Sum3 u = shfl_up(v, o);
+        if (lane >= o)
+            v = add(v, u);
+    }
+    return v;
+}
+
 // Exclusive scan over the CTA's threads; `total` is every thread's.
 __device__ __forceinline__ Sum3 cta_scan(Sum3 v, Sum3 *warp_sum, Sum3 &total)
 {
+    constexpr int kWarps = kTableThreads / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    Sum3 inc = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const Sum3 u{__shfl_up_sync(0xffffffffu, inc.pages, o), __shfl_up_sync(0xffffffffu, inc.toks, o),
-                     __shfl_up_sync(0xffffffffu, inc.taken, o)};
-        if (lane >= o)
-            inc = add(inc, u);
-    }
+    const Sum3 inc = warp_scan<32>(v);
     __syncthreads();   // an earlier scan's readers are done
     if (lane == 31)
         warp_sum[warp] = inc;
     __syncthreads();
-    Sum3 before{0, 0, 0};
-    total = Sum3{0, 0, 0};
-    for (int w = 0; w < kTableThreads / 32; ++w) {
-        if (w == warp)
-            before = total;
-        total = add(total, warp_sum[w]);
-    }
-    Sum3 exc{__shfl_up_sync(0xffffffffu, inc.pages, 1), __shfl_up_sync(0xffffffffu, inc.toks, 1),
-             __shfl_up_sync(0xffffffffu, inc.taken, 1)};
-    if (lane == 0)
-        exc = Sum3{0, 0, 0};
-    return add(before, exc);
+    // Every warp scans the warps' sums itself.
+    const Sum3 sums = warp_scan<kWarps>(lane < kWarps ? warp_sum[lane] : Sum3{0, 0, 0});
+    total = shfl(sums, kWarps - 1);
+    const Sum3 before = shfl(sums, warp > 0 ? warp - 1 : 0), prior = shfl_up(inc, 1);
+    Sum3 exc{0, 0, 0};
+    if (warp > 0)
+        exc = before;
+    if (lane > 0)
+        exc = add(exc, prior);
+    return exc;
 }
 
 // Sums of every block of nodes (more than one block only).
@@ -234,10 +250,6 @@ __global__ void __launch_bounds__(kTableThreads) table_fill_kernel(TableArgs a, 
         const uint32_t at = first_taken + (j - kept);
         return at < (uint32_t)a.num_free ? a.free_pages + at : nullptr;
     };
-    auto slot_of = [](int32_t page, uint32_t t) {
-        return page < 0 || page >= INT32_MAX / kPageSize ? -1 : page * kPageSize + (int32_t)(t % kPageSize);
-    };
-
     // Offsets: block b by CTA b (and b + grid ...).
     for (int b = cta; b < num_blocks; b += grid) {
         take_block(b);
@@ -246,88 +258,59 @@ __global__ void __launch_bounds__(kTableThreads) table_fill_kernel(TableArgs a, 
             a.tok_off[b * kBlockNodes + i] = (int32_t)s.off[1][i];
         }
     }
-    // Page ids: CTA's share of [0, max_pages), node blocks in turn.
+    // Page ids and slots together: a thread a page (its node by binary
+    // search), then the warp's pages' slots, half a warp a page.
     {
-        const int64_t share = ((int64_t)a.max_pages + grid - 1) / grid;
+        const int64_t share = ((int64_t)total.pages + grid - 1) / grid;
         const uint32_t lo = (uint32_t)min(share * cta, (int64_t)total.pages);
-        const uint32_t hi = (uint32_t)min(min(share * (cta + 1), (int64_t)a.max_pages), (int64_t)total.pages);
+        const uint32_t hi = (uint32_t)min(share * (cta + 1), (int64_t)total.pages);
+        const int lane = tid & 31;
         uint32_t at = lo;
         while (at < hi) {
             const int b = num_blocks > 1 ? find(s.blk[0], 0, num_blocks, at) : 0;
             take_block(b);
             const uint32_t end = min(hi, s.off[0][kBlockNodes]);
-            // Four pages a thread at a time: their loads overlap.
-            for (uint32_t x = at + tid; x < end; x += 4 * kTableThreads) {
-                const int32_t *from[4];
-                int32_t page[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t y = x + k * kTableThreads;
-                    from[k] = nullptr;
-                    if (y < end) {
-                        const int i = find(s.off[0], 0, kBlockNodes, y);
-                        from[k] = page_at(i, y - s.off[0][i]);
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    page[k] = from[k] ? *from[k] : -1;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (x + k * kTableThreads < end)
-                        a.page_id[x + k * kTableThreads] = page[k];
-            }
-            at = end;
-        }
-    }
-    // Slots: CTA's share of [0, max_tokens); past the last token, -1.
-    {
-        const int64_t share = (((int64_t)a.max_tokens + grid - 1) / grid + 3) & ~(int64_t)3;
-        const bool wide = (reinterpret_cast<uintptr_t>(a.slot) & 15u) == 0;
-        const int64_t lo = min(share * cta, (int64_t)a.max_tokens), hi = min(lo + share, (int64_t)a.max_tokens);
-        const uint32_t held = (uint32_t)min(hi, (int64_t)total.toks);
-        uint32_t at = (uint32_t)min(lo, (int64_t)total.toks);
-        for (int64_t x = max(lo, (int64_t)total.toks) + tid; x < hi; x += kTableThreads)
-            a.slot[x] = -1;
-        while (at < held) {
-            const int b = num_blocks > 1 ? find(s.blk[1], 0, num_blocks, at) : 0;
-            take_block(b);
-            const uint32_t end = min(held, s.off[1][kBlockNodes]);
-            // Four slots in a row a thread: one search, and mostly one page.
-            for (uint32_t x = at + 4 * tid; x < end; x += 4 * kTableThreads) {
-                int i = find(s.off[1], 0, kBlockNodes, x);
-                const int32_t *from[4];
-                uint32_t t[4];
-                int32_t page[4], slot[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    from[k] = nullptr;
-                    t[k] = 0;
-                    if (x + k < end) {
-                        while (s.off[1][i + 1] <= x + k)
-                            ++i;
-                        t[k] = (uint32_t)max(s.prev[i], 0) + (x + k - s.off[1][i]);
-                        from[k] = page_at(i, t[k] / kPageSize);
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    page[k] = !from[k] ? -1 : k > 0 && from[k] == from[k - 1] ? page[k - 1] : *from[k];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    slot[k] = slot_of(page[k], t[k]);
-                if (wide && x + 4 <= end && x % 4 == 0) {
-                    *reinterpret_cast<int4 *>(a.slot + x) = make_int4(slot[0], slot[1], slot[2], slot[3]);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (x + k < end)
-                            a.slot[x + k] = slot[k];
+            for (uint32_t x0 = at + (tid - lane); x0 < end; x0 += kTableThreads) {
+                const uint32_t x = min(x0 + lane, end - 1);
+                const int i = find(s.off[0], 0, kBlockNodes, x);
+                const uint32_t j = x - s.off[0][i], first = s.off[1][i], fresh = s.off[1][i + 1] - first;
+                const uint32_t prev = (uint32_t)max(s.prev[i], 0);
+                // The new tokens of this page: t0 .. t0 + count - 1 of the
+                // node, slots from q on.
+                const uint32_t t0 = max(prev, j * kPageSize);
+                const uint32_t t1 = min(prev + fresh, (j + 1) * kPageSize);
+                const uint32_t count = x0 + lane < end && fresh > 0 && t1 > t0 ? t1 - t0 : 0;
+                const uint32_t q = sat_add(first, t0 - min(t0, prev));
+                // Pages and slots only grow from here on: past both
+                // capacities there is nothing left to write.
+                if (__all_sync(0xffffffffu, x >= (uint32_t)a.max_pages && q >= (uint32_t)a.max_tokens))
+                    break;
+                const int32_t *from = page_at(i, j);
+                const int32_t page = from ? *from : -1;
+                if (x0 + lane < end && x < (uint32_t)a.max_pages)
+                    a.page_id[x] = page;
+                const int32_t value = page < 0 || page >= INT32_MAX / kPageSize ? -1 : page * kPageSize + (int32_t)(t0 % kPageSize);
+                uint32_t left = __ballot_sync(0xffffffffu, count > 0 && q < (uint32_t)a.max_tokens);
+                while (left) {
+                    const int b0 = __ffs((int)left) - 1;
+                    left &= left - 1;
+                    const int b1 = left ? __ffs((int)left) - 1 : -1;
+                    left &= left - 1;
+                    const int src = lane < 16 ? b0 : b1 < 0 ? b0 : b1;
+                    const uint32_t l = lane & 15;
+                    const uint32_t sq = __shfl_sync(0xffffffffu, q, src) + l;
+                    const uint32_t sn = __shfl_sync(0xffffffffu, count, src);
+                    const int32_t sv = __shfl_sync(0xffffffffu, value, src);
+                    if (l < sn && sq < (uint32_t)a.max_tokens && (lane < 16 || b1 >= 0))
+                        a.slot[sq] = sv < 0 ? -1 : sv + (int32_t)l;
                 }
             }
             at = end;
         }
     }
+    // Past the last token, -1.
+    for (int64_t x = (int64_t)total.toks + (int64_t)cta * kTableThreads + tid; x < a.max_tokens; x += (int64_t)grid * kTableThreads)
+        a.slot[x] = -1;
     // The ends of both offset arrays and the counts, by CTA 0: every CTA has
     // the totals, and the flags of all nodes (scanned, or of the sums).
     if (cta == 0) {
@@ -474,10 +457,11 @@ int deft_page_table(const int32_t *node_len, int32_t num_nodes, const int32_t *p
                 need ? static_cast<uint32_t *>(workspace) : nullptr};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const int blocks = (num_nodes + kBlockNodes - 1) / kBlockNodes;
-    // One CTA for every 1024 outputs, two an SM at most.
+    // One CTA for every 1024 outputs, at most one an SM: each repeats the
+    // scan of its nodes' block.
     const int64_t outputs = (int64_t)max_pages + max_tokens;
     const int64_t want = (outputs + 1023) / 1024;
-    const int grid = (int)(want < 1 ? 1 : want > 2 * num_sms() ? 2 * num_sms() : want);
+    const int grid = (int)(want < 1 ? 1 : want > num_sms() ? num_sms() : want);
     if (blocks > 1) {
         table_sums_kernel<<<blocks, kTableThreads, 0, st>>>(a);
         if (cudaGetLastError() != cudaSuccess)
