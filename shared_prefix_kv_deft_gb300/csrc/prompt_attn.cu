@@ -223,6 +223,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
     const int tile_tok = kPromptRows / G;
 
     // ---------------- set-up ----------------
+    // The launch may start while the stream's earlier kernels end: up to the
+    // grid-dependency wait only the plan is read, which no kernel writes.
+    const int u0 = a.plan.cta_off[blockIdx.x], u1 = a.plan.cta_off[blockIdx.x + 1];
     if (tid == 0) {
         grid_dep_launch();
         for (int i = 0; i < NST; ++i) {
@@ -261,7 +264,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
     const uint32_t tmem = *tmem_slot;
     if (tid == 0 && (base & 1023u) != 0)
         *err = 300;   // the swizzled operands need their atoms aligned
-    const int u0 = a.plan.cta_off[blockIdx.x], u1 = a.plan.cta_off[blockIdx.x + 1];
+    if (warp != 8)
+        grid_dep_wait();
     // A bounded wait of a whole warp; the first one that runs out leaves its
     // code.  A warpgroup may sit out many units (tile B of units that have
     // none): its first wait of a unit goes on for 64 limits, unless another
@@ -296,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                         break;
                     pg -= pages;
                     node = rec.x < 0 ? it.node : rec.x;
-                    rec = a.plan.nodes[node];
+                    rec = __ldg(a.plan.nodes + node);
                     first = a.node_page_off[node];
                 }
             };
@@ -336,11 +340,18 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                 tn = 0;
                 node = it.start_node;
                 pg = it.start_page + (lane & 7);
-                rec = a.plan.nodes[node];
+                rec = __ldg(a.plan.nodes + node);
                 first = a.node_page_off[node];
                 enter();
                 resolve();
             };
+            // The plan's part of the first unit comes into L1 before the wait.
+            if (u0 < u1) {
+                it = load_item(a.plan.items + unit / Hkv);
+                const int2 warm = __ldg(a.plan.nodes + it.start_node);
+                asm volatile("" ::"r"(warm.x));
+            }
+            grid_dep_wait();
             if (u0 < u1)
                 open_unit(u0);
             // A step loads K of the next tile and, beside it, V of the tile
@@ -703,8 +714,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                     // A whole tile in bf16: 64 dims of its rows to shared
                     // memory, and out as one box.  (Written from here, 32
                     // bytes of 32 rows a store, the rows cost the load/store
-                    // unit eight times as much: 275 us for the reasoning
-                    // tree's prefill against XXX.)
+                    // unit eight times as much: the reasoning tree's prefill
+                    // took 276 us instead of 267.)
                     const uint32_t row_s = base + L::out_off + w * kHalf + (uint32_t)r * 128;
 #pragma unroll 1
                     for (int c = 0; c < D / 64; ++c) {
@@ -864,8 +875,7 @@ int launch_dim(const PromptArgs &a, const PromptMaps &maps, int32_t ctas, cudaSt
         if (dev < 64)
             set.fetch_or(1ull << dev, std::memory_order_release);
     }
-    prompt_kernel<D><<<ctas, kThreads, Smem<D>::total, st>>>(a, maps);
-    return (int)cudaGetLastError();
+    return (int)launch_dependent(prompt_kernel<D>, dim3(ctas), dim3(kThreads), Smem<D>::total, st, a, maps);
 }
 
 }  // namespace
