@@ -36,6 +36,9 @@ __global__ void __launch_bounds__(kMergeThreads) prompt_merge_kernel(PromptArgs 
     constexpr int E = D / 32;
     using Vec = typename std::conditional<E == 4, float4, float2>::type;
     grid_dep_launch();
+    // The plan too is read behind the wait: the attention launch lets this
+    // one start before it has waited for the plan's copy itself.
+    grid_dep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int G = a.gqa_group, Hkv = a.num_kv_heads;
     const PromptMerge m = a.plan.merges[blockIdx.x / Hkv];
@@ -44,7 +47,6 @@ __global__ void __launch_bounds__(kMergeThreads) prompt_merge_kernel(PromptArgs 
     if (r >= rows)
         return;
     const size_t first = (size_t)m.part0 + (size_t)h * rows + r, step = (size_t)Hkv * rows;
-    grid_dep_wait();
     float M = -INFINITY;
     for (int j = lane; j < m.pieces; j += 32)
         M = fmaxf(M, a.lse_part[first + j * step]);

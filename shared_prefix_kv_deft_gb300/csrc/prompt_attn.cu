@@ -223,9 +223,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
     const int tile_tok = kPromptRows / G;
 
     // ---------------- set-up ----------------
-    // The launch may start while the stream's earlier kernels end: up to the
-    // grid-dependency wait only the plan is read, which no kernel writes.
-    const int u0 = a.plan.cta_off[blockIdx.x], u1 = a.plan.cta_off[blockIdx.x + 1];
+    // The launch may start while the stream's earlier work ends: nothing in
+    // global memory is read or written before the grid-dependency wait (the
+    // plan's copy may be among that work).
     if (tid == 0) {
         grid_dep_launch();
         for (int i = 0; i < NST; ++i) {
@@ -264,8 +264,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
     const uint32_t tmem = *tmem_slot;
     if (tid == 0 && (base & 1023u) != 0)
         *err = 300;   // the swizzled operands need their atoms aligned
-    if (warp != 8)
-        grid_dep_wait();
+    grid_dep_wait();
+    const int u0 = a.plan.cta_off[blockIdx.x], u1 = a.plan.cta_off[blockIdx.x + 1];
     // A bounded wait of a whole warp; the first one that runs out leaves its
     // code.  A warpgroup may sit out many units (tile B of units that have
     // none): its first wait of a unit goes on for 64 limits, unless another
@@ -345,13 +345,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                 enter();
                 resolve();
             };
-            // The plan's part of the first unit comes into L1 before the wait.
-            if (u0 < u1) {
-                it = load_item(a.plan.items + unit / Hkv);
-                const int2 warm = __ldg(a.plan.nodes + it.start_node);
-                asm volatile("" ::"r"(warm.x));
-            }
-            grid_dep_wait();
             if (u0 < u1)
                 open_unit(u0);
             // A step loads K of the next tile and, beside it, V of the tile

@@ -269,6 +269,26 @@ def test_captured_and_replayed():
     assert torch.equal(bufs.out.cpu(), ref[0]) and torch.equal(bufs.lse.cpu(), ref[1])
 
 
+def test_rebuilt_and_uploaded_before_every_step():
+    """One plan rebuilt for another batch before every step: the step reads
+    the plan its upload has just copied, never the one before (both batches
+    are cut into pieces, so the merge reads it too)."""
+    cases = [Case(**forest([5000, 31, 700], [40, 31, 1]), hkv=2, group=3, d=64, seed=7), Case(**forest([5000], [40]), hkv=2, group=3, d=64, seed=8),
+             Case(**forest([2000] * 30, [9] * 30), hkv=2, group=3, d=64, seed=9)]
+    refs = [c.run() for c in cases]
+    plan = cases[0].plan()
+    outs = []
+    for i in range(60):
+        c = cases[(i * 7 + i // 3) % 3]
+        plan.rebuild(c.parent, c.node_len, c.prompt_node, c.hkv, c.group, prompt_len=c.prompt_len)
+        plan.upload()
+        outs.append((c, deft.deft_prompt_attn(c.qd, c.kp, c.vp, c.npo, c.pid, plan)))
+    torch.cuda.synchronize()
+    for c, (out, lse) in outs:
+        out_ref, lse_ref = refs[cases.index(c)]
+        assert torch.equal(out.cpu(), out_ref) and torch.equal(lse.cpu(), lse_ref)
+
+
 def test_no_rows_and_refusals():
     c = Case(**forest([40], [0]), hkv=1, group=1, d=64)
     out, lse = c.run()
