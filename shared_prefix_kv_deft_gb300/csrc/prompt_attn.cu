@@ -205,6 +205,19 @@ __device__ __forceinline__ int attended(int32_t e, int pos)
     return (e & 32) ? min(cnt, max(0, pos + 1 - (e >> 6) * kPageSize)) : cnt;
 }
 
+// Rows of the query tiles that no box fills (a group that does not divide
+// 128): zeros, so that what lay there cannot ask for rescales.  One warp.
+template <int D>
+__device__ __noinline__ void zero_rows(uint8_t *q, int first)
+{
+    constexpr int kPieces = 2 * (D / 64) * 8;   // of one row: both tiles' halves, 16 bytes each
+    for (int x = threadIdx.x & 31; x < (kPromptRows - first) * kPieces; x += 32) {
+        const int row = first + x / kPieces, rest = x % kPieces;
+        *reinterpret_cast<uint4 *>(q + (rest >> 3) * kHalf + row * 128 + (rest & 7) * 16) = make_uint4(0, 0, 0, 0);
+    }
+    tc::fence_proxy_async();
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const __grid_constant__ PromptMaps maps)
 {
@@ -254,6 +267,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
             tc::prefetch_tmap(&maps.v8);
         }
     }
+    if (warp == 10)
+        zero_rows<D>(smem + L::q_off, tile_tok * G);
     if (warp == 9) {
         tc::tmem_alloc(smem_u32(tmem_slot), kTmemCols);
         tc::tmem_relinquish();
