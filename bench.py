@@ -263,8 +263,10 @@ class ClockSampler:
 # ---------------------------------------------------------------------------
 
 # Sources that decide what the phase-1 kernels read and write: the kernels,
-# their launch shapes and the planner (not the C-ABI glue).
+# their launch shapes and the planner (not the C-ABI glue, nor the prompt
+# path, which the timed steps do not run).
 HOST_GLUE = ("capi.cu", "noalloc.cu")
+PROMPT_PATH = ("kvcache.cu", "prompt.cu", "prompt_attn.cu", "prompt_internal.h", "prompt_plan.cpp")
 
 
 def strip_comments(src: str) -> str:
@@ -297,7 +299,7 @@ def kernel_source_hash():
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "shared_prefix_kv_deft_gb300", "csrc")
     for f in sorted(os.listdir(csrc)):
-        if f.endswith((".cu", ".cuh", ".h", ".cpp")) and f not in HOST_GLUE:
+        if f.endswith((".cu", ".cuh", ".h", ".cpp")) and f not in HOST_GLUE + PROMPT_PATH:
             with open(os.path.join(csrc, f), encoding="utf-8") as fh:
                 h.update(strip_comments(fh.read()).encode())
     return h.hexdigest()[:16]
