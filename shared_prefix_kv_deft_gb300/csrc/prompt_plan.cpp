@@ -25,8 +25,7 @@
 // units instead of 256 moved 75 MB of partials and cost more than it gained
 // (95 us against 55 us).
 #include <algorithm>
-#include <cstring>
-#include <queue>
+#include <vector>
 
 #include "prompt_internal.h"
 
@@ -57,16 +56,37 @@ struct Proto {
 
 int32_t pieces_of(const Proto &p, int32_t cap) { return 1 + (p.tiles() - 1) / cap; }
 
-using Slot = std::pair<double, int32_t>;   // (time a CTA is free, CTA)
-using Heap = std::priority_queue<Slot, std::vector<Slot>, std::greater<Slot>>;
-
-Heap idle_ctas()
-{
-    std::vector<Slot> v;
-    for (int32_t c = 0; c < kPromptCtas; ++c)
-        v.emplace_back(0.0, c);
-    return Heap(std::greater<Slot>(), std::move(v));
-}
+// The CTAs by the time they are free, earliest first (equal times: lowest
+// number): a tree of minima over one key a CTA, its time in 1/4096 tiles
+// above its number, so that giving the first more work is eight minima.
+struct Deal {
+    static constexpr int32_t kLeaves = 256;
+    static_assert(kPromptCtas <= kLeaves, "a CTA's number in eight bits");
+    uint64_t key[2 * kLeaves];
+    uint64_t end = 0;
+    Deal()
+    {
+        for (int32_t c = 0; c < kLeaves; ++c)
+            key[kLeaves + c] = c < kPromptCtas ? (uint64_t)c : UINT64_MAX;
+        for (int32_t i = kLeaves - 1; i > 0; --i)
+            key[i] = std::min(key[2 * i], key[2 * i + 1]);
+    }
+    // The CTA that takes a unit of this cost.
+    int32_t take(uint64_t cost)
+    {
+        const int32_t id = (int32_t)(key[1] & 255);
+        uint64_t x = key[1] + (cost << 8);
+        end = std::max(end, x >> 8);
+        int32_t i = kLeaves + id;
+        key[i] = x;
+        for (; i > 1; i >>= 1) {
+            x = std::min(x, key[i ^ 1]);
+            key[i >> 1] = x;
+        }
+        return id;
+    }
+    static uint64_t units(double tiles) { return (uint64_t)(tiles * 4096.0); }
+};
 
 bool head_major(size_t items, int32_t heads) { return (int64_t)items * heads > kMaxCostOrder; }
 
@@ -84,17 +104,13 @@ double simulate(const std::vector<Proto> &protos, int32_t heads, int32_t group, 
             cost.push_back(kCostUnit + (n > 1 ? kCostPiece : 0.0) + t * p.tile_cost());
     }
     std::sort(cost.begin(), cost.end(), std::greater<double>());
-    Heap heap = idle_ctas();
-    double end = 0;
-    for (const double c : cost)
-        for (int32_t h = 0; h < heads; ++h) {
-            Slot s = heap.top();
-            heap.pop();
-            s.first += c;
-            end = std::max(end, s.first);
-            heap.push(s);
-        }
-    return end + (slots > 0 ? kCostMerge + kCostSlot * slots : 0.0);
+    Deal deal;
+    for (const double c : cost) {
+        const uint64_t x = Deal::units(c);
+        for (int32_t h = 0; h < heads; ++h)
+            deal.take(x);
+    }
+    return (double)deal.end / 4096.0 + (slots > 0 ? kCostMerge + kCostSlot * slots : 0.0);
 }
 
 }  // namespace
@@ -261,25 +277,29 @@ int build_prompt_plan(const int32_t *parent, const int32_t *node_len, int32_t nu
     // The deal.
     const size_t units = cut.size() * num_kv_heads;
     const bool by_head = head_major(cut.size(), num_kv_heads);
-    auto item_of = [&](size_t u) { return by_head ? u % cut.size() : u / num_kv_heads; };
-    auto head_of = [&](size_t u) { return (int32_t)(by_head ? u / cut.size() : u % num_kv_heads); };
-    std::vector<int32_t> owner(units);
+    auto each_unit = [&](auto &&f) {   // in the order of the deal
+        const size_t items = cut.size(), heads = (size_t)num_kv_heads;
+        for (size_t x = 0; x < (by_head ? heads : items); ++x)
+            for (size_t y = 0; y < (by_head ? items : heads); ++y)
+                f(by_head ? y : x, by_head ? x : y);
+    };
+    std::vector<uint8_t> owner(units);
     p->cta_off.assign(kPromptCtas + 1, 0);
-    Heap heap = idle_ctas();
-    for (size_t u = 0; u < units; ++u) {
-        Slot s = heap.top();
-        heap.pop();
-        s.first += cut[item_of(u)].first;
-        owner[u] = s.second;
-        ++p->cta_off[s.second + 1];
-        heap.push(s);
-    }
+    Deal deal;
+    size_t u = 0;
+    each_unit([&](size_t i, size_t) {
+        const int32_t c = deal.take(Deal::units(cut[i].first));
+        owner[u++] = (uint8_t)c;
+        ++p->cta_off[c + 1];
+    });
     for (int32_t c = 0; c < kPromptCtas; ++c)
         p->cta_off[c + 1] += p->cta_off[c];
     std::vector<int32_t> at(p->cta_off.begin(), p->cta_off.end() - 1);
     p->cta_unit.resize(units);
-    for (size_t u = 0; u < units; ++u)
-        p->cta_unit[at[owner[u]]++] = (int32_t)item_of(u) * num_kv_heads + head_of(u);
+    u = 0;
+    each_unit([&](size_t i, size_t h) {
+        p->cta_unit[at[owner[u++]]++] = (int32_t)(i * num_kv_heads + h);
+    });
     p->items.reserve(cut.size());
     for (const auto &c : cut)
         p->items.push_back(c.second);
