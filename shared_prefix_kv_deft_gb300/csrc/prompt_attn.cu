@@ -27,14 +27,42 @@
 // is 0, which must not meet a NaN), K's need not be: their logits are
 // replaced.
 //
-// Bound: at 256 rows a KV tile costs 2 x 2 x 256 x 128 x d flop against 256 x
-// 128 exponentials; the tensor core's time is the longer one.
+// Bound: at 256 rows a KV tile costs 2 x 2 x 256 x 128 x d flop, 2048 clocks
+// of the tensor core at d = 128, against 256 x 128 exponentials (1024 clocks
+// of the special-function units) and, as shared-memory reads (Q and K for S,
+// V for PV) and TMA writes, about 2048 clocks of shared-memory bandwidth.
+// Measured: a tile step of about 2600 clocks, the tensor pipe 70% active; an
+// 8192-token prompt of 32/8 heads, d 128, 332 us (1.65 PFLOP/s), 32768
+// tokens 4.9 ms (1.8 PFLOP/s) until the power cap sets in (5.2-5.4 ms back
+// to back); d 64, where the softmax bounds it, 269 us (1.0 PFLOP/s).  Short
+// prompts pay about 4 us a unit for its end and the next one's start.
 //
-// Roles (12 warps): warps 0-3 and 4-7 softmax and output of tiles A and B (216 registers
-// a thread), warp 8 the TMA producer (a lane a page), warp 9 the MMA issuer;
-// the last warpgroup runs with 72 registers.  Every hand-off is an mbarrier,
-// every wait is bounded; a CTA whose wait runs out fills its rows with NaN,
-// records the code, waits for its copies and MMAs, frees TMEM and returns.
+// What the shape of the code is worth (one change each, same box):
+//   - One elected thread issues all MMAs, for both tiles.  With the warp
+//     voting and re-converging around its waits the 32768-token prompt took
+//     7.9 ms instead of 5.9; with warp-uniform code and an election around
+//     each group 6.6.
+//   - A thread that has committed MMAs gets past its next barrier only when
+//     they have ended.  So a step has one barrier for K and V together, the
+//     stage is freed by the softmax thread that sees the step's last S, and
+//     the issuer commits twice a step: 5.9 -> 5.2 ms.
+//   - The CTA's tiles are one sequence across its units, walked by one copy
+//     of the issuing code, and the units' records are read a unit ahead:
+//     what runs once a unit comes from a cold instruction cache (reasoning
+//     tree's prefill, 22 units a CTA: 389 -> 286 us).
+//   - Slower or equal: P handed over when three quarters of it are written
+//     (5.7 -> 6.1 ms), exponentials begun before the tile's maximum is known
+//     (5.9 ms, registers), an issuer a tile (equal; in turns 5.7 ms), an
+//     output warpgroup of its own (5.2-5.4 ms: 512 threads leave the softmax
+//     192 registers), output held back until the next unit's first P (5.3
+//     ms), three S buffers at d 64 (270 -> 287 us for 8192 tokens).
+//
+// Roles (12 warps): warps 0-3 and 4-7 softmax and output of tiles A and B
+// (216 registers a thread), warp 8 the TMA producer (a lane a page), warp 9
+// the MMA issuer; the last warpgroup runs with 72 registers.  Every hand-off
+// is an mbarrier, every wait is bounded; a CTA whose wait runs out fills its
+// rows with NaN, records the code, waits for its copies and MMAs, frees TMEM
+// and returns.
 #include <atomic>
 
 #include <cuda.h>

@@ -527,6 +527,53 @@ def test_prefill_then_tree_decode(hkv, group, d):
     assert (err <= (2 ** -8 + 2 * tol[rows][..., None]) * mean[rows] + 2 ** -8 * (ref[rows].abs() + 2 ** -8 * mean[rows]) + 2 ** -24).all()
 
 
+def test_pages_behind_four_gigabytes():
+    """A cache of 6.4 GB a pool: pages whose offsets pass 32 bits, in elements
+    and in bytes, written and read."""
+    hkv, d, pages = 8, 128, 200000
+    kp, vp = (torch.empty((pages, hkv, PAGE, d), dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    c = Case(**forest([300, 77], [300, 20]), hkv=hkv, group=1, d=d, seed=31)
+    free = np.concatenate([[0, 70000, 140000], np.arange(pages - 40, pages)]).astype(np.int32)
+    t = deft.deft_page_table(cu([300, 77]), cu(free), max_pages=30, max_tokens=377)
+    assert t.counts.tolist() == [24, 24, 377, 0] and t.slot.max().item() > 3 * 10 ** 6
+    deft.deft_kv_write(*(torch.cat(x).cuda() for x in (c.k, c.v)), t.slot, kp, vp)
+    plan = c.plan()
+    out, lse = deft.deft_prompt_attn(c.qd, kp, vp, t.page_off, t.page_id, plan)
+    c.compare(out.cpu(), lse.cpu())
+
+
+def test_two_layers_share_a_plan_and_a_workspace():
+    """Layer after layer with one plan, one workspace and one set of pages
+    each, as a model runs them on one stream."""
+    cases = [Case(**forest([3000, 40], [70, 40]), hkv=2, group=4, d=128, seed=s, shuffle=False) for s in (1, 2)]
+    plan = cases[0].plan()
+    ws = deft.alloc_buffers(plan, 110, 8, 128)
+    outs = []
+    for c in cases * 3:
+        b = deft.StepBuffers(torch.empty_like(ws.out), torch.empty_like(ws.lse), ws.workspace)
+        outs.append((c, deft.deft_prompt_attn(c.qd, c.kp, c.vp, c.npo, c.pid, plan, b)))
+    torch.cuda.synchronize()
+    for c, (out, lse) in outs:
+        c.compare(out.cpu(), lse.cpu())
+
+
+def test_behind_other_kernels_of_the_stream():
+    """The step behind kernels that make its inputs (it may start while they
+    end): q, the pages and the page table all written right before it."""
+    c = Case(**forest([700, 130], [300, 130]), hkv=2, group=2, d=128, seed=33)
+    plan = c.plan()
+    ref = c.run(plan=plan)
+    q, kp, vp = c.qd.clone(), c.kp.clone(), c.vp.clone()
+    for _ in range(20):
+        c.qd.zero_(), c.kp.zero_(), c.vp.zero_(), c.pid.zero_()
+        big = torch.randn(4096, 4096, device="cuda")
+        big = big @ big      # keeps the device busy while the rest is enqueued
+        c.qd.copy_(q), c.kp.copy_(kp), c.vp.copy_(vp)
+        c.pid.copy_(torch.from_numpy(c.ids))
+        out, lse = deft.deft_prompt_attn(c.qd, c.kp, c.vp, c.npo, c.pid, plan)
+        assert torch.equal(out.cpu(), ref[0]) and torch.equal(lse.cpu(), ref[1])
+
+
 @pytest.mark.parametrize("i", [1, 4])
 def test_workload_prefill(i):
     """Every node of a benchmark tree as a prompt."""
