@@ -34,7 +34,7 @@ namespace {
 
 // Estimated costs in KV tiles of a pair of query tiles (1.33 us each).
 constexpr double kCostSingle = 0.75;  // a KV tile against one query tile
-constexpr double kCostUnit = 3.0;     // a unit's start and end
+constexpr double kCostUnit = 2.0;     // a unit's start and end
 constexpr double kCostPiece = 1.5;    // a piece's fp32 rows (twice a bf16 tile's bytes, row by row)
 constexpr double kCostMerge = 3.0;    // the merge launch
 constexpr double kCostSlot = 1e-4;    // a partial row, written and read once through L2
