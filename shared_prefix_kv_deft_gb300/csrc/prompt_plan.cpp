@@ -214,7 +214,7 @@ int build_prompt_plan(const int32_t *parent, const int32_t *node_len, int32_t nu
         }
         const double even = total * num_kv_heads / kPromptCtas;
         double best = simulate(protos, num_kv_heads, gqa_group, cap);
-        for (const double part : {1.0, 0.6, 0.35, 0.2}) {
+        for (const double part : {1.4, 1.2, 1.0, 0.6}) {
             const int32_t c = std::max(kMinPieceTiles, (int32_t)(even * part + 0.999));
             if (c >= longest)
                 continue;
