@@ -491,7 +491,7 @@ int32_t deft_pages_refcount(const deft_pages_t *pool, int32_t page);
  * read) and prev_page_id [num_prev_ids], for the first num_prev_nodes <=
  * num_nodes nodes (the others are new; num_prev_nodes 0: no earlier table);
  * free_pages [num_free], distinct pages below 2^27 (deft_pages_alloc's).
- * Outputs (device int32), none of which may overlap an input:
+ * Outputs (device int32), none of which may overlap an input or another:
  *   node_page_off [num_nodes + 1], page_id [max_pages]: the page table;
  *   entries of page_id past the last page are left as they were;
  *   tok_off [num_nodes + 1]: where each node's new tokens begin among all
@@ -630,7 +630,8 @@ size_t deft_prompt_workspace_bytes(const deft_prompt_plan_t *plan, int32_t num_q
  *     num_kv_heads and num_q_heads / num_kv_heads the plan's (DEFT_ESTATE)
  *     and head_dim in {64, 128}; out 32-byte aligned (else DEFT_EINVAL).
  *   out: [rows][num_q_heads][head_dim], lse: fp32 [rows][num_q_heads],
- *     natural log; rows past the plan's are left as they were.
+ *     natural log; rows past the plan's are left as they were. out, lse and
+ *     the workspace overlap no input and not one another.
  * Cache slots past a node's last token, and pages past those its length
  * needs, never affect a result, whatever they hold.  The values of tokens in
  * the cache must be finite (a NaN or infinity in V reaches every row of the

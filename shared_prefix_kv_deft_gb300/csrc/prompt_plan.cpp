@@ -176,6 +176,10 @@ int build_prompt_plan(const int32_t *parent, const int32_t *node_len, int32_t nu
         const int32_t m = !prompt_len || prompt_len[i] == -1 ? L : prompt_len[i];
         if (m < 0 || m > L)
             return DEFT_ERANGE;
+        // Refused here, before the records of such a batch are made.
+        const int64_t pairs = ((int64_t)m + 2 * tile_tok - 1) / (2 * tile_tok);
+        if (((int64_t)protos.size() + pairs) * num_kv_heads > INT32_MAX / 8 || rows + m > INT32_MAX)
+            return DEFT_EUNSUPPORTED;
         for (int32_t t = 0; t < m; t += 2 * tile_tok) {
             Proto q{};
             q.it.row0 = (int32_t)(rows + t);
@@ -190,8 +194,6 @@ int build_prompt_plan(const int32_t *parent, const int32_t *node_len, int32_t nu
             protos.push_back(q);
         }
         rows += m;
-        if (rows > INT32_MAX)
-            return DEFT_EUNSUPPORTED;
         // Tokens seen: those above (exactly, not in pages), then 1 .. m of
         // the node's last m and all before them.
         int64_t up = 0;
@@ -199,8 +201,6 @@ int build_prompt_plan(const int32_t *parent, const int32_t *node_len, int32_t nu
             up += node_len[a];
         pair_tokens += (int64_t)m * (up + L - m) + (int64_t)m * (m + 1) / 2;
     }
-    if ((int64_t)protos.size() * num_kv_heads > INT32_MAX / 8)
-        return DEFT_EUNSUPPORTED;
     p->num_rows = (int32_t)rows;
 
     // Where to cut.
