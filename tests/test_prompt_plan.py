@@ -151,7 +151,7 @@ def test_rebuild_equals_a_fresh_plan_and_survives_errors():
     (dict(parent=None, node_len=[5], prompt_node=[0], gqa_group=0), EINVAL),
     (dict(parent=None, node_len=[5], prompt_node=[0], gqa_group=65), EINVAL),
     (dict(parent=None, node_len=[2 ** 31 - 1], prompt_node=[0], prompt_len=[1]), EUNSUPPORTED),
-    (dict(parent=None, node_len=[2 ** 28], prompt_node=[0] * 9, prompt_len=None, gqa_group=64), EUNSUPPORTED),
+    (dict(parent=None, node_len=[2 ** 28], prompt_node=[0], num_kv_heads=8, gqa_group=64), EUNSUPPORTED),
     (dict(parent=None, node_len=[], prompt_node=[]), EINVAL),
 ])
 def test_refusals(kw, status):
