@@ -21,9 +21,11 @@
 // the page ranges of the items are cut into pieces whose partial results a
 // second launch merges by log-sum-exp.  The cut is chosen by simulating the
 // deal for a few piece sizes and taking the shortest, the pieces' fp32 rows
-// and the merge counted: cutting a 4096-token prompt of 16 heads into 640
-// units instead of 256 moved 75 MB of partials and cost more than it gained
-// (95 us against 55 us).
+// and the merge counted.  Equal units that do not divide among the CTAs (the
+// next chunks of requests of a few lengths) are levelled by cutting only the
+// shortest items, a twentieth of the work, finely.  Cutting a 4096-token
+// prompt of 16 heads into 640 units instead of 256 moved 75 MB of partials
+// and cost more than it gained (95 us against 55 us).
 #include <algorithm>
 #include <vector>
 
@@ -54,7 +56,15 @@ struct Proto {
     double tile_cost() const { return it.tok_b > 0 ? 1.0 : kCostSingle; }
 };
 
-int32_t pieces_of(const Proto &p, int32_t cap) { return 1 + (p.tiles() - 1) / cap; }
+// Where ranges are cut: above `cap` tiles, and above `fine` where there are at
+// most `below`.
+struct Cuts {
+    int32_t cap = INT32_MAX, below = 0, fine = INT32_MAX;
+};
+int32_t pieces_of(const Proto &p, const Cuts &c)
+{
+    return 1 + (p.tiles() - 1) / (p.tiles() <= c.below ? std::min(c.cap, c.fine) : c.cap);
+}
 
 // The CTAs by the time they are free, earliest first (equal times: lowest
 // number): a tree of minima over one key a CTA, its time in 1/4096 tiles
@@ -90,14 +100,13 @@ struct Deal {
 
 bool head_major(size_t items, int32_t heads) { return (int64_t)items * heads > kMaxCostOrder; }
 
-// Length of the deal (costliest item first) when ranges are cut into pieces
-// of at most `cap` tiles.
-double simulate(const std::vector<Proto> &protos, int32_t heads, int32_t group, int32_t cap)
+// Length of the deal (costliest item first) when ranges are cut so.
+double simulate(const std::vector<Proto> &protos, int32_t heads, int32_t group, const Cuts &cuts)
 {
     std::vector<double> cost;
     double slots = 0;
     for (const Proto &p : protos) {
-        const int32_t n = pieces_of(p, cap), t = (p.tiles() + n - 1) / n;
+        const int32_t n = pieces_of(p, cuts), t = (p.tiles() + n - 1) / n;
         if (n > 1)
             slots += (double)n * (p.it.tok_a + p.it.tok_b) * group * heads;
         for (int32_t i = 0; i < n; ++i)
@@ -203,9 +212,10 @@ int build_prompt_plan(const int32_t *parent, const int32_t *node_len, int32_t nu
     }
     p->num_rows = (int32_t)rows;
 
-    // Where to cut.
-    int32_t cap = INT32_MAX;
-    if ((int64_t)protos.size() * num_kv_heads <= kMaxSimUnits && !protos.empty()) {
+    // Where to cut, if a cut can gain more than its merge costs.
+    Cuts cuts;
+    const int64_t whole = (int64_t)protos.size() * num_kv_heads;
+    if (whole <= kMaxSimUnits && !protos.empty()) {
         double total = 0;
         int32_t longest = 0;
         for (const Proto &q : protos) {
@@ -213,23 +223,43 @@ int build_prompt_plan(const int32_t *parent, const int32_t *node_len, int32_t nu
             longest = std::max(longest, q.tiles());
         }
         const double even = total * num_kv_heads / kPromptCtas;
-        double best = simulate(protos, num_kv_heads, gqa_group, cap);
-        for (const double part : {1.4, 1.2, 1.0, 0.6}) {
-            const int32_t c = std::max(kMinPieceTiles, (int32_t)(even * part + 0.999));
-            if (c >= longest)
-                continue;
+        double best = simulate(protos, num_kv_heads, gqa_group, cuts);
+        const double least = even + kCostUnit * (double)whole / kPromptCtas + kCostMerge;
+        auto try_cuts = [&](const Cuts &c) {
             const double t = simulate(protos, num_kv_heads, gqa_group, c);
             if (t < best) {
                 best = t;
-                cap = c;
+                cuts = c;
             }
+        };
+        for (const double part : {1.4, 1.2, 1.0, 0.6}) {
+            Cuts c;
+            c.cap = std::max(kMinPieceTiles, (int32_t)(even * part + 0.999));
+            if (best > least && c.cap < longest)
+                try_cuts(c);
+        }
+        if (best > least && cuts.cap == INT32_MAX) {
+            // The shortest items, a twentieth of the work, in small pieces.
+            std::vector<int32_t> tiles;
+            for (const Proto &q : protos)
+                tiles.push_back(q.tiles());
+            std::sort(tiles.begin(), tiles.end());
+            Cuts c;
+            double below = 0;
+            for (size_t i = 0; i < tiles.size() && below < 0.05 * total; ++i) {
+                c.below = tiles[i];
+                below += tiles[i];
+            }
+            c.fine = std::max(kMinPieceTiles, (int32_t)(even * 0.07 + 0.999));
+            if (c.fine < c.below)
+                try_cuts(c);
         }
     }
 
     // The items: pieces of equal length, whole KV tiles.
     std::vector<std::pair<double, PromptItem>> cut;
     for (Proto &q : protos) {
-        const int32_t n = pieces_of(q, cap), t = (q.tiles() + n - 1) / n;
+        const int32_t n = pieces_of(q, cuts), t = (q.tiles() + n - 1) / n;
         const int32_t all = std::max(q.pages_a, q.pages_b);
         const int32_t item_rows = (q.it.tok_a + q.it.tok_b) * gqa_group;
         const int64_t piece_slots = (int64_t)item_rows * num_kv_heads;

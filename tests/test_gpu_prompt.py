@@ -177,6 +177,16 @@ def test_split_ranges(lens, new, hkv, group, d):
 
 
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens,new,hkv,group", [
+    ([2227, 1960, 2297, 2209], [20] * 4, 8, 64), ([2768, 3693, 4128, 3056, 2370], [160] * 5, 4, 8)])
+def test_only_the_shortest_ranges_are_cut(lens, new, hkv, group, d):
+    c = Case(**forest(lens, new), hkv=hkv, group=group, d=d, seed=8)
+    plan = c.plan()
+    assert 0 < plan.stats["num_split_items"] < plan.stats["num_items"] // 3
+    c.check(plan=plan)
+
+
+@pytest.mark.parametrize("d", [64, 128])
 def test_chain_of_one_token_nodes(d):
     n = 40      # every page of the path holds one token
     Case([-1] + list(range(n - 1)), [1] * n, [n - 1, 17, 0], None, hkv=1, group=2, d=d).check()

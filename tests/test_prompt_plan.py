@@ -126,6 +126,20 @@ def test_many_units_are_not_split():
     assert max(load) < 1.1 * (sum(load) / 152)
 
 
+def test_equal_units_are_levelled_by_the_shortest():
+    """160 nearly equal units on 152 CTAs, and 512 units of eight lengths: the
+    shortest ranges alone are cut, into small pieces, and level the CTAs."""
+    plan = check_plan([-1] * 4, [2227, 1960, 2297, 2209], [0, 1, 2, 3], [20] * 4, 8, 64)
+    items = plan.get("items")
+    tiles = items[:, 6:8].max(axis=1)
+    whole, cut = tiles[items[:, 10] < 0], tiles[items[:, 10] >= 0]
+    assert plan.stats["num_split_items"] == 5 and len(whole) == 15 and cut.max() < whole.min()
+    plan = deft.PromptPlan(None, [5120 + 1408 * i for i in range(8)], list(range(8)), 8, 4, prompt_len=[512] * 8)
+    items, off, unit = plan.get("items"), plan.get("cta_off"), plan.get("cta_unit")
+    load = [sum(max(items[u // 8][6], items[u // 8][7]) for u in unit[off[c]:off[c + 1]]) for c in range(152)]
+    assert 0 < plan.stats["num_split_items"] <= 8 and max(load) < 1.05 * (sum(load) / 152)
+
+
 def test_rebuild_equals_a_fresh_plan_and_survives_errors():
     plan = deft.PromptPlan(None, [4000], [0], 4, 2)
     plan.rebuild([-1, 0], [100, 20], [1, 0], 2, 3, prompt_len=[5, -1])
