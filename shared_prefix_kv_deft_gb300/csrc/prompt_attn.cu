@@ -59,10 +59,10 @@
 //
 // Roles (12 warps): warps 0-3 and 4-7 softmax and output of tiles A and B
 // (216 registers a thread), warp 8 the TMA producer (a lane a page), warp 9
-// the MMA issuer; the last warpgroup runs with 72 registers.  Every hand-off
-// is an mbarrier, every wait is bounded; a CTA whose wait runs out fills its
-// rows with NaN, records the code, waits for its copies and MMAs, frees TMEM
-// and returns.
+// the MMA issuer, warp 10 zeroes the empty rows of V; these and warp 11 run
+// with 72 registers.  Every hand-off is an mbarrier, every wait is bounded; a
+// CTA whose wait runs out fills its rows with NaN, records the code, waits
+// for its copies and MMAs, frees TMEM and returns.
 #include <atomic>
 
 #include <cuda.h>
@@ -97,8 +97,10 @@ struct Smem {
     static constexpr uint32_t kv_off = 2 * tile;             // [stages][K, V]: [16 groups of 8 tokens][d half][8 tokens][128 B]
     static constexpr uint32_t out_off = kv_off + stages * 2 * tile;   // [2]: [128 rows][128 B] of output, swizzled
     static constexpr uint32_t meta_off = out_off + 2 * kHalf;
-    static constexpr uint32_t bar_off = meta_off + kMetaSlots * kMetaInts * 4;
-    static constexpr int num_bars = 3 * stages + 11;
+    static constexpr int fixes = stages + 1;                 // requests to zero rows of V
+    static constexpr uint32_t fix_off = meta_off + kMetaSlots * kMetaInts * 4;
+    static constexpr uint32_t bar_off = fix_off + ((fixes * kMetaInts * 4 + 7) & ~7);
+    static constexpr int num_bars = 3 * stages + 11 + fixes;
     static constexpr uint32_t misc_off = bar_off + num_bars * 8;   // TMEM base, error
     static constexpr uint32_t total = misc_off + 16;
     static_assert(total <= 227 * 1024, "shared memory of one CTA");
@@ -258,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
     volatile int *err = reinterpret_cast<volatile int *>(smem + L::misc_off + 4);
     auto bar = [&](int i) { return base + L::bar_off + 8u * (uint32_t)i; };
     constexpr int kFull = 0, kEmpty = NST, kQFull = 2 * NST, kQEmpty = kQFull + 2, kSFull = kQFull + 4,
-                  kPFull = kQFull + 6, kOFull = kQFull + 8, kDrain = kQFull + 10, kVLand = kQFull + 11;
+                  kPFull = kQFull + 6, kOFull = kQFull + 8, kDrain = kQFull + 10, kVLand = kQFull + 11, kFix = kVLand + NST;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int G = a.gqa_group, Hkv = a.num_kv_heads;
     const int tile_tok = kPromptRows / G;
@@ -283,6 +285,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
         tc::mbar_init(bar(kDrain), 1);
         for (int i = 0; i < NST; ++i)
             tc::mbar_init(bar(kVLand + i), 1);
+        for (int i = 0; i < L::fixes; ++i)
+            tc::mbar_init(bar(kFix + i), 1);
         *err = 0;
         tc::fence_mbar_init();
     }
@@ -312,9 +316,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
     // A bounded wait of a whole warp; the first one that runs out leaves its
     // code.  A warpgroup may sit out many units (tile B of units that have
     // none): its first wait of a unit goes on for 64 limits, unless another
-    // role has failed.
-    auto wait = [&](int b, uint32_t parity, int code, bool idle = false) -> bool {
-        for (int i = 0; i < (idle ? 64 : 1); ++i) {
+    // role has failed; the warp that zeroes rows of V may have nothing to do
+    // in the whole launch.
+    auto wait = [&](int b, uint32_t parity, int code, int limits = 1) -> bool {
+        for (int i = 0; i < limits; ++i) {
             if (__all_sync(0xffffffffu, tc::mbar_wait(bar(b), parity)))
                 return true;
             if (__any_sync(0xffffffffu, *err != 0))
@@ -394,7 +399,19 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
             // before: what the MMA issuer needs of one step.
             bool v_run8 = false;
             int v_page = 0, v_cnt = 0, v_h = 0;
-            uint32_t v_fix = 0, step = 0, land = 0;   // land: parity of V's own barriers, by stage
+            uint32_t v_fix = 0, step = 0, fixed = 0;   // fixed: requests to warp 10 so far
+            volatile int32_t *fix = reinterpret_cast<volatile int32_t *>(smem + L::fix_off);
+            auto ask = [&](int32_t what) {
+                const int x = (int)(fixed % L::fixes);
+                if (lane < 8)
+                    fix[x * kMetaInts + lane] = v_cnt;
+                if (lane == 0)
+                    fix[x * kMetaInts + 8] = what;
+                __syncwarp();
+                if (lane == 0)
+                    tc::mbar_arrive(bar(kFix + x));
+                ++fixed;
+            };
             auto copy = [&](uint32_t dst, const CUtensorMap *one, const CUtensorMap *eight, bool whole, int pg0, int head, int b) {
                 if (whole) {
                     if (lane == 0)
@@ -420,8 +437,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                         meta[ms + 8] = flags;
                     __syncwarp();
                 }
-                // V with partial pages lands on a barrier of its own: its
-                // empty rows are zeroed before the step is handed over.
+                // V with partial pages lands on a barrier of its own: warp 10
+                // zeroes its empty rows before the step is handed over, and
+                // the copies of the steps behind go out meanwhile.
                 if (lane == 0) {
                     tc::mbar_arrive_expect_tx(bar(kFull + s), (more ? L::tile : 0) + (step > 0 && !v_fix ? L::tile : 0));
                     if (v_fix)
@@ -434,6 +452,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                     copy(dst, &maps.k1, &maps.k8, run8, page, h, kFull + s);
                 if (step > 0)
                     copy(dst + L::tile, &maps.v1, &maps.v8, v_run8, v_page, v_h, (v_fix ? kVLand : kFull) + s);
+                if (v_fix)
+                    ask((int32_t)v_fix | s << 8);
                 if (more && t == 0) {
                     // The unit's rows, once the unit before has made its last
                     // S from the buffer.
@@ -454,26 +474,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                         ++step;
                         break;
                     }
-                }
-                if (v_fix) {
-                    // V rows past a node's last token: the page holds anything
-                    // there, and their P of 0 must not meet a NaN.
-                    ok = wait(kVLand + s, (land >> s) & 1, 303);
-                    land ^= 1u << s;
-                    for (; v_fix; v_fix &= v_fix - 1) {
-                        const int j = __ffs((int)v_fix) - 1, used = __shfl_sync(0xffffffffu, v_cnt, j);
-                        uint8_t *at = smem + L::kv_off + (uint32_t)s * 2 * L::tile + L::tile + (uint32_t)j * 2 * L::group;
-                        // 16 rows of D / 64 x 128 B, in 16-byte pieces
-                        for (int x = lane; x < (kPageSize - used) * (D / 64) * 8; x += 32) {
-                            const int row = used + x / ((D / 64) * 8), rest = x % ((D / 64) * 8);
-                            *reinterpret_cast<uint4 *>(at + (row >> 3) * L::group + (rest >> 3) * 1024 + (row & 7) * 128 +
-                                                       (rest & 7) * 16) = make_uint4(0, 0, 0, 0);
-                        }
-                    }
-                    tc::fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0)
-                        tc::mbar_arrive(bar(kFull + s));
                 }
                 if (!more) {
                     ++step;
@@ -499,6 +499,41 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                 for (int w = 0; w < 2; ++w)
                     if (nq[w])
                         tc::mbar_wait(bar(kQFull + w), (nq[w] - 1) & 1);
+            }
+            ask(-1);
+        } else if (warp == 10) {
+            // ---------------- empty rows of V ----------------
+            // V rows past a node's last token: the page holds anything there,
+            // and their P of 0 must not meet a NaN.  A request's slot is free
+            // again when its step's stage is, and there is one slot more than
+            // stages for the last request, which ends the loop.
+            volatile int32_t *fix = reinterpret_cast<volatile int32_t *>(smem + L::fix_off);
+            uint32_t land = 0;   // parity of V's own barriers, by stage
+            for (uint32_t i = 0;; ++i) {
+                const int x = (int)(i % L::fixes);
+                if (!wait(kFix + x, (i / L::fixes) & 1, 304, 4096))
+                    break;
+                const int32_t what = fix[x * kMetaInts + 8];
+                if (what < 0)
+                    break;
+                const int s = what >> 8, cnt = fix[x * kMetaInts + (lane & 7)];
+                if (!wait(kVLand + s, (land >> s) & 1, 303))
+                    break;
+                land ^= 1u << s;
+                for (uint32_t pages = (uint32_t)what & 255u; pages; pages &= pages - 1) {
+                    const int j = __ffs((int)pages) - 1, used = __shfl_sync(0xffffffffu, cnt, j);
+                    uint8_t *at = smem + L::kv_off + (uint32_t)s * 2 * L::tile + L::tile + (uint32_t)j * 2 * L::group;
+                    // 16 rows of D / 64 x 128 B, in 16-byte pieces
+                    for (int y = lane; y < (kPageSize - used) * (D / 64) * 8; y += 32) {
+                        const int row = used + y / ((D / 64) * 8), rest = y % ((D / 64) * 8);
+                        *reinterpret_cast<uint4 *>(at + (row >> 3) * L::group + (rest >> 3) * 1024 + (row & 7) * 128 +
+                                                   (rest & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                }
+                tc::fence_proxy_async();
+                __syncwarp();
+                if (lane == 0)
+                    tc::mbar_arrive(bar(kFull + s));
             }
         } else if (warp == 9) {
             // ---------------- MMA issue ----------------
@@ -641,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
             const bool frees = w == (it.tiles_b > 0);
             float m = -INFINITY, l = 0.f;
             for (int t = 0; t < nt; ++t) {
-                if (!wait(kSFull + w, ns & 1, 321 + w, t == 0)) {
+                if (!wait(kSFull + w, ns & 1, 321 + w, t == 0 ? 64 : 1)) {
                     ok = false;
                     break;
                 }
