@@ -20,12 +20,12 @@
 // has one operand type): half a step of 2^-8 on each probability, of the
 // size of the bf16 output's own rounding.
 //
-// Masks.  Only the tiles that hold a partial page, a page past the range or
-// own tokens past a row's position are masked; a tile's description (page
-// counts and positions) travels with its K and V.  V rows of slots past a
-// node's last token are zeroed in shared memory before the product (their P
-// is 0, which must not meet a NaN), K's need not be: their logits are
-// replaced.
+// Masks.  Only the pages that are partial, past the range or hold own tokens
+// past a row's position are masked (at d 64: the tiles that hold such a page);
+// a tile's description (page counts and positions, a bit a page for each
+// tile's mask) travels with its K and V.  V rows of slots past a node's last
+// token are zeroed in shared memory before the product (their P is 0, which
+// must not meet a NaN), K's need not be: their logits are replaced.
 //
 // Bound: at 256 rows a KV tile costs 2 x 2 x 256 x 128 x d flop, 2048 clocks
 // of the tensor core at d = 128, against 256 x 128 exponentials (1024 clocks
@@ -84,9 +84,9 @@ constexpr int kMetaSlots = 8;
 constexpr int kMetaInts = 12;           // 8 pages, flags
 constexpr float kRescale = 8.f;         // base-2 logits a row may exceed its running maximum by
 
-// flags of a tile's description
-constexpr int32_t kMaskA = 1, kMaskB = 2;   // tile A / B needs its mask
-constexpr int kFixShift = 8;                // pages whose V rows past the count are zeroed
+// flags of a tile's description, a bit a page: tile A's mask, tile B's, V rows
+// past the count to be zeroed
+constexpr int kMaskShift = 8, kFixShift = 16;
 
 template <int D>
 struct Smem {
@@ -372,8 +372,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                     mask_a = cnt < kPageSize || (own && last > it.pos0);
                     mask_b = cnt < kPageSize || (own && last > it.pos0 + it.tok_a);
                 }
-                flags = (__any_sync(0xffffffffu, mask_a) ? kMaskA : 0) | (__any_sync(0xffffffffu, mask_b) ? kMaskB : 0) |
-                        (int32_t)((__ballot_sync(0xffffffffu, cnt > 0 && cnt < kPageSize) & 255u) << kFixShift);
+                flags = (int32_t)((__ballot_sync(0xffffffffu, mask_a) & 255u) |
+                                  (__ballot_sync(0xffffffffu, mask_b) & 255u) << kMaskShift |
+                                  (__ballot_sync(0xffffffffu, cnt > 0 && cnt < kPageSize) & 255u) << kFixShift);
                 const int page0 = __shfl_sync(0xffffffffu, page, 0);
                 run8 = __all_sync(0xffffffffu, held && page == page0 + (lane & 7));
                 pg += kPromptTilePages;
@@ -695,9 +696,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                 for (int c = 0; c < 4; ++c)
                     tmem_ld_wait(sr + 32 * c);
                 const int ms = (int)((gt + t) % kMetaSlots) * kMetaInts;
-                if (meta[ms + 8] & (w ? kMaskB : kMaskA)) {
+                const int masked = meta[ms + 8] >> (w * kMaskShift) & 255;
+                if (masked) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
+                        // Two pages without a mask are passed over at d 128
+                        // (reasoning tree 261 -> 254 us); at d 64 the vote
+                        // costs more than it saves (trees 112.5 -> 114.5 us).
+                        if (D == 128 && !__any_sync(0xffffffffu, masked >> (2 * c) & 3))
+                            continue;
                         const uint32_t bits = ((1u << attended(meta[ms + 2 * c], pos)) - 1) |
                                               (((1u << attended(meta[ms + 2 * c + 1], pos)) - 1) << 16);
 #pragma unroll
