@@ -50,12 +50,17 @@
 //     of the issuing code, and the units' records are read a unit ahead:
 //     what runs once a unit comes from a cold instruction cache (reasoning
 //     tree's prefill, 22 units a CTA: 389 -> 286 us).
+//   - V's empty rows are zeroed by a warp of its own: done by the producer,
+//     no copy went out until V had landed (reasoning tree 266 -> 261 us).
 //   - Slower or equal: P handed over when three quarters of it are written
 //     (5.7 -> 6.1 ms), exponentials begun before the tile's maximum is known
 //     (5.9 ms, registers), an issuer a tile (equal; in turns 5.7 ms), an
 //     output warpgroup of its own (5.2-5.4 ms: 512 threads leave the softmax
 //     192 registers), output held back until the next unit's first P (5.3
-//     ms), three S buffers at d 64 (270 -> 287 us for 8192 tokens).
+//     ms), three S buffers at d 64 (270 -> 287 us for 8192 tokens); masks
+//     written into S in TMEM by a short loop, or a branch a page (few-shot
+//     438 -> 472 us, registers), or their bits made while S is on its way
+//     (equal).
 //
 // Roles (12 warps): warps 0-3 and 4-7 softmax and output of tiles A and B
 // (216 registers a thread), warp 8 the TMA producer (a lane a page), warp 9
