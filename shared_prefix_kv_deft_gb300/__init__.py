@@ -9,6 +9,7 @@ fails, an exception is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -489,6 +490,15 @@ class PagePool:
         return int(load().deft_pages_refcount(self.handle, int(page)))
 
 
+def _allocating_for(stream):
+    """Context in which tensors come from the memory of the stream that the
+    call runs on: a tensor of another stream's could still be in use there,
+    and one that the call drops would be handed out again while it runs."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return _torch.cuda.stream(_torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
 def _launch_stream(stream, *tensors) -> int:
     """The raw stream to launch on.  Raises unless every tensor is on the
     current CUDA device (the library launches there)."""
@@ -565,13 +575,15 @@ def deft_page_table(node_len, free_pages, prev=None, table: Optional[PageTable] 
     """deft_page_table: page table and slot map of the nodes' new tokens.
     prev: (prev_len, prev_page_off, prev_page_id) of the earlier table, None:
     every node starts empty.  table: the tensors to write (reused between
-    steps); None: allocated for max_pages and max_tokens."""
+    steps); None: allocated for max_pages and max_tokens, from the memory of
+    the stream the call runs on."""
     _need_torch()
     n, n_free = _index_tensor(node_len, "node_len"), _index_tensor(free_pages, "free_pages")
     if table is None:
         if max_pages is None or max_tokens is None:
             raise ValueError("max_pages and max_tokens are needed to allocate a table")
-        table = alloc_page_table(n, max_pages, max_tokens, node_len.device)
+        with _allocating_for(stream):
+            table = alloc_page_table(n, max_pages, max_tokens, node_len.device)
     off, ids, tok, slot, counts, ws = (table.page_off, table.page_id, table.tok_off, table.slot, table.counts,
                                        table.workspace)
     n_ids, n_slots = _index_tensor(ids, "page_id"), _index_tensor(slot, "slot")
@@ -711,14 +723,16 @@ def deft_prompt_attn(q, k_pages, v_pages, node_page_off, page_id, plan: PromptPl
                      scale: Optional[float] = None, out_dtype: int = DEFT_OUT_BF16, stream=None):
     """Causal attention of the plan's prompts: q [rows, num_q_heads,
     head_dim] bf16 (any token stride), rows packed prompt by prompt; returns
-    (out, lse).  bufs: alloc_buffers(plan, rows, num_q_heads, head_dim)."""
+    (out, lse).  bufs: alloc_buffers(plan, rows, num_q_heads, head_dim); None:
+    allocated from the memory of the stream the call runs on."""
     torch = _need_torch()
     shape, qs = q.shape, q.stride()
     if len(shape) != 3 or q.dtype != torch.bfloat16 or not _heads_packed(shape, qs):
         raise ValueError("q must be bf16 [rows, num_q_heads, head_dim] with the heads of a token contiguous")
     T, Hq, d = shape
     if bufs is None:
-        bufs = alloc_buffers(plan, T, Hq, d, q.device, out_dtype)
+        with _allocating_for(stream):
+            bufs = alloc_buffers(plan, T, Hq, d, q.device, out_dtype)
     out, lse, ws = bufs.out, bufs.lse, bufs.workspace
     pool = _check_pools(k_pages, v_pages, d)
     stats = plan.stats

@@ -552,6 +552,34 @@ def test_pages_behind_four_gigabytes():
     c.compare(out.cpu(), lse.cpu())
 
 
+@pytest.mark.parametrize("raw", [False, True])
+def test_buffers_allocated_by_a_call_on_another_stream(raw):
+    """Outputs and workspace that the call allocates itself belong to its
+    stream: what the current stream allocates and fills right behind the call
+    is other memory, although the call still waits for a busy stream."""
+    c = Case(**forest([3000, 500], [100, 500]), hkv=2, group=4, d=128, seed=41)
+    plan = c.plan()
+    ref = c.run(plan=plan)
+    ws = plan.workspace_bytes(8, 128)
+    lens, free = cu([700, 3]), cu(np.arange(60))
+    table = deft.deft_page_table(lens, free, max_pages=50, max_tokens=800)
+    side = torch.cuda.Stream()
+    big = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(5):
+        with torch.cuda.stream(side):
+            x = big @ big      # the side stream is busy when the call is enqueued
+        s = side.cuda_stream if raw else side
+        out, lse = deft.deft_prompt_attn(c.qd, c.kp, c.vp, c.npo, c.pid, plan, stream=s)
+        t = deft.deft_page_table(lens, free, max_pages=50, max_tokens=800, stream=s)
+        for n in (ws, out.numel() * 2, 4 * lse.numel(), 3200, 200):
+            torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        assert torch.equal(out.cpu(), ref[0]) and torch.equal(lse.cpu(), ref[1])
+        assert torch.equal(t.slot, table.slot) and torch.equal(t.counts, table.counts)
+        del out, lse, t, x
+
+
 def test_two_layers_share_a_plan_and_a_workspace():
     """Layer after layer with one plan, one workspace and one set of pages
     each, as a model runs them on one stream."""
