@@ -13,6 +13,12 @@
 // program order protects both: 2 x 128 columns of S / P and 2 x d of O fill
 // the 512 TMEM columns at d = 128.
 //
+// Warp-collective instructions (.sync.aligned: TMEM loads and stores, the
+// register split, TMEM's release) and named barriers want all 32 lanes at
+// the same instruction.  Whatever only some lanes run before one of them (an
+// arrival, the stores of a partly filled tile) ends in __syncwarp(), so that
+// the lanes' meeting does not hang on where the compiler joins a branch.
+//
 // A softmax thread owns one row: no exchange between threads.  The running
 // maximum is stale: it is raised, and O and the sum rescaled, only when a
 // logit exceeds it by 2^8 (base 2), decided per warp; the sum is fp32 over
@@ -335,6 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
     };
 
     if (warp >= 8) {
+        __syncwarp();
         tc::setmaxnreg_dec<kRegsOther>();
         if (warp == 8) {
             // ---------------- TMA producer ----------------
@@ -654,6 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
             __syncwarp();
         }
     } else {
+        __syncwarp();
         tc::setmaxnreg_inc<kRegsSoftmax>();
         // ---------------- softmax and output: one row a thread ----------------
         const int w = warp >> 2, r = tid & 127;
@@ -690,8 +698,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                 // S of this tile is made, and what came before it: both
                 // operands of the step are free (of its last S, B's if the
                 // unit has a B; a unit's first step is freed by the issuer).
-                if (frees && t > 0 && r == 0)
-                    tc::mbar_arrive(bar(kEmpty + (int)((gt + t) % NST)));
+                if (frees && t > 0 && (warp & 3) == 0) {
+                    if (lane == 0)
+                        tc::mbar_arrive(bar(kEmpty + (int)((gt + t) % NST)));
+                    __syncwarp();
+                }
                 tc::fence_after_sync();
                 uint32_t sr[128];
 #pragma unroll
@@ -785,6 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                 // are free behind this barrier.
                 if (r == 0)
                     bulk_wait_read();
+                __syncwarp();
                 if (tc::named_sync_or(1 + w, 128, !ok)) {
                     ok = false;
                     break;
@@ -810,6 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                         if (c > 0) {
                             if (r == 0)
                                 bulk_wait_read();   // the box before has been read
+                            __syncwarp();
                             tc::named_sync(1 + w, 128);
                         }
 #pragma unroll
@@ -825,35 +838,35 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                         tc::named_sync(1 + w, 128);
                         if (r == 0)
                             tma_store_3d(&maps.out, base + L::out_off + w * kHalf, 64 * c, h * G, it.row0 + before);
+                        __syncwarp();
                     }
                 } else {
-                uint8_t *dst = it.part0 >= 0 ? reinterpret_cast<uint8_t *>(a.o_part + slot * D)
-                                             : static_cast<uint8_t *>(a.out) + orow * D * (f32 ? 4 : 2);
-                // One copy of the code for the parts of a row: it runs once
-                // a unit, from a cold instruction cache.
+                    uint8_t *dst = it.part0 >= 0 ? reinterpret_cast<uint8_t *>(a.o_part + slot * D)
+                                                 : static_cast<uint8_t *>(a.out) + orow * D * (f32 ? 4 : 2);
+                    // One copy of the code for the parts of a row: it runs
+                    // once a unit, from a cold instruction cache.
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t o[32];
-                    tmem_ld32_issue(to + 32 * c, o);
-                    tmem_ld_wait(o);
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32_issue(to + 32 * c, o);
+                        tmem_ld_wait(o);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
-                    if (!held)
-                        continue;
-                    if (f32) {
+                        for (int i = 0; i < 32; ++i)
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+                        if (held && f32) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            store32(dst + 128 * c + 32 * i, o + 8 * i);
-                    } else {
-                        uint32_t x[16];
+                            for (int i = 0; i < 4; ++i)
+                                store32(dst + 128 * c + 32 * i, o + 8 * i);
+                        } else if (held) {
+                            uint32_t x[16];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            x[i] = tc::pack_bf16x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
-                        store32(dst + 64 * c, x);
-                        store32(dst + 64 * c + 32, x + 8);
+                            for (int i = 0; i < 16; ++i)
+                                x[i] = tc::pack_bf16x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+                            store32(dst + 64 * c, x);
+                            store32(dst + 64 * c + 32, x + 8);
+                        }
+                        __syncwarp();
                     }
-                }
                 }
             }
             if (held) {
@@ -867,6 +880,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
     }
     if (tid == 0 || tid == 128)
         bulk_wait_all();
+    __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
     if (*err) {
@@ -894,8 +908,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
             }
         }
     }
-    if (warp == 9)
+    if (warp == 9) {
+        __syncwarp();
         tc::tmem_dealloc(tmem, kTmemCols);
+    }
 }
 
 // ---- host ----

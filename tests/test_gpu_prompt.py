@@ -617,3 +617,18 @@ def test_workload_prefill(i):
     """Every node of a benchmark tree as a prompt."""
     s = W.config(i)
     Case(s.parent.tolist(), s.node_len.tolist(), list(range(s.num_nodes)), None, min(s.num_kv_heads, 2), s.gqa_group, s.head_dim, seed=i).check()
+
+
+@pytest.mark.parametrize("out_dtype", [deft.DEFT_OUT_BF16, deft.DEFT_OUT_F32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("group", [1, 3])
+@pytest.mark.parametrize("cut", [False, True])
+def test_partly_filled_tiles(cut, group, d, out_dtype):
+    """Query tiles whose last warp holds 1 to 31 rows, as tile A and as tile
+    B, of whole and of cut ranges, both output types."""
+    tile = 128 // group
+    m = sorted({1, 2, 10, 11, 21, 31, 33, tile - 1, tile + 1, tile + 11, 2 * tile - 1} - {tile, 2 * tile})
+    c = Case(**forest([3000 + 16 * x for x in m] if cut else m, m), hkv=1, group=group, d=d, seed=51)
+    plan = c.plan()
+    assert (plan.stats["num_split_items"] > 0) == cut
+    c.check(out_dtype=out_dtype, plan=plan)
