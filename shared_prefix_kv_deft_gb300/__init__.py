@@ -496,7 +496,10 @@ def _allocating_for(stream):
     and one that the call drops would be handed out again while it runs."""
     if stream is None:
         return contextlib.nullcontext()
-    return _torch.cuda.stream(_torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+    if isinstance(stream, int):
+        # ExternalStream(0) is a stream of torch's pool, not the default one.
+        stream = _torch.cuda.ExternalStream(stream) if stream else _torch.cuda.default_stream()
+    return _torch.cuda.stream(stream)
 
 
 def _launch_stream(stream, *tensors) -> int:

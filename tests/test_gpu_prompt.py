@@ -632,3 +632,54 @@ def test_partly_filled_tiles(cut, group, d, out_dtype):
     plan = c.plan()
     assert (plan.stats["num_split_items"] > 0) == cut
     c.check(out_dtype=out_dtype, plan=plan)
+
+
+def memory_stream(t):
+    """The stream whose memory tensor t lies in."""
+    return [s["stream"] for s in torch.cuda.memory_snapshot() if s["address"] <= t.data_ptr() < s["address"] + s["total_size"]][0]
+
+
+@pytest.mark.parametrize("default", [True, False])
+def test_memory_of_raw_handles(default):
+    """A raw handle, the default stream's 0 among them: what a call allocates
+    comes from that stream's memory, and goes back to it call after call."""
+    c = Case(**forest([3000, 500], [100, 500]), hkv=2, group=4, d=128, seed=42)
+    plan = c.plan()
+    ref = c.run(plan=plan)
+    lens, free = cu([700, 3]), cu(np.arange(60))
+    side = torch.cuda.Stream()
+    handle = 0 if default else side.cuda_stream
+    torch.cuda.synchronize()
+    held = None
+    for i in range(40):
+        with torch.cuda.stream(side if default else torch.cuda.default_stream()):
+            out, lse = deft.deft_prompt_attn(c.qd, c.kp, c.vp, c.npo, c.pid, plan, stream=handle)
+            t = deft.deft_page_table(lens, free, max_pages=50, max_tokens=800, stream=handle)
+        assert {memory_stream(x) for x in (out, lse, t.page_off, t.page_id, t.tok_off, t.slot, t.counts)} == {handle}
+        torch.cuda.synchronize()
+        assert torch.equal(out.cpu(), ref[0]) and torch.equal(lse.cpu(), ref[1])
+        if i == 2:
+            held = torch.cuda.memory_reserved()
+    assert torch.cuda.memory_reserved() == held
+
+
+def test_buffers_of_the_default_stream_by_its_handle():
+    """As test_buffers_allocated_by_a_call_on_another_stream, the streams
+    exchanged: the default stream is busy and named by its handle, 0, and a
+    side stream is the current one."""
+    c = Case(**forest([3000, 500], [100, 500]), hkv=2, group=4, d=128, seed=43)
+    plan = c.plan()
+    ref = c.run(plan=plan)
+    ws = plan.workspace_bytes(8, 128)
+    side = torch.cuda.Stream()
+    big = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(5):
+        x = big @ big
+        with torch.cuda.stream(side):
+            out, lse = deft.deft_prompt_attn(c.qd, c.kp, c.vp, c.npo, c.pid, plan, stream=0)
+            for n in (ws, out.numel() * 2, 4 * lse.numel()):
+                torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        assert torch.equal(out.cpu(), ref[0]) and torch.equal(lse.cpu(), ref[1])
+        del out, lse, x
