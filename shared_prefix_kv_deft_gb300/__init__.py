@@ -351,12 +351,13 @@ def alloc_buffers(plan: Plan, num_queries: int, num_q_heads: int, head_dim: int,
 def _attn(fn_name: str, q, k_pages, v_pages, node_page_off, page_id, plan: Plan,
           bufs: Optional[StepBuffers] = None, scale: Optional[float] = None,
           out_dtype: int = DEFT_OUT_BF16, stream=None, flags: int = 0):
-    import torch
+    torch = _need_torch()
     lib = load()
     Q, Hq, d = q.shape
     Hkv, P = k_pages.shape[1], k_pages.shape[2]
     if bufs is None:
-        bufs = alloc_buffers(plan, Q, Hq, d, q.device, out_dtype)
+        with _allocating_for(stream):
+            bufs = alloc_buffers(plan, Q, Hq, d, q.device, out_dtype)
     for t in (q, k_pages, v_pages):
         if t.dtype != torch.bfloat16 or not t.is_contiguous() or not t.is_cuda:
             raise ValueError("q, k_pages and v_pages must be contiguous bf16 CUDA tensors")
@@ -379,6 +380,7 @@ def _attn(fn_name: str, q, k_pages, v_pages, node_page_off, page_id, plan: Plan,
 def deft_tree_attn(q, k_pages, v_pages, node_page_off, page_id, plan: Plan, bufs=None,
                    scale=None, out_dtype=DEFT_OUT_BF16, stream=None, flags: int = 0):
     """One DeFT tree-attention step; returns (out, lse) device tensors.
+    bufs None: allocated from the memory of the stream the call runs on.
     flags (STEP_*): deft_tree_attn_ex's options; 0 calls deft_tree_attn."""
     return _attn("deft_tree_attn_ex" if flags else "deft_tree_attn", q, k_pages, v_pages,
                  node_page_off, page_id, plan, bufs, scale, out_dtype, stream, flags)

@@ -46,3 +46,32 @@ def test_current_stream_is_left_alone(monkeypatch):
     with deft._allocating_for(None):
         pass
     assert cuda.entered == []
+
+
+@pytest.mark.parametrize("call", ["deft_tree_attn", "deft_naive_attn", "deft_prompt_attn"])
+def test_steps_allocate_in_the_launch_streams_memory(monkeypatch, call):
+    """Every step that allocates its own buffers does so inside
+    _allocating_for(its stream)."""
+    import torch
+
+    class Allocated(Exception):
+        pass
+
+    inside = []
+
+    @contextlib.contextmanager
+    def allocating_for(stream):
+        inside.append(stream)
+        yield
+        inside.pop()
+
+    def alloc_buffers(*a):
+        raise Allocated(list(inside))
+
+    monkeypatch.setattr(deft, "_allocating_for", allocating_for)
+    monkeypatch.setattr(deft, "alloc_buffers", alloc_buffers)
+    q, pages = torch.zeros((1, 1, 64), dtype=torch.bfloat16), torch.zeros((1, 1, 16, 64), dtype=torch.bfloat16)
+    index = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(Allocated) as e:
+        getattr(deft, call)(q, pages, pages, index, index, None, stream=0x77)
+    assert e.value.args[0] == [0x77]

@@ -683,3 +683,25 @@ def test_buffers_of_the_default_stream_by_its_handle():
         torch.cuda.synchronize()
         assert torch.equal(out.cpu(), ref[0]) and torch.equal(lse.cpu(), ref[1])
         del out, lse, x
+
+
+@pytest.mark.parametrize("default", [True, False])
+@pytest.mark.parametrize("raw", [True, False])
+def test_tree_step_memory(raw, default):
+    """The tree steps' own buffers belong to the stream the step runs on too."""
+    s = W.tiny_tree()
+    layout = W.paged_layout(s)
+    t = W.make_tensors(s, layout, device="cuda:0")
+    plan = deft.Plan(s.parent, s.node_len, s.query_node, 64, s.gqa_group)
+    plan.upload()
+    args = (t.q, t.k_pages, t.v_pages, cu(layout.node_page_off), cu(layout.page_id), plan)
+    ref = deft.deft_tree_attn(*args)
+    side = torch.cuda.Stream()
+    on, current = (torch.cuda.default_stream(), side) if default else (side, torch.cuda.default_stream())
+    torch.cuda.synchronize()
+    for step in (deft.deft_tree_attn, deft.deft_naive_attn):
+        with torch.cuda.stream(current):
+            out, lse = step(*args, stream=on.cuda_stream if raw else on)
+        assert memory_stream(out) == memory_stream(lse) == on.cuda_stream
+        torch.cuda.synchronize()
+        assert (out - ref[0]).abs().max() <= 1e-2 and (lse - ref[1]).abs().max() <= 1e-3
