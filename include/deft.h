@@ -633,9 +633,12 @@ size_t deft_prompt_workspace_bytes(const deft_prompt_plan_t *plan, int32_t num_q
  *     natural log; rows past the plan's are left as they were. out, lse and
  *     the workspace overlap no input and not one another.
  * Cache slots past a node's last token, and pages past those its length
- * needs, never affect a result, whatever they hold.  The values of tokens in
- * the cache must be finite (a NaN or infinity in V reaches every row of the
- * tiles it is read in, attended or not).  page_id and node_page_off are
+ * needs, never affect a result, whatever they hold.  V's values of tokens in
+ * the cache must be finite (a NaN or infinity there reaches every row of the
+ * tiles it is read in, attended or not).  q and K may hold anything: a row
+ * with a logit that is NaN or +infinity is NaN in out and lse, one whose
+ * logits are all -infinity has out NaN and lse -infinity, however its range
+ * is cut, and no other row is affected.  page_id and node_page_off are
  * trusted, as in deft_tree_attn; a page outside [0, num_pages) reads as
  * zeros.  Steps of one plan may run at the same time on several streams,
  * each with its own outputs and workspace.  Never allocates, never

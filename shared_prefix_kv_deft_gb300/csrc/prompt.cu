@@ -8,6 +8,9 @@
 //     out = sum_j 2^((s_j - M) log2 e) v_j / l,  lse = M + ln l.
 // A range-split item's pieces hold (o, base-2 lse) of their own pages; the
 // merge weighs them by 2^(lse - max), as phase2.cu does for tree steps.
+// A NaN or +inf among a row's logits makes l, out and lse NaN, and so does a
+// NaN lse of one piece; logits that are all -inf give out NaN (0 / 0) and
+// lse -inf, whether the range is cut or not.
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -50,10 +53,11 @@ __global__ void __launch_bounds__(kMergeThreads) prompt_merge_kernel(PromptArgs 
     float M = -INFINITY;
     for (int j = lane; j < m.pieces; j += 32)
         M = fmaxf(M, a.lse_part[first + j * step]);
-    M = warp_max(M);
+    M = warp_max(M);   // (passes over NaN: the weights below bring it in)
+    const float base = M == -INFINITY ? 0.f : M;
     float acc[E] = {}, sum = 0.f;
     for (int j0 = 0; j0 < m.pieces; j0 += 32) {
-        const float w = j0 + lane < m.pieces ? exp2f(a.lse_part[first + (j0 + lane) * step] - M) : 0.f;
+        const float w = j0 + lane < m.pieces ? exp2f(a.lse_part[first + (j0 + lane) * step] - base) : 0.f;
         sum += w;
         const int n = min(32, m.pieces - j0);
         for (int j = 0; j < n; j += 4) {

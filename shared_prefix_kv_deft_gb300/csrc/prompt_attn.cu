@@ -803,7 +803,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                 }
                 ++no;
                 tc::fence_after_sync();
-                const float inv = l > 0.f ? __fdividef(1.f, l) : 0.f;
+                // l is 0 only where every logit is -inf, NaN where one is NaN
+                // or +inf: both reach the output (0 x inf, NaN) unguarded.
+                const float inv = __fdividef(1.f, l);
                 const bool f32 = it.part0 >= 0 || a.out_dtype == DEFT_OUT_F32;
                 if (!f32 && toks == tile_tok) {
                     // A whole tile in bf16: 64 dims of its rows to shared
@@ -870,7 +872,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                 }
             }
             if (held) {
-                const float lse2 = l > 0.f ? m + __log2f(l) : -INFINITY;
+                // -inf where nothing was seen (m = -inf, l = 0), NaN with l
+                const float lse2 = m + __log2f(l);
                 if (it.part0 >= 0)
                     a.lse_part[slot] = lse2;
                 else

@@ -705,3 +705,91 @@ def test_tree_step_memory(raw, default):
         assert memory_stream(out) == memory_stream(lse) == on.cuda_stream
         torch.cuda.synchronize()
         assert (out - ref[0]).abs().max() <= 1e-2 and (lse - ref[1]).abs().max() <= 1e-3
+
+
+def check_special(c, plan, out_dtype):
+    """out and lse of a case with non-finite q or K: NaN exactly where the
+    64-bit form is, the other rows within their bounds (of the finite values:
+    a logit of -infinity is exact)."""
+    out, lse = c.run(out_dtype, plan=plan)
+    ref, rlse, mean, _ = c.reference()
+    kept = c.q, c.k
+    c.q, c.k = c.q.nan_to_num(0, 0, 0), [x.nan_to_num(0, 0, 0) for x in c.k]
+    tol = c.reference()[3]
+    c.q, c.k = kept
+    bad = ref.isnan()
+    assert bad.any() and (bad.any(-1) == bad.all(-1)).all()
+    assert torch.equal(out.isnan(), bad)
+    good = ~bad.all(-1)
+    f32 = out.dtype == torch.float32
+    bound = (2 ** -8 + 2 * tol[..., None]) * mean + (0 if f32 else 2 ** -8) * (ref.abs() + 2 ** -8 * mean) + 2 ** -24
+    assert ((out.double() - ref).abs() <= bound)[good].all()
+    assert ((lse.double() - rlse).abs() <= tol)[good].all()
+    return lse, ~good
+
+
+SPECIAL = [([200], None, False), ([300, 40], [70, 40], False), ([4099, 150], [70, 150], True), ([5000], [200], True)]
+
+
+@pytest.mark.parametrize("out_dtype", [deft.DEFT_OUT_BF16, deft.DEFT_OUT_F32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("value", [NAN, math.inf, -math.inf])
+@pytest.mark.parametrize("lens,new,cut", SPECIAL)
+def test_non_finite_queries(lens, new, cut, value, d, out_dtype):
+    """A row whose query holds a NaN or an infinity (logits of both signs) is
+    NaN in out and lse, whole or cut; the rows beside it are not touched."""
+    c = Case(**forest(lens, new), hkv=2, group=3, d=d, seed=61)
+    plan = c.plan()
+    assert (plan.stats["num_split_items"] > 0) == cut
+    for row in (33, 60, 69):
+        c.q[row, 1, 5] = value      # one head of KV head 0
+    # the keys of the first two tokens: logits of both signs for every row
+    c.k[0][0, 0, 5], c.k[0][1, 0, 5] = 1, -1
+    c.kp[int(c.ids[c.off[0]]), 0, 0, 5], c.kp[int(c.ids[c.off[0]]), 0, 1, 5] = 1, -1
+    c.qd = c.q.cuda()
+    lse, bad = check_special(c, plan, out_dtype)
+    assert bad.sum() == 3 and lse[bad].isnan().all()
+
+
+@pytest.mark.parametrize("out_dtype", [deft.DEFT_OUT_BF16, deft.DEFT_OUT_F32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens,new,cut", SPECIAL)
+def test_logits_of_minus_infinity(lens, new, cut, d, out_dtype):
+    """A row whose logits are all -infinity has no softmax: out NaN, lse
+    -infinity, whole or cut."""
+    c = Case(**forest(lens, new), hkv=2, group=3, d=d, seed=62)
+    plan = c.plan()
+    assert (plan.stats["num_split_items"] > 0) == cut
+    c.k[0][:, 0, 5] = -1
+    for j in range(-(-lens[0] // PAGE)):
+        c.kp[int(c.ids[c.off[0] + j]), 0, :min(PAGE, lens[0] - PAGE * j), 5] = -1
+    c.q[33, 1, 5] = math.inf
+    c.q[60, 2, 5] = math.inf
+    c.qd = c.q.cuda()
+    lse, bad = check_special(c, plan, out_dtype)
+    assert bad.sum() == 2 and lse[33, 1] == lse[60, 2] == -math.inf
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("value", [NAN, math.inf])
+@pytest.mark.parametrize("place", [3, -50, -1])
+@pytest.mark.parametrize("lens,new,cut", SPECIAL)
+def test_non_finite_keys(lens, new, cut, place, value, d):
+    """A non-finite key reaches the rows that attend it, in whichever piece it
+    lies, and no other: NaN where its logit is NaN or +infinity."""
+    c = Case(**forest(lens, new), hkv=2, group=3, d=d, seed=63)
+    plan = c.plan()
+    assert (plan.stats["num_split_items"] > 0) == cut
+    at = place % lens[0]
+    c.k[0][at, 1, 7] = value
+    c.kp[int(c.ids[c.off[0] + at // PAGE]), 1, at % PAGE, 7] = value
+    # KV head 1's query heads 3, 4 and 5: logits of +, - and any sign there
+    c.q[:, 3, 7] = 1 + c.q[:, 3, 7].abs()
+    c.q[:, 4, 7] = -1 - c.q[:, 4, 7].abs()
+    c.qd = c.q.cuda()
+    lse, bad = check_special(c, plan, deft.DEFT_OUT_BF16)
+    assert not lse[bad].isfinite().any()
+    seen = torch.arange(sum(c.new)) < c.new[0]
+    seen[:c.new[0]] = torch.arange(lens[0] - c.new[0], lens[0]) >= at
+    assert not bad[~seen].any() and not bad[:, :3].any()
+    assert bad[seen][:, 3].all() and bad[seen][:, 4].all() == math.isnan(value)
