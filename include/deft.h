@@ -503,7 +503,10 @@ int32_t deft_pages_refcount(const deft_pages_t *pool, int32_t page);
  * No pages or tokens are written past max_pages / max_tokens; a page that
  * free_pages or the earlier table does not hold becomes -1, and so do its
  * tokens' slots.  A negative length counts as 0.  A table whose counts[3] is
- * not 0 must not be given to a step.
+ * not 0 must not be given to a step, nor be the next call's earlier table.
+ * The page numbers that free_pages and prev_page_id hold are copied without a
+ * check, which counts[3] does not cover: a number outside 0 .. 2^27 - 1 goes
+ * into page_id as it is, and its tokens' slots become -1.
  * At most 1,048,576 nodes, page_size 16 (DEFT_EUNSUPPORTED).  Above 2048
  * nodes a workspace of deft_page_table_workspace_bytes(num_nodes) bytes,
  * 256-byte aligned (DEFT_EWORKSPACE), whose contents need not be initialised

@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kTableThreads) table_fill_kernel(TableArgs a, 
                 const int32_t page = from ? *from : -1;
                 if (x0 + lane < end && x < (uint32_t)a.max_pages)
                     a.page_id[x] = page;
-                const int32_t value = page < 0 || page >= INT32_MAX / kPageSize ? -1 : page * kPageSize + (int32_t)(t0 % kPageSize);
+                const int32_t value = page < 0 || page > INT32_MAX / kPageSize ? -1 : page * kPageSize + (int32_t)(t0 % kPageSize);
                 uint32_t left = __ballot_sync(0xffffffffu, count > 0 && q < (uint32_t)a.max_tokens);
                 while (left) {
                     const int b0 = __ffs((int)left) - 1;

@@ -793,3 +793,16 @@ def test_non_finite_keys(lens, new, cut, place, value, d):
     seen[:c.new[0]] = torch.arange(lens[0] - c.new[0], lens[0]) >= at
     assert not bad[~seen].any() and not bad[:, :3].any()
     assert bad[seen][:, 3].all() and bad[seen][:, 4].all() == math.isnan(value)
+
+
+@pytest.mark.parametrize("nodes", [3, 3000])
+def test_page_table_highest_page(nodes):
+    """Page numbers up to 2^27 - 1, whose last slot is 2^31 - 1; a listed
+    number outside 0 .. 2^27 - 1 is copied to page_id and its slots are -1."""
+    top = 2 ** 27 - 1
+    lens, prev = [40, 20, 5] + [0] * (nodes - 3), [3, 0, 0]
+    free = [top - 1, top, 7, -4, 2 ** 27]
+    t = deft.deft_page_table(cu(lens), cu(free), prev=(cu(prev), cu([0, 1, 1]), cu([top])), max_pages=6, max_tokens=62)
+    assert t.counts.tolist() == [6, 5, 62, 0] and t.page_id.tolist() == [top] + free
+    base = [16 * top + i for i in range(3, 16)] + [16 * (top - 1) + i for i in range(16)] + [16 * top + i for i in range(8)]
+    assert t.slot.tolist() == base + [7 * 16 + i for i in range(16)] + [-1] * 9
