@@ -137,10 +137,10 @@ int build_prompt_plan(const int32_t *parent, const int32_t *node_len, int32_t nu
         if (parent && (parent[n] < -1 || parent[n] >= num_nodes))
             return DEFT_ERANGE;
     }
-    // Nearest ancestor with tokens and the pages above each node, parents
-    // first; a node met again on the way up belongs to a cycle.
+    // Nearest ancestor with tokens and the pages and tokens above each node,
+    // parents first; a node met again on the way up belongs to a cycle.
     p->nodes.assign(2 * (size_t)num_nodes, -1);
-    std::vector<int64_t> above(num_nodes, -1);
+    std::vector<int64_t> above(num_nodes, -1), tok_above(num_nodes, -1);
     std::vector<int32_t> way;
     std::vector<uint8_t> seen(num_nodes, 0);   // 1: on the way, 2: done
     for (int32_t n = 0; n < num_nodes; ++n) {
@@ -159,6 +159,7 @@ int build_prompt_plan(const int32_t *parent, const int32_t *node_len, int32_t nu
             p->nodes[2 * (size_t)x] = from;
             p->nodes[2 * (size_t)x + 1] = node_len[x];
             above[x] = from < 0 ? 0 : above[from] + pages_of(node_len[from]);
+            tok_above[x] = from < 0 ? 0 : tok_above[from] + node_len[from];
             if (above[x] + pages_of(node_len[x]) > (1 << 25) - 1)
                 return DEFT_EUNSUPPORTED;
             seen[x] = 2;
@@ -205,10 +206,7 @@ int build_prompt_plan(const int32_t *parent, const int32_t *node_len, int32_t nu
         rows += m;
         // Tokens seen: those above (exactly, not in pages), then 1 .. m of
         // the node's last m and all before them.
-        int64_t up = 0;
-        for (int32_t a = p->nodes[2 * (size_t)n]; m > 0 && a >= 0; a = p->nodes[2 * (size_t)a])
-            up += node_len[a];
-        pair_tokens += (int64_t)m * (up + L - m) + (int64_t)m * (m + 1) / 2;
+        pair_tokens += (int64_t)m * (tok_above[n] + L - m) + (int64_t)m * (m + 1) / 2;
     }
     p->num_rows = (int32_t)rows;
 

@@ -5,6 +5,7 @@ from __future__ import annotations
 
 import ctypes
 import random
+import time
 
 import numpy as np
 import pytest
@@ -265,3 +266,19 @@ def write_args(**kw):
 ])
 def test_write_argument_checks(kw, status):
     assert deft.load().deft_kv_write(*write_args(**kw)) == status
+
+
+def test_deep_chain():
+    """A chain of nodes, each a prompt: the tokens above a node are counted
+    once a node, not by a walk to the root for every prompt (60000 nodes took
+    3.8 s), and pair_tokens is their closed form."""
+    n = 60000
+    parent, lens = np.arange(-1, n - 1), np.arange(n) % 3      # empty nodes among them
+    t0 = time.process_time()
+    plan = deft.PromptPlan(parent, lens, np.arange(n), 1, 1)
+    spent = time.process_time() - t0
+    above = np.concatenate([[0], np.cumsum(lens)[:-1]]).astype(np.int64)
+    assert plan.stats["pair_tokens"] == int((lens * above + lens * (lens + 1) // 2).sum())
+    plan = deft.PromptPlan(parent, lens, [n - 1, n // 2, 0], 2, 4, prompt_len=[1, 0, -1])
+    assert plan.stats["pair_tokens"] == int(above[n - 1] + lens[n - 1])
+    assert spent < 1
