@@ -806,3 +806,75 @@ def test_page_table_highest_page(nodes):
     assert t.counts.tolist() == [6, 5, 62, 0] and t.page_id.tolist() == [top] + free
     base = [16 * top + i for i in range(3, 16)] + [16 * (top - 1) + i for i in range(16)] + [16 * top + i for i in range(8)]
     assert t.slot.tolist() == base + [7 * 16 + i for i in range(16)] + [-1] * 9
+
+
+@pytest.mark.parametrize("nodes", [511 * 2048 + 1, 1 << 20])
+def test_page_table_largest(nodes):
+    """The most nodes a call takes, 512 blocks of 2048, and one node in the
+    last block."""
+    rng = np.random.default_rng(nodes)
+    lens = rng.integers(0, 24, nodes)
+    n_prev = nodes - nodes // 3
+    prev = np.maximum(0, lens[:n_prev] + rng.integers(-20, 12, n_prev))
+    pages, prev_pages = -(-lens // PAGE), -(-prev // PAGE)
+    prev_off = np.concatenate([[0], np.cumsum(prev_pages)])
+    pool = rng.permutation(int(prev_off[-1]) + int(pages.sum()) + 5)
+    prev_id, free = pool[:prev_off[-1]], pool[prev_off[-1]:]
+    all_prev = np.concatenate([prev, np.zeros(nodes - n_prev, int)])
+    kept = np.minimum(-(-all_prev // PAGE), pages)
+    fresh = np.maximum(lens - all_prev, 0)
+    off, tok, take = (np.concatenate([[0], np.cumsum(x)]) for x in (pages, fresh, pages - kept))
+    node = np.repeat(np.arange(nodes), pages)
+    j = np.arange(off[-1]) - off[node]
+    old = j < kept[node]
+    ids = np.where(old, prev_id[np.where(old, np.concatenate([prev_off[:-1], np.zeros(nodes - n_prev, int)])[node] + j, 0)],
+                   free[np.where(old, 0, take[node] + j - kept[node])])
+    node = np.repeat(np.arange(nodes), fresh)
+    t = all_prev[node] + np.arange(tok[-1]) - tok[node]
+    slot = ids[off[node] + t // PAGE] * PAGE + t % PAGE
+    got = deft.deft_page_table(cu(lens), cu(free), prev=(cu(prev), cu(prev_off), cu(prev_id)), max_pages=len(ids) + 3, max_tokens=len(slot) + 37)
+    assert got.counts.tolist() == [off[-1], take[-1], tok[-1], 0]
+    assert np.array_equal(got.page_off.cpu().numpy(), off) and np.array_equal(got.tok_off.cpu().numpy(), tok)
+    assert np.array_equal(got.page_id.cpu().numpy()[:len(ids)], ids)
+    assert np.array_equal(got.slot.cpu().numpy(), np.concatenate([slot, np.full(37, -1)]))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_replays_write_everything(d):
+    """A captured step with a cut range: every replay writes out, lse and the
+    partial rows anew, whatever lies there before."""
+    c = Case(**forest([2000, 77], [60, 77]), hkv=2, group=4, d=d, seed=71)
+    plan = c.plan()
+    assert plan.stats["num_split_items"] > 0
+    bufs = deft.alloc_buffers(plan, 137, 8, d)
+    ref = c.run(plan=plan)
+    args = (c.qd, c.kp, c.vp, c.npo, c.pid, plan, bufs)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        deft.deft_prompt_attn(*args)
+    s.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        deft.deft_prompt_attn(*args)
+    for _ in range(3):
+        bufs.out.fill_(7)
+        bufs.lse.fill_(NAN)
+        bufs.workspace.fill_(255)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(bufs.out.cpu(), ref[0]) and torch.equal(bufs.lse.cpu(), ref[1])
+    assert plan.step_status() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_units_and_one_long_range(d):
+    """A decode batch of 160 requests and 8 KV heads with one context far
+    longer than the rest, whether the plan cuts it or not."""
+    Case(**forest([20000] + [300 + i for i in range(159)], [1] * 160), hkv=8, group=1, d=d, seed=72).check()
+
+
+@pytest.mark.parametrize("lens,new,hkv,group", [([2200] * 4, [20] * 4, 8, 64), ([8192] * 8, [512] * 8, 2, 4), ([1000] * 40, [9] * 40, 4, 5)])
+def test_equal_lengths(lens, new, hkv, group):
+    """Batches of one length, whose units do not divide among the CTAs."""
+    c = Case(**forest(lens, new), hkv=hkv, group=group, d=128, seed=73)
+    c.check()
