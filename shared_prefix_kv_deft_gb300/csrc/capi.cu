@@ -92,6 +92,24 @@ int prepare_step(const void *q, const void *k_pages, const void *v_pages, const 
     return DEFT_OK;
 }
 
+namespace {
+__global__ void stream_order_kernel() {}
+}  // namespace
+
+// A step without a phase-1 item (every path empty) is the merge launch alone,
+// which reads its slot lists before its grid-dependency wait because a
+// phase-1 launch has waited for the stream's earlier work ahead of it.  An
+// ordinary launch stands in for it here: as a programmatic dependent of the
+// kernel before, the merge could start while the plan's upload is under way
+// and take slots from the plan before.
+int order_mergeonly_step(const Partition &p, void *stream)
+{
+    if (!p.fma_items.empty() || !p.mma_items.empty())
+        return 0;
+    stream_order_kernel<<<1, 1, 0, reinterpret_cast<cudaStream_t>(stream)>>>();
+    return (int)cudaGetLastError();
+}
+
 }  // namespace deft
 
 namespace {
@@ -226,6 +244,8 @@ int launch_step(const Step &st, void *stream)
     const deft::LaunchTracer trace = [](const deft_trace_record &rec, void *s, const std::function<int()> &launch) {
         return traced(rec, s, launch);
     };
+    if (deft::order_mergeonly_step(*st.hp, stream))
+        return DEFT_ECUDA;
     return deft::dispatch_step(st.a, *st.dp, *st.hp, st.use_mma, st.naive ? 1 : 0, stream, trace) ? DEFT_ECUDA
                                                                                                  : DEFT_OK;
 }

@@ -30,6 +30,10 @@
 
 #include "deft_internal.h"
 
+namespace deft {
+int order_mergeonly_step(const Partition &p, void *stream);   // capi.cu
+}
+
 namespace {
 
 constexpr size_t kNoallocScratchBytes = DEFT_NOALLOC_SCRATCH_BYTES;
@@ -140,5 +144,7 @@ extern "C" int deft_tree_attn_noalloc(const void *q, const void *k_pages, const 
     const deft::LaunchTracer untraced = [](const deft_trace_record &, void *, const std::function<int()> &launch) {
         return launch();
     };
+    if (deft::order_mergeonly_step(p, stream))
+        return DEFT_ECUDA;
     return deft::dispatch_step(a, d, p, use_mma, 0, stream, untraced) ? DEFT_ECUDA : DEFT_OK;
 }

@@ -640,3 +640,36 @@ def test_every_query_attends_each_of_its_tokens_once(deft, cfg):
         bad = np.argwhere(got != want[:, None])
         assert bad.size == 0, f"{name}: query {bad[0][0]} head {bad[0][1]} attends " \
                               f"{got[tuple(bad[0])]} tokens, expected {want[bad[0][0]]}"
+
+
+@pytest.mark.parametrize("naive", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_pruned_to_nothing_behind_an_upload(deft, d, naive):
+    """A tree whose every path is pruned away runs the merge launch alone: it
+    reads the plan its upload has just copied, never the one before, and
+    leaves out = 0, lse = -inf."""
+    spec = W.random_tree(77, max_nodes=12, max_len=200, max_queries=24, q_heads=4, kv_heads=2, head_dim=d, forest=False)
+    layout = W.paged_layout(spec)
+    t = W.make_tensors(spec, layout, device="cuda")
+    npo = torch.from_numpy(layout.node_page_off).cuda()
+    pid = torch.from_numpy(layout.page_id).cuda()
+    plan = deft.Plan(spec.parent, spec.node_len, spec.query_node, 32, spec.gqa_group)
+    plan.upload()
+    step = deft.deft_naive_attn if naive else deft.deft_tree_attn
+    bufs = deft.alloc_buffers(plan, spec.num_queries, 4, d)
+    out, lse = step(t.q, t.k_pages, t.v_pages, npo, pid, plan, bufs)
+    ref = out.clone(), lse.clone()
+    assert torch.isfinite(lse).any()
+    outs = []
+    for i in range(40):
+        plan.update(np.zeros_like(spec.node_len) if i % 2 == 0 else spec.node_len)
+        plan.upload()
+        out, lse = step(t.q, t.k_pages, t.v_pages, npo, pid, plan, bufs)
+        outs.append((out.clone(), lse.clone()))
+    torch.cuda.synchronize()
+    for i, (out, lse) in enumerate(outs):
+        if i % 2 == 0:
+            assert (out == 0).all() and torch.isneginf(lse).all()
+        else:
+            assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
+    assert plan.step_status() == 0
