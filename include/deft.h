@@ -568,6 +568,9 @@ int deft_kv_write(const void *k, const void *v, int32_t in_dtype, int64_t k_stri
  *     node; 0: no rows.  A node may carry several prompts.  num_prompts may
  *     be 0.
  *   - num_kv_heads >= 1 and gqa_group in 1..64 of the layer it will run.
+ *   - Work is dealt to 152 CTAs, one for each SM of a whole GB300, whatever
+ *     the device has: results are the same elsewhere, but with fewer SMs the
+ *     last CTAs start only when others have ended, and more SMs stay idle.
  * DEFT_EINVAL: a null array, a negative length, a bad count; DEFT_ERANGE: a
  * parent, prompt_node or prompt_len out of range; DEFT_ECYCLE;
  * DEFT_EUNSUPPORTED: a path of 2^25 pages or more, or more work than 32-bit

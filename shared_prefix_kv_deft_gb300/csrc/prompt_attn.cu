@@ -15,9 +15,12 @@
 //
 // Warp-collective instructions (.sync.aligned: TMEM loads and stores, the
 // register split, TMEM's release) and named barriers want all 32 lanes at
-// the same instruction.  Whatever only some lanes run before one of them (an
-// arrival, the stores of a partly filled tile) ends in __syncwarp(), so that
-// the lanes' meeting does not hang on where the compiler joins a branch.
+// the same instruction.  What only some lanes do before one of them (an
+// arrival, the stores of a partly filled tile, a box's store) is therefore
+// one predicated instruction, or comes ahead of a vote or a __syncwarp(), so
+// that the lanes' meeting does not hang on where the compiler joins a branch.
+// (__syncwarp() at each of these places: few-shot prefill 452.6 us, 8192
+// tokens 340.9 us; so 449.0 and 339.4 us.)
 //
 // A softmax thread owns one row: no exchange between threads.  The running
 // maximum is stale: it is raised, and O and the sum rescaled, only when a
@@ -38,12 +41,13 @@
 // of the special-function units) and, as shared-memory reads (Q and K for S,
 // V for PV) and TMA writes, about 2048 clocks of shared-memory bandwidth.
 // Measured: a tile step of about 2600 clocks, the tensor pipe 70% active; an
-// 8192-token prompt of 32/8 heads, d 128, 332 us (1.65 PFLOP/s), 32768
-// tokens 4.9 ms (1.8 PFLOP/s) until the power cap sets in (5.2-5.4 ms back
-// to back); d 64, where the softmax bounds it, 269 us (1.0 PFLOP/s).  Short
+// 8192-token prompt of 32/8 heads, d 128, 339 us (1.62 PFLOP/s), 32768
+// tokens 5.0 ms (1.75 PFLOP/s) until the power cap sets in (5.2-5.5 ms back
+// to back); d 64, where the softmax bounds it, 267 us (1.0 PFLOP/s).  Short
 // prompts pay about 4 us a unit for its end and the next one's start.
 //
-// What the shape of the code is worth (one change each, same box):
+// What the shape of the code is worth (one change each, same box, each
+// measured on the kernel of its time):
 //   - One elected thread issues all MMAs, for both tiles.  With the warp
 //     voting and re-converging around its waits the 32768-token prompt took
 //     7.9 ms instead of 5.9; with warp-uniform code and an election around
@@ -186,14 +190,17 @@ __device__ __forceinline__ void st_shared16(uint32_t dst, const uint32_t *r)
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(dst), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
                  : "memory");
 }
-// 3-D box shared -> global of this thread, and the waits for its source to
-// have been read / for everything to be written.
-__device__ __forceinline__ void tma_store_3d(const void *tmap, uint32_t src, int c0, int c1, int c2)
+// 3-D box shared -> global by the thread with `on` (predicated, no branch),
+// and the waits for its source to have been read / for everything to be
+// written.
+__device__ __forceinline__ void tma_store_3d(bool on, const void *tmap, uint32_t src, int c0, int c1, int c2)
 {
     asm volatile(
-        "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];\n"
-        "cp.async.bulk.commit_group;\n" ::"l"(reinterpret_cast<uint64_t>(tmap)),
-        "r"(src), "r"(c0), "r"(c1), "r"(c2)
+        "{\n.reg .pred p;\n"
+        "setp.ne.u32 p, %5, 0;\n"
+        "@p cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];\n"
+        "@p cp.async.bulk.commit_group;\n}\n" ::"l"(reinterpret_cast<uint64_t>(tmap)),
+        "r"(src), "r"(c0), "r"(c1), "r"(c2), "r"((uint32_t)on)
         : "memory");
 }
 __device__ __forceinline__ void bulk_wait_read()
@@ -205,12 +212,16 @@ __device__ __forceinline__ void bulk_wait_all()
     asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
 }
 
-// 32 bytes to global memory, a whole sector a lane.
-__device__ __forceinline__ void store32(void *dst, const uint32_t *r)
+// 32 bytes to global memory, a whole sector a lane, by the lanes with `on`:
+// one predicated instruction, no branch.
+__device__ __forceinline__ void store32(bool on, void *dst, const uint32_t *r)
 {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(dst), "r"(r[0]), "r"(r[1]), "r"(r[2]),
-                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
+    asm volatile(
+        "{\n.reg .pred p;\n"
+        "setp.ne.u32 p, %9, 0;\n"
+        "@p st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n}\n" ::"l"(dst),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"((uint32_t)on)
+        : "memory");
 }
 
 // One lane of a converged warp.
@@ -329,9 +340,16 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
     // none): its first wait of a unit goes on for 64 limits, unless another
     // role has failed; the warp that zeroes rows of V may have nothing to do
     // in the whole launch.
-    auto wait = [&](int b, uint32_t parity, int code, int limits = 1) -> bool {
+    // A lane given a barrier `then` arrives there as soon as its own wait has
+    // ended, ahead of the vote in which the lanes meet again.
+    auto wait = [&](int b, uint32_t parity, int code, int limits = 1, int then = -1) -> bool {
         for (int i = 0; i < limits; ++i) {
-            if (__all_sync(0xffffffffu, tc::mbar_wait(bar(b), parity)))
+            const bool seen = tc::mbar_wait(bar(b), parity);
+            if (seen && then >= 0) {
+                tc::mbar_arrive(bar(then));
+                then = -1;
+            }
+            if (__all_sync(0xffffffffu, seen))
                 return true;
             if (__any_sync(0xffffffffu, *err != 0))
                 return false;
@@ -690,19 +708,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
             const bool frees = w == (it.tiles_b > 0);
             float m = -INFINITY, l = 0.f;
             for (int t = 0; t < nt; ++t) {
-                if (!wait(kSFull + w, ns & 1, 321 + w, t == 0 ? 64 : 1)) {
+                // S of this tile is made, and what came before it: both
+                // operands of the step are free (of its last S, B's if the
+                // unit has a B; a unit's first step is freed by the issuer).
+                const int free_bar = frees && t > 0 && r == 0 ? kEmpty + (int)((gt + t) % NST) : -1;
+                if (!wait(kSFull + w, ns & 1, 321 + w, t == 0 ? 64 : 1, free_bar)) {
                     ok = false;
                     break;
                 }
                 ++ns;
-                // S of this tile is made, and what came before it: both
-                // operands of the step are free (of its last S, B's if the
-                // unit has a B; a unit's first step is freed by the issuer).
-                if (frees && t > 0 && (warp & 3) == 0) {
-                    if (lane == 0)
-                        tc::mbar_arrive(bar(kEmpty + (int)((gt + t) % NST)));
-                    __syncwarp();
-                }
                 tc::fence_after_sync();
                 uint32_t sr[128];
 #pragma unroll
@@ -794,9 +808,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                 ok = ok && wait(kOFull + w, no & 1, 323 + w);
                 // The four warps go on, or end, together; the staging rows
                 // are free behind this barrier.
-                if (r == 0)
+                if ((warp & 3) == 0)
                     bulk_wait_read();
-                __syncwarp();
                 if (tc::named_sync_or(1 + w, 128, !ok)) {
                     ok = false;
                     break;
@@ -822,9 +835,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                         tmem_ld_wait(o);
                         tmem_ld_wait(o + 32);
                         if (c > 0) {
-                            if (r == 0)
+                            if ((warp & 3) == 0)
                                 bulk_wait_read();   // the box before has been read
-                            __syncwarp();
                             tc::named_sync(1 + w, 128);
                         }
 #pragma unroll
@@ -838,9 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                         }
                         tc::fence_proxy_async();
                         tc::named_sync(1 + w, 128);
-                        if (r == 0)
-                            tma_store_3d(&maps.out, base + L::out_off + w * kHalf, 64 * c, h * G, it.row0 + before);
-                        __syncwarp();
+                        tma_store_3d(r == 0, &maps.out, base + L::out_off + w * kHalf, 64 * c, h * G, it.row0 + before);
                     }
                 } else {
                     uint8_t *dst = it.part0 >= 0 ? reinterpret_cast<uint8_t *>(a.o_part + slot * D)
@@ -855,19 +865,18 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
-                        if (held && f32) {
+                        if (f32) {
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                store32(dst + 128 * c + 32 * i, o + 8 * i);
-                        } else if (held) {
+                                store32(held, dst + 128 * c + 32 * i, o + 8 * i);
+                        } else {
                             uint32_t x[16];
 #pragma unroll
                             for (int i = 0; i < 16; ++i)
                                 x[i] = tc::pack_bf16x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
-                            store32(dst + 64 * c, x);
-                            store32(dst + 64 * c + 32, x + 8);
+                            store32(held, dst + 64 * c, x);
+                            store32(held, dst + 64 * c + 32, x + 8);
                         }
-                        __syncwarp();
                     }
                 }
             }

@@ -1,6 +1,6 @@
 // prompt_internal.h -- the prompt plan (deft_prompt_plan_t) and what its
-// kernels read: host planning in prompt_plan.cpp, kernels and entry points
-// in prompt.cu.
+// kernels read: host planning in prompt_plan.cpp, the attention kernel in
+// prompt_attn.cu, entry points and the merge kernel in prompt.cu.
 #pragma once
 
 #include <cstdint>
@@ -12,7 +12,9 @@ namespace deft {
 
 constexpr int kPromptRows = 128;      // rows of a query tile (tokens x GQA group)
 constexpr int kPromptTilePages = 8;   // pages of a KV tile (128 tokens)
-constexpr int kPromptCtas = 152;      // CTAs the plan deals its units to (one per SM of the GB300)
+// CTAs the plan deals its units to, one per SM of a whole GB300 and the same
+// on any device: results do not depend on it, the balance does.
+constexpr int kPromptCtas = 152;
 
 // One work item: up to two neighbouring query tiles (A, then B) of a prompt
 // against a range of the pages of its path.  A unit is an item and a KV

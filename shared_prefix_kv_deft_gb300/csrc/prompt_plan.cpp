@@ -21,9 +21,12 @@
 // the page ranges of the items are cut into pieces whose partial results a
 // second launch merges by log-sum-exp.  The cut is chosen by simulating the
 // deal for a few piece sizes and taking the shortest, the pieces' fp32 rows
-// and the merge counted.  Equal units that do not divide among the CTAs (the
-// next chunks of requests of a few lengths) are levelled by cutting only the
-// shortest items, a twentieth of the work, finely.  Cutting a 4096-token
+// and the merge counted.  Units of a few near lengths that do not divide among
+// the CTAs (the next chunks of several requests) are levelled by cutting only
+// the shortest items, a twentieth of the work, finely.  A length bound picks
+// them, so a batch of one single length is not levelled (eight chunks of 512
+// at 8192 tokens, 32/8 heads: the longest CTA has 1.18 times the mean; 160
+// equal units: 1.9 times).  Cutting a 4096-token
 // prompt of 16 heads into 640 units instead of 256 moved 75 MB of partials
 // and cost more than it gained (95 us against 55 us).
 #include <algorithm>
@@ -41,7 +44,12 @@ constexpr double kCostPiece = 1.5;    // a piece's fp32 rows (twice a bf16 tile'
 constexpr double kCostMerge = 3.0;    // the merge launch
 constexpr double kCostSlot = 1e-4;    // a partial row, written and read once through L2
 constexpr int32_t kMinPieceTiles = 4; // shortest piece
-constexpr int64_t kMaxSimUnits = 8 * kPromptCtas;   // above, no split is looked for: many units balance by themselves
+// Above, no split is looked for: so many units of like length balance by
+// themselves, and each simulation costs host time in their number.  One far
+// longer unit among them is not cut and outlasts the rest (160 single tokens
+// of 8 heads, one at 131072 tokens and the others at 2048: 4.9 times the mean
+// load; a 512-token chunk at 65536 beside 200 such tokens: 1.4 times).
+constexpr int64_t kMaxSimUnits = 8 * kPromptCtas;
 constexpr int64_t kMaxCostOrder = 16 * kPromptCtas; // above, units go head by head (few-shot prefill, 10 units a CTA: 442 us by cost, 449 by head)
 
 int32_t pages_of(int64_t tokens) { return (int32_t)((tokens + kPageSize - 1) / kPageSize); }
