@@ -106,8 +106,10 @@ int order_mergeonly_step(const Partition &p, void *stream)
 {
     if (!p.fma_items.empty() || !p.mma_items.empty())
         return 0;
-    stream_order_kernel<<<1, 1, 0, reinterpret_cast<cudaStream_t>(stream)>>>();
-    return (int)cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = cfg.blockDim = dim3(1);
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    return (int)cudaLaunchKernelEx(&cfg, stream_order_kernel);
 }
 
 }  // namespace deft

@@ -38,6 +38,18 @@
 namespace deft {
 namespace {
 
+// An ordinary launch, with its own status: the thread's last error, which a
+// launch by <<<>>> is asked for, may be that of a call before.
+template <typename Args, typename... More>
+int launch(void (*kernel)(Args, More...), unsigned grid, int threads, cudaStream_t st, const Args &a, More... more)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = st;
+    return cudaLaunchKernelEx(&cfg, kernel, a, more...) == cudaSuccess ? DEFT_OK : DEFT_ECUDA;
+}
+
 constexpr int kTableThreads = 512;
 constexpr int kPerThread = 4;
 constexpr int kBlockNodes = kTableThreads * kPerThread;   // nodes scanned at once
@@ -417,8 +429,7 @@ int launch_write(const WriteArgs &a, cudaStream_t st)
     const int64_t blocks = (pieces + kWriteThreads * U - 1) / (kWriteThreads * U);
     if (blocks > INT32_MAX)
         return DEFT_EUNSUPPORTED;
-    kv_write_kernel<kF32, U><<<(unsigned)blocks, kWriteThreads, 0, st>>>(a, c8, pieces);
-    return cudaGetLastError() == cudaSuccess ? DEFT_OK : DEFT_ECUDA;
+    return launch(kv_write_kernel<kF32, U>, (unsigned)blocks, kWriteThreads, st, a, c8, pieces);
 }
 
 }  // namespace
@@ -466,15 +477,13 @@ int deft_page_table(const int32_t *node_len, int32_t num_nodes, const int32_t *p
     const int64_t want = (outputs + 1023) / 1024;
     const int grid = (int)(want < 1 ? 1 : want > num_sms() ? num_sms() : want);
     if (blocks > 1) {
-        table_sums_kernel<<<blocks, kTableThreads, 0, st>>>(a);
-        if (cudaGetLastError() != cudaSuccess)
+        if (launch(table_sums_kernel, (unsigned)blocks, kTableThreads, st, a) != DEFT_OK)
             return DEFT_ECUDA;
         return launch_dependent(table_fill_kernel, dim3(grid), dim3(kTableThreads), 0, st, a, blocks) == cudaSuccess
                    ? DEFT_OK
                    : DEFT_ECUDA;
     }
-    table_fill_kernel<<<grid, kTableThreads, 0, st>>>(a, 1);
-    return cudaGetLastError() == cudaSuccess ? DEFT_OK : DEFT_ECUDA;
+    return launch(table_fill_kernel, (unsigned)grid, kTableThreads, st, a, (int32_t)1);
 }
 
 int deft_kv_write(const void *k, const void *v, int32_t in_dtype, int64_t k_stride, int64_t v_stride,

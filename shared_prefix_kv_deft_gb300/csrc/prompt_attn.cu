@@ -816,8 +816,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a, const
                 }
                 ++no;
                 tc::fence_after_sync();
-                // l is 0 only where every logit is -inf, NaN where one is NaN
-                // or +inf: both reach the output (0 x inf, NaN) unguarded.
+                // l is NaN where a logit is NaN or +inf, 0 where all are -inf
+                // (or, in a piece, none is seen: the merge passes over such
+                // rows): both reach the output (NaN, 0 x inf) unguarded.
                 const float inv = __fdividef(1.f, l);
                 const bool f32 = it.part0 >= 0 || a.out_dtype == DEFT_OUT_F32;
                 if (!f32 && toks == tile_tok) {

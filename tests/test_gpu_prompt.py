@@ -11,6 +11,7 @@ the sum of n probabilities in fp32 by n 2^-24 of itself, ex2 by 2^-22.
 """
 from __future__ import annotations
 
+import ctypes
 import math
 import random
 
@@ -878,3 +879,34 @@ def test_equal_lengths(lens, new, hkv, group):
     """Batches of one length, whose units do not divide among the CTAs."""
     c = Case(**forest(lens, new), hkv=hkv, group=group, d=128, seed=73)
     c.check()
+
+
+def test_launches_report_their_own_errors():
+    """A call that failed before (a status read of a capturing stream: refused
+    by CUDA on the host, the graph dropped unused) does not show in the calls
+    behind it."""
+    rt = ctypes.CDLL(f"libcudart.so.{torch.version.cuda.split('.')[0]}")
+    plan = deft.PromptPlan(None, [5], [0], 1)
+    plan.upload()
+    side = torch.cuda.Stream()
+    raw, graph = ctypes.c_void_p(side.cuda_stream), ctypes.c_void_p()
+    k = torch.ones((40, 1, 64), dtype=torch.bfloat16, device="cuda")
+    kp, vp = (torch.zeros((3, 1, PAGE, 64), dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    lens = {n: cu([1] * n) for n in (40, 4000)}
+    free = cu(range(4000))
+    torch.cuda.synchronize()
+
+    def fail():
+        assert rt.cudaStreamBeginCapture(raw, 2) == 0      # relaxed
+        with pytest.raises(deft.DeftError):
+            plan.step_status(stream=side)
+        assert rt.cudaStreamEndCapture(raw, ctypes.byref(graph)) != 0
+        rt.cudaGetLastError()
+
+    fail()
+    deft.deft_kv_write(k, k, cu(range(40)), kp, vp)
+    assert (kp.transpose(1, 2).reshape(48, 64)[:40] == 1).all()
+    for n in (40, 4000):
+        fail()
+        t = deft.deft_page_table(lens[n], free, max_pages=n, max_tokens=n)
+        assert t.counts.tolist() == [n, n, n, 0] and t.slot.tolist() == list(range(0, 16 * n, 16))
