@@ -338,12 +338,12 @@ def _plain_rows(s, x, weight):
     x = x.float()
     d = x.shape[-1]
     if weight is not None:
-        # a fixed order of the sum's additions: halves onto one another, so
-        # that a value next to a border of the 4-bit format does not turn on it
-        sq, n = x * x, d
-        while n > 1:
-            n //= 2
-            sq = sq[..., :n] + sq[..., n:2 * n]
+        # a fixed order of the sum's additions, neighbours onto one another,
+        # so that a value next to a border of the 4-bit format does not turn
+        # on it
+        sq = x * x
+        while sq.shape[-1] > 1:
+            sq = sq[..., 0::2] + sq[..., 1::2]
         x = x * (1.0 / torch.sqrt(sq / d + EPS)) * weight.float()
     if s["cos_sin"] is not None:
         half = s["cos_sin"].shape[1] // 2
