@@ -548,6 +548,100 @@ int deft_kv_write(const void *k, const void *v, int32_t in_dtype, int64_t k_stri
                   int32_t num_kv_heads, int32_t head_dim, int32_t page_size, void *stream);
 
 /*
+ * deft_qkv_write -- a layer's new rows from its projection to the cache, in
+ * one launch: the norms and the rotation of the query and key heads, queries
+ * to q_out, keys and values into the pages (deft_kv_write with what comes
+ * before it).  Row t of q ([num_q_heads][head_dim]), k and v
+ * ([num_kv_heads][head_dim]), each contiguous and its own stride (elements)
+ * after the row before, in_dtype as for deft_kv_write (views of a fused
+ * projection's output need no copy).  For every head x of q and k, in fp32:
+ *   norm (q_norm / k_norm not NULL): x_i <- x_i * w_i / sqrt(mean of x^2 +
+ *     eps), w [head_dim] in the inputs' dtype, eps in [0, 1e30];
+ *   rotation (rot_dim > 0): with c, s = row position[t] of cos_sin, fp32
+ *     [num_positions][rot_dim], rot_dim / 2 cosines and then as many sines,
+ *     (a, b) <- (a c_i - b s_i, b c_i + a s_i) for i < rot_dim / 2 and (a, b)
+ *     = (x_i, x_{i + rot_dim / 2}), or (x_2i, x_{2i + 1}) when interleaved is
+ *     1.  Elements from rot_dim on stay.  A position outside [0,
+ *     num_positions) gives NaN in the rotated elements.
+ *   Then one rounding to bf16 (to nearest even).  Every operation before it
+ *   rounds to fp32 by itself, the squares are added neighbours first: the
+ *   result depends on nothing but the row.
+ * turn NULL: neither norm nor rotation.  v is only rounded.  q_out: bf16
+ * [num_tokens][num_q_heads][head_dim]; it may be q itself where q is bf16 and
+ * its stride a row, and overlaps nothing else.  num_q_heads 0: no queries (q
+ * and q_out are not read).  Every token's query is written, whatever its
+ * slot; slots and pages as for deft_kv_write (a slot outside the pool: K and V
+ * are not written; distinct otherwise).
+ * q, k, v, q_out, the pools, cos_sin and the norms' weights 16-byte aligned,
+ * strides multiples of 16 bytes and at least a row (DEFT_EINVAL); head_dim in
+ * {64, 128}, rot_dim a multiple of 16 up to head_dim (DEFT_EINVAL above it),
+ * page_size 16, fewer than 2^27 pages, tokens x (query and KV heads) below
+ * 2^31 (DEFT_EUNSUPPORTED).  Never allocates, never synchronises;
+ * stream-ordered on `stream`; may be captured into a CUDA graph.
+ */
+typedef struct deft_qk_turn {
+    const void *q_norm;        /* [head_dim], or NULL: no norm of q                  */
+    const void *k_norm;
+    float eps;
+    int32_t rot_dim;           /* 0: no rotation                                     */
+    int32_t interleaved;       /* 1: pairs of neighbours, 0: of halves               */
+    int32_t num_positions;
+    const float *cos_sin;      /* [num_positions][rot_dim]                           */
+    const int32_t *position;   /* [num_tokens]                                       */
+} deft_qk_turn;
+int deft_qkv_write(const void *q, const void *k, const void *v, int32_t in_dtype, int64_t q_stride, int64_t k_stride,
+                   int64_t v_stride, const int32_t *slot, int32_t num_tokens, const deft_qk_turn *turn, void *q_out,
+                   void *k_pages, void *v_pages, int32_t num_pages, int32_t num_q_heads, int32_t num_kv_heads,
+                   int32_t head_dim, int32_t page_size, void *stream);
+
+/*
+ * A KV cache in 4 bits.  k4_pages and v4_pages are [num_pages][num_kv_heads]
+ * blocks of deft_kv4_page_bytes(head_dim) = 9 * head_dim bytes: a page's
+ * elements, [16][head_dim / 2] bytes with element 2i in the low half of byte
+ * i and 2i + 1 in the high half, then its scales, [16][head_dim / 16].  16
+ * consecutive elements of a token share a scale s, an 8-bit float (sign, 4
+ * exponent bits, 3 mantissa bits; 0x7f NaN).  An element c is a 4-bit float
+ * (sign, 2 exponent bits, 1 mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6) and
+ * stands for c * s * g, where g is k_scale for K and v_scale for V, one
+ * number for a layer's pool that the caller keeps (1 suits normed keys: s
+ * covers magnitudes from 0.012 to 2688).  4.5 bits an element, 9/32 of bf16.
+ * Page tables and slots are those of the bf16 cache.
+ *
+ * deft_qkv_write4 -- deft_qkv_write into a 4-bit cache.  The bf16 value x
+ * that deft_qkv_write would store is held as follows: s = the 8-bit float
+ * nearest to (largest |x| of the block) / (6 g), at most 448, and c = the
+ * 4-bit float nearest to x / (s g), at most 6 in magnitude (0 where s is 0),
+ * the products and quotients correctly rounded to fp32; halfway cases go to
+ * the even code.  Infinities are held as the largest
+ * magnitude, a block with a NaN gets the scale NaN.  A token's row is written
+ * whole, so rows of one page may come from different calls.  k_scale and
+ * v_scale in [2^-60, 2^60] (DEFT_EINVAL).  Other arguments and errors as
+ * deft_qkv_write.
+ *
+ * deft_kv_unpack4 -- pages of a 4-bit cache as bf16 pages, for the calls that
+ * read those (deft_prompt_attn among them: a chunk of a prompt over cached
+ * context): page page_id[i] of k4_pages / v4_pages becomes page i of k_pages
+ * / v_pages, [num_listed][num_kv_heads][16][head_dim], for i < num_listed;
+ * c * s is exact, its product with g rounds to fp32 and then to bf16 (to
+ * nearest even; exact for g a power of two).  With a step's page_id listed
+ * whole, the bf16 pages' table is node_page_off with page_id[i] = i.  An entry
+ * outside [0, num_pages) leaves its page as it was; an entry may repeat.
+ * All pools 16-byte aligned, the bf16 ones overlapping no input (DEFT_EINVAL
+ * where they start at one); head_dim in {64, 128}, page_size 16
+ * (DEFT_EUNSUPPORTED), at most 2^18 heads.  Never allocates, never
+ * synchronises; stream-ordered on `stream`; may be captured into a CUDA
+ * graph.
+ */
+size_t deft_kv4_page_bytes(int32_t head_dim);   /* 0 for a head_dim that is not supported */
+int deft_qkv_write4(const void *q, const void *k, const void *v, int32_t in_dtype, int64_t q_stride, int64_t k_stride,
+                    int64_t v_stride, const int32_t *slot, int32_t num_tokens, const deft_qk_turn *turn, void *q_out,
+                    void *k4_pages, void *v4_pages, float k_scale, float v_scale, int32_t num_pages,
+                    int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t page_size, void *stream);
+int deft_kv_unpack4(const void *k4_pages, const void *v4_pages, float k_scale, float v_scale, int32_t num_pages,
+                    const int32_t *page_id, int32_t num_listed, void *k_pages, void *v_pages, int32_t num_kv_heads,
+                    int32_t head_dim, int32_t page_size, void *stream);
+
+/*
  * Prompts: causal attention of many tokens of a node at once, over the paged
  * cache (prefill; the DeFT Guide's causal tree mask, "Deep Dive", for whole
  * nodes: deft_plan_at gives single tokens of a node to the tree step, whose

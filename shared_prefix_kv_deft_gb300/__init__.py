@@ -49,7 +49,8 @@ EXPORTS = ["deft_plan", "deft_plan_at", "deft_plan_ex", "deft_plan_rebuild", "de
            "deft_page_table_workspace_bytes", "deft_page_table", "deft_kv_write", "deft_prompt_plan",
            "deft_prompt_plan_rebuild", "deft_prompt_plan_upload", "deft_prompt_plan_stats_get",
            "deft_prompt_plan_get", "deft_prompt_plan_free", "deft_prompt_workspace_bytes",
-           "deft_prompt_attn", "deft_prompt_status"]
+           "deft_prompt_attn", "deft_prompt_status", "deft_qkv_write", "deft_qkv_write4", "deft_kv4_page_bytes",
+           "deft_kv_unpack4"]
 
 KERNEL_NAMES = {0: "phase1_fma", 1: "phase1_mma", 2: "phase2_merge"}
 PLAN_TREE_ONLY = 1   # deft_plan_ex flags
@@ -97,6 +98,12 @@ class PromptStats(ctypes.Structure):
 
     def as_dict(self):
         return {n: getattr(self, n) for n, _ in self._fields_}
+
+
+class QkTurn(ctypes.Structure):
+    _fields_ = [("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("num_positions", ctypes.c_int32),
+                ("cos_sin", ctypes.c_void_p), ("position", ctypes.c_void_p)]
 
 
 _lib = None
@@ -162,6 +169,12 @@ def load(path: str = LIB_PATH):
     lib.deft_prompt_workspace_bytes.restype = sz
     lib.deft_prompt_attn.argtypes = [P, i64, i32, P, P, P, P, i32, i32, i32, i32, i32, f32, P, P, i32, P, P, sz, P]
     lib.deft_prompt_status.argtypes = [P, P, ctypes.POINTER(i32)]
+    qkv = [P, P, P, i32, i64, i64, i64, P, i32, ctypes.POINTER(QkTurn), P, P, P]
+    lib.deft_qkv_write.argtypes = qkv + [i32, i32, i32, i32, i32, P]
+    lib.deft_qkv_write4.argtypes = qkv + [f32, f32, i32, i32, i32, i32, i32, P]
+    lib.deft_kv4_page_bytes.argtypes = [i32]
+    lib.deft_kv4_page_bytes.restype = sz
+    lib.deft_kv_unpack4.argtypes = [P, P, f32, f32, i32, P, i32, P, P, i32, i32, i32, P]
     for fn in ("deft_plan", "deft_plan_at", "deft_plan_ex", "deft_plan_rebuild", "deft_plan_stats_get",
                "deft_plan_get", "deft_plan_upload", "deft_tree_attn", "deft_naive_attn", "deft_version",
                "deft_trace_enable", "deft_trace_read", "deft_tree_attn_noalloc", "deft_tree_attn_ex",
@@ -169,7 +182,8 @@ def load(path: str = LIB_PATH):
                "deft_pages_alloc", "deft_pages_retain", "deft_pages_release", "deft_pages_free_count",
                "deft_pages_refcount", "deft_page_table", "deft_kv_write", "deft_prompt_plan",
                "deft_prompt_plan_rebuild", "deft_prompt_plan_upload", "deft_prompt_plan_stats_get",
-               "deft_prompt_plan_get", "deft_prompt_attn", "deft_prompt_status"):
+               "deft_prompt_plan_get", "deft_prompt_attn", "deft_prompt_status", "deft_qkv_write", "deft_qkv_write4",
+               "deft_kv_unpack4"):
         getattr(lib, fn).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -649,6 +663,143 @@ def _check_pools(k_pages, v_pages, head_dim):
             v_pages.dtype != bf16 or not k_pages.is_contiguous() or not v_pages.is_contiguous():
         raise ValueError("k_pages and v_pages must be contiguous bf16 [pages, heads, page_size, head_dim], alike")
     return shape
+
+
+def kv4_page_bytes(head_dim: int) -> int:
+    """Bytes of one head's page of a 4-bit cache (0: not a head_dim it has)."""
+    return int(load().deft_kv4_page_bytes(int(head_dim)))
+
+
+def alloc_kv4_pages(num_pages: int, num_kv_heads: int, head_dim: int, device="cuda"):
+    """(k4_pages, v4_pages) of a 4-bit cache, uint8 [pages, heads, kv4_page_bytes(head_dim)]."""
+    import torch
+    shape = (int(num_pages), int(num_kv_heads), kv4_page_bytes(head_dim))
+    return tuple(torch.empty(shape, dtype=torch.uint8, device=device) for _ in "kv")
+
+
+def _check_pools4(k4_pages, v4_pages, head_dim):
+    """(pages, heads) of the 4-bit pools, after their checks."""
+    shape = k4_pages.shape
+    if len(shape) != 3 or v4_pages.shape != shape or shape[2] != 9 * head_dim or k4_pages.dtype != _torch.uint8 or \
+            v4_pages.dtype != _torch.uint8 or not k4_pages.is_contiguous() or not v4_pages.is_contiguous():
+        raise ValueError("k4_pages and v4_pages must be contiguous uint8 [pages, heads, 9 * head_dim], alike")
+    return shape
+
+
+def _qkv_args(q, k, v, slot, position, cos_sin, interleaved, q_norm, k_norm, eps, q_out, stream):
+    """The checked arguments of the append calls up to q_out, the tensors they
+    name, the heads and q_out itself."""
+    shape, dt = k.shape, k.dtype
+    if len(shape) != 3 or v.shape != shape or v.dtype != dt or dt not in (_torch.bfloat16, _torch.float32):
+        raise ValueError("k and v must be alike: [tokens, heads, head_dim], bf16 or fp32")
+    T, Hkv, d = shape
+    ks, vs = k.stride(), v.stride()
+    if not _heads_packed(shape, ks) or not _heads_packed(shape, vs):
+        raise ValueError("the heads of a token must be contiguous")
+    if _index_tensor(slot, "slot") != T:
+        raise ValueError("slot must have one entry per token")
+    used = [k, v, slot]
+    Hq, qs, q_ptr, out_ptr = 0, 0, None, None
+    if q is not None:
+        q_shape, q_st = q.shape, q.stride()
+        if len(q_shape) != 3 or q_shape[0] != T or q_shape[2] != d or q.dtype != dt or not _heads_packed(q_shape, q_st):
+            raise ValueError("q must be [tokens, heads, head_dim] of k's dtype with the heads of a token contiguous")
+        Hq, qs = q_shape[1], q_st[0]
+        if q_out is None:
+            with _allocating_for(stream):
+                q_out = _torch.empty((T, Hq, d), dtype=_torch.bfloat16, device=q.device)
+        elif q_out.shape != q_shape or q_out.dtype != _torch.bfloat16 or not q_out.is_contiguous():
+            raise ValueError("q_out must be contiguous bf16, shaped like q")
+        used += [q, q_out]
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None or q_norm is not None:
+        raise ValueError("q_out and q_norm go with q")
+    turn = None
+    if cos_sin is not None or q_norm is not None or k_norm is not None:
+        turn = QkTurn(eps=eps)
+        for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+            if w is not None:
+                if w.shape != (d,) or w.dtype != dt or not w.is_contiguous():
+                    raise ValueError(f"{name} must be a contiguous [head_dim] tensor of k's dtype")
+                setattr(turn, name, w.data_ptr())
+                used.append(w)
+        if cos_sin is not None:
+            if cos_sin.dim() != 2 or cos_sin.dtype != _torch.float32 or not cos_sin.is_contiguous():
+                raise ValueError("cos_sin must be contiguous fp32 [positions, rot_dim]")
+            if position is None or _index_tensor(position, "position") != T:
+                raise ValueError("position must have one entry per token")
+            turn.num_positions, turn.rot_dim = cos_sin.shape
+            turn.cos_sin, turn.position, turn.interleaved = cos_sin.data_ptr(), position.data_ptr(), bool(interleaved)
+            used += [cos_sin, position]
+    args = (q_ptr, k.data_ptr(), v.data_ptr(), DEFT_OUT_BF16 if dt == _torch.bfloat16 else DEFT_OUT_F32, qs, ks[0], vs[0],
+            slot.data_ptr(), T, None if turn is None else ctypes.byref(turn), out_ptr)
+    return args, used, (Hq, Hkv, d), q_out
+
+
+def deft_qkv_write(q, k, v, slot, k_pages, v_pages, position=None, cos_sin=None, interleaved: bool = False, q_norm=None,
+                   k_norm=None, eps: float = 1e-6, q_out=None, stream=None):
+    """deft_qkv_write: rows of a projection ([tokens, heads, head_dim], bf16 or
+    fp32, views with any token stride) to the cache: q and k normed for each
+    head (q_norm, k_norm: weights, None: no norm) and rotated (cos_sin
+    [positions, rot_dim]: cosines, then sines; None: no rotation) by position,
+    k and v into the pages at their slots; returns q_out, bf16 (allocated from
+    the memory of the stream the call runs on when None).  q None: k and v
+    alone."""
+    _need_torch()
+    args, used, (Hq, Hkv, d), q_out = _qkv_args(q, k, v, slot, position, cos_sin, interleaved, q_norm, k_norm, eps, q_out, stream)
+    pool = _check_pools(k_pages, v_pages, d)
+    if pool[1] != Hkv:
+        raise ValueError("k_pages and v_pages have another number of heads")
+    st = _launch_stream(stream, k_pages, v_pages, *used)
+    rc = load().deft_qkv_write(*args, k_pages.data_ptr(), v_pages.data_ptr(), pool[0], Hq, Hkv, d, pool[2], st)
+    if rc:
+        _check("deft_qkv_write", rc)
+    return q_out
+
+
+def deft_qkv_write4(q, k, v, slot, k4_pages, v4_pages, position=None, cos_sin=None, interleaved: bool = False,
+                    q_norm=None, k_norm=None, eps: float = 1e-6, q_out=None, k_scale: float = 1.0, v_scale: float = 1.0,
+                    stream=None):
+    """deft_qkv_write4: deft_qkv_write into the 4-bit pools of
+    alloc_kv4_pages, quantised with k_scale and v_scale."""
+    _need_torch()
+    args, used, (Hq, Hkv, d), q_out = _qkv_args(q, k, v, slot, position, cos_sin, interleaved, q_norm, k_norm, eps, q_out, stream)
+    pool = _check_pools4(k4_pages, v4_pages, d)
+    if pool[1] != Hkv:
+        raise ValueError("k4_pages and v4_pages have another number of heads")
+    st = _launch_stream(stream, k4_pages, v4_pages, *used)
+    rc = load().deft_qkv_write4(*args, k4_pages.data_ptr(), v4_pages.data_ptr(), k_scale, v_scale, pool[0], Hq, Hkv, d, 16, st)
+    if rc:
+        _check("deft_qkv_write4", rc)
+    return q_out
+
+
+def deft_kv_unpack4(k4_pages, v4_pages, page_id, k_pages=None, v_pages=None, k_scale: float = 1.0, v_scale: float = 1.0,
+                    stream=None):
+    """deft_kv_unpack4: the listed pages of a 4-bit cache as bf16 pages
+    [listed, heads, 16, head_dim], in the list's order; returns (k_pages,
+    v_pages), allocated from the memory of the stream the call runs on when
+    None."""
+    torch = _need_torch()
+    if k4_pages.dim() != 3 or k4_pages.shape[2] % 9:
+        raise ValueError("k4_pages must be [pages, heads, 9 * head_dim]")
+    pages, Hkv, d = k4_pages.shape[0], k4_pages.shape[1], k4_pages.shape[2] // 9
+    _check_pools4(k4_pages, v4_pages, d)
+    n = _index_tensor(page_id, "page_id")
+    if (k_pages is None) != (v_pages is None):
+        raise ValueError("k_pages and v_pages go together")
+    if k_pages is None:
+        with _allocating_for(stream):
+            k_pages, v_pages = (torch.empty((n, Hkv, 16, d), dtype=torch.bfloat16, device=k4_pages.device) for _ in "kv")
+    shape = _check_pools(k_pages, v_pages, d)
+    if shape[0] < n or shape[1] != Hkv or shape[2] != 16:
+        raise ValueError("k_pages and v_pages must hold the listed pages, [listed, heads, 16, head_dim]")
+    st = _launch_stream(stream, k4_pages, v4_pages, page_id, k_pages, v_pages)
+    rc = load().deft_kv_unpack4(k4_pages.data_ptr(), v4_pages.data_ptr(), k_scale, v_scale, pages, page_id.data_ptr(), n,
+                                k_pages.data_ptr(), v_pages.data_ptr(), Hkv, d, 16, st)
+    if rc:
+        _check("deft_kv_unpack4", rc)
+    return k_pages, v_pages
 
 
 PROMPT_ARRAYS = {"nodes": (0, 2), "items": (1, 12), "cta_off": (2, 1), "cta_unit": (3, 1), "merges": (4, 4)}
