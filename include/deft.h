@@ -424,8 +424,8 @@ int deft_tree_attn_noalloc(const void *q, const void *k_pages, const void *v_pag
 
 /*
  * Per-launch kernel timing, for measurement tools (no counterpart on the
- * pages).  While enabled, every kernel launch made by deft_tree_attn and
- * deft_naive_attn is bracketed by two CUDA events recorded on the launch
+ * pages).  While enabled, every kernel launch made by deft_tree_attn,
+ * deft_naive_attn and deft_tree_attn4 is bracketed by two CUDA events recorded on the launch
  * stream.  deft_trace_read waits for those events, writes up to `cap`
  * records (in launch order) to `out`, sets *count to the number written and
  * forgets all pending records.  Events are created on first use and reused;
@@ -440,7 +440,7 @@ typedef struct deft_trace_record {
     float ms;         /* event-measured duration                              */
 } deft_trace_record;
 
-enum { DEFT_K_PHASE1_FMA = 0, DEFT_K_PHASE1_MMA = 1, DEFT_K_PHASE2 = 2 };
+enum { DEFT_K_PHASE1_FMA = 0, DEFT_K_PHASE1_MMA = 1, DEFT_K_PHASE2 = 2, DEFT_K_PHASE1_KV4 = 3 };
 
 int deft_trace_enable(int32_t on);
 int deft_trace_read(deft_trace_record *out, int32_t cap, int32_t *count);
@@ -640,6 +640,38 @@ int deft_qkv_write4(const void *q, const void *k, const void *v, int32_t in_dtyp
 int deft_kv_unpack4(const void *k4_pages, const void *v4_pages, float k_scale, float v_scale, int32_t num_pages,
                     const int32_t *page_id, int32_t num_listed, void *k_pages, void *v_pages, int32_t num_kv_heads,
                     int32_t head_dim, int32_t page_size, void *stream);
+
+/*
+ * deft_tree_attn4 -- deft_tree_attn over a 4-bit cache: the same plans
+ * (deft_plan_at's positions and deft_plan_ex's flags included), page tables,
+ * q, out, lse, workspace and rules, with k4_pages and v4_pages as above and
+ * the k_scale and v_scale they were written with.
+ *   - Every product and sum is taken from the cache's exact values: fp16
+ *     products of q and c * s (both exact) summed in fp32, weights rounded
+ *     to fp16 (2^-11), the sums and lse in fp32.
+ *   - Any gqa_group a plan takes (1..64), head_dim in {64, 128}; one launch
+ *     for all row counts, then the merge of the queries that need it.  A
+ *     chunk of 256 tokens is 36 KB a head here: a larger chunk_target (512,
+ *     1024) leaves fewer partials to merge where there are requests or
+ *     branches enough to fill the device.
+ *   - Cache slots past a node's last token never affect a result, whatever
+ *     they hold.  A block whose scale is NaN (written from a NaN) counts as
+ *     NaN: in K for the rows that attend its token, in V for every row of the
+ *     work item that reads its page.  q may hold anything: a row with a logit
+ *     that is NaN or +infinity has NaN in out, and lse NaN or -infinity; no
+ *     other row is affected.  page_id and node_page_off are trusted, as in
+ *     deft_tree_attn (page_id may be NULL where no path has a token).
+ * Several steps of one plan may run at the same time, each with its own
+ * outputs and workspace (this call does not use the plan's work queues).  A
+ * kernel wait that runs out is reported by deft_step_status.  k_scale and
+ * v_scale in [2^-60, 2^60] (DEFT_EINVAL).  Never allocates, never
+ * synchronises; stream-ordered on `stream`; may be captured into a CUDA
+ * graph.
+ */
+int deft_tree_attn4(const void *q, const void *k4_pages, const void *v4_pages, float k_scale, float v_scale,
+                    const int32_t *node_page_off, const int32_t *page_id, int32_t num_pages, int32_t num_q_heads,
+                    int32_t num_kv_heads, int32_t head_dim, int32_t page_size, float scale, const deft_plan_t *plan,
+                    void *out, int32_t out_dtype, float *lse, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * Prompts: causal attention of many tokens of a node at once, over the paged

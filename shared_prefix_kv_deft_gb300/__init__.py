@@ -50,9 +50,9 @@ EXPORTS = ["deft_plan", "deft_plan_at", "deft_plan_ex", "deft_plan_rebuild", "de
            "deft_prompt_plan_rebuild", "deft_prompt_plan_upload", "deft_prompt_plan_stats_get",
            "deft_prompt_plan_get", "deft_prompt_plan_free", "deft_prompt_workspace_bytes",
            "deft_prompt_attn", "deft_prompt_status", "deft_qkv_write", "deft_qkv_write4", "deft_kv4_page_bytes",
-           "deft_kv_unpack4"]
+           "deft_kv_unpack4", "deft_tree_attn4"]
 
-KERNEL_NAMES = {0: "phase1_fma", 1: "phase1_mma", 2: "phase2_merge"}
+KERNEL_NAMES = {0: "phase1_fma", 1: "phase1_mma", 2: "phase2_merge", 3: "phase1_kv4"}
 PLAN_TREE_ONLY = 1   # deft_plan_ex flags
 PLAN_TENSOR_PACK = 2
 # deft_page_table's counts[3]
@@ -172,6 +172,7 @@ def load(path: str = LIB_PATH):
     qkv = [P, P, P, i32, i64, i64, i64, P, i32, ctypes.POINTER(QkTurn), P, P, P]
     lib.deft_qkv_write.argtypes = qkv + [i32, i32, i32, i32, i32, P]
     lib.deft_qkv_write4.argtypes = qkv + [f32, f32, i32, i32, i32, i32, i32, P]
+    lib.deft_tree_attn4.argtypes = [P, P, P, f32, f32] + attn[3:]
     lib.deft_kv4_page_bytes.argtypes = [i32]
     lib.deft_kv4_page_bytes.restype = sz
     lib.deft_kv_unpack4.argtypes = [P, P, f32, f32, i32, P, i32, P, P, i32, i32, i32, P]
@@ -183,7 +184,7 @@ def load(path: str = LIB_PATH):
                "deft_pages_refcount", "deft_page_table", "deft_kv_write", "deft_prompt_plan",
                "deft_prompt_plan_rebuild", "deft_prompt_plan_upload", "deft_prompt_plan_stats_get",
                "deft_prompt_plan_get", "deft_prompt_attn", "deft_prompt_status", "deft_qkv_write", "deft_qkv_write4",
-               "deft_kv_unpack4"):
+               "deft_kv_unpack4", "deft_tree_attn4"):
         getattr(lib, fn).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -800,6 +801,47 @@ def deft_kv_unpack4(k4_pages, v4_pages, page_id, k_pages=None, v_pages=None, k_s
     if rc:
         _check("deft_kv_unpack4", rc)
     return k_pages, v_pages
+
+
+def deft_tree_attn4(q, k4_pages, v4_pages, node_page_off, page_id, plan: Plan, bufs: Optional[StepBuffers] = None,
+                    scale: Optional[float] = None, out_dtype: int = DEFT_OUT_BF16, k_scale: float = 1.0,
+                    v_scale: float = 1.0, stream=None):
+    """deft_tree_attn4: one tree-attention step over the 4-bit pools of
+    alloc_kv4_pages, written with k_scale and v_scale; returns (out, lse).
+    bufs: alloc_buffers(plan, queries, num_q_heads, head_dim); None: allocated
+    from the memory of the stream the call runs on."""
+    torch = _need_torch()
+    shape = q.shape
+    if len(shape) != 3 or q.dtype != torch.bfloat16 or not q.is_contiguous():
+        raise ValueError("q must be contiguous bf16 [queries, num_q_heads, head_dim]")
+    Q, Hq, d = shape
+    pool = _check_pools4(k4_pages, v4_pages, d)
+    stats = plan.stats
+    if Q != stats["num_queries"]:
+        raise ValueError("q must have one row per query of the plan")
+    if _index_tensor(node_page_off, "node_page_off") < stats["num_nodes"]:
+        raise ValueError("node_page_off is shorter than the plan's nodes")
+    _index_tensor(page_id, "page_id")
+    if bufs is None:
+        with _allocating_for(stream):
+            bufs = alloc_buffers(plan, Q, Hq, d, q.device, out_dtype)
+    out, lse, ws = bufs.out, bufs.lse, bufs.workspace
+    odt = out.dtype
+    if out.shape != shape or odt not in (torch.bfloat16, torch.float32) or not out.is_contiguous():
+        raise ValueError("out must be contiguous bf16 or fp32, shaped like q")
+    if lse.shape != (Q, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous fp32 [queries, num_q_heads]")
+    st = _launch_stream(stream, q, k4_pages, v4_pages, node_page_off, page_id, out, lse, ws)
+    if Q == 0:
+        return out, lse
+    rc = load().deft_tree_attn4(
+        q.data_ptr(), k4_pages.data_ptr(), v4_pages.data_ptr(), k_scale, v_scale, node_page_off.data_ptr(),
+        page_id.data_ptr(), pool[0], Hq, pool[1], d, 16, 1.0 / math.sqrt(d) if scale is None else float(scale), plan.handle,
+        out.data_ptr(), DEFT_OUT_BF16 if odt == torch.bfloat16 else DEFT_OUT_F32, lse.data_ptr(), ws.data_ptr(),
+        ws.numel() * ws.element_size(), st)
+    if rc:
+        _check("deft_tree_attn4", rc)
+    return out, lse
 
 
 PROMPT_ARRAYS = {"nodes": (0, 2), "items": (1, 12), "cta_off": (2, 1), "cta_unit": (3, 1), "merges": (4, 4)}

@@ -45,7 +45,7 @@ WorkLayout work_layout(int64_t slots, int32_t num_q_heads, int32_t head_dim)
 int prepare_step(const void *q, const void *k_pages, const void *v_pages, const int32_t *node_page_off,
                  const int32_t *page_id, int32_t num_pages, int32_t num_q_heads, int32_t num_kv_heads,
                  int32_t head_dim, int32_t page_size, float scale, const deft_plan_t *plan, void *out,
-                 int32_t out_dtype, float *lse, int32_t flags, AttnArgs &a, bool &use_mma)
+                 int32_t out_dtype, float *lse, int32_t flags, AttnArgs &a, bool &use_mma, bool kv4)
 {
     if (!plan || !q || !k_pages || !v_pages || !node_page_off || !page_id || !out || !lse)
         return DEFT_EINVAL;
@@ -67,7 +67,7 @@ int prepare_step(const void *q, const void *k_pages, const void *v_pages, const 
     use_mma = mma_supported(head_dim) && !(flags & DEFT_STEP_CUDA_CORES);
     // The CUDA-core kernel holds at most kFmaMaxRows rows per item; one query
     // of a larger GQA group needs the tensor-core path.
-    if (plan->gqa_group > kFmaMaxRows && !use_mma)
+    if (plan->gqa_group > kFmaMaxRows && !use_mma && !kv4)
         return DEFT_EUNSUPPORTED;
     a = AttnArgs{};
     a.q = q;
@@ -211,10 +211,11 @@ struct Step {
 int check_step(const void *q, const void *k_pages, const void *v_pages, const int32_t *node_page_off,
                const int32_t *page_id, int32_t num_pages, int32_t num_q_heads, int32_t num_kv_heads,
                int32_t head_dim, int32_t page_size, float scale, const deft_plan_t *plan, void *out,
-               int32_t out_dtype, float *lse, void *workspace, size_t workspace_bytes, int32_t flags, Step &st)
+               int32_t out_dtype, float *lse, void *workspace, size_t workspace_bytes, int32_t flags, Step &st,
+               bool kv4 = false)
 {
     int rc = deft::prepare_step(q, k_pages, v_pages, node_page_off, page_id, num_pages, num_q_heads, num_kv_heads,
-                                head_dim, page_size, scale, plan, out, out_dtype, lse, flags, st.a, st.use_mma);
+                                head_dim, page_size, scale, plan, out, out_dtype, lse, flags, st.a, st.use_mma, kv4);
     if (rc != DEFT_OK)
         return rc;
     if (!plan->uploaded)
@@ -566,6 +567,30 @@ int deft_tree_attn_host(const void *q_host, void *q, const void *k_pages, const 
         cudaMemcpyAsync(lse_host, lse, rows * sizeof(float), cudaMemcpyDeviceToHost, cs) != cudaSuccess)
         return DEFT_ECUDA;
     return DEFT_OK;
+}
+
+int deft_tree_attn4(const void *q, const void *k4_pages, const void *v4_pages, float k_scale, float v_scale,
+                    const int32_t *node_page_off, const int32_t *page_id, int32_t num_pages, int32_t num_q_heads,
+                    int32_t num_kv_heads, int32_t head_dim, int32_t page_size, float scale, const deft_plan_t *plan,
+                    void *out, int32_t out_dtype, float *lse, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!(k_scale >= 0x1p-60f && k_scale <= 0x1p60f) || !(v_scale >= 0x1p-60f && v_scale <= 0x1p60f))
+        return DEFT_EINVAL;
+    // No page is read where no query's path has a token.
+    if (!page_id && plan && plan->tree.fma_items.empty() && plan->tree.mma_items.empty())
+        page_id = node_page_off;
+    Step st;
+    const int rc = check_step(q, k4_pages, v4_pages, node_page_off, page_id, num_pages, num_q_heads, num_kv_heads,
+                              head_dim, page_size, scale, plan, out, out_dtype, lse, workspace, workspace_bytes, 0, st,
+                              true);
+    if (rc != DEFT_OK || st.empty)
+        return rc;
+    const deft::LaunchTracer trace = [](const deft_trace_record &rec, void *s, const std::function<int()> &launch) {
+        return traced(rec, s, launch);
+    };
+    if (deft::order_mergeonly_step(*st.hp, stream))
+        return DEFT_ECUDA;
+    return deft::dispatch_step4(st.a, *st.dp, *st.hp, k_scale, v_scale, stream, trace) ? DEFT_ECUDA : DEFT_OK;
 }
 
 int deft_naive_attn(const void *q, const void *k_pages, const void *v_pages,

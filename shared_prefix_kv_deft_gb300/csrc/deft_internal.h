@@ -352,11 +352,12 @@ struct AttnArgs {
 // The argument checks shared by every step entry point (flags: DEFT_STEP_*).
 // On DEFT_OK, `a` holds everything but the workspace pointers (o_part,
 // lse_part) and use_mma says whether >= 16-row items run on the
-// tensor cores.  The plan's upload state is the caller's to check.
+// tensor cores.  kv4: a step over a 4-bit cache, whose one kernel takes any
+// group.  The plan's upload state is the caller's to check.
 int prepare_step(const void *q, const void *k_pages, const void *v_pages, const int32_t *node_page_off,
                  const int32_t *page_id, int32_t num_pages, int32_t num_q_heads, int32_t num_kv_heads,
                  int32_t head_dim, int32_t page_size, float scale, const deft_plan_t *plan, void *out,
-                 int32_t out_dtype, float *lse, int32_t flags, AttnArgs &a, bool &use_mma);
+                 int32_t out_dtype, float *lse, int32_t flags, AttnArgs &a, bool &use_mma, bool kv4 = false);
 
 // Launchers (return a cudaError_t cast to int; 0 = success).
 //
@@ -405,6 +406,10 @@ using LaunchTracer = std::function<int(const deft_trace_record &rec, void *strea
 // dp's host copy.  Returns a cudaError_t as int.
 int dispatch_step(AttnArgs a, const DevPartition &dp, const Partition &hp, bool use_mma, int32_t family,
                   void *stream, const LaunchTracer &trace);
+// The same over a 4-bit cache (k_pages / v_pages of `a` are its pools): one
+// phase-1 launch and the merge (phase1_kv4.cu).
+int dispatch_step4(const AttnArgs &a, const DevPartition &dp, const Partition &hp, float k_scale, float v_scale, void *stream,
+                   const LaunchTracer &trace);
 // Row bucket of an item with `rows` rows: smallest b with rows <= 2^b.
 inline int row_bucket(int rows) { return rows <= 1 ? 0 : rows <= 2 ? 1 : rows <= 4 ? 2 : rows <= 8 ? 3 : 4; }
 // Rows per softmax warpgroup of a tensor-core item with `rows` rows (two
