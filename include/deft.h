@@ -661,8 +661,8 @@ int deft_kv_unpack4(const void *k4_pages, const void *v4_pages, float k_scale, f
  *     that is NaN or +infinity has NaN in out, and lse NaN or -infinity; no
  *     other row is affected.  page_id and node_page_off are trusted, as in
  *     deft_tree_attn (page_id may be NULL where no path has a token).
- * Several steps of one plan may run at the same time, each with its own
- * outputs and workspace (this call does not use the plan's work queues).  A
+ * out 16-byte aligned (DEFT_EINVAL).  Several steps of one plan may run at
+ * the same time, each with its own outputs and workspace (this call does not use the plan's work queues).  A
  * kernel wait that runs out is reported by deft_step_status.  k_scale and
  * v_scale in [2^-60, 2^60] (DEFT_EINVAL).  Never allocates, never
  * synchronises; stream-ordered on `stream`; may be captured into a CUDA

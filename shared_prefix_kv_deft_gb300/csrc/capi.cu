@@ -576,6 +576,8 @@ int deft_tree_attn4(const void *q, const void *k4_pages, const void *v4_pages, f
 {
     if (!(k_scale >= 0x1p-60f && k_scale <= 0x1p60f) || !(v_scale >= 0x1p-60f && v_scale <= 0x1p60f))
         return DEFT_EINVAL;
+    if ((uintptr_t)out & 15u)
+        return DEFT_EINVAL;
     // No page is read where no query's path has a token.
     if (!page_id && plan && plan->tree.fma_items.empty() && plan->tree.mma_items.empty())
         page_id = node_page_off;

@@ -37,36 +37,37 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kStages = 4;
-constexpr int kRowsMax = 64;
 constexpr float kUp = 4.f, kLift = 11.f;
+constexpr double kFill = 2.0;
 constexpr unsigned kAll = 0xffffffffu;
 
+// One launch: items [first, first + n) of one of the partition's two lists.
 struct Kv4Args {
     AttnArgs a;
     float k_scale, v_scale;
-    int32_t n_mma, n_fma;      // items of the partition's two lists
-    int32_t mma_narrow;        // tensor-core items below this have their row masks split at 16
+    int32_t first, n;
+    int32_t wide;              // 1: of the tensor-core list
+    int32_t mma_narrow;        // tensor-core items below this have their row masks split at 16, not 32
+    int32_t heads;             // KV heads a CTA takes (1, 2 or 4)
+    int32_t head_groups;       // CTAs of an item
+    int32_t last;              // 1: not the step's first phase-1 launch
 };
 
-template <int D>
+template <int D, int NT>
 struct Cfg {
     using P = kv4::Page<D>;
+    static constexpr bool kQSmem = NT > 2;                                // Q^T fragments in shared memory
     static constexpr uint32_t kStage = 2 * P::kBytes;                     // K, then V, of one page
-    static constexpr uint32_t kQRow = 2 * D + 16;                        // bytes of a row of Q, padded
-    static constexpr uint32_t ring = 0;                                   // [warp][stage]; at the end [warp][16][D] fp32
-    static constexpr uint32_t ring_bytes = kWarps * kStages * kStage > kWarps * 16 * D * 4 ? kWarps * kStages * kStage
-                                                                                            : kWarps * 16 * D * 4;
-    static constexpr uint32_t q = ring + ring_bytes;                      // [64] rows
-    static constexpr uint32_t qf = q + kRowsMax * kQRow;                  // [64] what a row's S is multiplied by
-    static constexpr uint32_t ml = qf + kRowsMax * 4;                     // [warp][16] m, l
-    static constexpr uint32_t seg = ml + kWarps * 16 * 8;                 // [256] mask (8 B), page, begin, len; [257] first slice
-    static constexpr uint32_t bars = seg + kMaxSegsPerChunk * 24 + 8;
-    static constexpr uint32_t total = bars + kWarps * kStages * 8 + 16;
+    static constexpr uint32_t kState = NT * (1 + D / 16) * 512;           // a warp's state when warps join
+    static constexpr uint32_t ring_raw = kWarps * kStages * kStage;       // [warp][stage]; at the end two states
+    static constexpr uint32_t ring_bytes = ring_raw > 2 * kState ? ring_raw : (2 * kState + 127) / 128 * 128;
+    static constexpr uint32_t q = ring_bytes;                             // [warp][NT * D / 32][lane] 16 bytes
+    static constexpr uint32_t seg = q + (kQSmem ? kWarps * NT * (D / 32) * 512 : 0);
+    static constexpr uint32_t bars = seg + kMaxSegsPerChunk * 24 + 8;     // [256] mask (8 B), page, begin, len; [257] first slice
+    static constexpr uint32_t total = bars + kWarps * kStages * 8;
+    static constexpr int kCtas = NT == 1 ? 4 : NT == 2 ? 3 : 2;           // that an SM is meant to hold
     static_assert(kStage % 16 == 0 && q % 16 == 0 && seg % 8 == 0 && bars % 8 == 0, "alignment");
-};
-
-struct Slice {
-    int page, seg, lo, hi;   // tokens lo .. hi - 1 of the page
+    static_assert((total + 1024) * kCtas <= 228 * 1024, "shared memory of an SM");
 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -91,13 +92,27 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads) phase1_kv4_kernel(Kv4Args ka, DevPartition p)
+__device__ __forceinline__ float pow2(int e)   // -126 <= e <= 127
 {
-    using C = Cfg<D>;
+    return __int_as_float((127 + e) << 23);
+}
+
+// A slice: the tokens of one page that belong to one segment.  `desc` holds
+// tokens lo .. hi - 1 of the page and the segment; bit 31: all 16 tokens, for
+// all of the warp's rows.
+__device__ __forceinline__ uint32_t slice_desc(int seg, int lo, int hi, bool whole)
+{
+    return (whole ? 1u << 31 : 0u) | (uint32_t)seg << 16 | (uint32_t)lo << 8 | (uint32_t)hi;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel(Kv4Args ka, DevPartition p)
+{
+    using C = Cfg<D, NT>;
     using P = kv4::Page<D>;
     constexpr int KW = D / 32;      // words of a lane's K elements: dims (D / 4) t ..
     constexpr int VW = D / 64;      // words of a lane's V elements: dims (D / 8) g ..
+    constexpr int NR = 8 * NT;      // rows of a warp
     extern __shared__ __align__(128) uint8_t smem[];
     const AttnArgs &a = ka.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -106,8 +121,6 @@ __global__ void __launch_bounds__(kThreads) phase1_kv4_kernel(Kv4Args ka, DevPar
     int32_t *seg_page = reinterpret_cast<int32_t *>(smem + C::seg + kMaxSegsPerChunk * 8);   // first page's index in page_id
     int32_t *seg_begin = seg_page + kMaxSegsPerChunk, *seg_len = seg_begin + kMaxSegsPerChunk;
     int32_t *seg_first = seg_len + kMaxSegsPerChunk;                                         // [257] slices before the segment
-    float *qf = reinterpret_cast<float *>(smem + C::qf);
-    float2 *ml = reinterpret_cast<float2 *>(smem + C::ml);
     const uint32_t bars = base + C::bars + warp * kStages * 8;
 
     if (lane == 0) {
@@ -115,155 +128,181 @@ __global__ void __launch_bounds__(kThreads) phase1_kv4_kernel(Kv4Args ka, DevPar
             tc::mbar_init(bars + s * 8, 1);
         tc::fence_mbar_init();
     }
-    grid_dep_wait();
+    if (a.wait_prior)
+        grid_dep_wait();
     grid_dep_launch();
 
-    // ---- the unit ----
+    // ---- the item ----
     const int Hkv = a.num_kv_heads, Hq = a.num_q_heads, G = a.gqa_group;
-    const int unit = blockIdx.x, it = unit / Hkv, h = unit - it * Hkv;
-    const bool wide = it < ka.n_mma;
-    const int item = wide ? it : it - ka.n_mma;
-    const int32_t *triple = (wide ? p.mma_items : p.fma_items) + 3 * (size_t)item;
+    const int it = blockIdx.x / ka.head_groups, hg = blockIdx.x - it * ka.head_groups;
+    const int item = ka.first + it;
+    const int32_t *triple = (ka.wide ? p.mma_items : p.fma_items) + 3 * (size_t)item;
     const int c = triple[0], qb = triple[1], R = (triple[2] - qb) * G;
+    const int rm0 = (ka.wide ? p.mma_rmask_off : p.fma_rmask_off)[item];
+    const uint32_t direct = !ka.wide && a.direct ? p.fma_direct[item] : 0u;
     const int cq0 = p.chunk_q_off[c] + qb;
     const int sb = p.chunk_seg_off[c], nseg = p.chunk_seg_off[c + 1] - sb;
-    const uint32_t direct = !wide && a.direct ? p.fma_direct[item] : 0u;
-    const int rm0 = wide ? p.mma_rmask_off[item] : p.fma_rmask_off[item];
-    for (int s = tid; s < nseg; s += kThreads) {
-        const int len = p.seg_tok_len[sb + s], tb = p.seg_tok_begin[sb + s];
-        seg_page[s] = a.node_page_off[p.seg_node[sb + s]] + tb / kPageSize;
-        seg_begin[s] = tb % kPageSize;
-        seg_len[s] = len;
-        seg_first[s + 1] = (tb % kPageSize + len + kPageSize - 1) / kPageSize;
-        if (wide) {
-            const uint4 w = reinterpret_cast<const uint4 *>(p.mma_rmask)[rm0 + s];
-            seg_mask[s] = (uint64_t)w.x | (uint64_t)w.z << (item < ka.mma_narrow ? 16 : 32);
-        } else {
-            seg_mask[s] = p.fma_rmask[rm0 + s];
-        }
-    }
-    if (tid == 0)
-        seg_first[0] = 0;
-    // ---- Q, a row a warp: bf16 -> fp16 times a power of two ----
-    const int groups = R <= 8 * NT ? 1 : R <= 16 * NT ? 2 : 4;     // warps' worth of rows
-    for (int r = warp; r < groups * 8 * NT; r += kWarps) {
-        float x[D / 32];
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-            x[i] = 0.f;
-        if (r < R) {
-            const int head = h * G + r % G;
-            const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(a.q) +
-                                       ((size_t)p.chunk_q[cq0 + r / G] * Hq + head) * D + lane * (D / 32);
-#pragma unroll
-            for (int i = 0; i < D / 32; i += 2) {
-                const float2 v = bf16x2_to_float2(*reinterpret_cast<const uint32_t *>(src + i));
-                x[i] = v.x;
-                x[i + 1] = v.y;
-            }
-        }
-        float big = 0.f;   // the largest finite magnitude
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-            if (fabsf(x[i]) < INFINITY)
-                big = fmaxf(big, fabsf(x[i]));
-        big = warp_max(big);
-        // 2^e in two factors: e reaches from -113 to 147.
-        const int e = big > 0.f ? 14 - ilogbf(big) : 0, e1 = e / 2, e2 = e - e1;
-        const float up1 = __int_as_float((127 + e1) << 23), up2 = __int_as_float((127 + e2) << 23);
-#pragma unroll
-        for (int i = 0; i < D / 32; i += 2)
-            *reinterpret_cast<uint32_t *>(smem + C::q + r * C::kQRow + (lane * (D / 32) + i) * 2) =
-                f16x2(x[i] * up1 * up2, x[i + 1] * up1 * up2);
-        if (lane == 0)
-            qf[r] = a.scale_log2 * __int_as_float((127 - e1) << 23) * ka.k_scale * __int_as_float((127 - e2) << 23);
-    }
-    __syncthreads();
-    if (warp == 0) {
-        // Slices before each segment: an inclusive scan of the counts.
-        int before = 0;
-        for (int s0 = 0; s0 < nseg; s0 += 32) {
-            int n = s0 + lane < nseg ? seg_first[s0 + lane + 1] : 0;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(kAll, n, o);
-                if (lane >= o)
-                    n += y;
-            }
-            if (s0 + lane < nseg)
-                seg_first[s0 + lane + 1] = before + n;
-            before += __shfl_sync(kAll, n, 31);
-        }
-    }
-    __syncthreads();
+    auto row_mask = [&](int s) -> uint64_t {
+        if (!ka.wide)
+            return p.fma_rmask[rm0 + s];
+        const uint4 w = reinterpret_cast<const uint4 *>(p.mma_rmask)[rm0 + s];
+        return (uint64_t)w.x | (uint64_t)w.z << (item < ka.mma_narrow ? 16 : 32);
+    };
+    // The warp's part: rows [row0, row0 + NR) of KV head h, slices ts, ts +
+    // TS, ...
+    const int groups = R <= NR ? 1 : 2;                 // (a CTA's share of heads leaves room for both)
+    const int TS = kWarps / (ka.heads * groups);
+    const int ts = warp % TS, rg = warp / TS % groups, h = hg * ka.heads + warp / (TS * groups);
+    const int row0 = rg * NR;
+    const bool idle = h >= Hkv;
 
-    // ---- the warp's rows and slices ----
-    const int rg = warp % groups, ts = warp / groups, TS = kWarps / groups;
-    const int row0 = rg * 8 * NT;
-    const int total = seg_first[nseg];
-    const int mine = total > ts && row0 < R ? (total - ts + TS - 1) / TS : 0;
-    uint32_t qa[NT][KW * 4];        // Q^T fragments: two registers a step of 16 dims
-    float f[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const uint8_t *src = smem + C::q + (row0 + 8 * n + g) * C::kQRow + t * (D / 2);
-#pragma unroll
-        for (int i = 0; i < KW; ++i) {
-            const uint4 w = *reinterpret_cast<const uint4 *>(src + 16 * i);
-            qa[n][4 * i] = w.x, qa[n][4 * i + 1] = w.y, qa[n][4 * i + 2] = w.z, qa[n][4 * i + 3] = w.w;
+    // One segment (a piece of a longer node) is the common case; the table of
+    // several is made by the CTA.
+    uint64_t mask0 = 0;
+    int page0 = 0, begin0 = 0, len0 = 0, total;
+    if (nseg == 1) {
+        len0 = p.seg_tok_len[sb];
+        const int tb = p.seg_tok_begin[sb];
+        page0 = a.node_page_off[p.seg_node[sb]] + tb / kPageSize;
+        begin0 = tb % kPageSize;
+        mask0 = row_mask(0);
+        total = (begin0 + len0 + kPageSize - 1) / kPageSize;
+    } else {
+        for (int s = tid; s < nseg; s += kThreads) {
+            const int len = p.seg_tok_len[sb + s], tb = p.seg_tok_begin[sb + s];
+            seg_page[s] = a.node_page_off[p.seg_node[sb + s]] + tb / kPageSize;
+            seg_begin[s] = tb % kPageSize;
+            seg_len[s] = len;
+            seg_first[s + 1] = (tb % kPageSize + len + kPageSize - 1) / kPageSize;
+            seg_mask[s] = row_mask(s);
         }
-        f[n][0] = qf[row0 + 8 * n + 2 * t];
-        f[n][1] = qf[row0 + 8 * n + 2 * t + 1];
+        if (tid == 0)
+            seg_first[0] = 0;
+        __syncthreads();
+        if (warp == 0) {
+            // Slices before each segment: an inclusive scan of the counts.
+            int before = 0;
+            for (int s0 = 0; s0 < nseg; s0 += 32) {
+                int n = s0 + lane < nseg ? seg_first[s0 + lane + 1] : 0;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(kAll, n, o);
+                    if (lane >= o)
+                        n += y;
+                }
+                if (s0 + lane < nseg)
+                    seg_first[s0 + lane + 1] = before + n;
+                before += __shfl_sync(kAll, n, 31);
+            }
+        }
+        __syncthreads();
+        total = seg_first[nseg];
     }
-    // Slice i of the warp, by lane i % 32 for the batch it lies in.
-    Slice batch{0, 0, 0, 0};
-    auto fill_batch = [&](int b) {
-        const int i = b * 32 + lane;
-        if (i < mine) {
-            const int x = ts + i * TS;
-            int lo = 0, hi = nseg;
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
+    const int mine = !idle && total > ts ? (total - ts + TS - 1) / TS : 0;
+    const uint64_t row_bits = R >= 64 ? ~0ull : (1ull << R) - 1;
+    const uint32_t my_rows = (uint32_t)(row_bits >> row0) & (uint32_t)((1ull << NR) - 1);
+
+    // ---- slices: 32 at a time, each held (and its copy issued) by a lane ----
+    const uint8_t *k4 = static_cast<const uint8_t *>(a.k_pages), *v4 = static_cast<const uint8_t *>(a.v_pages);
+    const uint64_t pol = tc::l2_kv_policy(false);
+    const uint32_t ring = base + warp * kStages * C::kStage;
+    auto get_slice = [&](int i, int &page, uint32_t &desc) {
+        if (i >= mine)
+            return;
+        const int x = ts + i * TS;
+        int seg = 0, j = x, pg = page0, begin = begin0, len = len0;
+        uint64_t mask = mask0;
+        if (nseg > 1) {
+            int hi = nseg;
+            while (hi - seg > 1) {
+                const int mid = (seg + hi) >> 1;
                 if (seg_first[mid] <= x)
-                    lo = mid;
+                    seg = mid;
                 else
                     hi = mid;
             }
-            const int j = x - seg_first[lo];
-            batch.page = a.page_id[seg_page[lo] + j];
-            batch.seg = lo;
-            batch.lo = max(0, seg_begin[lo] - j * kPageSize);
-            batch.hi = min(kPageSize, seg_begin[lo] + seg_len[lo] - j * kPageSize);
+            j = x - seg_first[seg];
+            pg = seg_page[seg], begin = seg_begin[seg], len = seg_len[seg], mask = seg_mask[seg];
         }
+        page = a.page_id[pg + j];
+        const int lo = max(0, begin - j * kPageSize), hi = min(kPageSize, begin + len - j * kPageSize);
+        desc = slice_desc(seg, lo, hi, hi - lo == kPageSize && ((uint32_t)(mask >> row0) & my_rows) == my_rows);
     };
-    const uint8_t *k4 = static_cast<const uint8_t *>(a.k_pages), *v4 = static_cast<const uint8_t *>(a.v_pages);
-    const uint64_t pol = tc::l2_kv_policy(false);
-    const uint32_t ring = base + C::ring + warp * kStages * C::kStage;
-    auto copy = [&](int i, int page) {   // lane 0
-        const uint32_t dst = ring + (i % kStages) * C::kStage, bar = bars + (i % kStages) * 8;
-        const size_t at = ((size_t)page * Hkv + h) * P::kBytes;
-        tc::mbar_arrive_expect_tx(bar, C::kStage);
-        tc::bulk_load(dst, k4 + at, P::kBytes, bar, pol);
-        tc::bulk_load(dst + P::kBytes, v4 + at, P::kBytes, bar, pol);
-    };
-    fill_batch(0);
-    // The next batch's slices are taken when its first copy is due.
-    Slice next = batch;
-    int issued = 0, next_batch = 0;
+    int next_page = 0;
+    uint32_t cur = 0, next = 0;     // the batch in hand, and the one whose copies go out
+    int next_batch = 0;
+    get_slice(lane, next_page, next);
+    cur = next;
     auto issue = [&](int i) {
         if (i / 32 != next_batch) {
-            const Slice keep = batch;
             next_batch = i / 32;
-            fill_batch(next_batch);
-            next = batch;
-            batch = keep;
+            get_slice(i + lane, next_page, next);
         }
-        const int page = __shfl_sync(kAll, next.page, i & 31);
-        if (lane == 0)
-            copy(i, page);
+        if (lane == (i & 31)) {
+            const uint32_t dst = ring + (i % kStages) * C::kStage, bar = bars + (i % kStages) * 8;
+            const size_t at = ((size_t)next_page * Hkv + h) * P::kBytes;
+            tc::mbar_arrive_expect_tx(bar, C::kStage);
+            tc::bulk_load(dst, k4 + at, P::kBytes, bar, pol);
+            tc::bulk_load(dst + P::kBytes, v4 + at, P::kBytes, bar, pol);
+        }
     };
+    __syncwarp();   // the barriers are there
+    int issued = 0;
     for (; issued < mine && issued < kStages; ++issued)
         issue(issued);
+
+    // ---- Q^T fragments: lane (g, t) holds dims (D / 4) t .. of row g ----
+    uint32_t qa[C::kQSmem ? 1 : NT][KW * 4];
+    uint4 *qs = reinterpret_cast<uint4 *>(smem + C::q) + warp * NT * KW * 32 + lane;
+    float f[NT][2];                 // what rows 2t and 2t + 1 of S are multiplied by
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int r = row0 + 8 * n + g;
+        uint32_t w[KW * 4];
+#pragma unroll
+        for (int i = 0; i < KW * 4; ++i)
+            w[i] = 0u;
+        if (r < R && !idle) {
+            const int k = r / G;
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
+                                                               ((size_t)p.chunk_q[cq0 + k] * Hq + h * G + (r - k * G)) * D) +
+                               t * KW;
+#pragma unroll
+            for (int i = 0; i < KW; ++i) {
+                const uint4 v = src[i];
+                w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+            }
+        }
+        float big = 0.f;            // the row's largest finite magnitude
+#pragma unroll
+        for (int i = 0; i < KW * 4; ++i) {
+            const float2 v = bf16x2_to_float2(w[i] & 0x7fff7fffu);
+            big = v.x < INFINITY ? fmaxf(big, v.x) : big;
+            big = v.y < INFINITY ? fmaxf(big, v.y) : big;
+        }
+        big = fmaxf(big, __shfl_xor_sync(kAll, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(kAll, big, 2));
+        // 2^e in two factors: e reaches from -113 to 147.
+        const int e = big > 0.f ? 14 - ilogbf(big) : 0, e1 = e / 2, e2 = e - e1;
+        const float up1 = pow2(e1), up2 = pow2(e2);
+        const float fr = a.scale_log2 * pow2(-e1) * ka.k_scale * pow2(-e2);
+        f[n][0] = __shfl_sync(kAll, fr, 8 * t);
+        f[n][1] = __shfl_sync(kAll, fr, 8 * t + 4);
+#pragma unroll
+        for (int i = 0; i < KW * 4; ++i) {
+            const float2 v = bf16x2_to_float2(w[i]);
+            w[i] = f16x2(v.x * up1 * up2, v.y * up1 * up2);
+        }
+        if constexpr (C::kQSmem) {
+#pragma unroll
+            for (int i = 0; i < KW; ++i)
+                qs[(n * KW + i) * 32] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < KW * 4; ++i)
+                qa[n][i] = w[i];
+        }
+    }
 
     float o[D / 16][NT][4];
     float m[NT][2], l[NT][2];
@@ -275,41 +314,45 @@ __global__ void __launch_bounds__(kThreads) phase1_kv4_kernel(Kv4Args ka, DevPar
         m[n][0] = m[n][1] = -INFINITY;
         l[n][0] = l[n][1] = 0.f;
     }
-    const uint64_t row_bits = R >= 64 ? ~0ull : (1ull << R) - 1;
-    const uint64_t my_rows = (row_bits >> row0) & ((1ull << (8 * NT)) - 1);
+    // MMA row r holds token r ^ (r >> 1 & 1) of the page: then the eight lanes
+    // of a 16-byte read of K and the sixteen of an 8-byte read of V, whose
+    // rows are 64 bytes, meet the fewest bank conflicts (24 reads of
+    // shared memory a page, not 40).
+    const int kg = g ^ (g >> 1 & 1);
+    const int vx = 2 * t + (t & 1), vy = 2 * t + 1 - (t & 1);
     bool ok = true;
     for (int i = 0; i < mine; ++i) {
         if (i > 0 && (i & 31) == 0)
-            batch = next;      // (issue() is at most kStages ahead: it has filled this batch)
-        const int seg = __shfl_sync(kAll, batch.seg, i & 31);
-        const int lo = __shfl_sync(kAll, batch.lo, i & 31), hi = __shfl_sync(kAll, batch.hi, i & 31);
+            cur = next;      // (issue() is at most kStages ahead: it has filled this batch)
+        const uint32_t desc = __shfl_sync(kAll, cur, i & 31);
         if (!__all_sync(kAll, tc::mbar_wait(bars + (i % kStages) * 8, (i / kStages) & 1))) {
             ok = false;
             break;
         }
-        const uint8_t *ks = smem + C::ring + (warp * kStages + i % kStages) * C::kStage, *vs = ks + P::kBytes;
+        const uint8_t *ks = smem + (warp * kStages + i % kStages) * C::kStage, *vs = ks + P::kBytes;
+        const bool whole = desc >> 31;
         // ---- S^T ----
         float s[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
             s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
         {
-            uint32_t w0[KW], w1[KW], sc0[D / 64], sc1[D / 64];
+            uint32_t w0[KW], w1[KW], sc0[KW / 2], sc1[KW / 2];
             if constexpr (D == 128) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(ks + g * P::kRow + t * 16);
-                const uint4 y = *reinterpret_cast<const uint4 *>(ks + (g + 8) * P::kRow + t * 16);
+                const uint4 x = *reinterpret_cast<const uint4 *>(ks + kg * P::kRow + t * 16);
+                const uint4 y = *reinterpret_cast<const uint4 *>(ks + (kg + 8) * P::kRow + t * 16);
                 w0[0] = x.x, w0[1] = x.y, w0[2] = x.z, w0[3] = x.w;
                 w1[0] = y.x, w1[1] = y.y, w1[2] = y.z, w1[3] = y.w;
-                const uint32_t u = kv4::scales2(*reinterpret_cast<const uint16_t *>(ks + P::kScales + g * P::kScaleRow + t * 2));
-                const uint32_t v = kv4::scales2(*reinterpret_cast<const uint16_t *>(ks + P::kScales + (g + 8) * P::kScaleRow + t * 2));
+                const uint32_t u = kv4::scales2(*reinterpret_cast<const uint16_t *>(ks + P::kScales + kg * P::kScaleRow + t * 2));
+                const uint32_t v = kv4::scales2(*reinterpret_cast<const uint16_t *>(ks + P::kScales + (kg + 8) * P::kScaleRow + t * 2));
                 sc0[0] = __byte_perm(u, 0, 0x1010), sc0[1] = __byte_perm(u, 0, 0x3232);
                 sc1[0] = __byte_perm(v, 0, 0x1010), sc1[1] = __byte_perm(v, 0, 0x3232);
             } else {
-                const uint2 x = *reinterpret_cast<const uint2 *>(ks + g * P::kRow + t * 8);
-                const uint2 y = *reinterpret_cast<const uint2 *>(ks + (g + 8) * P::kRow + t * 8);
+                const uint2 x = *reinterpret_cast<const uint2 *>(ks + kg * P::kRow + t * 8);
+                const uint2 y = *reinterpret_cast<const uint2 *>(ks + (kg + 8) * P::kRow + t * 8);
                 w0[0] = x.x, w0[1] = x.y;
                 w1[0] = y.x, w1[1] = y.y;
-                const uint32_t u = ks[P::kScales + g * P::kScaleRow + t], v = ks[P::kScales + (g + 8) * P::kScaleRow + t];
+                const uint32_t u = ks[P::kScales + kg * P::kScaleRow + t], v = ks[P::kScales + (kg + 8) * P::kScaleRow + t];
                 sc0[0] = kv4::scales2(u | u << 8);
                 sc1[0] = kv4::scales2(v | v << 8);
             }
@@ -325,28 +368,40 @@ __global__ void __launch_bounds__(kThreads) phase1_kv4_kernel(Kv4Args ka, DevPar
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    mma16816(s[n], x[0], y[0], x[1], y[1], qa[n][4 * w], qa[n][4 * w + 1]);
-                    mma16816(s[n], x[2], y[2], x[3], y[3], qa[n][4 * w + 2], qa[n][4 * w + 3]);
+                    uint4 q;
+                    if constexpr (C::kQSmem)
+                        q = qs[(n * KW + w) * 32];
+                    else
+                        q = make_uint4(qa[n][4 * w], qa[n][4 * w + 1], qa[n][4 * w + 2], qa[n][4 * w + 3]);
+                    mma16816(s[n], x[0], y[0], x[1], y[1], q.x, q.y);
+                    mma16816(s[n], x[2], y[2], x[3], y[3], q.z, q.w);
                 }
             }
         }
         // ---- softmax ----
-        const uint64_t rows = (seg_mask[seg] >> row0) & my_rows;
-        const bool whole = hi - lo == kPageSize && rows == my_rows;
         bool grow = false;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 4; ++j)
                 s[n][j] *= f[n][j & 1];
-                if (!whole) {
-                    const int tok = g + (j >> 1) * 8, row = 8 * n + 2 * t + (j & 1);
+        const int lo = desc >> 8 & 255, hi = desc & 255;
+        if (!whole) {
+            const uint32_t rows = (uint32_t)((nseg > 1 ? seg_mask[desc >> 16 & 0x7fff] : mask0) >> row0);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int tok = kg + (j >> 1) * 8, row = 8 * n + 2 * t + (j & 1);
                     if (tok < lo || tok >= hi || !((rows >> row) & 1))
                         s[n][j] = -INFINITY;
                 }
-                grow |= s[n][j] > m[n][j & 1] + kUp;
-            }
         }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                grow |= s[n][j] > m[n][j & 1] + kUp;
         if (__any_sync(kAll, grow)) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -381,26 +436,32 @@ __global__ void __launch_bounds__(kThreads) phase1_kv4_kernel(Kv4Args ka, DevPar
         }
         // ---- O^T ----
         {
-            uint32_t sv[2];     // scales of tokens (2t, 2t + 1) and (2t + 8, 2t + 9)
+            uint32_t sv[2], vw[2][2][VW];     // by token pair: scales, words of both tokens
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const int tok = 2 * t + 8 * q;
-                const uint8_t *src = vs + P::kScales + tok * P::kScaleRow + (D == 128 ? g : g >> 1);
-                uint32_t x = src[0], y = src[P::kScaleRow];
+                const uint8_t *sx = vs + P::kScales + (D == 128 ? g : g >> 1);
+                uint32_t x = sx[(vx + 8 * q) * P::kScaleRow], y = sx[(vy + 8 * q) * P::kScaleRow];
                 if (!whole) {   // (what a page holds beside the segment's tokens may be anything)
-                    x = tok >= lo && tok < hi ? x : 0u;
-                    y = tok + 1 >= lo && tok + 1 < hi ? y : 0u;
+                    x = vx + 8 * q >= lo && vx + 8 * q < hi ? x : 0u;
+                    y = vy + 8 * q >= lo && vy + 8 * q < hi ? y : 0u;
                 }
                 sv[q] = kv4::scales2(x | y << 8);
+                const uint8_t *rx = vs + (vx + 8 * q) * P::kRow + g * (D / 16), *ry = vs + (vy + 8 * q) * P::kRow + g * (D / 16);
+                if constexpr (D == 128) {
+                    const uint2 u = *reinterpret_cast<const uint2 *>(rx), v = *reinterpret_cast<const uint2 *>(ry);
+                    vw[q][0][0] = u.x, vw[q][0][1] = u.y;
+                    vw[q][1][0] = v.x, vw[q][1][1] = v.y;
+                } else {
+                    vw[q][0][0] = *reinterpret_cast<const uint32_t *>(rx);
+                    vw[q][1][0] = *reinterpret_cast<const uint32_t *>(ry);
+                }
             }
 #pragma unroll
             for (int w = 0; w < VW; ++w) {
                 uint32_t e[2][4], od[2][4];   // even and odd dims of the word, by token pair
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    const uint8_t *src = vs + (2 * t + 8 * q) * P::kRow + g * (D / 16) + 4 * w;
-                    const uint32_t x = *reinterpret_cast<const uint32_t *>(src);
-                    const uint32_t y = *reinterpret_cast<const uint32_t *>(src + P::kRow);
+                    const uint32_t x = vw[q][0][w], y = vw[q][1][w];
                     kv4::unpack8((x & 0x0f0f0f0fu) | (y << 4 & 0xf0f0f0f0u), e[q]);
                     kv4::unpack8((x >> 4 & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u), od[q]);
 #pragma unroll
@@ -434,87 +495,126 @@ __global__ void __launch_bounds__(kThreads) phase1_kv4_kernel(Kv4Args ka, DevPar
             l[n][0] = l[n][1] = __int_as_float(0x7fffffff);
     }
 
-    // ---- the warps' states, joined ----
+    // ---- the states of the warps that shared the slices, joined by halves:
+    // the upper half writes its state, lane by lane, the lower takes it in ----
+    if (TS > 1) {
+        for (int half = TS / 2; half >= 1; half /= 2) {
+            __syncthreads();   // the ring, or the states before, have been read
+            const int pair = (warp / TS) * half + (ts & (half - 1));
+            float *st = reinterpret_cast<float *>(smem) + (size_t)pair * (C::kState / 4);
+            if (ts >= half && ts < 2 * half) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NT; ++n) {
+                    reinterpret_cast<float4 *>(st)[n * 32 + lane] = make_float4(m[n][0], m[n][1], l[n][0], l[n][1]);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            float x = l[n][j];
-            x += __shfl_xor_sync(kAll, x, 4);
-            x += __shfl_xor_sync(kAll, x, 8);
-            x += __shfl_xor_sync(kAll, x, 16);
-            if (g == 0)
-                ml[warp * 16 + 8 * n + 2 * t + j] = make_float2(m[n][j], x);
-        }
-    __syncthreads();   // every warp's copies have been read
-    float *os = reinterpret_cast<float *>(smem + C::ring);
+                    for (int d = 0; d < D / 16; ++d)
+                        reinterpret_cast<float4 *>(st)[(NT + n * (D / 16) + d) * 32 + lane] =
+                            make_float4(o[d][n][0], o[d][n][1], o[d][n][2], o[d][n][3]);
+                }
+            }
+            __syncthreads();
+            if (ts < half) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NT; ++n) {
+                    const float4 x = reinterpret_cast<const float4 *>(st)[n * 32 + lane];
+                    const float mj[2] = {x.x, x.y}, lj[2] = {x.z, x.w};
+                    float wa[2], wb[2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            float *dst = os + (warp * 16 + 8 * n + 2 * t + j) * D + g * (D / 8);
+                    for (int j = 0; j < 2; ++j) {
+                        const float M = fmaxf(m[n][j], mj[j]);
+                        wa[j] = M == -INFINITY ? 1.f : tc::ex2(m[n][j] - M);
+                        wb[j] = M == -INFINITY ? 1.f : tc::ex2(mj[j] - M);
+                        m[n][j] = M;
+                        l[n][j] = l[n][j] * wa[j] + lj[j] * wb[j];
+                    }
 #pragma unroll
-            for (int i = 0; i < D / 16; i += 2)
-                *reinterpret_cast<float4 *>(dst + 2 * i) =
-                    make_float4(o[i][n][j], o[i][n][j + 2], o[i + 1][n][j], o[i + 1][n][j + 2]);
-        }
-    __syncthreads();
-    for (int r = warp; r < R; r += kWarps) {
-        const int grp = r / (8 * NT), in = r - grp * 8 * NT;
-        float M = -INFINITY;
-        for (int k = 0; k < TS; ++k)
-            M = fmaxf(M, ml[(grp + k * groups) * 16 + in].x);
-        float sum = 0.f, acc[D / 32];
-#pragma unroll
-        for (int e = 0; e < D / 32; ++e)
-            acc[e] = 0.f;
-        for (int k = 0; k < TS; ++k) {
-            const int w = grp + k * groups;
-            const float2 s = ml[w * 16 + in];
-            const float wt = M == -INFINITY ? 1.f : tc::ex2(s.x - M);
-            sum = fmaf(wt, s.y, sum);
-            const float *src = os + (w * 16 + in) * D + lane * (D / 32);
-#pragma unroll
-            for (int e = 0; e < D / 32; ++e)
-                acc[e] = fmaf(wt, src[e], acc[e]);
-        }
-        // sum is 0 where the row attends no token, NaN where a logit was.
-        const float inv = sum == 0.f ? 0.f : ka.v_scale / sum;
-        const float lse2 = sum == 0.f ? -INFINITY : M + log2f(sum) - kLift;
-        const int k = r / G, head = h * G + r % G;
-        if (r < 32 && ((direct >> r) & 1u)) {
-            const size_t row = (size_t)p.chunk_q[cq0 + k] * Hq + head;
-#pragma unroll
-            for (int e = 0; e < D / 32; ++e)
-                store_out(a, row, lane * (D / 32) + e, D, acc[e] * inv);
-            if (lane == 0)
-                a.lse_out[row] = direct_lse(lse2);
-        } else {
-            const size_t row = (size_t)(cq0 + k) * Hq + head;
-#pragma unroll
-            for (int e = 0; e < D / 32; ++e)
-                a.o_part[row * D + lane * (D / 32) + e] = acc[e] * inv;
-            // (+inf, so that the merge's weight for it is NaN and not 0)
-            if (lane == 0)
-                a.lse_part[row] = lse2 == lse2 ? lse2 : INFINITY;
+                    for (int d = 0; d < D / 16; ++d) {
+                        const float4 y = reinterpret_cast<const float4 *>(st)[(NT + n * (D / 16) + d) * 32 + lane];
+                        o[d][n][0] = o[d][n][0] * wa[0] + y.x * wb[0];
+                        o[d][n][1] = o[d][n][1] * wa[1] + y.y * wb[1];
+                        o[d][n][2] = o[d][n][2] * wa[0] + y.z * wb[0];
+                        o[d][n][3] = o[d][n][3] * wa[1] + y.w * wb[1];
+                    }
+                }
+            }
         }
     }
+
+    // ---- out: lane (g, t) holds dims (D / 8) g .. of rows 2t and 2t + 1 ----
+    if (ts == 0 && !idle) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float sum = l[n][j];
+                sum += __shfl_xor_sync(kAll, sum, 4);
+                sum += __shfl_xor_sync(kAll, sum, 8);
+                sum += __shfl_xor_sync(kAll, sum, 16);
+                const int r = row0 + 8 * n + 2 * t + j;
+                if (r >= R)
+                    continue;
+                // sum is 0 where the row attends no token, NaN where a logit was.
+                const float inv = sum == 0.f ? 0.f : ka.v_scale / sum;
+                const float lse2 = sum == 0.f ? -INFINITY : m[n][j] + log2f(sum) - kLift;
+                const int k = r / G, head = h * G + (r - k * G);
+                const bool straight = r < 32 && ((direct >> r) & 1u);
+                const size_t row = (size_t)(straight ? p.chunk_q[cq0 + k] : cq0 + k) * Hq + head;
+                const size_t at = row * D + g * (D / 8);
+                if (straight && a.out_dtype == DEFT_OUT_BF16) {
+#pragma unroll
+                    for (int d = 0; d < D / 16; d += 4) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const __nv_bfloat162 b = __floats2bfloat162_rn(o[d + x][n][j] * inv, o[d + x][n][j + 2] * inv);
+                            w[x] = *reinterpret_cast<const uint32_t *>(&b);
+                        }
+                        reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + at)[d / 4] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                } else {
+                    float4 *dst = reinterpret_cast<float4 *>((straight ? static_cast<float *>(a.out) : a.o_part) + at);
+#pragma unroll
+                    for (int d = 0; d < D / 16; d += 2)
+                        dst[d / 2] = make_float4(o[d][n][j] * inv, o[d][n][j + 2] * inv, o[d + 1][n][j] * inv, o[d + 1][n][j + 2] * inv);
+                }
+                if (g == 0) {
+                    if (straight)
+                        a.lse_out[row] = direct_lse(lse2);
+                    else    // (+inf, so that the merge's weight for it is NaN and not 0)
+                        a.lse_part[row] = lse2 == lse2 ? lse2 : INFINITY;
+                }
+            }
+    }
+    // The merge waits for this launch alone: its last CTA waits for the ones
+    // before.
+    if (ka.last && blockIdx.x == gridDim.x - 1)
+        grid_dep_wait();
 }
 
-template <int D>
-int launch(const Kv4Args &ka, const DevPartition &p, cudaStream_t st)
+template <int D, int NT>
+int launch(Kv4Args ka, const DevPartition &p, cudaStream_t st)
 {
-    constexpr int NT = 2;
-    const int64_t units = (int64_t)(ka.n_mma + ka.n_fma) * ka.a.num_kv_heads;
-    if (units == 0)
-        return 0;
-    if (units > INT32_MAX)
+    ka.head_groups = (ka.a.num_kv_heads + ka.heads - 1) / ka.heads;
+    const int64_t ctas = (int64_t)ka.n * ka.head_groups;
+    if (ctas > INT32_MAX)
         return (int)cudaErrorInvalidConfiguration;
     auto *kernel = phase1_kv4_kernel<D, NT>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::total);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, NT>::total);
     if (e != cudaSuccess)
         return (int)e;
-    return (int)launch_dependent(kernel, dim3((unsigned)units), dim3(kThreads), Cfg<D>::total, st, ka, p);
+    return (int)launch_dependent(kernel, dim3((unsigned)ctas), dim3(kThreads), Cfg<D, NT>::total, st, ka, p);
+}
+
+// KV heads a CTA takes: as many as give each of its warps (or pair of warps,
+// for two groups of rows) a unit of its own, but fewer, several warps sharing
+// a unit's pages, where that would leave the device short of warps.
+int heads_per_cta(int64_t items, int32_t hkv, int groups, int ctas_per_sm)
+{
+    const double full = kFill * kWarps * ctas_per_sm * num_sms();
+    int heads = kWarps / groups;
+    while (heads > 1 && (hkv % heads != 0 || (double)items * hkv * (kWarps / heads) < full))
+        heads /= 2;
+    return heads;
 }
 
 }  // namespace
@@ -522,13 +622,32 @@ int launch(const Kv4Args &ka, const DevPartition &p, cudaStream_t st)
 int dispatch_step4(const AttnArgs &a, const DevPartition &dp, const Partition &hp, float k_scale, float v_scale, void *stream,
                    const LaunchTracer &trace)
 {
-    const Kv4Args ka{a, k_scale, v_scale, dp.num_mma_items, dp.num_fma_items, hp.mma_bucket_off[1]};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (ka.n_mma + ka.n_fma > 0) {
-        const int r = trace({DEFT_K_PHASE1_KV4, 0, 0, 0, ka.n_mma + ka.n_fma, 0.f}, stream,
-                            [&] { return a.head_dim == 128 ? launch<128>(ka, dp, st) : launch<64>(ka, dp, st); });
+    Kv4Args ka{};
+    ka.a = a;
+    ka.k_scale = k_scale, ka.v_scale = v_scale;
+    ka.mma_narrow = hp.mma_bucket_off[1];
+    // One launch for each width, the widest first: 17 to 64 rows (the
+    // tensor-core list), 9 to 16, up to 8.
+    struct Part {
+        int32_t wide, first, n, nt;
+    };
+    const int32_t few = hp.fma_bucket_off[4], all = dp.num_fma_items;
+    const Part parts[3] = {{1, 0, dp.num_mma_items, 4}, {0, few, all - few, 2}, {0, 0, few, 1}};
+    for (const Part &x : parts) {
+        if (x.n == 0)
+            continue;
+        ka.wide = x.wide, ka.first = x.first, ka.n = x.n;
+        ka.heads = heads_per_cta(x.n, a.num_kv_heads, x.nt == 4 ? 2 : 1, x.nt == 4 ? 2 : x.nt == 2 ? 3 : 4);
+        const int r = trace({DEFT_K_PHASE1_KV4, 0, x.nt, 0, x.n, 0.f}, stream, [&] {
+            if (a.head_dim == 128)
+                return x.nt == 4 ? launch<128, 4>(ka, dp, st) : x.nt == 2 ? launch<128, 2>(ka, dp, st) : launch<128, 1>(ka, dp, st);
+            return x.nt == 4 ? launch<64, 4>(ka, dp, st) : x.nt == 2 ? launch<64, 2>(ka, dp, st) : launch<64, 1>(ka, dp, st);
+        });
         if (r)
             return r;
+        ka.a.wait_prior = 0;
+        ka.last = 1;
     }
     const int32_t nq = a.direct ? dp.num_merge_q : dp.num_queries;
     if (nq == 0)
