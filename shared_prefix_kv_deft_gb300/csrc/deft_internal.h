@@ -406,8 +406,22 @@ using LaunchTracer = std::function<int(const deft_trace_record &rec, void *strea
 // dp's host copy.  Returns a cudaError_t as int.
 int dispatch_step(AttnArgs a, const DevPartition &dp, const Partition &hp, bool use_mma, int32_t family,
                   void *stream, const LaunchTracer &trace);
-// The same over a 4-bit cache (k_pages / v_pages of `a` are its pools): one
-// phase-1 launch and the merge (phase1_kv4.cu).
+// A phase-1 launch over a 4-bit cache: items [first, first + n) of one of
+// the partition's two lists.
+struct Kv4Args {
+    AttnArgs a;                // k_pages, v_pages: the 4-bit pools
+    float k_scale, v_scale;
+    int32_t first, n;
+    int32_t wide;              // 1: of the tensor-core list
+    int32_t mma_narrow;        // tensor-core items below this have their row masks split at 16, not 32
+    int32_t heads;             // KV heads a CTA takes (1, 2 or 4)
+    int32_t head_groups;       // CTAs of an item
+    int32_t last;              // 1: not the step's first phase-1 launch
+};
+// Tensor-core items of at most 32 or 64 rows at head_dim 128.
+int launch_phase1_kv4_mma(const Kv4Args &ka, const DevPartition &p, int rows, void *stream);
+// dispatch_step over a 4-bit cache: phase-1 launches by width, and the merge
+// (phase1_kv4.cu).
 int dispatch_step4(const AttnArgs &a, const DevPartition &dp, const Partition &hp, float k_scale, float v_scale, void *stream,
                    const LaunchTracer &trace);
 // Row bucket of an item with `rows` rows: smallest b with rows <= 2^b.

@@ -38,20 +38,8 @@ namespace {
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kStages = 4;
 constexpr float kUp = 4.f, kLift = 11.f;
-constexpr double kFill = 2.0;
+constexpr double kFill = 1.0;
 constexpr unsigned kAll = 0xffffffffu;
-
-// One launch: items [first, first + n) of one of the partition's two lists.
-struct Kv4Args {
-    AttnArgs a;
-    float k_scale, v_scale;
-    int32_t first, n;
-    int32_t wide;              // 1: of the tensor-core list
-    int32_t mma_narrow;        // tensor-core items below this have their row masks split at 16, not 32
-    int32_t heads;             // KV heads a CTA takes (1, 2 or 4)
-    int32_t head_groups;       // CTAs of an item
-    int32_t last;              // 1: not the step's first phase-1 launch
-};
 
 template <int D, int NT>
 struct Cfg {
@@ -627,22 +615,25 @@ int dispatch_step4(const AttnArgs &a, const DevPartition &dp, const Partition &h
     ka.a = a;
     ka.k_scale = k_scale, ka.v_scale = v_scale;
     ka.mma_narrow = hp.mma_bucket_off[1];
-    // One launch for each width, the widest first: 17 to 64 rows (the
-    // tensor-core list), 9 to 16, up to 8.
+    // One launch for each width, the widest first: 33 to 64 and 16 to 32 rows
+    // (the tensor-core list; on mma.sync at head_dim 64), 9 to 15, up to 8.
     struct Part {
-        int32_t wide, first, n, nt;
+        int32_t wide, first, n, rows;
     };
-    const int32_t few = hp.fma_bucket_off[4], all = dp.num_fma_items;
-    const Part parts[3] = {{1, 0, dp.num_mma_items, 4}, {0, few, all - few, 2}, {0, 0, few, 1}};
+    const int32_t few = hp.fma_bucket_off[4], all = dp.num_fma_items, narrow = hp.mma_bucket_off[1], mma = dp.num_mma_items;
+    const bool tc = a.head_dim == 128;
+    const Part parts[4] = {{1, tc ? narrow : 0, tc ? mma - narrow : mma, 64}, {1, 0, tc ? narrow : 0, 32}, {0, few, all - few, 16}, {0, 0, few, 8}};
     for (const Part &x : parts) {
         if (x.n == 0)
             continue;
         ka.wide = x.wide, ka.first = x.first, ka.n = x.n;
-        ka.heads = heads_per_cta(x.n, a.num_kv_heads, x.nt == 4 ? 2 : 1, x.nt == 4 ? 2 : x.nt == 2 ? 3 : 4);
-        const int r = trace({DEFT_K_PHASE1_KV4, 0, x.nt, 0, x.n, 0.f}, stream, [&] {
+        ka.heads = heads_per_cta(x.n, a.num_kv_heads, x.rows > 16 ? 2 : 1, x.rows > 16 ? 2 : x.rows > 8 ? 3 : 4);
+        const int r = trace({DEFT_K_PHASE1_KV4, 0, x.rows, 0, x.n, 0.f}, stream, [&] {
+            if (x.wide)
+                return tc ? launch_phase1_kv4_mma(ka, dp, x.rows, stream) : launch<64, 4>(ka, dp, st);
             if (a.head_dim == 128)
-                return x.nt == 4 ? launch<128, 4>(ka, dp, st) : x.nt == 2 ? launch<128, 2>(ka, dp, st) : launch<128, 1>(ka, dp, st);
-            return x.nt == 4 ? launch<64, 4>(ka, dp, st) : x.nt == 2 ? launch<64, 2>(ka, dp, st) : launch<64, 1>(ka, dp, st);
+                return x.rows > 8 ? launch<128, 2>(ka, dp, st) : launch<128, 1>(ka, dp, st);
+            return x.rows > 8 ? launch<64, 2>(ka, dp, st) : launch<64, 1>(ka, dp, st);
         });
         if (r)
             return r;

@@ -1,0 +1,497 @@
+// phase1_kv4_mma.cu -- phase-1 partial attention over a 4-bit KV cache on
+// tcgen05 tensor cores, for work items with 16 to 64 rows and head_dim 128
+// (the other units: phase1_kv4.cu, with the mathematics that both share).
+//
+// Tokens on the MMA's M, rows on its N, as in the bf16 kernel:
+//     S^T[128 tok x RP]  = K_tile . Q^T            (TMEM, fp32)
+//     O^T[128 d   x RP] += V_tile^T . P^T          (TMEM, fp32)
+// RP = 32 or 64.  The cache's 4 bits become fp16 in shared memory once for
+// all rows: a thread takes half a row of K and of V of every tile (32 bytes
+// and four scales each, fetched a tile ahead straight into registers), 128
+// rows a tile from wherever the chunk's tokens lie, none beside them.  At 64
+// rows a token costs a thread its unpacking (some 90 instructions for 64
+// elements of K and as many of V) and 32 exponentials; mma.sync, at an eighth
+// of the tensor rate and with every fragment unpacked again for each 32 rows,
+// took four times as long.
+//
+// A CTA of eight warps takes one unit, and two CTAs share an SM: one unpacks
+// and exponentiates while the other waits.  All warps do the same work: for
+// tile t they unpack V(t) while S(t) runs, then turn S(t) into P(t) (a thread
+// a token and half the columns), unpack K(t + 1), meet at one barrier, and one
+// thread issues P(t).V(t) and S(t + 1).  Column maxima are raised only when a
+// logit passes one by more than 2^4 (a vote); sums of the weights stay with
+// the threads until the end.  Every wait is bounded.
+#include "kv4.cuh"
+#include "merge.cuh"
+#include "tcgen05.cuh"
+
+namespace deft {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kD = 128, kTile = 128;
+constexpr float kUp = 4.f, kLift = 11.f;
+constexpr unsigned kAll = 0xffffffffu;
+constexpr uint32_t kRowGroup = 2048;    // 8 tokens x 128 dims of fp16: two 1 KB swizzle atoms (d halves)
+constexpr uint32_t kTileBytes = 16 * kRowGroup;
+constexpr uint32_t kTmemCols = 128;     // S at 0, O at 64
+
+template <int RP>
+struct Cfg {
+    static constexpr uint32_t k = 0;                            // [16 groups][d half][8 tok][128 B]
+    static constexpr uint32_t v = k + kTileBytes;
+    static constexpr uint32_t p = v + kTileBytes;               // [128 tok][128 B]
+    static constexpr uint32_t q_half = RP * 128;
+    static constexpr uint32_t q = p + kTile * 128;              // [d half][RP rows][128 B]
+    static constexpr uint32_t col = q + 2 * q_half;             // [RP] (factor, maximum - lift)
+    static constexpr uint32_t red = col + RP * 8;               // [4 warps][RP]
+    static constexpr uint32_t seg = red + 4 * RP * 4;           // [256] position, page, begin; [256] mask (8 B)
+    static constexpr uint32_t misc = seg + kMaxSegsPerChunk * 20;
+    static constexpr uint32_t bars = misc + 16;                 // S, O
+    static constexpr uint32_t total = bars + 16;
+    static constexpr uint32_t alloc = total + 1024;
+    static_assert(q % 1024 == 0 && p % 1024 == 0, "128-byte-swizzle atoms");
+    static_assert(2 * (alloc + 1024) <= 228 * 1024, "two CTAs an SM");
+};
+
+// kind::f16 with fp16 A and B, fp32 D.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_mn)
+{
+    return tc::idesc_bf16(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
+}
+
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi)
+{
+    const __half2 r = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+__device__ __forceinline__ float pow2(int e)   // -126 <= e <= 127
+{
+    return __int_as_float((127 + e) << 23);
+}
+
+// Half a token's row: 64 elements and their scales.
+struct HalfRow {
+    uint4 w[2];
+    uint32_t s;
+    __device__ __forceinline__ void zero()
+    {
+        w[0] = w[1] = make_uint4(0, 0, 0, 0);
+        s = 0;
+    }
+    __device__ __forceinline__ void load(const uint8_t *page, int tok, int half)
+    {
+        using P = kv4::Page<kD>;
+        const uint4 *src = reinterpret_cast<const uint4 *>(page + tok * P::kRow) + 2 * half;
+        w[0] = __ldg(src);
+        w[1] = __ldg(src + 1);
+        s = __ldg(reinterpret_cast<const uint32_t *>(page + P::kScales + tok * P::kScaleRow) + half);
+    }
+    // As fp16 into the swizzled row at `dst` (row r of its group of eight).
+    __device__ __forceinline__ void unpack(uint8_t *dst, int r) const
+    {
+        const uint32_t x[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+        const uint32_t a = kv4::scales2(s), b = kv4::scales2(s >> 16);
+        const uint32_t sc[4] = {__byte_perm(a, 0, 0x1010), __byte_perm(a, 0, 0x3232), __byte_perm(b, 0, 0x1010),
+                                __byte_perm(b, 0, 0x3232)};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint32_t h[4];
+            kv4::unpack8(x[i], h);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                h[k] = kv4::hmul2(h[k], sc[i / 2]);
+            *reinterpret_cast<uint4 *>(dst + ((i ^ r) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+    }
+};
+
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[N])
+{
+    static_assert(N == 16 || N == 32, "columns");
+    if constexpr (N == 32)
+        tc::tmem_ld32(addr, v);
+    else
+        tc::tmem_ld16(addr, v);
+}
+template <int N>
+__device__ __forceinline__ void tmem_store(uint32_t addr, const float (&v)[N])
+{
+    if constexpr (N == 32)
+        tc::tmem_st32(addr, v);
+    else
+        tc::tmem_st16(addr, v);
+}
+
+// Column i's reduction over the warp's lanes, to lane i (i + 16 as well for
+// 16 columns).
+template <bool kMax, int N>
+__device__ __forceinline__ float reduce_columns(const float (&x)[N], int lane)
+{
+    float v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        v[i] = x[i];
+    if constexpr (N == 16) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float y = __shfl_xor_sync(kAll, v[i], 16);
+            v[i] = kMax ? fmaxf(v[i], y) : v[i] + y;
+        }
+    }
+#pragma unroll
+    for (int o = N / 2; o >= 1; o >>= 1) {
+        const bool upper = (lane & o) != 0;
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const float send = upper ? v[i] : v[i + o], keep = upper ? v[i + o] : v[i];
+            const float y = __shfl_xor_sync(kAll, send, o);
+            v[i] = kMax ? fmaxf(keep, y) : keep + y;
+        }
+    }
+    return v[0];
+}
+
+template <int RP>
+__global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka, DevPartition p)
+{
+    using C = Cfg<RP>;
+    using P = kv4::Page<kD>;
+    constexpr int NC = RP / 2;      // columns of a thread
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t *smem = smem_raw + (base - raw);
+    const AttnArgs &a = ka.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int half = warp >> 2, row = (warp & 3) * 32 + lane;      // tile row, half of its dims and of the columns
+    float2 *col = reinterpret_cast<float2 *>(smem + C::col);
+    float *red = reinterpret_cast<float *>(smem + C::red);
+    int32_t *seg_pos = reinterpret_cast<int32_t *>(smem + C::seg), *seg_page = seg_pos + kMaxSegsPerChunk,
+            *seg_begin = seg_page + kMaxSegsPerChunk;
+    uint64_t *seg_mask = reinterpret_cast<uint64_t *>(seg_begin + kMaxSegsPerChunk);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::misc);
+    const uint32_t bar_s = base + C::bars, bar_o = bar_s + 8;
+
+    if (warp == 0) {
+        tc::tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+        tc::tmem_relinquish();
+    }
+    if (tid == 0) {
+        tc::mbar_init(bar_s, 1);
+        tc::mbar_init(bar_o, 1);
+        tc::fence_mbar_init();
+    }
+    if (a.wait_prior)
+        grid_dep_wait();
+    grid_dep_launch();
+
+    // ---- the unit ----
+    const int Hkv = a.num_kv_heads, Hq = a.num_q_heads, G = a.gqa_group;
+    const int it = blockIdx.x / Hkv, h = blockIdx.x - it * Hkv, item = ka.first + it;
+    const int32_t *triple = p.mma_items + 3 * (size_t)item;
+    const int c = triple[0], qb = triple[1], R = (triple[2] - qb) * G;
+    const int rm0 = p.mma_rmask_off[item];
+    const int cq0 = p.chunk_q_off[c] + qb, T = p.chunk_tokens[c];
+    const int sb = p.chunk_seg_off[c], nseg = p.chunk_seg_off[c + 1] - sb;
+    for (int s = tid; s < nseg; s += kThreads) {
+        const int tb = p.seg_tok_begin[sb + s];
+        seg_pos[s] = p.seg_chunk_pos[sb + s];
+        seg_page[s] = a.node_page_off[p.seg_node[sb + s]] + tb / kPageSize;
+        seg_begin[s] = tb % kPageSize;
+        const uint4 w = reinterpret_cast<const uint4 *>(p.mma_rmask)[rm0 + s];
+        seg_mask[s] = (uint64_t)w.x | (uint64_t)w.z << (item < ka.mma_narrow ? 16 : 32);
+    }
+    // ---- Q^T: bf16 -> fp16 times a power of two for each row ----
+    {
+        constexpr int TPR = kThreads / RP, DT = kD / TPR;   // threads of a row, dims of a thread
+        const int r = tid / TPR, part = tid % TPR;
+        uint32_t w[DT / 2];
+#pragma unroll
+        for (int i = 0; i < DT / 2; ++i)
+            w[i] = 0u;
+        if (r < R) {
+            const int k = r / G;
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
+                                                               ((size_t)p.chunk_q[cq0 + k] * Hq + h * G + (r - k * G)) * kD + part * DT);
+#pragma unroll
+            for (int i = 0; i < DT / 8; ++i) {
+                const uint4 x = src[i];
+                w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+            }
+        }
+        float big = 0.f;            // the row's largest finite magnitude
+#pragma unroll
+        for (int i = 0; i < DT / 2; ++i) {
+            const float2 x = bf16x2_to_float2(w[i] & 0x7fff7fffu);
+            big = x.x < INFINITY ? fmaxf(big, x.x) : big;
+            big = x.y < INFINITY ? fmaxf(big, x.y) : big;
+        }
+#pragma unroll
+        for (int o = 1; o < TPR; o <<= 1)
+            big = fmaxf(big, __shfl_xor_sync(kAll, big, o));
+        // 2^e in two factors: e reaches from -113 to 147.
+        const int e = big > 0.f ? 14 - ilogbf(big) : 0, e1 = e / 2, e2 = e - e1;
+        const float up1 = pow2(e1), up2 = pow2(e2);
+#pragma unroll
+        for (int i = 0; i < DT / 8; ++i) {
+            uint32_t x[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 y = bf16x2_to_float2(w[4 * i + j]);
+                x[j] = f16x2(y.x * up1 * up2, y.y * up1 * up2);
+            }
+            const int chunk = part * (DT / 8) + i;          // of the row's sixteen
+            *reinterpret_cast<uint4 *>(smem + C::q + (chunk >> 3) * C::q_half + r * 128 + (((chunk & 7) ^ (r & 7)) << 4)) =
+                make_uint4(x[0], x[1], x[2], x[3]);
+        }
+        // A column of no row has weights of 0: 2^(0 * S - inf).
+        if (part == 0)
+            col[r] = r < R ? make_float2(a.scale_log2 * pow2(-e1) * ka.k_scale * pow2(-e2), -INFINITY) : make_float2(0.f, INFINITY);
+    }
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t tm_s = tmem + ((uint32_t)(warp & 3) << 21) + half * NC, tm_o = tm_s + 64;
+
+    // ---- rows of the chunk ----
+    const int ntiles = (T + kTile - 1) / kTile;
+    const uint8_t *k4 = static_cast<const uint8_t *>(a.k_pages) + (size_t)h * P::kBytes;
+    const uint8_t *v4 = static_cast<const uint8_t *>(a.v_pages) + (size_t)h * P::kBytes;
+    const size_t page_step = (size_t)Hkv * P::kBytes;
+    struct Where {
+        int page, tok, seg;     // page -1: no token
+    };
+    auto where = [&](int t) {
+        Where w{-1, 0, 0};
+        const int x = t * kTile + row;
+        if (x < T) {
+            int hi = nseg;
+            while (hi - w.seg > 1) {
+                const int mid = (w.seg + hi) >> 1;
+                if (seg_pos[mid] <= x)
+                    w.seg = mid;
+                else
+                    hi = mid;
+            }
+            const int j = x - seg_pos[w.seg] + seg_begin[w.seg];
+            w.page = a.page_id[seg_page[w.seg] + j / kPageSize];
+            w.tok = j % kPageSize;
+        }
+        return w;
+    };
+    auto load = [&](HalfRow &x, const uint8_t *pool, const Where &w) {
+        if (w.page >= 0)
+            x.load(pool + (size_t)w.page * page_step, w.tok, half);
+        else
+            x.zero();
+    };
+    uint8_t *row_k = smem + C::k + (row >> 3) * kRowGroup + half * 1024 + (row & 7) * 128;
+    uint8_t *row_v = row_k + (C::v - C::k);
+    const uint32_t row_bits = R >= RP ? 0xffffffffu >> (32 - NC)
+                                      : (uint32_t)((((1ull << R) - 1) >> (half * NC)) & (0xffffffffu >> (32 - NC)));
+
+    float l[NC];
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+        l[i] = 0.f;
+    bool ok = true;
+    HalfRow kr, vr;
+    Where w0 = where(0), w1 = where(1), w2{-1, 0, 0};      // of tiles t, t + 1, t + 2
+    load(kr, k4, w0);
+    load(vr, v4, w0);
+    kr.unpack(row_k, row & 7);
+    load(kr, k4, w1);
+    w2 = where(2);
+    tc::fence_proxy_async();
+    __syncthreads();
+    constexpr uint32_t idesc_s = idesc_f16(kTile, RP, 0, 0), idesc_o = idesc_f16(kD, RP, 1, 1);
+    auto issue_s = [&]() {
+        const uint64_t dk = tc::smem_desc(base + C::k, 16, kRowGroup), dq = tc::smem_desc(base + C::q, 16, 1024);
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+            tc::mma_bf16(tmem, dk + (((s >> 2) * 1024 + (s & 3) * 32) >> 4), dq + (((s >> 2) * C::q_half + (s & 3) * 32) >> 4),
+                         idesc_s, s > 0 ? 1u : 0u);
+        tc::mma_commit(bar_s);
+    };
+    if (tid == 0)
+        issue_s();
+    for (int t = 0; t < ntiles; ++t) {
+        // ---- V(t), once P(t - 1).V(t - 1) is done; meanwhile S(t) runs ----
+        if (t > 0 && ok)
+            ok = tc::mbar_wait(bar_o, (t - 1) & 1);
+        vr.unpack(row_v, row & 7);
+        load(vr, v4, w1);
+        // ---- P(t) ----
+        if (ok)
+            ok = tc::mbar_wait(bar_s, t & 1);
+        tc::fence_after_sync();
+        __syncwarp();
+        float x[NC];
+        tmem_load<NC>(tm_s, x);
+        uint32_t seen = 0;
+        if (t * kTile + row < T)
+            seen = (uint32_t)(seg_mask[w0.seg] >> (half * NC)) & row_bits;
+        const bool whole = __all_sync(kAll, seen == row_bits);
+        const float4 *cf = reinterpret_cast<const float4 *>(col + half * NC);
+        bool grow = false;
+        auto logits = [&]() {       // S -> exponents of the weights
+#pragma unroll
+            for (int i = 0; i < NC; i += 2) {
+                const float4 f = cf[i / 2];
+                x[i] = fmaf(x[i], f.x, -f.y);
+                x[i + 1] = fmaf(x[i + 1], f.z, -f.w);
+            }
+            if (!whole) {
+#pragma unroll
+                for (int i = 0; i < NC; ++i)
+                    x[i] = (seen >> i) & 1u ? x[i] : -INFINITY;
+            }
+        };
+        logits();
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+            grow |= x[i] > kLift + kUp;
+        if (__syncthreads_or(grow)) {
+            // Maxima over the tile, from S again.
+            tmem_load<NC>(tm_s, x);
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+                x[i] = (seen >> i) & 1u ? x[i] * col[half * NC + i].x : -INFINITY;
+            const float top = reduce_columns<true, NC>(x, lane);
+            if (lane < NC)
+                red[(warp & 3) * RP + half * NC + lane] = top;
+            __syncthreads();
+            float now = 0.f, alpha = 1.f;
+            if (tid < RP) {
+                const float was = col[tid].y;       // maximum - lift; +inf: no row
+                const float big = fmaxf(fmaxf(red[tid], red[RP + tid]), fmaxf(red[2 * RP + tid], red[3 * RP + tid])) - kLift;
+                now = was == INFINITY ? was : fmaxf(was, big);
+                alpha = now == was ? 1.f : tc::ex2(was - now);
+            }
+            __syncthreads();
+            if (tid < RP) {
+                col[tid].y = now;
+                red[tid] = alpha;
+            }
+            __syncthreads();
+            const float *al = red + half * NC;
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+                l[i] *= al[i];
+            if (t > 0) {
+                tmem_load<NC>(tm_o, x);
+#pragma unroll
+                for (int i = 0; i < NC; ++i)
+                    x[i] *= al[i];
+                tmem_store<NC>(tm_o, x);
+            }
+            tmem_load<NC>(tm_s, x);
+            logits();
+        }
+        uint8_t *dst = smem + C::p + row * 128;
+#pragma unroll
+        for (int i = 0; i < NC; i += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float y0 = tc::ex2(x[i + 2 * j]), y1 = tc::ex2(x[i + 2 * j + 1]);
+                l[i + 2 * j] += y0;
+                l[i + 2 * j + 1] += y1;
+                w[j] = f16x2(y0, y1);
+            }
+            *reinterpret_cast<uint4 *>(dst + ((((half * NC + i) >> 3) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        // ---- K(t + 1) ----
+        if (t + 1 < ntiles)
+            kr.unpack(row_k, row & 7);
+        load(kr, k4, w2);
+        w0 = w1;
+        w1 = w2;
+        w2 = where(t + 3);
+        tc::fence_proxy_async();
+        tc::fence_before_sync();
+        __syncthreads();
+        if (tid == 0) {
+            tc::fence_after_sync();
+            const uint64_t dv = tc::smem_desc(base + C::v, 1024, kRowGroup), dp = tc::smem_desc(base + C::p, kTile * 128, 1024);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                tc::mma_bf16(tmem + 64, dv + ((k * 2 * kRowGroup) >> 4), dp + ((k * 2048) >> 4), idesc_o, t > 0 || k > 0 ? 1u : 0u);
+            tc::mma_commit(bar_o);
+            if (t + 1 < ntiles)
+                issue_s();
+        }
+    }
+    // ---- out ----
+    if (ok)
+        ok = tc::mbar_wait(bar_o, (ntiles - 1) & 1);
+    tc::fence_after_sync();
+    {
+        const float sum = reduce_columns<false, NC>(l, lane);
+        if (lane < NC)
+            red[(warp & 3) * RP + half * NC + lane] = sum;
+    }
+    const bool failed = __syncthreads_or(!ok);
+    if (failed && tid == 0)
+        report_failure(p.status, 402);
+    if (tid < RP && tid < R) {
+        float sum = (red[tid] + red[RP + tid]) + (red[2 * RP + tid] + red[3 * RP + tid]);
+        if (failed)
+            sum = __int_as_float(0x7fffffff);
+        // sum is 0 where the row attends no token, NaN where a logit was.
+        const float lse2 = sum == 0.f ? -INFINITY : col[tid].y + log2f(sum);
+        const int k = tid / G;
+        // (+inf, so that the merge's weight for it is NaN and not 0)
+        a.lse_part[(size_t)(cq0 + k) * Hq + h * G + (tid - k * G)] = lse2 == lse2 ? lse2 : INFINITY;
+        col[tid].x = sum == 0.f ? 0.f : ka.v_scale / sum;
+    }
+    __syncwarp();
+    float o[NC];
+    tmem_load<NC>(tm_o, o);
+    __syncthreads();
+    {
+        int r = half * NC;
+        int k = r / G, j = r - k * G;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            if (r + i < R)
+                a.o_part[((size_t)(cq0 + k) * Hq + h * G + j) * kD + row] = o[i] * col[r + i].x;
+            if (++j == G) {
+                j = 0;
+                ++k;
+            }
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 0)
+        tc::tmem_dealloc(tmem, kTmemCols);
+    if (ka.last && blockIdx.x == gridDim.x - 1)
+        grid_dep_wait();
+}
+
+template <int RP>
+int launch(const Kv4Args &ka, const DevPartition &p, cudaStream_t st)
+{
+    const int64_t ctas = (int64_t)ka.n * ka.a.num_kv_heads;
+    if (ctas > INT32_MAX)
+        return (int)cudaErrorInvalidConfiguration;
+    auto *kernel = phase1_kv4_mma_kernel<RP>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<RP>::alloc);
+    if (e != cudaSuccess)
+        return (int)e;
+    return (int)launch_dependent(kernel, dim3((unsigned)ctas), dim3(kThreads), Cfg<RP>::alloc, st, ka, p);
+}
+
+}  // namespace
+
+int launch_phase1_kv4_mma(const Kv4Args &ka, const DevPartition &p, int rows, void *stream)
+{
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    return rows <= 32 ? launch<32>(ka, p, st) : launch<64>(ka, p, st);
+}
+
+}  // namespace deft
