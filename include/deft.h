@@ -658,8 +658,8 @@ int deft_kv_unpack4(const void *k4_pages, const void *v4_pages, float k_scale, f
  *     they hold.  A block whose scale is NaN (written from a NaN) counts as
  *     NaN: in K for the rows that attend its token, in V for every row of the
  *     work item that reads its page.  q may hold anything: a row with a logit
- *     that is NaN or +infinity has NaN in out, and lse NaN or -infinity; no
- *     other row is affected.  page_id and node_page_off are trusted, as in
+ *     that is NaN or +infinity has NaN in out and lse; no other row is
+ *     affected.  page_id and node_page_off are trusted, as in
  *     deft_tree_attn (page_id may be NULL where no path has a token).
  * out 16-byte aligned (DEFT_EINVAL).  Several steps of one plan may run at
  * the same time, each with its own outputs and workspace (this call does not use the plan's work queues).  A

@@ -592,7 +592,9 @@ int deft_tree_attn4(const void *q, const void *k4_pages, const void *v4_pages, f
     };
     if (deft::order_mergeonly_step(*st.hp, stream))
         return DEFT_ECUDA;
-    return deft::dispatch_step4(st.a, *st.dp, *st.hp, k_scale, v_scale, stream, trace) ? DEFT_ECUDA : DEFT_OK;
+    return deft::dispatch_step4(st.a, *st.dp, *st.hp, k_scale, v_scale, plan->stats.max_slots_per_query, stream, trace)
+               ? DEFT_ECUDA
+               : DEFT_OK;
 }
 
 int deft_naive_attn(const void *q, const void *k_pages, const void *v_pages,

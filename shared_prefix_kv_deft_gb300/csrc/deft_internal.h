@@ -422,8 +422,9 @@ struct Kv4Args {
 int launch_phase1_kv4_mma(const Kv4Args &ka, const DevPartition &p, int rows, void *stream);
 // dispatch_step over a 4-bit cache: phase-1 launches by width, and the merge
 // (phase1_kv4.cu).
-int dispatch_step4(const AttnArgs &a, const DevPartition &dp, const Partition &hp, float k_scale, float v_scale, void *stream,
-                   const LaunchTracer &trace);
+// max_slots: the most partials a query has.
+int dispatch_step4(const AttnArgs &a, const DevPartition &dp, const Partition &hp, float k_scale, float v_scale,
+                   int32_t max_slots, void *stream, const LaunchTracer &trace);
 // Row bucket of an item with `rows` rows: smallest b with rows <= 2^b.
 inline int row_bucket(int rows) { return rows <= 1 ? 0 : rows <= 2 ? 1 : rows <= 4 ? 2 : rows <= 8 ? 3 : 4; }
 // Rows per softmax warpgroup of a tensor-core item with `rows` rows (two

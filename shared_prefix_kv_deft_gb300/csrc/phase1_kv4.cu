@@ -53,7 +53,7 @@ struct Cfg {
     static constexpr uint32_t seg = q + (kQSmem ? kWarps * NT * (D / 32) * 512 : 0);
     static constexpr uint32_t bars = seg + kMaxSegsPerChunk * 24 + 8;     // [256] mask (8 B), page, begin, len; [257] first slice
     static constexpr uint32_t total = bars + kWarps * kStages * 8;
-    static constexpr int kCtas = NT == 1 ? 4 : NT == 2 ? 3 : 2;           // that an SM is meant to hold
+    static constexpr int kCtas = NT == 1 ? 5 : NT == 2 ? 3 : 2;           // that an SM is meant to hold
     static_assert(kStage % 16 == 0 && q % 16 == 0 && seg % 8 == 0 && bars % 8 == 0, "alignment");
     static_assert((total + 1024) * kCtas <= 228 * 1024, "shared memory of an SM");
 };
@@ -83,6 +83,34 @@ __device__ __forceinline__ uint32_t f16x2(float lo, float hi)
 __device__ __forceinline__ float pow2(int e)   // -126 <= e <= 127
 {
     return __int_as_float((127 + e) << 23);
+}
+
+// The exponent of the power of two that puts a row's largest finite
+// magnitude in [2^14, 2^15): N pairs of bf16 in each of the row's LANES
+// neighbouring lanes (-113 to 147; 0 for a row of zeros).
+template <int N, int LANES>
+__device__ __forceinline__ int row_exponent(const uint32_t (&w)[N])
+{
+    uint32_t big = 0;               // magnitudes order as integers
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        big = __vmaxu2(big, w[i] & 0x7fff7fffu);
+    big = max(big & 0xffffu, big >> 16);
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1)
+        big = max(big, __shfl_xor_sync(kAll, big, o));
+    if (__any_sync(kAll, big >= 0x7f80u)) {     // infinities, NaN: without them
+        big = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint32_t lo = w[i] & 0x7fffu, hi = w[i] >> 16 & 0x7fffu;
+            big = max(big, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+        }
+#pragma unroll
+        for (int o = 1; o < LANES; o <<= 1)
+            big = max(big, __shfl_xor_sync(kAll, big, o));
+    }
+    return big == 0 ? 0 : big >= 0x80u ? 14 + 127 - (int)(big >> 7) : 14 + 133 - (31 - __clz((int)big));
 }
 
 // A slice: the tokens of one page that belong to one segment.  `desc` holds
@@ -194,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
     const uint8_t *k4 = static_cast<const uint8_t *>(a.k_pages), *v4 = static_cast<const uint8_t *>(a.v_pages);
     const uint64_t pol = tc::l2_kv_policy(false);
     const uint32_t ring = base + warp * kStages * C::kStage;
-    auto get_slice = [&](int i, int &page, uint32_t &desc) {
+    auto get_slice = [&](int i, size_t &at, uint32_t &desc) {
         if (i >= mine)
             return;
         const int x = ts + i * TS;
@@ -212,26 +240,25 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
             j = x - seg_first[seg];
             pg = seg_page[seg], begin = seg_begin[seg], len = seg_len[seg], mask = seg_mask[seg];
         }
-        page = a.page_id[pg + j];
+        at = ((size_t)a.page_id[pg + j] * Hkv + h) * P::kBytes;
         const int lo = max(0, begin - j * kPageSize), hi = min(kPageSize, begin + len - j * kPageSize);
         desc = slice_desc(seg, lo, hi, hi - lo == kPageSize && ((uint32_t)(mask >> row0) & my_rows) == my_rows);
     };
-    int next_page = 0;
+    size_t next_at = 0;
     uint32_t cur = 0, next = 0;     // the batch in hand, and the one whose copies go out
     int next_batch = 0;
-    get_slice(lane, next_page, next);
+    get_slice(lane, next_at, next);
     cur = next;
     auto issue = [&](int i) {
         if (i / 32 != next_batch) {
             next_batch = i / 32;
-            get_slice(i + lane, next_page, next);
+            get_slice(i + lane, next_at, next);
         }
         if (lane == (i & 31)) {
             const uint32_t dst = ring + (i % kStages) * C::kStage, bar = bars + (i % kStages) * 8;
-            const size_t at = ((size_t)next_page * Hkv + h) * P::kBytes;
             tc::mbar_arrive_expect_tx(bar, C::kStage);
-            tc::bulk_load(dst, k4 + at, P::kBytes, bar, pol);
-            tc::bulk_load(dst + P::kBytes, v4 + at, P::kBytes, bar, pol);
+            tc::bulk_load(dst, k4 + next_at, P::kBytes, bar, pol);
+            tc::bulk_load(dst + P::kBytes, v4 + next_at, P::kBytes, bar, pol);
         }
     };
     __syncwarp();   // the barriers are there
@@ -261,25 +288,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
                 w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
             }
         }
-        float big = 0.f;            // the row's largest finite magnitude
-#pragma unroll
-        for (int i = 0; i < KW * 4; ++i) {
-            const float2 v = bf16x2_to_float2(w[i] & 0x7fff7fffu);
-            big = v.x < INFINITY ? fmaxf(big, v.x) : big;
-            big = v.y < INFINITY ? fmaxf(big, v.y) : big;
-        }
-        big = fmaxf(big, __shfl_xor_sync(kAll, big, 1));
-        big = fmaxf(big, __shfl_xor_sync(kAll, big, 2));
-        // 2^e in two factors: e reaches from -113 to 147.
-        const int e = big > 0.f ? 14 - ilogbf(big) : 0, e1 = e / 2, e2 = e - e1;
-        const float up1 = pow2(e1), up2 = pow2(e2);
-        const float fr = a.scale_log2 * pow2(-e1) * ka.k_scale * pow2(-e2);
+        // 2^e, in two factors for rows below 2^-112 (e reaches 147).
+        const int e = row_exponent<KW * 4, 4>(w), e1 = min(e, 126), e2 = e - e1;
+        const float up = pow2(e1), fr = a.scale_log2 * pow2(-e1) * ka.k_scale * pow2(-e2);
         f[n][0] = __shfl_sync(kAll, fr, 8 * t);
         f[n][1] = __shfl_sync(kAll, fr, 8 * t + 4);
+        if (e2 == 0) {
 #pragma unroll
-        for (int i = 0; i < KW * 4; ++i) {
-            const float2 v = bf16x2_to_float2(w[i]);
-            w[i] = f16x2(v.x * up1 * up2, v.y * up1 * up2);
+            for (int i = 0; i < KW * 4; ++i) {
+                const float2 v = bf16x2_to_float2(w[i]);
+                w[i] = f16x2(v.x * up, v.y * up);
+            }
+        } else {
+            const float up2 = pow2(e2);
+#pragma unroll
+            for (int i = 0; i < KW * 4; ++i) {
+                const float2 v = bf16x2_to_float2(w[i]);
+                w[i] = f16x2(v.x * up * up2, v.y * up * up2);
+            }
         }
         if constexpr (C::kQSmem) {
 #pragma unroll
@@ -293,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
     }
 
     float o[D / 16][NT][4];
-    float m[NT][2], l[NT][2];
+    float m[NT][2], l[NT][2];       // maxima less kLift, sums
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -367,13 +393,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
             }
         }
         // ---- softmax ----
-        bool grow = false;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                s[n][j] *= f[n][j & 1];
+        // The weights' exponents: s f - m + kLift; above kLift + kUp (an m of
+        // -inf, as at the start, among them) the maxima are raised first.
         const int lo = desc >> 8 & 255, hi = desc & 255;
+        float x[NT][4];
+        bool grow = false;
+        auto exponents = [&]() {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    x[n][j] = fmaf(s[n][j], f[n][j & 1], -m[n][j & 1]);
+        };
+        exponents();
         if (!whole) {
             const uint32_t rows = (uint32_t)((nseg > 1 ? seg_mask[desc >> 16 & 0x7fff] : mask0) >> row0);
 #pragma unroll
@@ -381,27 +413,29 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int tok = kg + (j >> 1) * 8, row = 8 * n + 2 * t + (j & 1);
-                    if (tok < lo || tok >= hi || !((rows >> row) & 1))
-                        s[n][j] = -INFINITY;
+                    if (tok < lo || tok >= hi || !((rows >> row) & 1)) {
+                        s[n][j] = -INFINITY;    // (f is positive)
+                        x[n][j] = -INFINITY;
+                    }
                 }
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                grow |= s[n][j] > m[n][j & 1] + kUp;
+                grow |= x[n][j] > kLift + kUp;
         if (__any_sync(kAll, grow)) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    float x = fmaxf(s[n][j], s[n][j + 2]);
-                    x = fmaxf(x, __shfl_xor_sync(kAll, x, 4));
-                    x = fmaxf(x, __shfl_xor_sync(kAll, x, 8));
-                    x = fmaxf(x, __shfl_xor_sync(kAll, x, 16));
-                    x = fmaxf(m[n][j], x);
-                    const float alpha = x == -INFINITY ? 1.f : tc::ex2(m[n][j] - x);
-                    m[n][j] = x;
+                    float y = fmaxf(s[n][j] * f[n][j], s[n][j + 2] * f[n][j]);
+                    y = fmaxf(y, __shfl_xor_sync(kAll, y, 4));
+                    y = fmaxf(y, __shfl_xor_sync(kAll, y, 8));
+                    y = fmaxf(y, __shfl_xor_sync(kAll, y, 16));
+                    y = fmaxf(m[n][j], y - kLift);
+                    const float alpha = y == m[n][j] ? 1.f : tc::ex2(m[n][j] - y);
+                    m[n][j] = y;
                     l[n][j] *= alpha;
 #pragma unroll
                     for (int d = 0; d < D / 16; ++d) {
@@ -410,13 +444,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
                     }
                 }
             }
+            exponents();
+            // A masked place, also in a row whose maximum is still -inf.
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    x[n][j] = s[n][j] == -INFINITY ? -INFINITY : x[n][j];
         }
         uint32_t pb[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0] - kLift, m1 = m[n][1] == -INFINITY ? 0.f : m[n][1] - kLift;
-            const float p0 = tc::ex2(s[n][0] - m0), p1 = tc::ex2(s[n][1] - m1);
-            const float p2 = tc::ex2(s[n][2] - m0), p3 = tc::ex2(s[n][3] - m1);
+            const float p0 = tc::ex2(x[n][0]), p1 = tc::ex2(x[n][1]), p2 = tc::ex2(x[n][2]), p3 = tc::ex2(x[n][3]);
             l[n][0] += p0 + p2;
             l[n][1] += p1 + p3;
             pb[n][0] = transpose8(f16x2(p0, p1));
@@ -543,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
                     continue;
                 // sum is 0 where the row attends no token, NaN where a logit was.
                 const float inv = sum == 0.f ? 0.f : ka.v_scale / sum;
-                const float lse2 = sum == 0.f ? -INFINITY : m[n][j] + log2f(sum) - kLift;
+                const float lse2 = sum == 0.f ? -INFINITY : m[n][j] + log2f(sum);
                 const int k = r / G, head = h * G + (r - k * G);
                 const bool straight = r < 32 && ((direct >> r) & 1u);
                 const size_t row = (size_t)(straight ? p.chunk_q[cq0 + k] : cq0 + k) * Hq + head;
@@ -605,10 +644,142 @@ int heads_per_cta(int64_t items, int32_t hkv, int groups, int ctas_per_sm)
     return heads;
 }
 
+// The merge of each row's partials by their lse, as phase2.cu's, with W warps
+// a row: a path of many chunks (33 of 256 tokens in 8192) is read by four
+// warps at once instead of in a chain of 16 loads and then one after another
+// (measured on 64 requests of 64 to 8192 tokens).  Also, lse is NaN
+// where a logit was.
+template <int D, int W>
+__global__ void __launch_bounds__(kThreads) merge4_kernel(AttnArgs a, const int32_t *__restrict__ q_slot_off,
+                                                          const int32_t *__restrict__ q_slot,
+                                                          const int32_t *__restrict__ queries, int32_t nq)
+{
+    constexpr int E = D / 32, KP = 8;     // elements of a lane, partials loaded at once
+    __shared__ float st[kWarps][D + 2];
+    grid_dep_launch();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % W;
+    const int64_t job = (int64_t)blockIdx.x * (kWarps / W) + warp / W;
+    const bool live = job < (int64_t)nq * a.num_q_heads;
+    const int i = live ? (int)(job / a.num_q_heads) : 0, h = (int)(job - (int64_t)i * a.num_q_heads);
+    const int q = queries ? queries[i] : i;
+    const int s0 = q_slot_off[q], n = live ? q_slot_off[q + 1] - s0 : 0;
+    float M = -INFINITY, sum = 0.f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        acc[e] = 0.f;
+    bool waited = false;
+    for (int b = part; b < n; b += 32 * W) {
+        const int k = b + lane * W, here = min(32, (n - b + W - 1) / W);
+        size_t row = 0;
+        if (k < n)
+            row = (size_t)q_slot[s0 + k] * a.num_q_heads + h;
+        if (!waited)
+            grid_dep_wait();       // the phase-1 launches have completed
+        waited = true;
+        const float l = k < n ? a.lse_part[row] : -INFINITY;
+        const float top = fmaxf(M, warp_max(l));
+        if (top == -INFINITY)
+            continue;              // partials that attended nothing
+        const float keep = tc::ex2(M - top), w = k < n ? tc::ex2(l - top) : 0.f;
+        M = top;
+        sum = sum * keep + warp_sum(w);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            acc[e] *= keep;
+        for (int j0 = 0; j0 < here; j0 += KP) {
+            float v[KP][E], wj[KP];
+#pragma unroll
+            for (int j = 0; j < KP; ++j) {
+                const size_t r = __shfl_sync(kAll, row, (j0 + j) & 31);
+                wj[j] = __shfl_sync(kAll, w, (j0 + j) & 31);
+                const float *src = a.o_part + r * D + lane * E;
+                if (j0 + j >= here) {
+                    wj[j] = 0.f;
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        v[j][e] = 0.f;
+                } else if constexpr (E == 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(src);
+                    v[j][0] = x.x, v[j][1] = x.y, v[j][2] = x.z, v[j][3] = x.w;
+                } else {
+                    const float2 x = *reinterpret_cast<const float2 *>(src);
+                    v[j][0] = x.x, v[j][1] = x.y;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < KP; ++j)
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    acc[e] = fmaf(wj[j], v[j][e], acc[e]);
+        }
+    }
+    if (!waited)
+        grid_dep_wait();
+    if constexpr (W > 1) {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            st[warp][lane * E + e] = acc[e];
+        if (lane == 0) {
+            st[warp][D] = M;
+            st[warp][D + 1] = sum;
+        }
+        __syncthreads();
+        if (part != 0)
+            return;
+        float top = M;
+        for (int w = 1; w < W; ++w)
+            top = fmaxf(top, st[warp + w][D]);
+        sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            acc[e] = 0.f;
+        for (int w = 0; w < W; ++w) {
+            const float x = st[warp + w][D] == -INFINITY ? 0.f : tc::ex2(st[warp + w][D] - top);
+            sum = fmaf(x, st[warp + w][D + 1], sum);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                acc[e] = fmaf(x, st[warp + w][lane * E + e], acc[e]);
+        }
+        M = top;
+    }
+    if (!live)
+        return;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const size_t row = (size_t)q * a.num_q_heads + h;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        acc[e] *= inv;
+    if (a.out_dtype == DEFT_OUT_F32) {
+        float *o = static_cast<float *>(a.out) + row * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+            *reinterpret_cast<float2 *>(o + e) = make_float2(acc[e], acc[e + 1]);
+    } else {
+        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.out) + row * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+            *reinterpret_cast<__nv_bfloat162 *>(o + e) = __floats2bfloat162_rn(acc[e], acc[e + 1]);
+    }
+    if (lane == 0)
+        a.lse_out[row] = sum == 0.f ? -INFINITY : direct_lse(M + log2f(sum));
+}
+
+template <int D>
+int launch_merge4(const AttnArgs &a, const DevPartition &p, const int32_t *queries, int32_t nq, int32_t slots, cudaStream_t st)
+{
+    const int64_t rows = (int64_t)nq * a.num_q_heads;
+    const int per = slots > 8 ? 1 : kWarps;
+    const int64_t ctas = (rows + per - 1) / per;
+    if (ctas > INT32_MAX)
+        return (int)cudaErrorInvalidConfiguration;
+    return (int)launch_dependent(per == 1 ? merge4_kernel<D, kWarps> : merge4_kernel<D, 1>, dim3((unsigned)ctas), dim3(kThreads), 0, st, a,
+                                 p.q_slot_off, p.q_slot, queries, nq);
+}
+
 }  // namespace
 
-int dispatch_step4(const AttnArgs &a, const DevPartition &dp, const Partition &hp, float k_scale, float v_scale, void *stream,
-                   const LaunchTracer &trace)
+int dispatch_step4(const AttnArgs &a, const DevPartition &dp, const Partition &hp, float k_scale, float v_scale,
+                   int32_t max_slots, void *stream, const LaunchTracer &trace)
 {
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     Kv4Args ka{};
@@ -627,7 +798,7 @@ int dispatch_step4(const AttnArgs &a, const DevPartition &dp, const Partition &h
         if (x.n == 0)
             continue;
         ka.wide = x.wide, ka.first = x.first, ka.n = x.n;
-        ka.heads = heads_per_cta(x.n, a.num_kv_heads, x.rows > 16 ? 2 : 1, x.rows > 16 ? 2 : x.rows > 8 ? 3 : 4);
+        ka.heads = heads_per_cta(x.n, a.num_kv_heads, x.rows > 16 ? 2 : 1, x.rows > 16 ? 2 : x.rows > 8 ? 3 : 5);
         const int r = trace({DEFT_K_PHASE1_KV4, 0, x.rows, 0, x.n, 0.f}, stream, [&] {
             if (x.wide)
                 return tc ? launch_phase1_kv4_mma(ka, dp, x.rows, stream) : launch<64, 4>(ka, dp, st);
@@ -644,7 +815,9 @@ int dispatch_step4(const AttnArgs &a, const DevPartition &dp, const Partition &h
     if (nq == 0)
         return 0;
     const int32_t *qlist = nq < dp.num_queries ? dp.merge_q : nullptr;
-    return trace({DEFT_K_PHASE2, 0, 0, 0, nq, 0.f}, stream, [&] { return launch_phase2(a, dp, qlist, nq, stream); });
+    return trace({DEFT_K_PHASE2, 0, 0, 0, nq, 0.f}, stream, [&] {
+        return a.head_dim == 128 ? launch_merge4<128>(a, dp, qlist, nq, max_slots, st) : launch_merge4<64>(a, dp, qlist, nq, max_slots, st);
+    });
 }
 
 }  // namespace deft
