@@ -36,16 +36,17 @@ namespace deft {
 namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kStages = 4;
 constexpr float kUp = 4.f, kLift = 11.f;
-constexpr double kFill = 1.0;
 constexpr unsigned kAll = 0xffffffffu;
 
 template <int D, int NT>
 struct Cfg {
     using P = kv4::Page<D>;
     static constexpr bool kQSmem = NT > 2;                                // Q^T fragments in shared memory
-    static constexpr uint32_t kStage = 2 * P::kBytes;                     // K, then V, of one page
+    static constexpr int kPages = NT == 1 ? 2 : 1;                        // pages of a step
+    static constexpr int kStages = 4 / kPages;
+    static constexpr uint32_t kPage = 2 * P::kBytes;                      // K, then V
+    static constexpr uint32_t kStage = kPages * kPage;
     static constexpr uint32_t kState = NT * (1 + D / 16) * 512;           // a warp's state when warps join
     static constexpr uint32_t ring_raw = kWarps * kStages * kStage;       // [warp][stage]; at the end two states
     static constexpr uint32_t ring_bytes = ring_raw > 2 * kState ? ring_raw : (2 * kState + 127) / 128 * 128;
@@ -53,7 +54,7 @@ struct Cfg {
     static constexpr uint32_t seg = q + (kQSmem ? kWarps * NT * (D / 32) * 512 : 0);
     static constexpr uint32_t bars = seg + kMaxSegsPerChunk * 24 + 8;     // [256] mask (8 B), page, begin, len; [257] first slice
     static constexpr uint32_t total = bars + kWarps * kStages * 8;
-    static constexpr int kCtas = NT == 1 ? 5 : NT == 2 ? 3 : 2;           // that an SM is meant to hold
+    static constexpr int kCtas = NT == 1 ? 4 : NT == 2 ? 3 : 2;           // that an SM is meant to hold
     static_assert(kStage % 16 == 0 && q % 16 == 0 && seg % 8 == 0 && bars % 8 == 0, "alignment");
     static_assert((total + 1024) * kCtas <= 228 * 1024, "shared memory of an SM");
 };
@@ -61,7 +62,7 @@ struct Cfg {
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -129,6 +130,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
     constexpr int KW = D / 32;      // words of a lane's K elements: dims (D / 4) t ..
     constexpr int VW = D / 64;      // words of a lane's V elements: dims (D / 8) g ..
     constexpr int NR = 8 * NT;      // rows of a warp
+    constexpr int PP = C::kPages, kStages = C::kStages, kBatch = 32 / PP;
     extern __shared__ __align__(128) uint8_t smem[];
     const AttnArgs &a = ka.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -164,8 +166,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
         const uint4 w = reinterpret_cast<const uint4 *>(p.mma_rmask)[rm0 + s];
         return (uint64_t)w.x | (uint64_t)w.z << (item < ka.mma_narrow ? 16 : 32);
     };
-    // The warp's part: rows [row0, row0 + NR) of KV head h, slices ts, ts +
-    // TS, ...
+    // The warp's part: rows [row0, row0 + NR) of KV head h; of the slices, PP
+    // a step, steps ts, ts + TS, ...
     const int groups = R <= NR ? 1 : 2;                 // (a CTA's share of heads leaves room for both)
     const int TS = kWarps / (ka.heads * groups);
     const int ts = warp % TS, rg = warp / TS % groups, h = hg * ka.heads + warp / (TS * groups);
@@ -214,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
         __syncthreads();
         total = seg_first[nseg];
     }
-    const int mine = !idle && total > ts ? (total - ts + TS - 1) / TS : 0;
+    const int steps = (total + PP - 1) / PP, mine = !idle && steps > ts ? (steps - ts + TS - 1) / TS : 0;
     const uint64_t row_bits = R >= 64 ? ~0ull : (1ull << R) - 1;
     const uint32_t my_rows = (uint32_t)(row_bits >> row0) & (uint32_t)((1ull << NR) - 1);
 
@@ -222,10 +224,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
     const uint8_t *k4 = static_cast<const uint8_t *>(a.k_pages), *v4 = static_cast<const uint8_t *>(a.v_pages);
     const uint64_t pol = tc::l2_kv_policy(false);
     const uint32_t ring = base + warp * kStages * C::kStage;
-    auto get_slice = [&](int i, size_t &at, uint32_t &desc) {
-        if (i >= mine)
+    // The lane's slice of the batch of steps from `first` on.
+    auto get_slice = [&](int first, size_t &at, uint32_t &desc) {
+        const int i = first + lane / PP, x = (ts + i * TS) * PP + lane % PP;
+        desc = 0;               // no token
+        if (i >= mine || x >= total)
             return;
-        const int x = ts + i * TS;
         int seg = 0, j = x, pg = page0, begin = begin0, len = len0;
         uint64_t mask = mask0;
         if (nseg > 1) {
@@ -247,18 +251,22 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
     size_t next_at = 0;
     uint32_t cur = 0, next = 0;     // the batch in hand, and the one whose copies go out
     int next_batch = 0;
-    get_slice(lane, next_at, next);
+    get_slice(0, next_at, next);
     cur = next;
     auto issue = [&](int i) {
-        if (i / 32 != next_batch) {
-            next_batch = i / 32;
-            get_slice(i + lane, next_at, next);
+        if (i / kBatch != next_batch) {
+            next_batch = i / kBatch;
+            get_slice(next_batch * kBatch, next_at, next);
         }
-        if (lane == (i & 31)) {
-            const uint32_t dst = ring + (i % kStages) * C::kStage, bar = bars + (i % kStages) * 8;
-            tc::mbar_arrive_expect_tx(bar, C::kStage);
-            tc::bulk_load(dst, k4 + next_at, P::kBytes, bar, pol);
-            tc::bulk_load(dst + P::kBytes, v4 + next_at, P::kBytes, bar, pol);
+        const int first = i % kBatch * PP, n = min(PP, total - (ts + i * TS) * PP);
+        const uint32_t dst = ring + (i % kStages) * C::kStage, bar = bars + (i % kStages) * 8;
+        if (lane == first)
+            tc::mbar_arrive_expect_tx(bar, n * C::kPage);
+        __syncwarp();
+        if (lane >= first && lane < first + n) {
+            const uint32_t to = dst + (lane - first) * C::kPage;
+            tc::bulk_load(to, k4 + next_at, P::kBytes, bar, pol);
+            tc::bulk_load(to + P::kBytes, v4 + next_at, P::kBytes, bar, pol);
         }
     };
     __syncwarp();   // the barriers are there
@@ -336,21 +344,28 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
     const int vx = 2 * t + (t & 1), vy = 2 * t + 1 - (t & 1);
     bool ok = true;
     for (int i = 0; i < mine; ++i) {
-        if (i > 0 && (i & 31) == 0)
+        if (i > 0 && i % kBatch == 0)
             cur = next;      // (issue() is at most kStages ahead: it has filled this batch)
-        const uint32_t desc = __shfl_sync(kAll, cur, i & 31);
+        uint32_t desc[PP];
+        bool whole = true;
+#pragma unroll
+        for (int p2 = 0; p2 < PP; ++p2) {
+            desc[p2] = __shfl_sync(kAll, cur, i % kBatch * PP + p2);
+            whole &= desc[p2] >> 31 != 0;
+        }
         if (!__all_sync(kAll, tc::mbar_wait(bars + (i % kStages) * 8, (i / kStages) & 1))) {
             ok = false;
             break;
         }
-        const uint8_t *ks = smem + (warp * kStages + i % kStages) * C::kStage, *vs = ks + P::kBytes;
-        const bool whole = desc >> 31;
+        const uint8_t *stage = smem + (warp * kStages + i % kStages) * C::kStage;
         // ---- S^T ----
-        float s[NT][4];
+        float s[PP][NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-            s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-        {
+        for (int p2 = 0; p2 < PP; ++p2) {
+            const uint8_t *ks = stage + p2 * C::kPage;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                s[p2][n][0] = s[p2][n][1] = s[p2][n][2] = s[p2][n][3] = 0.f;
             uint32_t w0[KW], w1[KW], sc0[KW / 2], sc1[KW / 2];
             if constexpr (D == 128) {
                 const uint4 x = *reinterpret_cast<const uint4 *>(ks + kg * P::kRow + t * 16);
@@ -387,49 +402,59 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
                         q = qs[(n * KW + w) * 32];
                     else
                         q = make_uint4(qa[n][4 * w], qa[n][4 * w + 1], qa[n][4 * w + 2], qa[n][4 * w + 3]);
-                    mma16816(s[n], x[0], y[0], x[1], y[1], q.x, q.y);
-                    mma16816(s[n], x[2], y[2], x[3], y[3], q.z, q.w);
+                    mma16816(s[p2][n], x[0], y[0], x[1], y[1], q.x, q.y);
+                    mma16816(s[p2][n], x[2], y[2], x[3], y[3], q.z, q.w);
                 }
             }
         }
         // ---- softmax ----
         // The weights' exponents: s f - m + kLift; above kLift + kUp (an m of
         // -inf, as at the start, among them) the maxima are raised first.
-        const int lo = desc >> 8 & 255, hi = desc & 255;
-        float x[NT][4];
+        float x[PP][NT][4];
         bool grow = false;
         auto exponents = [&]() {
+#pragma unroll
+            for (int p2 = 0; p2 < PP; ++p2)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        x[p2][n][j] = fmaf(s[p2][n][j], f[n][j & 1], -m[n][j & 1]);
+        };
+        exponents();
+        if (!whole) {
+#pragma unroll
+            for (int p2 = 0; p2 < PP; ++p2) {
+                const int lo = desc[p2] >> 8 & 255, hi = desc[p2] & 255;
+                const uint32_t rows = (uint32_t)((nseg > 1 ? seg_mask[desc[p2] >> 16 & 0x7fff] : mask0) >> row0);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int tok = kg + (j >> 1) * 8, row = 8 * n + 2 * t + (j & 1);
+                        if (tok < lo || tok >= hi || !((rows >> row) & 1)) {
+                            s[p2][n][j] = -INFINITY;    // (f is positive)
+                            x[p2][n][j] = -INFINITY;
+                        }
+                    }
+            }
+        }
+#pragma unroll
+        for (int p2 = 0; p2 < PP; ++p2)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    x[n][j] = fmaf(s[n][j], f[n][j & 1], -m[n][j & 1]);
-        };
-        exponents();
-        if (!whole) {
-            const uint32_t rows = (uint32_t)((nseg > 1 ? seg_mask[desc >> 16 & 0x7fff] : mask0) >> row0);
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int tok = kg + (j >> 1) * 8, row = 8 * n + 2 * t + (j & 1);
-                    if (tok < lo || tok >= hi || !((rows >> row) & 1)) {
-                        s[n][j] = -INFINITY;    // (f is positive)
-                        x[n][j] = -INFINITY;
-                    }
-                }
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                grow |= x[n][j] > kLift + kUp;
+                    grow |= x[p2][n][j] > kLift + kUp;
         if (__any_sync(kAll, grow)) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    float y = fmaxf(s[n][j] * f[n][j], s[n][j + 2] * f[n][j]);
+                    float y = -INFINITY;
+#pragma unroll
+                    for (int p2 = 0; p2 < PP; ++p2)
+                        y = fmaxf(y, fmaxf(s[p2][n][j] * f[n][j], s[p2][n][j + 2] * f[n][j]));
                     y = fmaxf(y, __shfl_xor_sync(kAll, y, 4));
                     y = fmaxf(y, __shfl_xor_sync(kAll, y, 8));
                     y = fmaxf(y, __shfl_xor_sync(kAll, y, 16));
@@ -447,22 +472,30 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
             exponents();
             // A masked place, also in a row whose maximum is still -inf.
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int p2 = 0; p2 < PP; ++p2)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    x[n][j] = s[n][j] == -INFINITY ? -INFINITY : x[n][j];
-        }
-        uint32_t pb[NT][2];
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const float p0 = tc::ex2(x[n][0]), p1 = tc::ex2(x[n][1]), p2 = tc::ex2(x[n][2]), p3 = tc::ex2(x[n][3]);
-            l[n][0] += p0 + p2;
-            l[n][1] += p1 + p3;
-            pb[n][0] = transpose8(f16x2(p0, p1));
-            pb[n][1] = transpose8(f16x2(p2, p3));
+                    for (int j = 0; j < 4; ++j)
+                        x[p2][n][j] = s[p2][n][j] == -INFINITY ? -INFINITY : x[p2][n][j];
         }
+        uint32_t pb[PP][NT][2];
+#pragma unroll
+        for (int p2 = 0; p2 < PP; ++p2)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float p0 = tc::ex2(x[p2][n][0]), p1 = tc::ex2(x[p2][n][1]);
+                const float p3 = tc::ex2(x[p2][n][3]), q0 = tc::ex2(x[p2][n][2]);
+                l[n][0] += p0 + q0;
+                l[n][1] += p1 + p3;
+                pb[p2][n][0] = transpose8(f16x2(p0, p1));
+                pb[p2][n][1] = transpose8(f16x2(q0, p3));
+            }
         // ---- O^T ----
-        {
+#pragma unroll
+        for (int p2 = 0; p2 < PP; ++p2) {
+            const uint8_t *vs = stage + p2 * C::kPage + P::kBytes;
+            const int lo = desc[p2] >> 8 & 255, hi = desc[p2] & 255;
             uint32_t sv[2], vw[2][2][VW];     // by token pair: scales, words of both tokens
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -501,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
                 for (int k = 0; k < 4; ++k)
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
-                        mma16816(o[4 * w + k][n], e[0][k], od[0][k], e[1][k], od[1][k], pb[n][0], pb[n][1]);
+                        mma16816(o[4 * w + k][n], e[0][k], od[0][k], e[1][k], od[1][k], pb[p2][n][0], pb[p2][n][1]);
             }
         }
         // The stage is free once every lane has read it.
@@ -632,14 +665,13 @@ int launch(Kv4Args ka, const DevPartition &p, cudaStream_t st)
     return (int)launch_dependent(kernel, dim3((unsigned)ctas), dim3(kThreads), Cfg<D, NT>::total, st, ka, p);
 }
 
-// KV heads a CTA takes: as many as give each of its warps (or pair of warps,
-// for two groups of rows) a unit of its own, but fewer, several warps sharing
-// a unit's pages, where that would leave the device short of warps.
-int heads_per_cta(int64_t items, int32_t hkv, int groups, int ctas_per_sm)
+// KV heads that a CTA takes, of the most it can (a unit a warp, or a pair of
+// warps for two groups of rows): fewer, several warps then sharing a unit's
+// pages, while all CTAs still run at once.
+int heads_per_cta(int64_t items, int32_t hkv, int most, int64_t slots)
 {
-    const double full = kFill * kWarps * ctas_per_sm * num_sms();
-    int heads = kWarps / groups;
-    while (heads > 1 && (hkv % heads != 0 || (double)items * hkv * (kWarps / heads) < full))
+    int heads = most;
+    while (heads > 1 && items * (hkv / (heads / 2)) <= slots)
         heads /= 2;
     return heads;
 }
@@ -797,19 +829,36 @@ int dispatch_step4(const AttnArgs &a, const DevPartition &dp, const Partition &h
     for (const Part &x : parts) {
         if (x.n == 0)
             continue;
-        ka.wide = x.wide, ka.first = x.first, ka.n = x.n;
-        ka.heads = heads_per_cta(x.n, a.num_kv_heads, x.rows > 16 ? 2 : 1, x.rows > 16 ? 2 : x.rows > 8 ? 3 : 5);
-        const int r = trace({DEFT_K_PHASE1_KV4, 0, x.rows, 0, x.n, 0.f}, stream, [&] {
-            if (x.wide)
-                return tc ? launch_phase1_kv4_mma(ka, dp, x.rows, stream) : launch<64, 4>(ka, dp, st);
-            if (a.head_dim == 128)
-                return x.rows > 8 ? launch<128, 2>(ka, dp, st) : launch<128, 1>(ka, dp, st);
-            return x.rows > 8 ? launch<64, 2>(ka, dp, st) : launch<64, 1>(ka, dp, st);
-        });
-        if (r)
-            return r;
-        ka.a.wait_prior = 0;
-        ka.last = 1;
+        ka.wide = x.wide;
+        // Items are sorted by length: whole rounds of CTAs with as many heads
+        // as they take, and the rest, the shorter ones, over more CTAs (64
+        // requests: 830 CTAs of four heads are one round of 760 and 70 that
+        // would keep the device waiting for their whole length).
+        const bool tcgen = x.wide && tc;
+        const int64_t slots = (int64_t)(x.rows > 16 ? 2 : x.rows > 8 ? 3 : 4) * num_sms();
+        int most = x.rows > 16 ? 2 : 4;
+        while (a.num_kv_heads % most != 0)
+            most /= 2;
+        const int32_t groups = a.num_kv_heads / most;
+        int32_t bulk = tcgen ? x.n : (int32_t)((int64_t)x.n * groups / slots * slots / groups);
+        for (int32_t done = 0; done < x.n;) {
+            const bool rest = done >= bulk;
+            ka.first = x.first + done;
+            ka.n = rest ? x.n - done : bulk;
+            ka.heads = rest ? heads_per_cta(ka.n, a.num_kv_heads, most, slots) : most;
+            const int r = trace({DEFT_K_PHASE1_KV4, 0, x.rows, 0, ka.n, 0.f}, stream, [&] {
+                if (x.wide)
+                    return tc ? launch_phase1_kv4_mma(ka, dp, x.rows, stream) : launch<64, 4>(ka, dp, st);
+                if (a.head_dim == 128)
+                    return x.rows > 8 ? launch<128, 2>(ka, dp, st) : launch<128, 1>(ka, dp, st);
+                return x.rows > 8 ? launch<64, 2>(ka, dp, st) : launch<64, 1>(ka, dp, st);
+            });
+            if (r)
+                return r;
+            done += ka.n;
+            ka.a.wait_prior = 0;
+            ka.last = 1;
+        }
     }
     const int32_t nq = a.direct ? dp.num_merge_q : dp.num_queries;
     if (nq == 0)

@@ -15,12 +15,14 @@
 // took four times as long.
 //
 // A CTA of eight warps takes one unit, and two CTAs share an SM: one unpacks
-// and exponentiates while the other waits.  All warps do the same work: for
-// tile t they unpack V(t) while S(t) runs, then turn S(t) into P(t) (a thread
-// a token and half the columns), unpack K(t + 1), meet at one barrier, and one
-// thread issues P(t).V(t) and S(t + 1).  Column maxima are raised only when a
-// logit passes one by more than 2^4 (a vote); sums of the weights stay with
-// the threads until the end.  Every wait is bounded.
+// and exponentiates while the other waits.  All warps do the same work.  For
+// tile t they unpack K(t + 1), read S(t) (a thread a token and half the
+// columns) and vote at a barrier whether a column's maximum has to be raised
+// (when a logit passes it by more than 2^4); one thread issues S(t + 1) into
+// S's other buffer; they write P(t), unpack V(t), and at a second barrier
+// P(t).V(t) is issued.  Both products so run while the next operand is
+// unpacked.  Sums of the weights stay with the threads until the end.  Every
+// wait is bounded.
 #include "kv4.cuh"
 #include "merge.cuh"
 #include "tcgen05.cuh"
@@ -34,7 +36,7 @@ constexpr float kUp = 4.f, kLift = 11.f;
 constexpr unsigned kAll = 0xffffffffu;
 constexpr uint32_t kRowGroup = 2048;    // 8 tokens x 128 dims of fp16: two 1 KB swizzle atoms (d halves)
 constexpr uint32_t kTileBytes = 16 * kRowGroup;
-constexpr uint32_t kTmemCols = 128;     // S at 0, O at 64
+constexpr uint32_t kTmemCols = 256;     // S at 0 and 64, O at 128
 
 template <int RP>
 struct Cfg {
@@ -43,7 +45,7 @@ struct Cfg {
     static constexpr uint32_t p = v + kTileBytes;               // [128 tok][128 B]
     static constexpr uint32_t q_half = RP * 128;
     static constexpr uint32_t q = p + kTile * 128;              // [d half][RP rows][128 B]
-    static constexpr uint32_t col = q + 2 * q_half;             // [RP] (factor, maximum - lift)
+    static constexpr uint32_t col = q + 2 * q_half;             // [RP] factor, [RP] lift - maximum
     static constexpr uint32_t red = col + RP * 8;               // [4 warps][RP]
     static constexpr uint32_t seg = red + 4 * RP * 4;           // [256] position, page, begin; [256] mask (8 B)
     static constexpr uint32_t misc = seg + kMaxSegsPerChunk * 20;
@@ -167,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
     const AttnArgs &a = ka.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int half = warp >> 2, row = (warp & 3) * 32 + lane;      // tile row, half of its dims and of the columns
-    float2 *col = reinterpret_cast<float2 *>(smem + C::col);
+    float *col_f = reinterpret_cast<float *>(smem + C::col), *col_y = col_f + RP;
     float *red = reinterpret_cast<float *>(smem + C::red);
     int32_t *seg_pos = reinterpret_cast<int32_t *>(smem + C::seg), *seg_page = seg_pos + kMaxSegsPerChunk,
             *seg_begin = seg_page + kMaxSegsPerChunk;
@@ -249,12 +251,15 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
         }
         // A column of no row has weights of 0: 2^(0 * S - inf).
         if (part == 0)
-            col[r] = r < R ? make_float2(a.scale_log2 * pow2(-e1) * ka.k_scale * pow2(-e2), -INFINITY) : make_float2(0.f, INFINITY);
+        {
+            col_f[r] = r < R ? a.scale_log2 * pow2(-e1) * ka.k_scale * pow2(-e2) : 0.f;
+            col_y[r] = r < R ? INFINITY : -INFINITY;
+        }
     }
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    const uint32_t tm_s = tmem + ((uint32_t)(warp & 3) << 21) + half * NC, tm_o = tm_s + 64;
+    const uint32_t tm_s = tmem + ((uint32_t)(warp & 3) << 21) + half * NC, tm_o = tm_s + 128;
 
     // ---- rows of the chunk ----
     const int ntiles = (T + kTile - 1) / kTile;
@@ -293,10 +298,10 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
     const uint32_t row_bits = R >= RP ? 0xffffffffu >> (32 - NC)
                                       : (uint32_t)((((1ull << R) - 1) >> (half * NC)) & (0xffffffffu >> (32 - NC)));
 
-    float l[NC];
+    f32x2 l[NC / 2];
 #pragma unroll
-    for (int i = 0; i < NC; ++i)
-        l[i] = 0.f;
+    for (int i = 0; i < NC / 2; ++i)
+        l[i] = f2_pack(0.f, 0.f);
     bool ok = true;
     HalfRow kr, vr;
     Where w0 = where(0), w1 = where(1), w2{-1, 0, 0};      // of tiles t, t + 1, t + 2
@@ -308,106 +313,149 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
     tc::fence_proxy_async();
     __syncthreads();
     constexpr uint32_t idesc_s = idesc_f16(kTile, RP, 0, 0), idesc_o = idesc_f16(kD, RP, 1, 1);
-    auto issue_s = [&]() {
+    auto issue_s = [&](int t) {
         const uint64_t dk = tc::smem_desc(base + C::k, 16, kRowGroup), dq = tc::smem_desc(base + C::q, 16, 1024);
 #pragma unroll
         for (int s = 0; s < 8; ++s)
-            tc::mma_bf16(tmem, dk + (((s >> 2) * 1024 + (s & 3) * 32) >> 4), dq + (((s >> 2) * C::q_half + (s & 3) * 32) >> 4),
-                         idesc_s, s > 0 ? 1u : 0u);
+            tc::mma_bf16(tmem + (t & 1) * 64, dk + (((s >> 2) * 1024 + (s & 3) * 32) >> 4),
+                         dq + (((s >> 2) * C::q_half + (s & 3) * 32) >> 4), idesc_s, s > 0 ? 1u : 0u);
         tc::mma_commit(bar_s);
     };
     if (tid == 0)
-        issue_s();
+        issue_s(0);
     for (int t = 0; t < ntiles; ++t) {
-        // ---- V(t), once P(t - 1).V(t - 1) is done; meanwhile S(t) runs ----
-        if (t > 0 && ok)
-            ok = tc::mbar_wait(bar_o, (t - 1) & 1);
-        vr.unpack(row_v, row & 7);
-        load(vr, v4, w1);
-        // ---- P(t) ----
+        // ---- S(t) has been read from K's buffer: K(t + 1) ----
         if (ok)
             ok = tc::mbar_wait(bar_s, t & 1);
+        if (t + 1 < ntiles) {
+            kr.unpack(row_k, row & 7);
+            load(kr, k4, w2);
+        }
+        // ---- exponents of the weights ----
         tc::fence_after_sync();
         __syncwarp();
-        float x[NC];
-        tmem_load<NC>(tm_s, x);
+        f32x2 x[NC / 2];
+        const uint32_t tm_st = tm_s + (t & 1) * 64;
+        auto read = [&](uint32_t from) {
+            float v[NC];
+            tmem_load<NC>(from, v);
+#pragma unroll
+            for (int i = 0; i < NC / 2; ++i)
+                x[i] = f2_pack(v[2 * i], v[2 * i + 1]);
+        };
+        read(tm_st);
         uint32_t seen = 0;
         if (t * kTile + row < T)
             seen = (uint32_t)(seg_mask[w0.seg] >> (half * NC)) & row_bits;
         const bool whole = __all_sync(kAll, seen == row_bits);
-        const float4 *cf = reinterpret_cast<const float4 *>(col + half * NC);
-        bool grow = false;
-        auto logits = [&]() {       // S -> exponents of the weights
+        const ulonglong2 *cf = reinterpret_cast<const ulonglong2 *>(col_f + half * NC),
+                         *cy = reinterpret_cast<const ulonglong2 *>(col_y + half * NC);
+        auto hide = [&]() {
 #pragma unroll
-            for (int i = 0; i < NC; i += 2) {
-                const float4 f = cf[i / 2];
-                x[i] = fmaf(x[i], f.x, -f.y);
-                x[i + 1] = fmaf(x[i + 1], f.z, -f.w);
-            }
-            if (!whole) {
-#pragma unroll
-                for (int i = 0; i < NC; ++i)
-                    x[i] = (seen >> i) & 1u ? x[i] : -INFINITY;
+            for (int i = 0; i < NC / 2; ++i) {
+                const float2 v = f2_unpack(x[i]);
+                x[i] = f2_pack((seen >> (2 * i)) & 1u ? v.x : -INFINITY, (seen >> (2 * i + 1)) & 1u ? v.y : -INFINITY);
             }
         };
-        logits();
+        auto exponents = [&]() {
 #pragma unroll
-        for (int i = 0; i < NC; ++i)
-            grow |= x[i] > kLift + kUp;
-        if (__syncthreads_or(grow)) {
+            for (int i = 0; i < NC / 2; i += 2) {
+                const ulonglong2 f = cf[i / 2], y = cy[i / 2];
+                x[i] = f2_fma(x[i], f.x, y.x);
+                x[i + 1] = f2_fma(x[i + 1], f.y, y.y);
+            }
+            if (!whole)
+                hide();
+        };
+        exponents();
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NC / 2; ++i) {
+            const float2 v = f2_unpack(x[i]);
+            top = fmaxf(top, fmaxf(v.x, v.y));
+        }
+        tc::fence_proxy_async();
+        tc::fence_before_sync();
+        const bool raise = __syncthreads_or(top > kLift + kUp);
+        if (tid == 0 && t + 1 < ntiles) {
+            tc::fence_after_sync();
+            issue_s(t + 1);
+        }
+        // P(t - 1).V(t - 1) is done: P, V and O are free.
+        if (t > 0 && ok)
+            ok = tc::mbar_wait(bar_o, (t - 1) & 1);
+        __syncwarp();
+        if (raise) {
             // Maxima over the tile, from S again.
-            tmem_load<NC>(tm_s, x);
+            tc::fence_after_sync();
+            read(tm_st);
+            hide();
+            float v[NC];
 #pragma unroll
-            for (int i = 0; i < NC; ++i)
-                x[i] = (seen >> i) & 1u ? x[i] * col[half * NC + i].x : -INFINITY;
-            const float top = reduce_columns<true, NC>(x, lane);
+            for (int i = 0; i < NC / 2; ++i) {
+                const float2 y = f2_unpack(x[i]);
+                v[2 * i] = y.x;
+                v[2 * i + 1] = y.y;
+            }
+            const float big_s = reduce_columns<true, NC>(v, lane);      // (f is positive)
             if (lane < NC)
-                red[(warp & 3) * RP + half * NC + lane] = top;
+                red[(warp & 3) * RP + half * NC + lane] = big_s;
             __syncthreads();
             float now = 0.f, alpha = 1.f;
             if (tid < RP) {
-                const float was = col[tid].y;       // maximum - lift; +inf: no row
-                const float big = fmaxf(fmaxf(red[tid], red[RP + tid]), fmaxf(red[2 * RP + tid], red[3 * RP + tid])) - kLift;
-                now = was == INFINITY ? was : fmaxf(was, big);
-                alpha = now == was ? 1.f : tc::ex2(was - now);
+                const float was = col_y[tid];       // lift - maximum; -inf: no row
+                const float big = fmaxf(fmaxf(red[tid], red[RP + tid]), fmaxf(red[2 * RP + tid], red[3 * RP + tid]));
+                now = was == -INFINITY || big == -INFINITY ? was : fminf(was, kLift - big * col_f[tid]);
+                alpha = now == was ? 1.f : tc::ex2(now - was);
             }
             __syncthreads();
             if (tid < RP) {
-                col[tid].y = now;
+                col_y[tid] = now;
                 red[tid] = alpha;
             }
             __syncthreads();
-            const float *al = red + half * NC;
+            const ulonglong2 *al = reinterpret_cast<const ulonglong2 *>(red + half * NC);
 #pragma unroll
-            for (int i = 0; i < NC; ++i)
-                l[i] *= al[i];
-            if (t > 0) {
-                tmem_load<NC>(tm_o, x);
-#pragma unroll
-                for (int i = 0; i < NC; ++i)
-                    x[i] *= al[i];
-                tmem_store<NC>(tm_o, x);
+            for (int i = 0; i < NC / 2; i += 2) {
+                const ulonglong2 y = al[i / 2];
+                l[i] = f2_mul(l[i], y.x);
+                l[i + 1] = f2_mul(l[i + 1], y.y);
             }
-            tmem_load<NC>(tm_s, x);
-            logits();
+            if (t > 0) {
+                read(tm_o);
+#pragma unroll
+                for (int i = 0; i < NC / 2; i += 2) {
+                    const ulonglong2 y = al[i / 2];
+                    x[i] = f2_mul(x[i], y.x);
+                    x[i + 1] = f2_mul(x[i + 1], y.y);
+                }
+#pragma unroll
+                for (int i = 0; i < NC / 2; ++i) {
+                    const float2 y = f2_unpack(x[i]);
+                    v[2 * i] = y.x;
+                    v[2 * i + 1] = y.y;
+                }
+                tmem_store<NC>(tm_o, v);
+            }
+            read(tm_st);
+            exponents();
         }
+        // ---- P(t), V(t) ----
         uint8_t *dst = smem + C::p + row * 128;
 #pragma unroll
         for (int i = 0; i < NC; i += 8) {
             uint32_t w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float y0 = tc::ex2(x[i + 2 * j]), y1 = tc::ex2(x[i + 2 * j + 1]);
-                l[i + 2 * j] += y0;
-                l[i + 2 * j + 1] += y1;
+                const float2 y = f2_unpack(x[i / 2 + j]);
+                const float y0 = tc::ex2(y.x), y1 = tc::ex2(y.y);
+                l[i / 2 + j] = f2_add(l[i / 2 + j], f2_pack(y0, y1));
                 w[j] = f16x2(y0, y1);
             }
             *reinterpret_cast<uint4 *>(dst + ((((half * NC + i) >> 3) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        // ---- K(t + 1) ----
-        if (t + 1 < ntiles)
-            kr.unpack(row_k, row & 7);
-        load(kr, k4, w2);
+        vr.unpack(row_v, row & 7);
+        load(vr, v4, w1);
         w0 = w1;
         w1 = w2;
         w2 = where(t + 3);
@@ -419,10 +467,8 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
             const uint64_t dv = tc::smem_desc(base + C::v, 1024, kRowGroup), dp = tc::smem_desc(base + C::p, kTile * 128, 1024);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                tc::mma_bf16(tmem + 64, dv + ((k * 2 * kRowGroup) >> 4), dp + ((k * 2048) >> 4), idesc_o, t > 0 || k > 0 ? 1u : 0u);
+                tc::mma_bf16(tmem + 128, dv + ((k * 2 * kRowGroup) >> 4), dp + ((k * 2048) >> 4), idesc_o, t > 0 || k > 0 ? 1u : 0u);
             tc::mma_commit(bar_o);
-            if (t + 1 < ntiles)
-                issue_s();
         }
     }
     // ---- out ----
@@ -430,7 +476,14 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
         ok = tc::mbar_wait(bar_o, (ntiles - 1) & 1);
     tc::fence_after_sync();
     {
-        const float sum = reduce_columns<false, NC>(l, lane);
+        float v[NC];
+#pragma unroll
+        for (int i = 0; i < NC / 2; ++i) {
+            const float2 y = f2_unpack(l[i]);
+            v[2 * i] = y.x;
+            v[2 * i + 1] = y.y;
+        }
+        const float sum = reduce_columns<false, NC>(v, lane);
         if (lane < NC)
             red[(warp & 3) * RP + half * NC + lane] = sum;
     }
@@ -442,11 +495,11 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
         if (failed)
             sum = __int_as_float(0x7fffffff);
         // sum is 0 where the row attends no token, NaN where a logit was.
-        const float lse2 = sum == 0.f ? -INFINITY : col[tid].y + log2f(sum);
+        const float lse2 = sum == 0.f ? -INFINITY : log2f(sum) - col_y[tid];
         const int k = tid / G;
         // (+inf, so that the merge's weight for it is NaN and not 0)
         a.lse_part[(size_t)(cq0 + k) * Hq + h * G + (tid - k * G)] = lse2 == lse2 ? lse2 : INFINITY;
-        col[tid].x = sum == 0.f ? 0.f : ka.v_scale / sum;
+        col_f[tid] = sum == 0.f ? 0.f : ka.v_scale / sum;
     }
     __syncwarp();
     float o[NC];
@@ -458,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             if (r + i < R)
-                a.o_part[((size_t)(cq0 + k) * Hq + h * G + j) * kD + row] = o[i] * col[r + i].x;
+                a.o_part[((size_t)(cq0 + k) * Hq + h * G + j) * kD + row] = o[i] * col_f[r + i];
             if (++j == G) {
                 j = 0;
                 ++k;
