@@ -575,8 +575,8 @@ int deft_kv_write(const void *k, const void *v, int32_t in_dtype, int64_t k_stri
  * q, k, v, q_out, the pools, cos_sin and the norms' weights 16-byte aligned,
  * strides multiples of 16 bytes and at least a row (DEFT_EINVAL); head_dim in
  * {64, 128}, rot_dim a multiple of 16 up to head_dim (DEFT_EINVAL above it),
- * page_size 16, fewer than 2^27 pages, tokens x (query and KV heads) below
- * 2^31 (DEFT_EUNSUPPORTED).  Never allocates, never synchronises;
+ * page_size 16, fewer than 2^27 pages, tokens x (query heads + 2 KV heads)
+ * below 2^31 (DEFT_EUNSUPPORTED).  Never allocates, never synchronises;
  * stream-ordered on `stream`; may be captured into a CUDA graph.
  */
 typedef struct deft_qk_turn {

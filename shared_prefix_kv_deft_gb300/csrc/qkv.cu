@@ -18,9 +18,13 @@
 //
 // Layout.  D / 16 lanes hold a head's row, two 8-element pieces each: pieces
 // (j, j + R/16) where the rotation pairs them, so that both elements of a
-// pair are in one lane, else (2j, 2j + 1).  A warp takes up to C rounds of
+// pair are in one lane, else (2j, 2j + 1).  A warp takes one or two rounds of
 // 32 / (D / 16) heads of one kind (q, k or v) of one token, all loads ahead
-// of the arithmetic; the token's cos and sin stay in registers over them.
+// of the arithmetic, on packed pairs; the token's cos and sin stay in
+// registers over them.  32768 tokens (32/8 heads of 128, bf16): 167 us, 4.9
+// TB/s; the 822 MB at the measured copy rate take 121.  Bound by issue slots
+// and loads in flight together: persistent CTAs fed by a ring of bulk copies
+// in shared memory took the same 164 us, with more instructions.
 #include <cstdint>
 
 #include "common.cuh"
@@ -33,6 +37,15 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr unsigned kAll = 0xffffffffu;
+// Heads a group of lanes takes, and the CTAs that an SM is to hold (which sets
+// the registers): rows in flight against warps in flight.  32768 tokens of
+// bf16, 32/8 heads of 128: 1 and 5 196 us, 2 and 3 180, 2 and 4 163, 2 and 5
+// 193, 3 and 4 172; 10007 tokens of fp32, 12/4 heads of 64: 1 and 4 21.0 us, 1
+// and 5 20.4, 2 and 3 23.6.
+template <bool kF32>
+struct Shape {
+    static constexpr int kHeads = kF32 ? 1 : 2, kCtas = kF32 ? 5 : 4;
+};
 
 struct QkvArgs {
     const void *q, *k, *v;
@@ -69,21 +82,20 @@ struct Piece {
         if constexpr (kF32)
             v[1] = kOnce ? __ldcs(p + 1) : p[1];
     }
-    __device__ __forceinline__ void floats(float (&f)[8]) const
+    // As packed pairs of neighbours.
+    __device__ __forceinline__ void pairs(f32x2 (&x)[4]) const
     {
         if constexpr (kF32) {
-            const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                f[i] = __uint_as_float(w[i]);
-        } else {
-            const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 t = bf16x2_to_float2(w[i]);
-                f[2 * i] = t.x;
-                f[2 * i + 1] = t.y;
+            for (int i = 0; i < 2; ++i) {
+                x[2 * i] = f2_pack(__uint_as_float(v[i].x), __uint_as_float(v[i].y));
+                x[2 * i + 1] = f2_pack(__uint_as_float(v[i].z), __uint_as_float(v[i].w));
             }
+        } else {
+            x[0] = bf16x2_to_f2(v[0].x);
+            x[1] = bf16x2_to_f2(v[0].y);
+            x[2] = bf16x2_to_f2(v[0].z);
+            x[3] = bf16x2_to_f2(v[0].w);
         }
     }
 };
@@ -94,14 +106,15 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-__device__ __forceinline__ float square_sum(const float (&x)[8])
+__device__ __forceinline__ float square_sum(const f32x2 (&x)[4])
 {
-    float s[8];
+    float s[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        s[i] = __fmul_rn(x[i], x[i]);
-    return __fadd_rn(__fadd_rn(__fadd_rn(s[0], s[1]), __fadd_rn(s[2], s[3])),
-                     __fadd_rn(__fadd_rn(s[4], s[5]), __fadd_rn(s[6], s[7])));
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = f2_unpack(f2_mul(x[i], x[i]));
+        s[i] = __fadd_rn(v.x, v.y);
+    }
+    return __fadd_rn(__fadd_rn(s[0], s[1]), __fadd_rn(s[2], s[3]));
 }
 
 // The lane's two pieces of a row, by where the rotation wants them.
@@ -158,10 +171,10 @@ struct Place {
     }
 };
 
-template <int D, bool kF32, bool k4, int C>
-__global__ void __launch_bounds__(kThreads) qkv_kernel(QkvArgs a)
+template <int D, bool kF32, bool k4>
+__global__ void __launch_bounds__(kThreads, Shape<kF32>::kCtas) qkv_kernel(QkvArgs a)
 {
-    constexpr int kLanes = D / 16, kRows = 32 / kLanes;
+    constexpr int kLanes = D / 16, kRows = 32 / kLanes, C = Shape<kF32>::kHeads;
     const int lane = threadIdx.x & 31, sub = lane / kLanes;
     const uint32_t per_token = (uint32_t)(a.q_tasks + 2 * a.kv_tasks);
     const uint32_t task = blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -194,73 +207,77 @@ __global__ void __launch_bounds__(kThreads) qkv_kernel(QkvArgs a)
             raw[c][1].zero();
         }
     }
-    // The lane's eight angles: pairs of its two pieces, or of both pieces'
-    // neighbours.
+    // The lane's eight angles: of the elements of both its pieces, or of the
+    // pieces' pairs of neighbours.
     const bool turns = at.j < half;
-    float cs[8], sn[8];
+    f32x2 cs[4], sn[4];
     if (turns) {
         const int32_t pos = a.position[tok];
         if ((uint32_t)pos < (uint32_t)a.num_positions) {
-            const float4 *t = reinterpret_cast<const float4 *>(a.cos_sin + (int64_t)pos * half * 16) + at.j * 2;
-            const float4 c0 = __ldg(t), c1 = __ldg(t + 1), s0 = __ldg(t + half * 2), s1 = __ldg(t + half * 2 + 1);
-            cs[0] = c0.x, cs[1] = c0.y, cs[2] = c0.z, cs[3] = c0.w;
-            cs[4] = c1.x, cs[5] = c1.y, cs[6] = c1.z, cs[7] = c1.w;
-            sn[0] = s0.x, sn[1] = s0.y, sn[2] = s0.z, sn[3] = s0.w;
-            sn[4] = s1.x, sn[5] = s1.y, sn[6] = s1.z, sn[7] = s1.w;
+            const ulonglong2 *t = reinterpret_cast<const ulonglong2 *>(a.cos_sin + (int64_t)pos * half * 16) + at.j * 2;
+            const ulonglong2 c0 = __ldg(t), c1 = __ldg(t + 1), s0 = __ldg(t + half * 2), s1 = __ldg(t + half * 2 + 1);
+            cs[0] = c0.x, cs[1] = c0.y, cs[2] = c1.x, cs[3] = c1.y;
+            sn[0] = s0.x, sn[1] = s0.y, sn[2] = s1.x, sn[3] = s1.y;
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                cs[i] = sn[i] = __int_as_float(0x7fffffff);
+            for (int i = 0; i < 4; ++i)
+                cs[i] = sn[i] = f2_pack(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
         }
     }
     const void *norm = kind == 0 ? a.q_norm : kind == 1 ? a.k_norm : nullptr;
-    Piece<kF32> w0, w1;
-    if (norm) {
-        w0.template load<false>(norm, at.p0 * 8);
-        w1.template load<false>(norm, at.p1 * 8);
-    }
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int h = head0 + c * kRows;
-        float x[2][8];
-        raw[c][0].floats(x[0]);
-        raw[c][1].floats(x[1]);
+        f32x2 x[2][4];
+        raw[c][0].pairs(x[0]);
+        raw[c][1].pairs(x[1]);
         if (norm) {
             const float ss = at.row_sum(square_sum(x[0]), square_sum(x[1]));
             const float r = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(ss, 1.f / D), a.eps)));
-            float w[8];
-            w0.floats(w);
+            const f32x2 r2 = f2_pack(r, r);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                x[0][i] = __fmul_rn(__fmul_rn(x[0][i], r), w[i]);
-            w1.floats(w);
+            for (int p = 0; p < 2; ++p) {
+                Piece<kF32> wp;
+                wp.template load<false>(norm, (p == 0 ? at.p0 : at.p1) * 8);
+                f32x2 w[4];
+                wp.pairs(w);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                x[1][i] = __fmul_rn(__fmul_rn(x[1][i], r), w[i]);
+                for (int i = 0; i < 4; ++i)
+                    x[p][i] = f2_mul(f2_mul(x[p][i], r2), w[i]);
+            }
         }
         if (turns) {
-            auto turn = [](float &u, float &v, float co, float si) {
-                const float t = __fsub_rn(__fmul_rn(u, co), __fmul_rn(v, si));
-                v = __fadd_rn(__fmul_rn(v, co), __fmul_rn(u, si));
-                u = t;
-            };
             if (a.split) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    turn(x[0][i], x[1][i], cs[i], sn[i]);
+                for (int i = 0; i < 4; ++i) {
+                    // (Scalar: the assembler fuses packed products into the
+                    // packed sum behind them, whatever rounding they name.)
+                    const float2 u = f2_unpack(x[0][i]), v = f2_unpack(x[1][i]), co = f2_unpack(cs[i]), si = f2_unpack(sn[i]);
+                    const f32x2 t = f2_pack(__fsub_rn(__fmul_rn(u.x, co.x), __fmul_rn(v.x, si.x)), __fsub_rn(__fmul_rn(u.y, co.y), __fmul_rn(v.y, si.y)));
+                    x[1][i] = f2_pack(__fadd_rn(__fmul_rn(v.x, co.x), __fmul_rn(u.x, si.x)), __fadd_rn(__fmul_rn(v.y, co.y), __fmul_rn(u.y, si.y)));
+                    x[0][i] = t;
+                }
             } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    turn(x[0][2 * i], x[0][2 * i + 1], cs[i], sn[i]);
-                    turn(x[1][2 * i], x[1][2 * i + 1], cs[4 + i], sn[4 + i]);
+                for (int i = 0; i < 8; ++i) {       // pair i % 4 of piece i / 4, angle i
+                    f32x2 &y = x[i / 4][i % 4];
+                    const float2 v = f2_unpack(y), c2 = f2_unpack(cs[i / 2]), s2 = f2_unpack(sn[i / 2]);
+                    const float co = i % 2 ? c2.y : c2.x, si = i % 2 ? s2.y : s2.x;
+                    y = f2_pack(__fsub_rn(__fmul_rn(v.x, co), __fmul_rn(v.y, si)), __fadd_rn(__fmul_rn(v.y, co), __fmul_rn(v.x, si)));
                 }
             }
         }
         uint4 o[2];
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
-            o[p] = make_uint4(bf16x2(x[p][0], x[p][1]), bf16x2(x[p][2], x[p][3]), bf16x2(x[p][4], x[p][5]),
-                              bf16x2(x[p][6], x[p][7]));
+        for (int p = 0; p < 2; ++p) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 v = f2_unpack(x[p][i]);
+                w[i] = bf16x2(v.x, v.y);
+            }
+            o[p] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
         const bool live = h < heads;
         if (kind == 0) {
             if (live) {
@@ -276,15 +293,16 @@ __global__ void __launch_bounds__(kThreads) qkv_kernel(QkvArgs a)
                 dst[at.p1] = o[1];
             }
         } else {
-            float y[2][8], m[2] = {0.f, 0.f};
+            float m[2];
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                Piece<false> t;
-                t.v[0] = o[p];
-                t.floats(y[p]);
+                const uint32_t w[4] = {o[p].x, o[p].y, o[p].z, o[p].w};
+                m[p] = 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    m[p] = kv4::max_nan(m[p], fabsf(y[p][i]));
+                for (int i = 0; i < 4; ++i) {
+                    const float2 v = bf16x2_to_float2(w[i] & 0x7fff7fffu);
+                    m[p] = kv4::max_nan(m[p], kv4::max_nan(v.x, v.y));
+                }
             }
             at.block_max(m[0], m[1]);
             using P = kv4::Page<D>;
@@ -294,8 +312,16 @@ __global__ void __launch_bounds__(kThreads) qkv_kernel(QkvArgs a)
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 const int piece = p == 0 ? at.p0 : at.p1;
+                const uint32_t w[4] = {o[p].x, o[p].y, o[p].z, o[p].w};
+                float y[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 v = bf16x2_to_float2(w[i]);
+                    y[2 * i] = v.x;
+                    y[2 * i + 1] = v.y;
+                }
                 const uint32_t s = kv4::scale_of(m[p], six);
-                const uint32_t codes = kv4::pack8(y[p], m[p], __fmul_rn(kv4::scale_value(s), g));
+                const uint32_t codes = kv4::pack8(y, m[p], __fmul_rn(kv4::scale_value(s), g));
                 if (live) {
                     *reinterpret_cast<uint32_t *>(page + line * P::kRow + piece * 4) = codes;
                     if ((piece & 1) == 0)
@@ -358,22 +384,22 @@ int launch(void (*kernel)(Args), dim3 grid, cudaStream_t st, const Args &a)
     return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? DEFT_OK : DEFT_ECUDA;
 }
 
-template <int D, bool kF32, bool k4, int C>
+template <int D, bool kF32, bool k4>
 int launch_qkv(QkvArgs a, cudaStream_t st)
 {
-    constexpr int kRound = C * (32 / (D / 16));   // heads a warp takes
+    constexpr int kRound = Shape<kF32>::kHeads * (32 / (D / 16));   // heads a warp takes
     a.q_tasks = (a.num_q_heads + kRound - 1) / kRound;
     a.kv_tasks = (a.num_kv_heads + kRound - 1) / kRound;
     const int64_t tasks = (int64_t)a.num_tokens * (a.q_tasks + 2 * a.kv_tasks);
     if (tasks > INT32_MAX)
         return DEFT_EUNSUPPORTED;
-    return launch(qkv_kernel<D, kF32, k4, C>, dim3((unsigned)((tasks + kWarps - 1) / kWarps)), st, a);
+    return launch(qkv_kernel<D, kF32, k4>, dim3((unsigned)((tasks + kWarps - 1) / kWarps)), st, a);
 }
 
 template <int D, bool k4>
 int pick_qkv(const QkvArgs &a, bool f32, cudaStream_t st)
 {
-    return f32 ? launch_qkv<D, true, k4, 1>(a, st) : launch_qkv<D, false, k4, 1>(a, st);
+    return f32 ? launch_qkv<D, true, k4>(a, st) : launch_qkv<D, false, k4>(a, st);
 }
 
 bool good_scale(float g)
@@ -402,6 +428,8 @@ int check_qkv(const void *q, const void *k, const void *v, int32_t in_dtype, int
     const int64_t es = in_dtype == DEFT_OUT_F32 ? 4 : 2;
     if (q_row > (1 << 24) || kv_row > (1 << 24))
         return DEFT_EINVAL;
+    if ((int64_t)num_tokens * (num_q_heads + 2 * (int64_t)num_kv_heads) > INT32_MAX)
+        return DEFT_EUNSUPPORTED;
     if (num_tokens > 0 && (!k || !v || !slot || (num_q_heads > 0 && (!q || !q_out))))
         return DEFT_EINVAL;
     uintptr_t all = (uintptr_t)k | (uintptr_t)v | (uintptr_t)k_pool | (uintptr_t)v_pool | (uintptr_t)t.q_norm |

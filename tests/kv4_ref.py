@@ -69,6 +69,26 @@ def turned(x, weight, eps, cos_sin, position, interleaved):
     return x
 
 
+def turned32(x, weight, eps, cos_sin, position, interleaved):
+    """The same in 32 bits, each operation rounded by itself and the squares
+    added neighbours first, as the calls document it: float32, to be rounded
+    to bf16."""
+    f = np.float32
+    x = x.astype(f)
+    if weight is not None:
+        sq = x * x
+        while sq.shape[-1] > 1:
+            sq = sq[..., 0::2] + sq[..., 1::2]
+        x = x * (f(1) / np.sqrt(sq * f(1 / x.shape[-1]) + f(eps))) * weight.astype(f)
+    if cos_sin is not None:
+        r = cos_sin.shape[1] // 2
+        c, s = cos_sin[position][:, None, :r], cos_sin[position][:, None, r:]
+        ia, ib = (np.arange(0, 2 * r, 2), np.arange(1, 2 * r, 2)) if interleaved else (np.arange(r), np.arange(r, 2 * r))
+        a, b, x = x[..., ia], x[..., ib], x.copy()
+        x[..., ia], x[..., ib] = a * c - b * s, b * c + a * s
+    return x
+
+
 def bf16(x):
     """float64 -> the nearest bf16 value (ties to even), as float64."""
     u = np.asarray(x, dtype=np.float64).astype(np.float32).view(np.uint32).astype(np.uint64)

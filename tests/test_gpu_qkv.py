@@ -107,6 +107,18 @@ def test_qkv_write(c):
         assert (f64(pool)[free // 16, :, free % 16] == 7).all()
 
 
+@pytest.mark.parametrize("c", CASES)
+def test_each_operation_rounds_by_itself(c):
+    """Bit for bit what 32-bit arithmetic gives, operation by operation."""
+    r = Rows(**c)
+    kp, vp = r.pools()
+    q = deft.deft_qkv_write(r.q, r.k, r.v, cu(r.slot), kp, vp, **r.kw)
+    kept = np.nonzero(r.slot >= 0)[0]
+    for got, x, w, rows in ((f64(q), r.q, r.w[0], slice(None)), (r.at(f64(kp), kept), r.k, r.w[1], kept)):
+        want = ref.turned32(f64(x), None if w is None else f64(w), 1e-5, r.cos_sin, r.position, r.interleaved)
+        assert want.dtype == np.float32 and (got == ref.bf16(want)[rows]).all()
+
+
 @pytest.mark.parametrize("g", [(1.0, 1.0), (0.25, 4.0), (0.37, 1.9)])
 @pytest.mark.parametrize("c", CASES)
 def test_qkv_write4(c, g):
