@@ -82,12 +82,18 @@ struct HalfRow {
         w[0] = w[1] = make_uint4(0, 0, 0, 0);
         s = 0;
     }
-    __device__ __forceinline__ void load(const uint8_t *page, int tok, int half)
+    __device__ __forceinline__ void load(const uint8_t *page, int tok, int half, bool sectors)
     {
         using P = kv4::Page<kD>;
         const uint4 *src = reinterpret_cast<const uint4 *>(page + tok * P::kRow) + 2 * half;
-        w[0] = __ldg(src);
-        w[1] = __ldg(src + 1);
+        if (sectors) {
+            asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                         : "=r"(w[0].x), "=r"(w[0].y), "=r"(w[0].z), "=r"(w[0].w), "=r"(w[1].x), "=r"(w[1].y), "=r"(w[1].z), "=r"(w[1].w)
+                         : "l"(src));
+        } else {
+            w[0] = __ldg(src);
+            w[1] = __ldg(src + 1);
+        }
         s = __ldg(reinterpret_cast<const uint32_t *>(page + P::kScales + tok * P::kScaleRow) + half);
     }
     // As fp16 into the swizzled row at `dst` (row r of its group of eight).
@@ -267,29 +273,31 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
     const uint8_t *v4 = static_cast<const uint8_t *>(a.v_pages) + (size_t)h * P::kBytes;
     const size_t page_step = (size_t)Hkv * P::kBytes;
     struct Where {
-        int page, tok, seg;     // page -1: no token
+        int page, meta;     // page -1: no token; segment x 16 + place in the page
     };
     auto where = [&](int t) {
-        Where w{-1, 0, 0};
+        Where w{-1, 0};
         const int x = t * kTile + row;
         if (x < T) {
-            int hi = nseg;
-            while (hi - w.seg > 1) {
-                const int mid = (w.seg + hi) >> 1;
+            int seg = 0, hi = nseg;
+            while (hi - seg > 1) {
+                const int mid = (seg + hi) >> 1;
                 if (seg_pos[mid] <= x)
-                    w.seg = mid;
+                    seg = mid;
                 else
                     hi = mid;
             }
-            const int j = x - seg_pos[w.seg] + seg_begin[w.seg];
-            w.page = a.page_id[seg_page[w.seg] + j / kPageSize];
-            w.tok = j % kPageSize;
+            const int j = x - seg_pos[seg] + seg_begin[seg];
+            w.page = a.page_id[seg_page[seg] + j / kPageSize];
+            w.meta = seg * kPageSize + j % kPageSize;
         }
         return w;
     };
+    // (A half row is one 32-byte sector where the pools are aligned so.)
+    const bool sectors = (((uintptr_t)a.k_pages | (uintptr_t)a.v_pages) & 31u) == 0;
     auto load = [&](HalfRow &x, const uint8_t *pool, const Where &w) {
         if (w.page >= 0)
-            x.load(pool + (size_t)w.page * page_step, w.tok, half);
+            x.load(pool + (size_t)w.page * page_step, w.meta % kPageSize, half, sectors);
         else
             x.zero();
     };
@@ -304,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
         l[i] = f2_pack(0.f, 0.f);
     bool ok = true;
     HalfRow kr, vr;
-    Where w0 = where(0), w1 = where(1), w2{-1, 0, 0};      // of tiles t, t + 1, t + 2
+    Where w0 = where(0), w1 = where(1), w2{-1, 0};      // of tiles t, t + 1, t + 2
     load(kr, k4, w0);
     load(vr, v4, w0);
     kr.unpack(row_k, row & 7);
@@ -346,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
         read(tm_st);
         uint32_t seen = 0;
         if (t * kTile + row < T)
-            seen = (uint32_t)(seg_mask[w0.seg] >> (half * NC)) & row_bits;
+            seen = (uint32_t)(seg_mask[w0.meta / kPageSize] >> (half * NC)) & row_bits;
         const bool whole = __all_sync(kAll, seen == row_bits);
         const ulonglong2 *cf = reinterpret_cast<const ulonglong2 *>(col_f + half * NC),
                          *cy = reinterpret_cast<const ulonglong2 *>(col_y + half * NC);
