@@ -36,19 +36,18 @@ constexpr float kUp = 4.f, kLift = 11.f;
 constexpr unsigned kAll = 0xffffffffu;
 constexpr uint32_t kRowGroup = 2048;    // 8 tokens x 128 dims of fp16: two 1 KB swizzle atoms (d halves)
 constexpr uint32_t kTileBytes = 16 * kRowGroup;
-constexpr uint32_t kTmemCols = 256;     // S at 0 and 64, O at 128
+constexpr uint32_t kTmemCols = 256;     // S at 0 and 64, O at 128, K's tile (fp16 pairs) at 192
 
 template <int RP>
 struct Cfg {
-    static constexpr uint32_t k = 0;                            // [16 groups][d half][8 tok][128 B]
-    static constexpr uint32_t v = k + kTileBytes;
+    static constexpr uint32_t v = 0;                            // [16 groups][d half][8 tok][128 B]
     static constexpr uint32_t p = v + kTileBytes;               // [128 tok][128 B]
     static constexpr uint32_t q_half = RP * 128;
     static constexpr uint32_t q = p + kTile * 128;              // [d half][RP rows][128 B]
     static constexpr uint32_t col = q + 2 * q_half;             // [RP] factor, [RP] lift - maximum
     static constexpr uint32_t red = col + RP * 8;               // [4 warps][RP]
     static constexpr uint32_t seg = red + 4 * RP * 4;           // [256] position, page, begin; [256] mask (8 B)
-    static constexpr uint32_t misc = seg + kMaxSegsPerChunk * 20;
+    static constexpr uint32_t misc = seg + kMaxSegsPerChunk * 20;   // TMEM base, extremes of the rows' exponents
     static constexpr uint32_t bars = misc + 16;                 // S, O
     static constexpr uint32_t total = bars + 16;
     static constexpr uint32_t alloc = total + 1024;
@@ -96,61 +95,68 @@ struct HalfRow {
         }
         s = __ldg(reinterpret_cast<const uint32_t *>(page + P::kScales + tok * P::kScaleRow) + half);
     }
-    // As fp16 into the swizzled row at `dst` (row r of its group of eight).
-    __device__ __forceinline__ void unpack(uint8_t *dst, int r) const
+    // Words 4 b .. 4 b + 3 as fp16, eight elements each.
+    template <typename F>
+    __device__ __forceinline__ void each(int b, F f) const
     {
-        const uint32_t x[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
-        const uint32_t a = kv4::scales2(s), b = kv4::scales2(s >> 16);
-        const uint32_t sc[4] = {__byte_perm(a, 0, 0x1010), __byte_perm(a, 0, 0x3232), __byte_perm(b, 0, 0x1010),
-                                __byte_perm(b, 0, 0x3232)};
+        const uint32_t x[4] = {w[b].x, w[b].y, w[b].z, w[b].w};
+        const uint32_t a = kv4::scales2(b == 0 ? s : s >> 16);
+        const uint32_t sc[2] = {__byte_perm(a, 0, 0x1010), __byte_perm(a, 0, 0x3232)};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < 4; ++i) {
             uint32_t h[4];
             kv4::unpack8(x[i], h);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 h[k] = kv4::hmul2(h[k], sc[i / 2]);
-            *reinterpret_cast<uint4 *>(dst + ((i ^ r) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+            f(i, h);
+        }
+    }
+    // Into the swizzled row at `dst` (row r of its group of eight).
+    __device__ __forceinline__ void to_smem(uint8_t *dst, int r) const
+    {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+            each(b, [&](int i, const uint32_t (&h)[4]) {
+                *reinterpret_cast<uint4 *>(dst + (((4 * b + i) ^ r) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+            });
+    }
+    // Into 32 columns of the thread's TMEM lane.
+    __device__ __forceinline__ void to_tmem(uint32_t addr) const
+    {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            float v[16];
+            each(b, [&](int i, const uint32_t (&h)[4]) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    v[4 * i + k] = __uint_as_float(h[k]);
+            });
+            tc::tmem_st16(addr + 16 * b, v);
         }
     }
 };
 
-template <int N>
-__device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[N])
+// D[tmem] (+)= A[tmem] . B[smem], kind::f16.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
 {
-    static_assert(N == 16 || N == 32, "columns");
-    if constexpr (N == 32)
-        tc::tmem_ld32(addr, v);
-    else
-        tc::tmem_ld16(addr, v);
-}
-template <int N>
-__device__ __forceinline__ void tmem_store(uint32_t addr, const float (&v)[N])
-{
-    if constexpr (N == 32)
-        tc::tmem_st32(addr, v);
-    else
-        tc::tmem_st16(addr, v);
+    asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                 : "memory");
 }
 
-// Column i's reduction over the warp's lanes, to lane i (i + 16 as well for
-// 16 columns).
-template <bool kMax, int N>
-__device__ __forceinline__ float reduce_columns(const float (&x)[N], int lane)
+// Column i's reduction over the warp's lanes, to lanes i and i + 16.
+template <bool kMax>
+__device__ __forceinline__ float reduce_columns(float (&v)[16], int lane)
 {
-    float v[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-        v[i] = x[i];
-    if constexpr (N == 16) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float y = __shfl_xor_sync(kAll, v[i], 16);
-            v[i] = kMax ? fmaxf(v[i], y) : v[i] + y;
-        }
+    for (int i = 0; i < 16; ++i) {
+        const float y = __shfl_xor_sync(kAll, v[i], 16);
+        v[i] = kMax ? fmaxf(v[i], y) : v[i] + y;
     }
 #pragma unroll
-    for (int o = N / 2; o >= 1; o >>= 1) {
+    for (int o = 8; o >= 1; o >>= 1) {
         const bool upper = (lane & o) != 0;
 #pragma unroll
         for (int i = 0; i < o; ++i) {
@@ -181,6 +187,7 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
             *seg_begin = seg_page + kMaxSegsPerChunk;
     uint64_t *seg_mask = reinterpret_cast<uint64_t *>(seg_begin + kMaxSegsPerChunk);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::misc);
+    int *ext = reinterpret_cast<int *>(smem + C::misc) + 1;     // least, greatest exponent of a row
     const uint32_t bar_s = base + C::bars, bar_o = bar_s + 8;
 
     if (warp == 0) {
@@ -191,7 +198,10 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
         tc::mbar_init(bar_s, 1);
         tc::mbar_init(bar_o, 1);
         tc::fence_mbar_init();
+        ext[0] = 1000;
+        ext[1] = -1000;
     }
+    __syncthreads();
     if (a.wait_prior)
         grid_dep_wait();
     grid_dep_launch();
@@ -212,10 +222,11 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
         const uint4 w = reinterpret_cast<const uint4 *>(p.mma_rmask)[rm0 + s];
         seg_mask[s] = (uint64_t)w.x | (uint64_t)w.z << (item < ka.mma_narrow ? 16 : 32);
     }
-    // ---- Q^T: bf16 -> fp16 times a power of two for each row ----
+    // ---- Q^T: bf16 -> fp16 times a power of two ----
+    bool uniform;
     {
         constexpr int TPR = kThreads / RP, DT = kD / TPR;   // threads of a row, dims of a thread
-        const int r = tid / TPR, part = tid % TPR;
+        const int r = tid / TPR, piece = tid % TPR;
         uint32_t w[DT / 2];
 #pragma unroll
         for (int i = 0; i < DT / 2; ++i)
@@ -223,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
         if (r < R) {
             const int k = r / G;
             const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
-                                                               ((size_t)p.chunk_q[cq0 + k] * Hq + h * G + (r - k * G)) * kD + part * DT);
+                                                               ((size_t)p.chunk_q[cq0 + k] * Hq + h * G + (r - k * G)) * kD + piece * DT);
 #pragma unroll
             for (int i = 0; i < DT / 8; ++i) {
                 const uint4 x = src[i];
@@ -240,8 +251,20 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
 #pragma unroll
         for (int o = 1; o < TPR; o <<= 1)
             big = fmaxf(big, __shfl_xor_sync(kAll, big, o));
+        int e = big > 0.f ? 14 - ilogbf(big) : 1 << 20;        // (a row of zeros takes any)
+        // Rows within 2^8 of one another share the power of two, and with it
+        // the factor of their logits: fp16 holds the smallest one's elements
+        // down to 2^-31 of its largest.
+        if (piece == 0 && e < 1 << 20) {
+            atomicMin(ext, e);
+            atomicMax(ext + 1, e);
+        }
+        __syncthreads();
+        uniform = ext[1] - ext[0] <= 8;
+        if (uniform || e == 1 << 20)
+            e = ext[0] == 1000 ? 0 : ext[0];
         // 2^e in two factors: e reaches from -113 to 147.
-        const int e = big > 0.f ? 14 - ilogbf(big) : 0, e1 = e / 2, e2 = e - e1;
+        const int e1 = e / 2, e2 = e - e1;
         const float up1 = pow2(e1), up2 = pow2(e2);
 #pragma unroll
         for (int i = 0; i < DT / 8; ++i) {
@@ -251,14 +274,13 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
                 const float2 y = bf16x2_to_float2(w[4 * i + j]);
                 x[j] = f16x2(y.x * up1 * up2, y.y * up1 * up2);
             }
-            const int chunk = part * (DT / 8) + i;          // of the row's sixteen
+            const int chunk = piece * (DT / 8) + i;         // of the row's sixteen
             *reinterpret_cast<uint4 *>(smem + C::q + (chunk >> 3) * C::q_half + r * 128 + (((chunk & 7) ^ (r & 7)) << 4)) =
                 make_uint4(x[0], x[1], x[2], x[3]);
         }
-        // A column of no row has weights of 0: 2^(0 * S - inf).
-        if (part == 0)
-        {
-            col_f[r] = r < R ? a.scale_log2 * pow2(-e1) * ka.k_scale * pow2(-e2) : 0.f;
+        // A column of no row has weights of 0: 2^(f * 0 - inf).
+        if (piece == 0) {
+            col_f[r] = a.scale_log2 * pow2(-e1) * ka.k_scale * pow2(-e2);
             col_y[r] = r < R ? INFINITY : -INFINITY;
         }
     }
@@ -301,8 +323,9 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
         else
             x.zero();
     };
-    uint8_t *row_k = smem + C::k + (row >> 3) * kRowGroup + half * 1024 + (row & 7) * 128;
-    uint8_t *row_v = row_k + (C::v - C::k);
+    uint8_t *row_v = smem + C::v + (row >> 3) * kRowGroup + half * 1024 + (row & 7) * 128;
+    const uint32_t tm_k = tmem + ((uint32_t)(warp & 3) << 21) + 192 + half * 32;
+    const f32x2 common = f2_pack(col_f[0], col_f[0]);
     const uint32_t row_bits = R >= RP ? 0xffffffffu >> (32 - NC)
                                       : (uint32_t)((((1ull << R) - 1) >> (half * NC)) & (0xffffffffu >> (32 - NC)));
 
@@ -315,72 +338,90 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
     Where w0 = where(0), w1 = where(1), w2{-1, 0};      // of tiles t, t + 1, t + 2
     load(kr, k4, w0);
     load(vr, v4, w0);
-    kr.unpack(row_k, row & 7);
+    kr.to_tmem(tm_k);
     load(kr, k4, w1);
     w2 = where(2);
     tc::fence_proxy_async();
+    tc::fence_before_sync();
     __syncthreads();
     constexpr uint32_t idesc_s = idesc_f16(kTile, RP, 0, 0), idesc_o = idesc_f16(kD, RP, 1, 1);
     auto issue_s = [&](int t) {
-        const uint64_t dk = tc::smem_desc(base + C::k, 16, kRowGroup), dq = tc::smem_desc(base + C::q, 16, 1024);
+        const uint64_t dq = tc::smem_desc(base + C::q, 16, 1024);
 #pragma unroll
         for (int s = 0; s < 8; ++s)
-            tc::mma_bf16(tmem + (t & 1) * 64, dk + (((s >> 2) * 1024 + (s & 3) * 32) >> 4),
-                         dq + (((s >> 2) * C::q_half + (s & 3) * 32) >> 4), idesc_s, s > 0 ? 1u : 0u);
+            mma_ts(tmem + (t & 1) * 64, tmem + 192 + 8 * s, dq + (((s >> 2) * C::q_half + (s & 3) * 32) >> 4), idesc_s,
+                   s > 0 ? 1u : 0u);
         tc::mma_commit(bar_s);
     };
-    if (tid == 0)
+    if (tid == 0) {
+        tc::fence_after_sync();
         issue_s(0);
+    }
     for (int t = 0; t < ntiles; ++t) {
         // ---- S(t) has been read from K's buffer: K(t + 1) ----
         if (ok)
             ok = tc::mbar_wait(bar_s, t & 1);
+        tc::fence_after_sync();
+        __syncwarp();
         if (t + 1 < ntiles) {
-            kr.unpack(row_k, row & 7);
+            kr.to_tmem(tm_k);
             load(kr, k4, w2);
         }
         // ---- exponents of the weights ----
-        tc::fence_after_sync();
-        __syncwarp();
-        f32x2 x[NC / 2];
+        // Sixteen columns at a time, read from TMEM again where they are
+        // needed again: all of them would not fit beside the sums and the rows
+        // that are on their way.
         const uint32_t tm_st = tm_s + (t & 1) * 64;
+        f32x2 x[8];
         auto read = [&](uint32_t from) {
-            float v[NC];
-            tmem_load<NC>(from, v);
+            float v[16];
+            tc::tmem_ld16(from, v);
 #pragma unroll
-            for (int i = 0; i < NC / 2; ++i)
+            for (int i = 0; i < 8; ++i)
                 x[i] = f2_pack(v[2 * i], v[2 * i + 1]);
         };
-        read(tm_st);
         uint32_t seen = 0;
         if (t * kTile + row < T)
             seen = (uint32_t)(seg_mask[w0.meta / kPageSize] >> (half * NC)) & row_bits;
         const bool whole = __all_sync(kAll, seen == row_bits);
-        const ulonglong2 *cf = reinterpret_cast<const ulonglong2 *>(col_f + half * NC),
-                         *cy = reinterpret_cast<const ulonglong2 *>(col_y + half * NC);
-        auto hide = [&]() {
+        auto hide = [&](int c) {
 #pragma unroll
-            for (int i = 0; i < NC / 2; ++i) {
+            for (int i = 0; i < 8; ++i) {
                 const float2 v = f2_unpack(x[i]);
-                x[i] = f2_pack((seen >> (2 * i)) & 1u ? v.x : -INFINITY, (seen >> (2 * i + 1)) & 1u ? v.y : -INFINITY);
+                x[i] = f2_pack((seen >> (c + 2 * i)) & 1u ? v.x : -INFINITY, (seen >> (c + 2 * i + 1)) & 1u ? v.y : -INFINITY);
             }
         };
-        auto exponents = [&]() {
+        auto exponents = [&](int c) {       // of columns c .. c + 15
+            read(tm_st + c);
+            const ulonglong2 *cf = reinterpret_cast<const ulonglong2 *>(col_f + half * NC + c),
+                             *cy = reinterpret_cast<const ulonglong2 *>(col_y + half * NC + c);
+            if (uniform) {
 #pragma unroll
-            for (int i = 0; i < NC / 2; i += 2) {
-                const ulonglong2 f = cf[i / 2], y = cy[i / 2];
-                x[i] = f2_fma(x[i], f.x, y.x);
-                x[i + 1] = f2_fma(x[i + 1], f.y, y.y);
+                for (int i = 0; i < 8; i += 2) {
+                    const ulonglong2 y = cy[i / 2];
+                    x[i] = f2_fma(x[i], common, y.x);
+                    x[i + 1] = f2_fma(x[i + 1], common, y.y);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    const ulonglong2 f = cf[i / 2], y = cy[i / 2];
+                    x[i] = f2_fma(x[i], f.x, y.x);
+                    x[i + 1] = f2_fma(x[i + 1], f.y, y.y);
+                }
             }
             if (!whole)
-                hide();
+                hide(c);
         };
-        exponents();
         float top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < NC / 2; ++i) {
-            const float2 v = f2_unpack(x[i]);
-            top = fmaxf(top, fmaxf(v.x, v.y));
+        for (int c = 0; c < NC; c += 16) {
+            exponents(c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 v = f2_unpack(x[i]);
+                top = fmaxf(top, fmaxf(v.x, v.y));
+            }
         }
         tc::fence_proxy_async();
         tc::fence_before_sync();
@@ -396,18 +437,21 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
         if (raise) {
             // Maxima over the tile, from S again.
             tc::fence_after_sync();
-            read(tm_st);
-            hide();
-            float v[NC];
 #pragma unroll
-            for (int i = 0; i < NC / 2; ++i) {
-                const float2 y = f2_unpack(x[i]);
-                v[2 * i] = y.x;
-                v[2 * i + 1] = y.y;
+            for (int c = 0; c < NC; c += 16) {
+                read(tm_st + c);
+                hide(c);
+                float v[16];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 y = f2_unpack(x[i]);
+                    v[2 * i] = y.x;
+                    v[2 * i + 1] = y.y;
+                }
+                const float big = reduce_columns<true>(v, lane);        // (factors are positive)
+                if (lane < 16)
+                    red[(warp & 3) * RP + half * NC + c + lane] = big;
             }
-            const float big_s = reduce_columns<true, NC>(v, lane);      // (f is positive)
-            if (lane < NC)
-                red[(warp & 3) * RP + half * NC + lane] = big_s;
             __syncthreads();
             float now = 0.f, alpha = 1.f;
             if (tid < RP) {
@@ -422,47 +466,45 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
                 red[tid] = alpha;
             }
             __syncthreads();
-            const ulonglong2 *al = reinterpret_cast<const ulonglong2 *>(red + half * NC);
 #pragma unroll
-            for (int i = 0; i < NC / 2; i += 2) {
-                const ulonglong2 y = al[i / 2];
-                l[i] = f2_mul(l[i], y.x);
-                l[i + 1] = f2_mul(l[i + 1], y.y);
-            }
-            if (t > 0) {
-                read(tm_o);
+            for (int c = 0; c < NC; c += 16) {
+                const f32x2 *al = reinterpret_cast<const f32x2 *>(red + half * NC + c);
 #pragma unroll
-                for (int i = 0; i < NC / 2; i += 2) {
-                    const ulonglong2 y = al[i / 2];
-                    x[i] = f2_mul(x[i], y.x);
-                    x[i + 1] = f2_mul(x[i + 1], y.y);
+                for (int i = 0; i < 8; ++i)
+                    l[c / 2 + i] = f2_mul(l[c / 2 + i], al[i]);
+                if (t > 0) {
+                    read(tm_o + c);
+                    float v[16];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 y = f2_unpack(f2_mul(x[i], al[i]));
+                        v[2 * i] = y.x;
+                        v[2 * i + 1] = y.y;
+                    }
+                    tc::tmem_st16(tm_o + c, v);
                 }
-#pragma unroll
-                for (int i = 0; i < NC / 2; ++i) {
-                    const float2 y = f2_unpack(x[i]);
-                    v[2 * i] = y.x;
-                    v[2 * i + 1] = y.y;
-                }
-                tmem_store<NC>(tm_o, v);
             }
-            read(tm_st);
-            exponents();
         }
         // ---- P(t), V(t) ----
         uint8_t *dst = smem + C::p + row * 128;
 #pragma unroll
-        for (int i = 0; i < NC; i += 8) {
-            uint32_t w[4];
+        for (int c = 0; c < NC; c += 16) {
+            if (NC > 16 || raise)
+                exponents(c);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 y = f2_unpack(x[i / 2 + j]);
-                const float y0 = tc::ex2(y.x), y1 = tc::ex2(y.y);
-                l[i / 2 + j] = f2_add(l[i / 2 + j], f2_pack(y0, y1));
-                w[j] = f16x2(y0, y1);
+            for (int i = 0; i < 16; i += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 y = f2_unpack(x[i / 2 + j]);
+                    const float y0 = tc::ex2(y.x), y1 = tc::ex2(y.y);
+                    l[(c + i) / 2 + j] = f2_add(l[(c + i) / 2 + j], f2_pack(y0, y1));
+                    w[j] = f16x2(y0, y1);
+                }
+                *reinterpret_cast<uint4 *>(dst + ((((half * NC + c + i) >> 3) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            *reinterpret_cast<uint4 *>(dst + ((((half * NC + i) >> 3) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        vr.unpack(row_v, row & 7);
+        vr.to_smem(row_v, row & 7);
         load(vr, v4, w1);
         w0 = w1;
         w1 = w2;
@@ -484,16 +526,19 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
         ok = tc::mbar_wait(bar_o, (ntiles - 1) & 1);
     tc::fence_after_sync();
     {
-        float v[NC];
 #pragma unroll
-        for (int i = 0; i < NC / 2; ++i) {
-            const float2 y = f2_unpack(l[i]);
-            v[2 * i] = y.x;
-            v[2 * i + 1] = y.y;
+        for (int c = 0; c < NC; c += 16) {
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 y = f2_unpack(l[c / 2 + i]);
+                v[2 * i] = y.x;
+                v[2 * i + 1] = y.y;
+            }
+            const float sum = reduce_columns<false>(v, lane);
+            if (lane < 16)
+                red[(warp & 3) * RP + half * NC + c + lane] = sum;
         }
-        const float sum = reduce_columns<false, NC>(v, lane);
-        if (lane < NC)
-            red[(warp & 3) * RP + half * NC + lane] = sum;
     }
     const bool failed = __syncthreads_or(!ok);
     if (failed && tid == 0)
@@ -509,15 +554,15 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
         a.lse_part[(size_t)(cq0 + k) * Hq + h * G + (tid - k * G)] = lse2 == lse2 ? lse2 : INFINITY;
         col_f[tid] = sum == 0.f ? 0.f : ka.v_scale / sum;
     }
-    __syncwarp();
-    float o[NC];
-    tmem_load<NC>(tm_o, o);
     __syncthreads();
-    {
-        int r = half * NC;
+#pragma unroll
+    for (int c = 0; c < NC; c += 16) {
+        float o[16];
+        tc::tmem_ld16(tm_o + c, o);
+        const int r = half * NC + c;
         int k = r / G, j = r - k * G;
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
+        for (int i = 0; i < 16; ++i) {
             if (r + i < R)
                 a.o_part[((size_t)(cq0 + k) * Hq + h * G + j) * kD + row] = o[i] * col_f[r + i];
             if (++j == G) {
