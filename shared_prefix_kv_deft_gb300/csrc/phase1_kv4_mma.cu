@@ -222,72 +222,24 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
         const uint4 w = reinterpret_cast<const uint4 *>(p.mma_rmask)[rm0 + s];
         seg_mask[s] = (uint64_t)w.x | (uint64_t)w.z << (item < ka.mma_narrow ? 16 : 32);
     }
-    // ---- Q^T: bf16 -> fp16 times a power of two ----
-    bool uniform;
-    {
+    // The thread's piece of a row of Q, on its way while the pages are looked up.
         constexpr int TPR = kThreads / RP, DT = kD / TPR;   // threads of a row, dims of a thread
-        const int r = tid / TPR, piece = tid % TPR;
-        uint32_t w[DT / 2];
+        const int q_row = tid / TPR, piece = tid % TPR;
+        uint32_t qw[DT / 2];
 #pragma unroll
         for (int i = 0; i < DT / 2; ++i)
-            w[i] = 0u;
-        if (r < R) {
-            const int k = r / G;
+            qw[i] = 0u;
+        if (q_row < R) {
+            const int k = q_row / G;
             const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
-                                                               ((size_t)p.chunk_q[cq0 + k] * Hq + h * G + (r - k * G)) * kD + piece * DT);
+                                                               ((size_t)p.chunk_q[cq0 + k] * Hq + h * G + (q_row - k * G)) * kD + piece * DT);
 #pragma unroll
             for (int i = 0; i < DT / 8; ++i) {
                 const uint4 x = src[i];
-                w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
+                qw[4 * i] = x.x, qw[4 * i + 1] = x.y, qw[4 * i + 2] = x.z, qw[4 * i + 3] = x.w;
             }
         }
-        float big = 0.f;            // the row's largest finite magnitude
-#pragma unroll
-        for (int i = 0; i < DT / 2; ++i) {
-            const float2 x = bf16x2_to_float2(w[i] & 0x7fff7fffu);
-            big = x.x < INFINITY ? fmaxf(big, x.x) : big;
-            big = x.y < INFINITY ? fmaxf(big, x.y) : big;
-        }
-#pragma unroll
-        for (int o = 1; o < TPR; o <<= 1)
-            big = fmaxf(big, __shfl_xor_sync(kAll, big, o));
-        int e = big > 0.f ? 14 - ilogbf(big) : 1 << 20;        // (a row of zeros takes any)
-        // Rows within 2^8 of one another share the power of two, and with it
-        // the factor of their logits: fp16 holds the smallest one's elements
-        // down to 2^-31 of its largest.
-        if (piece == 0 && e < 1 << 20) {
-            atomicMin(ext, e);
-            atomicMax(ext + 1, e);
-        }
-        __syncthreads();
-        uniform = ext[1] - ext[0] <= 8;
-        if (uniform || e == 1 << 20)
-            e = ext[0] == 1000 ? 0 : ext[0];
-        // 2^e in two factors: e reaches from -113 to 147.
-        const int e1 = e / 2, e2 = e - e1;
-        const float up1 = pow2(e1), up2 = pow2(e2);
-#pragma unroll
-        for (int i = 0; i < DT / 8; ++i) {
-            uint32_t x[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 y = bf16x2_to_float2(w[4 * i + j]);
-                x[j] = f16x2(y.x * up1 * up2, y.y * up1 * up2);
-            }
-            const int chunk = piece * (DT / 8) + i;         // of the row's sixteen
-            *reinterpret_cast<uint4 *>(smem + C::q + (chunk >> 3) * C::q_half + r * 128 + (((chunk & 7) ^ (r & 7)) << 4)) =
-                make_uint4(x[0], x[1], x[2], x[3]);
-        }
-        // A column of no row has weights of 0: 2^(f * 0 - inf).
-        if (piece == 0) {
-            col_f[r] = a.scale_log2 * pow2(-e1) * ka.k_scale * pow2(-e2);
-            col_y[r] = r < R ? INFINITY : -INFINITY;
-        }
-    }
-    __syncthreads();
-    tc::fence_after_sync();
-    const uint32_t tmem = *tmem_slot;
-    const uint32_t tm_s = tmem + ((uint32_t)(warp & 3) << 21) + half * NC, tm_o = tm_s + 128;
+    __syncthreads();    // the segments
 
     // ---- rows of the chunk ----
     const int ntiles = (T + kTile - 1) / kTile;
@@ -323,6 +275,61 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
         else
             x.zero();
     };
+    HalfRow kr, vr;
+    Where w0 = where(0), w1 = where(1), w2{-1, 0};      // of tiles t, t + 1, t + 2
+    load(kr, k4, w0);
+    load(vr, v4, w0);
+    // ---- Q^T: bf16 -> fp16 times a power of two ----
+    bool uniform;
+    {
+        float big = 0.f;            // the row's largest finite magnitude
+#pragma unroll
+        for (int i = 0; i < DT / 2; ++i) {
+            const float2 x = bf16x2_to_float2(qw[i] & 0x7fff7fffu);
+            big = x.x < INFINITY ? fmaxf(big, x.x) : big;
+            big = x.y < INFINITY ? fmaxf(big, x.y) : big;
+        }
+#pragma unroll
+        for (int o = 1; o < TPR; o <<= 1)
+            big = fmaxf(big, __shfl_xor_sync(kAll, big, o));
+        int e = big > 0.f ? 14 - ilogbf(big) : 1 << 20;        // (a row of zeros takes any)
+        // Rows within 2^8 of one another share the power of two, and with it
+        // the factor of their logits: fp16 holds the smallest one's elements
+        // down to 2^-31 of its largest.
+        if (piece == 0 && e < 1 << 20) {
+            atomicMin(ext, e);
+            atomicMax(ext + 1, e);
+        }
+        __syncthreads();
+        uniform = ext[1] - ext[0] <= 8;
+        if (uniform || e == 1 << 20)
+            e = ext[0] == 1000 ? 0 : ext[0];
+        // 2^e in two factors: e reaches from -113 to 147.
+        const int e1 = e / 2, e2 = e - e1;
+        const float up1 = pow2(e1), up2 = pow2(e2);
+#pragma unroll
+        for (int i = 0; i < DT / 8; ++i) {
+            uint32_t x[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 y = bf16x2_to_float2(qw[4 * i + j]);
+                x[j] = f16x2(y.x * up1 * up2, y.y * up1 * up2);
+            }
+            const int chunk = piece * (DT / 8) + i;         // of the row's sixteen
+            *reinterpret_cast<uint4 *>(smem + C::q + (chunk >> 3) * C::q_half + q_row * 128 + (((chunk & 7) ^ (q_row & 7)) << 4)) =
+                make_uint4(x[0], x[1], x[2], x[3]);
+        }
+        // A column of no row has weights of 0: 2^(f * 0 - inf).
+        if (piece == 0) {
+            col_f[q_row] = a.scale_log2 * pow2(-e1) * ka.k_scale * pow2(-e2);
+            col_y[q_row] = q_row < R ? INFINITY : -INFINITY;
+        }
+    }
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t tm_s = tmem + ((uint32_t)(warp & 3) << 21) + half * NC, tm_o = tm_s + 128;
+
     uint8_t *row_v = smem + C::v + (row >> 3) * kRowGroup + half * 1024 + (row & 7) * 128;
     const uint32_t tm_k = tmem + ((uint32_t)(warp & 3) << 21) + 192 + half * 32;
     const f32x2 common = f2_pack(col_f[0], col_f[0]);
@@ -334,10 +341,6 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
     for (int i = 0; i < NC / 2; ++i)
         l[i] = f2_pack(0.f, 0.f);
     bool ok = true;
-    HalfRow kr, vr;
-    Where w0 = where(0), w1 = where(1), w2{-1, 0};      // of tiles t, t + 1, t + 2
-    load(kr, k4, w0);
-    load(vr, v4, w0);
     kr.to_tmem(tm_k);
     load(kr, k4, w1);
     w2 = where(2);
