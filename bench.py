@@ -263,10 +263,11 @@ class ClockSampler:
 # ---------------------------------------------------------------------------
 
 # Sources that decide what the phase-1 kernels read and write: the kernels,
-# their launch shapes and the planner (not the C-ABI glue, nor the prompt
-# path, which the timed steps do not run).
+# their launch shapes and the planner (not the C-ABI glue, nor the prompt path
+# and the calls of the 4-bit cache, which the timed steps do not run).
 HOST_GLUE = ("capi.cu", "noalloc.cu")
 PROMPT_PATH = ("kvcache.cu", "prompt.cu", "prompt_attn.cu", "prompt_internal.h", "prompt_plan.cpp")
+KV4_PATH = ("kv4.cuh", "kv4_internal.h", "phase1_kv4.cu", "phase1_kv4_mma.cu", "qkv.cu")
 
 
 def strip_comments(src: str) -> str:
@@ -299,7 +300,7 @@ def kernel_source_hash():
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "shared_prefix_kv_deft_gb300", "csrc")
     for f in sorted(os.listdir(csrc)):
-        if f.endswith((".cu", ".cuh", ".h", ".cpp")) and f not in HOST_GLUE + PROMPT_PATH:
+        if f.endswith((".cu", ".cuh", ".h", ".cpp")) and f not in HOST_GLUE + PROMPT_PATH + KV4_PATH:
             with open(os.path.join(csrc, f), encoding="utf-8") as fh:
                 h.update(strip_comments(fh.read()).encode())
     return h.hexdigest()[:16]

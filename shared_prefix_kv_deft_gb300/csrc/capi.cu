@@ -15,6 +15,7 @@
 #include <cuda_runtime.h>
 
 #include "deft_internal.h"
+#include "kv4_internal.h"
 
 namespace deft {
 
@@ -42,10 +43,12 @@ WorkLayout work_layout(int64_t slots, int32_t num_q_heads, int32_t head_dim)
     return w;
 }
 
-int prepare_step(const void *q, const void *k_pages, const void *v_pages, const int32_t *node_page_off,
-                 const int32_t *page_id, int32_t num_pages, int32_t num_q_heads, int32_t num_kv_heads,
-                 int32_t head_dim, int32_t page_size, float scale, const deft_plan_t *plan, void *out,
-                 int32_t out_dtype, float *lse, int32_t flags, AttnArgs &a, bool &use_mma, bool kv4)
+namespace {
+// prepare_step; kv4: a step over a 4-bit cache, whose kernels take any group.
+int prepare(const void *q, const void *k_pages, const void *v_pages, const int32_t *node_page_off,
+            const int32_t *page_id, int32_t num_pages, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+            int32_t page_size, float scale, const deft_plan_t *plan, void *out, int32_t out_dtype, float *lse,
+            int32_t flags, AttnArgs &a, bool &use_mma, bool kv4)
 {
     if (!plan || !q || !k_pages || !v_pages || !node_page_off || !page_id || !out || !lse)
         return DEFT_EINVAL;
@@ -92,9 +95,17 @@ int prepare_step(const void *q, const void *k_pages, const void *v_pages, const 
     return DEFT_OK;
 }
 
-namespace {
 __global__ void stream_order_kernel() {}
 }  // namespace
+
+int prepare_step(const void *q, const void *k_pages, const void *v_pages, const int32_t *node_page_off,
+                 const int32_t *page_id, int32_t num_pages, int32_t num_q_heads, int32_t num_kv_heads,
+                 int32_t head_dim, int32_t page_size, float scale, const deft_plan_t *plan, void *out,
+                 int32_t out_dtype, float *lse, int32_t flags, AttnArgs &a, bool &use_mma)
+{
+    return prepare(q, k_pages, v_pages, node_page_off, page_id, num_pages, num_q_heads, num_kv_heads, head_dim,
+                   page_size, scale, plan, out, out_dtype, lse, flags, a, use_mma, false);
+}
 
 // A step without a phase-1 item (every path empty) is the merge launch alone,
 // which reads its slot lists before its grid-dependency wait because a
@@ -214,8 +225,8 @@ int check_step(const void *q, const void *k_pages, const void *v_pages, const in
                int32_t out_dtype, float *lse, void *workspace, size_t workspace_bytes, int32_t flags, Step &st,
                bool kv4 = false)
 {
-    int rc = deft::prepare_step(q, k_pages, v_pages, node_page_off, page_id, num_pages, num_q_heads, num_kv_heads,
-                                head_dim, page_size, scale, plan, out, out_dtype, lse, flags, st.a, st.use_mma, kv4);
+    int rc = deft::prepare(q, k_pages, v_pages, node_page_off, page_id, num_pages, num_q_heads, num_kv_heads, head_dim,
+                           page_size, scale, plan, out, out_dtype, lse, flags, st.a, st.use_mma, kv4);
     if (rc != DEFT_OK)
         return rc;
     if (!plan->uploaded)

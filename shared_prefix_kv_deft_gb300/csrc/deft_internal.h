@@ -352,12 +352,11 @@ struct AttnArgs {
 // The argument checks shared by every step entry point (flags: DEFT_STEP_*).
 // On DEFT_OK, `a` holds everything but the workspace pointers (o_part,
 // lse_part) and use_mma says whether >= 16-row items run on the
-// tensor cores.  kv4: a step over a 4-bit cache, whose one kernel takes any
-// group.  The plan's upload state is the caller's to check.
+// tensor cores.  The plan's upload state is the caller's to check.
 int prepare_step(const void *q, const void *k_pages, const void *v_pages, const int32_t *node_page_off,
                  const int32_t *page_id, int32_t num_pages, int32_t num_q_heads, int32_t num_kv_heads,
                  int32_t head_dim, int32_t page_size, float scale, const deft_plan_t *plan, void *out,
-                 int32_t out_dtype, float *lse, int32_t flags, AttnArgs &a, bool &use_mma, bool kv4 = false);
+                 int32_t out_dtype, float *lse, int32_t flags, AttnArgs &a, bool &use_mma);
 
 // Launchers (return a cudaError_t cast to int; 0 = success).
 //
@@ -406,25 +405,6 @@ using LaunchTracer = std::function<int(const deft_trace_record &rec, void *strea
 // dp's host copy.  Returns a cudaError_t as int.
 int dispatch_step(AttnArgs a, const DevPartition &dp, const Partition &hp, bool use_mma, int32_t family,
                   void *stream, const LaunchTracer &trace);
-// A phase-1 launch over a 4-bit cache: items [first, first + n) of one of
-// the partition's two lists.
-struct Kv4Args {
-    AttnArgs a;                // k_pages, v_pages: the 4-bit pools
-    float k_scale, v_scale;
-    int32_t first, n;
-    int32_t wide;              // 1: of the tensor-core list
-    int32_t mma_narrow;        // tensor-core items below this have their row masks split at 16, not 32
-    int32_t heads;             // KV heads a CTA takes (1, 2 or 4)
-    int32_t head_groups;       // CTAs of an item
-    int32_t last;              // 1: not the step's first phase-1 launch
-};
-// Tensor-core items of at most 32 or 64 rows at head_dim 128.
-int launch_phase1_kv4_mma(const Kv4Args &ka, const DevPartition &p, int rows, void *stream);
-// dispatch_step over a 4-bit cache: phase-1 launches by width, and the merge
-// (phase1_kv4.cu).
-// max_slots: the most partials a query has.
-int dispatch_step4(const AttnArgs &a, const DevPartition &dp, const Partition &hp, float k_scale, float v_scale,
-                   int32_t max_slots, void *stream, const LaunchTracer &trace);
 // Row bucket of an item with `rows` rows: smallest b with rows <= 2^b.
 inline int row_bucket(int rows) { return rows <= 1 ? 0 : rows <= 2 ? 1 : rows <= 4 ? 2 : rows <= 8 ? 3 : 4; }
 // Rows per softmax warpgroup of a tensor-core item with `rows` rows (two

@@ -29,6 +29,7 @@
 // own ring of bulk copies, and join their states in shared memory at the end.
 // Every wait is bounded.
 #include "kv4.cuh"
+#include "kv4_internal.h"
 #include "merge.cuh"
 #include "tcgen05.cuh"
 

@@ -24,6 +24,7 @@
 // unpacked.  Sums of the weights stay with the threads until the end.  Every
 // wait is bounded.
 #include "kv4.cuh"
+#include "kv4_internal.h"
 #include "merge.cuh"
 #include "tcgen05.cuh"
 
