@@ -626,8 +626,8 @@ int deft_qkv_write(const void *q, const void *k, const void *v, int32_t in_dtype
  * nearest even; exact for g a power of two).  With a step's page_id listed
  * whole, the bf16 pages' table is node_page_off with page_id[i] = i.  An entry
  * outside [0, num_pages) leaves its page as it was; an entry may repeat.
- * All pools 16-byte aligned, the bf16 ones overlapping no input (DEFT_EINVAL
- * where they start at one); head_dim in {64, 128}, page_size 16
+ * The 4-bit pools 16-byte aligned, the bf16 ones 32-byte aligned and
+ * overlapping no input (DEFT_EINVAL where they start at one); head_dim in {64, 128}, page_size 16
  * (DEFT_EUNSUPPORTED), at most 2^18 heads.  Never allocates, never
  * synchronises; stream-ordered on `stream`; may be captured into a CUDA
  * graph.

@@ -691,7 +691,8 @@ def _qkv_args(q, k, v, slot, position, cos_sin, interleaved, q_norm, k_norm, eps
     """The checked arguments of the append calls up to q_out, the tensors they
     name, the heads and q_out itself."""
     shape, dt = k.shape, k.dtype
-    if len(shape) != 3 or v.shape != shape or v.dtype != dt or dt not in (_torch.bfloat16, _torch.float32):
+    bf16 = dt is _torch.bfloat16
+    if len(shape) != 3 or v.shape != shape or v.dtype is not dt or not (bf16 or dt is _torch.float32):
         raise ValueError("k and v must be alike: [tokens, heads, head_dim], bf16 or fp32")
     T, Hkv, d = shape
     ks, vs = k.stride(), v.stride()
@@ -700,41 +701,50 @@ def _qkv_args(q, k, v, slot, position, cos_sin, interleaved, q_norm, k_norm, eps
     if _index_tensor(slot, "slot") != T:
         raise ValueError("slot must have one entry per token")
     used = [k, v, slot]
-    Hq, qs, q_ptr, out_ptr = 0, 0, None, None
+    Hq = qs = 0
+    q_ptr = out_ptr = None
     if q is not None:
         q_shape, q_st = q.shape, q.stride()
-        if len(q_shape) != 3 or q_shape[0] != T or q_shape[2] != d or q.dtype != dt or not _heads_packed(q_shape, q_st):
+        if len(q_shape) != 3 or q_shape[0] != T or q_shape[2] != d or q.dtype is not dt or not _heads_packed(q_shape, q_st):
             raise ValueError("q must be [tokens, heads, head_dim] of k's dtype with the heads of a token contiguous")
         Hq, qs = q_shape[1], q_st[0]
         if q_out is None:
             with _allocating_for(stream):
                 q_out = _torch.empty((T, Hq, d), dtype=_torch.bfloat16, device=q.device)
-        elif q_out.shape != q_shape or q_out.dtype != _torch.bfloat16 or not q_out.is_contiguous():
+        elif q_out.shape != q_shape or q_out.dtype is not _torch.bfloat16 or not q_out.is_contiguous():
             raise ValueError("q_out must be contiguous bf16, shaped like q")
-        used += [q, q_out]
+        used += (q, q_out)
         q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None or q_norm is not None:
         raise ValueError("q_out and q_norm go with q")
     turn = None
     if cos_sin is not None or q_norm is not None or k_norm is not None:
-        turn = QkTurn(eps=eps)
-        for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
-            if w is not None:
-                if w.shape != (d,) or w.dtype != dt or not w.is_contiguous():
-                    raise ValueError(f"{name} must be a contiguous [head_dim] tensor of k's dtype")
-                setattr(turn, name, w.data_ptr())
-                used.append(w)
+        qn = kn = table = pos = None
+        rows = rot = 0
+        if q_norm is not None:
+            qn = _norm_pointer(q_norm, d, dt, "q_norm")
+            used.append(q_norm)
+        if k_norm is not None:
+            kn = _norm_pointer(k_norm, d, dt, "k_norm")
+            used.append(k_norm)
         if cos_sin is not None:
-            if cos_sin.dim() != 2 or cos_sin.dtype != _torch.float32 or not cos_sin.is_contiguous():
+            if cos_sin.dim() != 2 or cos_sin.dtype is not _torch.float32 or not cos_sin.is_contiguous():
                 raise ValueError("cos_sin must be contiguous fp32 [positions, rot_dim]")
             if position is None or _index_tensor(position, "position") != T:
                 raise ValueError("position must have one entry per token")
-            turn.num_positions, turn.rot_dim = cos_sin.shape
-            turn.cos_sin, turn.position, turn.interleaved = cos_sin.data_ptr(), position.data_ptr(), bool(interleaved)
-            used += [cos_sin, position]
-    args = (q_ptr, k.data_ptr(), v.data_ptr(), DEFT_OUT_BF16 if dt == _torch.bfloat16 else DEFT_OUT_F32, qs, ks[0], vs[0],
-            slot.data_ptr(), T, None if turn is None else ctypes.byref(turn), out_ptr)
+            rows, rot = cos_sin.shape
+            table, pos = cos_sin.data_ptr(), position.data_ptr()
+            used += (cos_sin, position)
+        turn = ctypes.byref(QkTurn(qn, kn, eps, rot, 1 if interleaved else 0, rows, table, pos))
+    args = (q_ptr, k.data_ptr(), v.data_ptr(), DEFT_OUT_BF16 if bf16 else DEFT_OUT_F32, qs, ks[0], vs[0], slot.data_ptr(), T,
+            turn, out_ptr)
     return args, used, (Hq, Hkv, d), q_out
+
+
+def _norm_pointer(w, head_dim, dtype, name):
+    if w.shape != (head_dim,) or w.dtype is not dtype or not w.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [head_dim] tensor of k's dtype")
+    return w.data_ptr()
 
 
 def deft_qkv_write(q, k, v, slot, k_pages, v_pages, position=None, cos_sin=None, interleaved: bool = False, q_norm=None,

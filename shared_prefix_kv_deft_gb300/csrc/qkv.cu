@@ -18,7 +18,9 @@
 //
 // Layout.  D / 16 lanes hold a head's row, two 8-element pieces each: pieces
 // (j, j + R/16) where the rotation pairs them, so that both elements of a
-// pair are in one lane, else (2j, 2j + 1).  A warp takes one or two rounds of
+// pair are in one lane, else (j, j + D/16), so that every access covers whole
+// sectors (with neighbouring pieces in a lane the v rows' 16-byte stores left
+// half sectors to the L2).  A warp takes one or two rounds of
 // 32 / (D / 16) heads of one kind (q, k or v) of one token, all loads ahead
 // of the arithmetic, on packed pairs; the token's cos and sin stay in
 // registers over them.  32768 tokens (32/8 heads of 128, bf16): 167 us, 4.9
@@ -117,11 +119,12 @@ __device__ __forceinline__ float square_sum(const f32x2 (&x)[4])
     return __fadd_rn(__fadd_rn(s[0], s[1]), __fadd_rn(s[2], s[3]));
 }
 
-// The lane's two pieces of a row, by where the rotation wants them.
+// The lane's two pieces of a row: j and j + half for the lanes j < half (where
+// the rotation pairs pieces half apart), 2j and 2j + 1 for the others.
 template <int D>
 struct Place {
-    static constexpr int kLanes = D / 16;   // lanes of a row
-    int half;     // > 0: lane j < half holds pieces j and j + half
+    static constexpr int kLanes = D / 16;   // lanes of a row; as `half`: no lane is another
+    int half;
     int j;        // lane in the row
     int p0, p1;   // its pieces
     __device__ __forceinline__ Place(int lane, int half_) : half(half_), j(lane % kLanes)
@@ -151,7 +154,7 @@ struct Place {
             }
             return __fadd_rn(a, b);
         }
-        float s = half == 0 ? __fadd_rn(a, b) : __fadd_rn(of(2 * j, a, b), of(2 * j + 1, a, b));
+        float s = __fadd_rn(of(2 * j, a, b), of(2 * j + 1, a, b));
 #pragma unroll
         for (int o = 1; o < kLanes; o <<= 1)
             s = __fadd_rn(s, __shfl_xor_sync(kAll, s, o));
@@ -161,11 +164,9 @@ struct Place {
     // piece of its block.
     __device__ __forceinline__ void block_max(float &a, float &b) const
     {
-        if (half == 0) {
-            a = b = kv4::max_nan(a, b);
-            return;
-        }
-        const float x = of(p0 ^ 1, a, b), y = of(p1 ^ 1, a, b);
+        const bool whole = half == kLanes;      // then the other piece is the neighbouring lane's
+        const float x = whole ? __shfl_xor_sync(kAll, a, 1) : of(p0 ^ 1, a, b);
+        const float y = whole ? __shfl_xor_sync(kAll, b, 1) : of(p1 ^ 1, a, b);
         a = kv4::max_nan(a, x);
         b = kv4::max_nan(b, y);
     }
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kF32>::kCtas) qkv_kernel(QkvAr
     if (kind != 0 && (uint32_t)slot >= (uint32_t)a.num_pages * kPageSize)
         return;
     const int half = kind == 2 ? 0 : a.half;
-    const Place<D> at(lane, a.split ? half : 0);
+    const Place<D> at(lane, a.split && half > 0 ? half : kLanes);
     const int head0 = part * (C * kRows) + sub;
 
     Piece<kF32> raw[C][2];
@@ -207,15 +208,16 @@ __global__ void __launch_bounds__(kThreads, Shape<kF32>::kCtas) qkv_kernel(QkvAr
             raw[c][1].zero();
         }
     }
-    // The lane's eight angles: of the elements of both its pieces, or of the
-    // pieces' pairs of neighbours.
-    const bool turns = at.j < half;
+    // The lane's eight angles: those of its elements (both pieces' are the
+    // same), or four for each piece's pairs of neighbours.
+    const bool turns0 = a.split ? at.j < half : at.p0 < 2 * half, turns1 = a.split ? turns0 : at.p1 < 2 * half;
     f32x2 cs[4], sn[4];
-    if (turns) {
+    if (turns0) {
         const int32_t pos = a.position[tok];
         if ((uint32_t)pos < (uint32_t)a.num_positions) {
-            const ulonglong2 *t = reinterpret_cast<const ulonglong2 *>(a.cos_sin + (int64_t)pos * half * 16) + at.j * 2;
-            const ulonglong2 c0 = __ldg(t), c1 = __ldg(t + 1), s0 = __ldg(t + half * 2), s1 = __ldg(t + half * 2 + 1);
+            const ulonglong2 *t = reinterpret_cast<const ulonglong2 *>(a.cos_sin + (int64_t)pos * half * 16);
+            const int i0 = a.split ? 2 * at.j : at.p0, i1 = a.split ? 2 * at.j + 1 : turns1 ? at.p1 : at.p0;
+            const ulonglong2 c0 = __ldg(t + i0), c1 = __ldg(t + i1), s0 = __ldg(t + half * 2 + i0), s1 = __ldg(t + half * 2 + i1);
             cs[0] = c0.x, cs[1] = c0.y, cs[2] = c1.x, cs[3] = c1.y;
             sn[0] = s0.x, sn[1] = s0.y, sn[2] = s1.x, sn[3] = s1.y;
         } else {
@@ -246,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kF32>::kCtas) qkv_kernel(QkvAr
                     x[p][i] = f2_mul(f2_mul(x[p][i], r2), w[i]);
             }
         }
-        if (turns) {
+        if (turns0) {
             if (a.split) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -260,6 +262,8 @@ __global__ void __launch_bounds__(kThreads, Shape<kF32>::kCtas) qkv_kernel(QkvAr
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {       // pair i % 4 of piece i / 4, angle i
+                    if (i == 4 && !turns1)
+                        break;
                     f32x2 &y = x[i / 4][i % 4];
                     const float2 v = f2_unpack(y), c2 = f2_unpack(cs[i / 2]), s2 = f2_unpack(sn[i / 2]);
                     const float co = i % 2 ? c2.y : c2.x, si = i % 2 ? s2.y : s2.x;
@@ -332,6 +336,11 @@ __global__ void __launch_bounds__(kThreads, Shape<kF32>::kCtas) qkv_kernel(QkvAr
     }
 }
 
+// Blocks a thread has in flight.  6007 pages of 8 heads of 128 (504 MB, 74 us at
+// the measured copy rate): 77.9 us, at 1 block 79.9; with two 16-byte stores in
+// place of one of 32 bytes, which leaves half sectors to the L2, 88.1 and more.
+constexpr int kUnpack = 4;
+
 struct UnpackArgs {
     const uint8_t *k4, *v4;
     const int32_t *page_id;
@@ -354,23 +363,37 @@ __global__ void __launch_bounds__(kThreads) unpack4_kernel(UnpackArgs a)
     const uint8_t *src = (is_v ? a.v4 : a.k4) + (int64_t)page * a.num_kv_heads * P::kBytes;
     uint4 *dst = (is_v ? a.v_pages : a.k_pages) + (int64_t)blockIdx.x * a.num_kv_heads * (kPageSize * D / 8);
     const int blocks = a.num_kv_heads * D;
-    for (int b = threadIdx.x; b < blocks; b += kThreads) {
-        const int h = b / D, i = b % D;
-        const uint8_t *head = src + (int64_t)h * P::kBytes;
-        const uint2 w = __ldcs(reinterpret_cast<const uint2 *>(head) + i);
-        const uint32_t s = __ldcs(head + P::kScales + i);
-        const uint32_t s2 = kv4::scales2(s | s << 8);
-        uint32_t h0[4], h1[4], o[8];
-        kv4::unpack8(w.x, h0);
-        kv4::unpack8(w.y, h1);
+    for (int b0 = threadIdx.x; b0 < blocks; b0 += kUnpack * kThreads) {
+        uint2 w[kUnpack];
+        uint32_t s[kUnpack];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const uint32_t t = kv4::hmul2(k < 4 ? h0[k & 3] : h1[k & 3], s2);
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&t));
-            o[k] = bf16x2(f.x * g, f.y * g);
+        for (int u = 0; u < kUnpack; ++u) {
+            const int b = b0 + u * kThreads;
+            if (b < blocks) {
+                const uint8_t *head = src + (int64_t)(b / D) * P::kBytes;
+                w[u] = __ldcs(reinterpret_cast<const uint2 *>(head) + b % D);
+                s[u] = __ldcs(head + P::kScales + b % D);
+            }
         }
-        dst[2 * b] = make_uint4(o[0], o[1], o[2], o[3]);
-        dst[2 * b + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+#pragma unroll
+        for (int u = 0; u < kUnpack; ++u) {
+            const int b = b0 + u * kThreads;
+            if (b >= blocks)
+                break;
+            const uint32_t s2 = kv4::scales2(s[u] | s[u] << 8);
+            uint32_t h0[4], h1[4], o[8];
+            kv4::unpack8(w[u].x, h0);
+            kv4::unpack8(w[u].y, h1);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t t = kv4::hmul2(k < 4 ? h0[k & 3] : h1[k & 3], s2);
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&t));
+                o[k] = bf16x2(f.x * g, f.y * g);
+            }
+            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + 2 * b), "r"(o[0]), "r"(o[1]),
+                         "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                         : "memory");
+        }
     }
 }
 
@@ -521,7 +544,7 @@ int deft_kv_unpack4(const void *k4_pages, const void *v4_pages, float k_scale, f
         return DEFT_OK;
     if (!page_id || !k_pages || !v_pages || k_pages == v_pages || k_pages == k4_pages || k_pages == v4_pages ||
         v_pages == k4_pages || v_pages == v4_pages ||
-        (((uintptr_t)k4_pages | (uintptr_t)v4_pages | (uintptr_t)k_pages | (uintptr_t)v_pages) & 15u))
+        (((uintptr_t)k4_pages | (uintptr_t)v4_pages) & 15u) || (((uintptr_t)k_pages | (uintptr_t)v_pages) & 31u))
         return DEFT_EINVAL;
     UnpackArgs a{static_cast<const uint8_t *>(k4_pages), static_cast<const uint8_t *>(v4_pages), page_id,
                  static_cast<uint4 *>(k_pages), static_cast<uint4 *>(v_pages), k_scale, v_scale,

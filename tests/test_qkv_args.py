@@ -66,7 +66,7 @@ def unpack_args(**kw):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(k4=None), EINVAL), (dict(v4=None), EINVAL), (dict(page_id=None), EINVAL), (dict(kp=None), EINVAL), (dict(vp=3 * A), EINVAL),
-    (dict(kp=A), EINVAL), (dict(vp=2 * A), EINVAL), (dict(kp=A + 8), EINVAL), (dict(num_pages=0), EINVAL), (dict(listed=-1), EINVAL),
+    (dict(kp=A), EINVAL), (dict(vp=2 * A), EINVAL), (dict(kp=3 * A + 16), EINVAL), (dict(k4=A + 8), EINVAL), (dict(num_pages=0), EINVAL), (dict(listed=-1), EINVAL),
     (dict(hkv=0), EINVAL), (dict(kg=0.0), EINVAL), (dict(vg=float("nan")), EINVAL), (dict(head_dim=96), EUNSUPPORTED),
     (dict(page_size=32), EUNSUPPORTED), (dict(listed=0), 0), (dict(hkv=1 << 19), EINVAL)])
 def test_unpack4_argument_checks(kw, status):
