@@ -23,10 +23,11 @@
 // half sectors to the L2).  A warp takes one or two rounds of
 // 32 / (D / 16) heads of one kind (q, k or v) of one token, all loads ahead
 // of the arithmetic, on packed pairs; the token's cos and sin stay in
-// registers over them.  32768 tokens (32/8 heads of 128, bf16): 167 us, 4.9
+// registers over them.  32768 tokens (32/8 heads of 128, bf16): 154 us, 5.35
 // TB/s; the 822 MB at the measured copy rate take 121.  Bound by issue slots
 // and loads in flight together: persistent CTAs fed by a ring of bulk copies
-// in shared memory took the same 164 us, with more instructions.
+// in shared memory took as long as rows read straight into registers, with
+// more instructions.
 #include <cstdint>
 
 #include "common.cuh"
@@ -41,9 +42,9 @@ constexpr int kWarps = kThreads / 32;
 constexpr unsigned kAll = 0xffffffffu;
 // Heads a group of lanes takes, and the CTAs that an SM is to hold (which sets
 // the registers): rows in flight against warps in flight.  32768 tokens of
-// bf16, 32/8 heads of 128: 1 and 5 196 us, 2 and 3 180, 2 and 4 163, 2 and 5
-// 193, 3 and 4 172; 10007 tokens of fp32, 12/4 heads of 64: 1 and 4 21.0 us, 1
-// and 5 20.4, 2 and 3 23.6.
+// bf16, 32/8 heads of 128: 2 and 4 154 us, 2 and 3 174, 2 and 5 178, 3 and 4
+// 160, 4 and 3 164, 1 and 5 194; 10007 tokens of fp32, 12/4 heads of 64: 1 and
+// 4 21.0 us, 1 and 5 20.4, 2 and 3 23.6 (18.6 since).
 template <bool kF32>
 struct Shape {
     static constexpr int kHeads = kF32 ? 1 : 2, kCtas = kF32 ? 5 : 4;
@@ -121,13 +122,13 @@ __device__ __forceinline__ float square_sum(const f32x2 (&x)[4])
 
 // The lane's two pieces of a row: j and j + half for the lanes j < half (where
 // the rotation pairs pieces half apart), 2j and 2j + 1 for the others.
-template <int D>
+template <int D, bool kWhole>
 struct Place {
     static constexpr int kLanes = D / 16;   // lanes of a row; as `half`: no lane is another
-    int half;
+    int half;                               // (kWhole: it is that)
     int j;        // lane in the row
     int p0, p1;   // its pieces
-    __device__ __forceinline__ Place(int lane, int half_) : half(half_), j(lane % kLanes)
+    __device__ __forceinline__ Place(int lane, int half_) : half(kWhole ? kLanes : half_), j(lane % kLanes)
     {
         const bool paired = j < half;
         p0 = paired ? j : 2 * j;
@@ -146,7 +147,7 @@ struct Place {
     // The row's sum of the pieces' sums, neighbours first.
     __device__ __forceinline__ float row_sum(float a, float b) const
     {
-        if (half == kLanes) {       // pieces j and j + kLanes: both halves of the row
+        if (kWhole || half == kLanes) {     // pieces j and j + kLanes: both halves of the row
 #pragma unroll
             for (int o = 1; o < kLanes; o <<= 1) {
                 a = __fadd_rn(a, __shfl_xor_sync(kAll, a, o));
@@ -164,7 +165,7 @@ struct Place {
     // piece of its block.
     __device__ __forceinline__ void block_max(float &a, float &b) const
     {
-        const bool whole = half == kLanes;      // then the other piece is the neighbouring lane's
+        const bool whole = kWhole || half == kLanes;    // then the other piece is the neighbouring lane's
         const float x = whole ? __shfl_xor_sync(kAll, a, 1) : of(p0 ^ 1, a, b);
         const float y = whole ? __shfl_xor_sync(kAll, b, 1) : of(p1 ^ 1, a, b);
         a = kv4::max_nan(a, x);
@@ -172,7 +173,8 @@ struct Place {
     }
 };
 
-template <int D, bool kF32, bool k4>
+// kWhole: the rotation turns whole heads, in halves.
+template <int D, bool kF32, bool k4, bool kWhole>
 __global__ void __launch_bounds__(kThreads, Shape<kF32>::kCtas) qkv_kernel(QkvArgs a)
 {
     constexpr int kLanes = D / 16, kRows = 32 / kLanes, C = Shape<kF32>::kHeads;
@@ -192,8 +194,9 @@ __global__ void __launch_bounds__(kThreads, Shape<kF32>::kCtas) qkv_kernel(QkvAr
     // (An unsigned comparison: a negative slot is past the end too.)
     if (kind != 0 && (uint32_t)slot >= (uint32_t)a.num_pages * kPageSize)
         return;
-    const int half = kind == 2 ? 0 : a.half;
-    const Place<D> at(lane, a.split && half > 0 ? half : kLanes);
+    const int half = kind == 2 ? 0 : kWhole ? kLanes : a.half;
+    const bool split = kWhole || a.split;
+    const Place<D, kWhole> at(lane, split && half > 0 ? half : kLanes);
     const int head0 = part * (C * kRows) + sub;
 
     Piece<kF32> raw[C][2];
@@ -210,13 +213,13 @@ __global__ void __launch_bounds__(kThreads, Shape<kF32>::kCtas) qkv_kernel(QkvAr
     }
     // The lane's eight angles: those of its elements (both pieces' are the
     // same), or four for each piece's pairs of neighbours.
-    const bool turns0 = a.split ? at.j < half : at.p0 < 2 * half, turns1 = a.split ? turns0 : at.p1 < 2 * half;
+    const bool turns0 = split ? at.j < half : at.p0 < 2 * half, turns1 = split ? turns0 : at.p1 < 2 * half;
     f32x2 cs[4], sn[4];
     if (turns0) {
         const int32_t pos = a.position[tok];
         if ((uint32_t)pos < (uint32_t)a.num_positions) {
             const ulonglong2 *t = reinterpret_cast<const ulonglong2 *>(a.cos_sin + (int64_t)pos * half * 16);
-            const int i0 = a.split ? 2 * at.j : at.p0, i1 = a.split ? 2 * at.j + 1 : turns1 ? at.p1 : at.p0;
+            const int i0 = split ? 2 * at.j : at.p0, i1 = split ? 2 * at.j + 1 : turns1 ? at.p1 : at.p0;
             const ulonglong2 c0 = __ldg(t + i0), c1 = __ldg(t + i1), s0 = __ldg(t + half * 2 + i0), s1 = __ldg(t + half * 2 + i1);
             cs[0] = c0.x, cs[1] = c0.y, cs[2] = c1.x, cs[3] = c1.y;
             sn[0] = s0.x, sn[1] = s0.y, sn[2] = s1.x, sn[3] = s1.y;
@@ -249,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kF32>::kCtas) qkv_kernel(QkvAr
             }
         }
         if (turns0) {
-            if (a.split) {
+            if (split) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     // (Scalar: the assembler fuses packed products into the
@@ -407,7 +410,7 @@ int launch(void (*kernel)(Args), dim3 grid, cudaStream_t st, const Args &a)
     return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? DEFT_OK : DEFT_ECUDA;
 }
 
-template <int D, bool kF32, bool k4>
+template <int D, bool kF32, bool k4, bool kWhole>
 int launch_qkv(QkvArgs a, cudaStream_t st)
 {
     constexpr int kRound = Shape<kF32>::kHeads * (32 / (D / 16));   // heads a warp takes
@@ -416,13 +419,17 @@ int launch_qkv(QkvArgs a, cudaStream_t st)
     const int64_t tasks = (int64_t)a.num_tokens * (a.q_tasks + 2 * a.kv_tasks);
     if (tasks > INT32_MAX)
         return DEFT_EUNSUPPORTED;
-    return launch(qkv_kernel<D, kF32, k4>, dim3((unsigned)((tasks + kWarps - 1) / kWarps)), st, a);
+    return launch(qkv_kernel<D, kF32, k4, kWhole>, dim3((unsigned)((tasks + kWarps - 1) / kWarps)), st, a);
 }
 
 template <int D, bool k4>
 int pick_qkv(const QkvArgs &a, bool f32, cudaStream_t st)
 {
-    return f32 ? launch_qkv<D, true, k4>(a, st) : launch_qkv<D, false, k4>(a, st);
+    // (With the rotation's place known: 32768 tokens 162 -> 154 us, 16384 into
+    // 4 bits and back 116 -> 106 us.)
+    if (a.split && a.half == D / 16)
+        return f32 ? launch_qkv<D, true, k4, true>(a, st) : launch_qkv<D, false, k4, true>(a, st);
+    return f32 ? launch_qkv<D, true, k4, false>(a, st) : launch_qkv<D, false, k4, false>(a, st);
 }
 
 bool good_scale(float g)
