@@ -250,6 +250,38 @@ def test_queries_of_any_magnitude(power):
     check(t, want, scale=0.25)
 
 
+@pytest.mark.parametrize("queries", [3, 20, 50])
+def test_rows_of_very_different_magnitudes(queries):
+    """Rows of one item from 2^-40 to 2^20 of one another, one of zeros; and
+    rows near one another, all tiny."""
+    t = Tree([-1] + [0] * queries, [700] + [3 + i % 20 for i in range(queries)], list(range(1, queries + 1)), 2, 2, 128, seed=queries)
+    q = t.q.copy()
+    e = np.random.default_rng(1).integers(-40, 4, (queries, 4, 1))
+    t.q = f64(torch.from_numpy((q * 2.0 ** e).astype(np.float32)).bfloat16())
+    t.q[1, 2] = 0
+    check(t, t.run(t.plan()))
+    t.q = q * 2.0 ** -90
+    check(t, t.run(t.plan(), scale=2.0 ** 86), scale=2.0 ** 86)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_pools_that_start_at_any_16_bytes(d):
+    t = Tree([-1] + [0] * 20, [500] + [40] * 20, list(range(1, 21)), 2, 1, d)
+    plan = t.plan()
+    q, k4, v4, off, ids = t.tensors()
+    want = deft.deft_tree_attn4(q, k4, v4, off, ids, plan)
+    for by in (16, 48):
+        moved = []
+        for p in (k4, v4):
+            flat = torch.empty(p.numel() + 64, dtype=torch.uint8, device="cuda")
+            at = flat[by:by + p.numel()].view(p.shape)
+            at.copy_(p)
+            assert at.data_ptr() % 32 == 16
+            moved.append(at)
+        got = deft.deft_tree_attn4(q, *moved, off, ids, plan)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_rows_that_are_not_finite():
     """An infinite or NaN query element, a NaN key: NaN in the rows that reach
     it, all others as without it."""
@@ -271,6 +303,19 @@ def test_rows_that_are_not_finite():
     hit[[0, 3], 4:] = True
     assert np.isnan(out[hit]).all() and not np.isfinite(lse[hit]).any()
     assert (out[~hit] == f64(base[0])[~hit]).all()
+
+
+def test_rows_that_are_not_finite_among_many():
+    """The same where the prefix is one item of 40 rows."""
+    t = Tree([-1] + [0] * 20, [600] + [17] * 20, list(range(1, 21)), 2, 2, 128)
+    plan = t.plan()
+    base = [f64(x) for x in t.run(plan)]
+    t.q[4, 0, 9], t.q[11, 3, 100], t.q[19, 1, 0] = np.inf, np.nan, -np.inf
+    out, lse = (f64(x) for x in t.run(plan))
+    hit = np.zeros((20, 4), bool)
+    hit[4, 0] = hit[11, 3] = hit[19, 1] = True
+    assert np.isnan(out[hit]).any(-1).all() and np.isnan(lse[hit]).all()
+    assert (out[~hit] == base[0][~hit]).all() and (lse[~hit] == base[1][~hit]).all()
 
 
 def test_long_path():

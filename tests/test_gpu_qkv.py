@@ -345,6 +345,26 @@ def test_rows_behind_4gb():
         assert (f64(vp[t, :, s % 16]) == ref.values(c, sc, 1.0)).all()
 
 
+def test_pools_that_start_at_any_16_bytes():
+    r = Rows(T=20, hq=2, hkv=2, d=64, rot=64)
+    a = r.pools4()
+    q = deft.deft_qkv_write4(r.q, r.k, r.v, cu(r.slot), *a, **r.kw)
+    b = [torch.empty(p.numel() + 16, dtype=torch.uint8, device="cuda")[16:].view(p.shape).fill_(0xA5) for p in a]
+    q2 = deft.deft_qkv_write4(r.q, r.k, r.v, cu(r.slot), *b, **r.kw)
+    assert torch.equal(q, q2) and torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    ids = cu(np.arange(r.pages))
+    assert torch.equal(deft.deft_kv_unpack4(*a, ids)[0], deft.deft_kv_unpack4(*b, ids)[0])
+    n = r.pages * 2 * 16 * 64
+    out = [torch.empty(n + 8, dtype=torch.bfloat16, device="cuda")[8:].view(r.pages, 2, 16, 64) for _ in "kv"]
+    with pytest.raises(deft.DeftError):      # 32-byte stores
+        deft.deft_kv_unpack4(*a, ids, *out)
+    deft.deft_qkv_write(r.q, r.k, r.v, cu(r.slot), *out, **r.kw)
+    c = r.pools()
+    deft.deft_qkv_write(r.q, r.k, r.v, cu(r.slot), *c, **r.kw)
+    kept = np.arange(r.T)
+    assert (r.at(f64(out[0]), kept) == r.at(f64(c[0]), kept)).all() and (r.at(f64(out[1]), kept) == r.at(f64(c[1]), kept)).all()
+
+
 def test_stream_and_graph():
     """On a stream of its own, allocating its output there, and captured."""
     r = Rows(T=64, hq=8, hkv=2, d=128, rot=128)
