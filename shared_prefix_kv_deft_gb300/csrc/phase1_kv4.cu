@@ -222,11 +222,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
     const uint32_t my_rows = (uint32_t)(row_bits >> row0) & (uint32_t)((1ull << NR) - 1);
 
     // ---- slices: 32 at a time, each held (and its copy issued) by a lane ----
-    const uint8_t *k4 = static_cast<const uint8_t *>(a.k_pages), *v4 = static_cast<const uint8_t *>(a.v_pages);
     const uint64_t pol = tc::l2_kv_policy(false);
     const uint32_t ring = base + warp * kStages * C::kStage;
     // The lane's slice of the batch of steps from `first` on.
-    auto get_slice = [&](int first, size_t &at, uint32_t &desc) {
+    auto get_slice = [&](int first, const uint8_t *&k, const uint8_t *&v, uint32_t &desc) {
         const int i = first + lane / PP, x = (ts + i * TS) * PP + lane % PP;
         desc = 0;               // no token
         if (i >= mine || x >= total)
@@ -245,29 +244,29 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
             j = x - seg_first[seg];
             pg = seg_page[seg], begin = seg_begin[seg], len = seg_len[seg], mask = seg_mask[seg];
         }
-        at = ((size_t)a.page_id[pg + j] * Hkv + h) * P::kBytes;
+        const size_t at = ((size_t)a.page_id[pg + j] * Hkv + h) * P::kBytes;
+        k = static_cast<const uint8_t *>(a.k_pages) + at;
+        v = static_cast<const uint8_t *>(a.v_pages) + at;
         const int lo = max(0, begin - j * kPageSize), hi = min(kPageSize, begin + len - j * kPageSize);
         desc = slice_desc(seg, lo, hi, hi - lo == kPageSize && ((uint32_t)(mask >> row0) & my_rows) == my_rows);
     };
-    size_t next_at = 0;
+    const uint8_t *next_k = nullptr, *next_v = nullptr;
     uint32_t cur = 0, next = 0;     // the batch in hand, and the one whose copies go out
-    int next_batch = 0;
-    get_slice(0, next_at, next);
+    get_slice(0, next_k, next_v, next);
     cur = next;
+    const uint32_t lane_ring = ring + lane % PP * C::kPage;
     auto issue = [&](int i) {
-        if (i / kBatch != next_batch) {
-            next_batch = i / kBatch;
-            get_slice(next_batch * kBatch, next_at, next);
-        }
-        const int first = i % kBatch * PP, n = min(PP, total - (ts + i * TS) * PP);
-        const uint32_t dst = ring + (i % kStages) * C::kStage, bar = bars + (i % kStages) * 8;
+        const int first = i % kBatch * PP;
+        if (first == 0 && i > 0)
+            get_slice(i, next_k, next_v, next);
+        const uint32_t bar = bars + (i % kStages) * 8;
         if (lane == first)
-            tc::mbar_arrive_expect_tx(bar, n * C::kPage);
+            tc::mbar_arrive_expect_tx(bar, min(PP, total - (ts + i * TS) * PP) * C::kPage);
         __syncwarp();
-        if (lane >= first && lane < first + n) {
-            const uint32_t to = dst + (lane - first) * C::kPage;
-            tc::bulk_load(to, k4 + next_at, P::kBytes, bar, pol);
-            tc::bulk_load(to + P::kBytes, v4 + next_at, P::kBytes, bar, pol);
+        if (lane / PP == i % kBatch && next != 0) {
+            const uint32_t to = lane_ring + (i % kStages) * C::kStage;
+            tc::bulk_load(to, next_k, P::kBytes, bar, pol);
+            tc::bulk_load(to + P::kBytes, next_v, P::kBytes, bar, pol);
         }
     };
     __syncwarp();   // the barriers are there
@@ -358,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
             ok = false;
             break;
         }
-        const uint8_t *stage = smem + (warp * kStages + i % kStages) * C::kStage;
+        uint8_t *stage = smem + (warp * kStages + i % kStages) * C::kStage;
         // ---- S^T ----
         float s[PP][NT][4];
 #pragma unroll
@@ -438,7 +437,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
                             x[p2][n][j] = -INFINITY;
                         }
                     }
+                // What a page holds beside the segment's tokens may be
+                // anything: V's scales there become 0.
+                constexpr int kWords = P::kScaleRow / 4;        // of a token's scales
+                uint32_t *sc = reinterpret_cast<uint32_t *>(stage + p2 * C::kPage + P::kBytes + P::kScales);
+                if (lane < kPageSize * kWords && (lane / kWords < lo || lane / kWords >= hi))
+                    sc[lane] = 0u;
             }
+            tc::fence_proxy_async();    // (the stage's next page is a bulk copy)
+            __syncwarp();
         }
 #pragma unroll
         for (int p2 = 0; p2 < PP; ++p2)
@@ -496,16 +503,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
 #pragma unroll
         for (int p2 = 0; p2 < PP; ++p2) {
             const uint8_t *vs = stage + p2 * C::kPage + P::kBytes;
-            const int lo = desc[p2] >> 8 & 255, hi = desc[p2] & 255;
             uint32_t sv[2], vw[2][2][VW];     // by token pair: scales, words of both tokens
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const uint8_t *sx = vs + P::kScales + (D == 128 ? g : g >> 1);
-                uint32_t x = sx[(vx + 8 * q) * P::kScaleRow], y = sx[(vy + 8 * q) * P::kScaleRow];
-                if (!whole) {   // (what a page holds beside the segment's tokens may be anything)
-                    x = vx + 8 * q >= lo && vx + 8 * q < hi ? x : 0u;
-                    y = vy + 8 * q >= lo && vy + 8 * q < hi ? y : 0u;
-                }
+                const uint32_t x = sx[(vx + 8 * q) * P::kScaleRow], y = sx[(vy + 8 * q) * P::kScaleRow];
                 sv[q] = kv4::scales2(x | y << 8);
                 const uint8_t *rx = vs + (vx + 8 * q) * P::kRow + g * (D / 16), *ry = vs + (vy + 8 * q) * P::kRow + g * (D / 16);
                 if constexpr (D == 128) {
