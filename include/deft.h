@@ -649,17 +649,19 @@ int deft_kv_unpack4(const void *k4_pages, const void *v4_pages, float k_scale, f
  *   - Every product and sum is taken from the cache's exact values: fp16
  *     products of q and c * s (both exact) summed in fp32, weights rounded
  *     to fp16 (2^-11), the sums and lse in fp32.
- *   - Any gqa_group a plan takes (1..64), head_dim in {64, 128}; one launch
- *     for all row counts, then the merge of the queries that need it.  A
+ *   - Any gqa_group a plan takes (1..64), head_dim in {64, 128}; a launch
+ *     for each width of work items that the plan has (up to 8, to 15, to 32
+ *     and to 64 rows), then the merge of the queries that need it.  A
  *     chunk of 256 tokens is 36 KB a head here: a larger chunk_target (512,
  *     1024) leaves fewer partials to merge where there are requests or
  *     branches enough to fill the device.
  *   - Cache slots past a node's last token never affect a result, whatever
  *     they hold.  A block whose scale is NaN (written from a NaN) counts as
  *     NaN: in K for the rows that attend its token, in V for every row of the
- *     work item that reads its page.  q may hold anything: a row with a logit
- *     that is NaN or +infinity has NaN in out and lse; no other row is
- *     affected.  page_id and node_page_off are trusted, as in
+ *     work item that reads its page.  q may hold anything: a row with an
+ *     infinity or NaN of its own, and one with a logit that is NaN or above
+ *     fp32's largest, has NaN in out and lse (a logit below fp32's least may
+ *     give NaN too); no other row is affected.  page_id and node_page_off are trusted, as in
  *     deft_tree_attn (page_id may be NULL where no path has a token).
  * out 16-byte aligned (DEFT_EINVAL).  Several steps of one plan may run at
  * the same time, each with its own outputs and workspace (this call does not use the plan's work queues).  A

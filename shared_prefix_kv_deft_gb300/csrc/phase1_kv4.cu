@@ -1,5 +1,7 @@
 // phase1_kv4.cu -- phase-1 partial attention of a tree step over a 4-bit KV
-// cache (kv4.cuh), for every row count and both head sizes.
+// cache (kv4.cuh) on mma.sync, for units of up to 15 rows, and at head_dim 64
+// for all (phase1_kv4_mma.cu: 16 to 64 rows at head_dim 128); the merge of
+// the partials; the step's launches.
 //
 // A unit is (work item, KV head), as in the bf16 kernels: for the unit's rows
 // r (a query and a member of its head group) over the chunk's tokens j that
@@ -24,10 +26,24 @@
 // passes it by more than 2^4: at most 2^15, and weights down to 2^-35 of the
 // largest count.
 //
-// A CTA of four warps takes a unit.  Rows beyond 16 go to further warps;
-// the warps of 16 rows deal the unit's pages among themselves, each with its
-// own ring of bulk copies, and join their states in shared memory at the end.
-// Every wait is bounded.
+// A warp takes a unit, fed by its own ring of bulk copies (four pages), and a
+// CTA of four warps the KV heads of an item, which share its tables; where
+// that leaves SMs idle (heads_per_cta), two or four warps deal a unit's pages
+// among themselves and join their states in shared memory at the end.  Up to
+// 8 rows a step takes two pages, so that two chains of products and
+// exponentials overlap.  Every wait is bounded.
+//
+// What bounds it is the warps' latency: 64 requests of 64 to 8192 tokens,
+// 32/8 heads of 128, step of 37.4 us for 115 MB (17 us at the measured copy
+// rate).  A page costs a warp some 300 instructions, half of them on the ALU
+// pipe (unpacking, its floor, is 128: a conversion to a pair of fp16 is one
+// instruction with any byte of its operand for free, masking and shifting V's
+// nibbles together six a word), and each scheduler issues one in two cycles
+// from its four warps.  Measured and left: bytes put apart by mul.hi or the
+// pairs made by integer arithmetic (44.7, 48.4 us, then against 37.9), five
+// CTAs an SM with fewer registers (39.1).
+#include <cfloat>
+
 #include "kv4.cuh"
 #include "kv4_internal.h"
 #include "merge.cuh"
@@ -38,6 +54,7 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr float kUp = 4.f, kLift = 11.f;
+#define kNaN __int_as_float(0x7fffffff)
 constexpr unsigned kAll = 0xffffffffu;
 
 template <int D, int NT>
@@ -55,7 +72,7 @@ struct Cfg {
     static constexpr uint32_t seg = q + (kQSmem ? kWarps * NT * (D / 32) * 512 : 0);
     static constexpr uint32_t bars = seg + kMaxSegsPerChunk * 24 + 8;     // [256] mask (8 B), page, begin, len; [257] first slice
     static constexpr uint32_t total = bars + kWarps * kStages * 8;
-    static constexpr int kCtas = NT == 1 ? 4 : NT == 2 ? 3 : 2;           // that an SM is meant to hold
+    static constexpr int kCtas = NT == 1 ? 4 : NT == 2 ? 3 : 2;           // that an SM is to hold
     static_assert(kStage % 16 == 0 && q % 16 == 0 && seg % 8 == 0 && bars % 8 == 0, "alignment");
     static_assert((total + 1024) * kCtas <= 228 * 1024, "shared memory of an SM");
 };
@@ -89,9 +106,10 @@ __device__ __forceinline__ float pow2(int e)   // -126 <= e <= 127
 
 // The exponent of the power of two that puts a row's largest finite
 // magnitude in [2^14, 2^15): N pairs of bf16 in each of the row's LANES
-// neighbouring lanes (-113 to 147; 0 for a row of zeros).
+// neighbouring lanes (-113 to 147; 0 for a row of zeros).  Infinities become
+// NaN, so that a logit of -inf is a masked one.
 template <int N, int LANES>
-__device__ __forceinline__ int row_exponent(const uint32_t (&w)[N])
+__device__ __forceinline__ int row_exponent(uint32_t (&w)[N])
 {
     uint32_t big = 0;               // magnitudes order as integers
 #pragma unroll
@@ -107,6 +125,7 @@ __device__ __forceinline__ int row_exponent(const uint32_t (&w)[N])
         for (int i = 0; i < N; ++i) {
             const uint32_t lo = w[i] & 0x7fffu, hi = w[i] >> 16 & 0x7fffu;
             big = max(big, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+            w[i] |= (lo == 0x7f80u ? 0x40u : 0u) | (hi == 0x7f80u ? 0x400000u : 0u);
         }
 #pragma unroll
         for (int o = 1; o < LANES; o <<= 1)
@@ -298,7 +317,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
         }
         // 2^e, in two factors for rows below 2^-112 (e reaches 147).
         const int e = row_exponent<KW * 4, 4>(w), e1 = min(e, 126), e2 = e - e1;
-        const float up = pow2(e1), fr = a.scale_log2 * pow2(-e1) * ka.k_scale * pow2(-e2);
+        // (A factor past fp32, for a row near its end, leaves logits of 0.)
+        const float up = pow2(e1), fr = fminf(a.scale_log2 * pow2(-e1) * ka.k_scale * pow2(-e2), FLT_MAX);
         f[n][0] = __shfl_sync(kAll, fr, 8 * t);
         f[n][1] = __shfl_sync(kAll, fr, 8 * t + 4);
         if (e2 == 0) {
@@ -467,6 +487,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
                     y = fmaxf(y, __shfl_xor_sync(kAll, y, 8));
                     y = fmaxf(y, __shfl_xor_sync(kAll, y, 16));
                     y = fmaxf(m[n][j], y - kLift);
+                    y = y == INFINITY ? kNaN : y;       // a logit past fp32: for good, through l
                     const float alpha = y == m[n][j] ? 1.f : tc::ex2(m[n][j] - y);
                     m[n][j] = y;
                     l[n][j] *= alpha;
@@ -555,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
             report_failure(p.status, 401);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-            l[n][0] = l[n][1] = __int_as_float(0x7fffffff);
+            l[n][0] = l[n][1] = kNaN;
     }
 
     // ---- the states of the warps that shared the slices, joined by halves:
@@ -682,8 +703,9 @@ int heads_per_cta(int64_t items, int32_t hkv, int most, int64_t slots)
 // The merge of each row's partials by their lse, as phase2.cu's, with W warps
 // a row: a path of many chunks (33 of 256 tokens in 8192) is read by four
 // warps at once instead of in a chain of 16 loads and then one after another
-// (measured on 64 requests of 64 to 8192 tokens).  Also, lse is NaN
-// where a logit was.
+// (64 requests of 64 to 8192 tokens in chunks of 256; with at most 8 partials
+// a row a warp reads them all at once, and four warps only added a barrier).
+// Also, lse is NaN where a logit was.
 template <int D, int W>
 __global__ void __launch_bounds__(kThreads) merge4_kernel(AttnArgs a, const int32_t *__restrict__ q_slot_off,
                                                           const int32_t *__restrict__ q_slot,

@@ -5,14 +5,24 @@
 // Tokens on the MMA's M, rows on its N, as in the bf16 kernel:
 //     S^T[128 tok x RP]  = K_tile . Q^T            (TMEM, fp32)
 //     O^T[128 d   x RP] += V_tile^T . P^T          (TMEM, fp32)
-// RP = 32 or 64.  The cache's 4 bits become fp16 in shared memory once for
-// all rows: a thread takes half a row of K and of V of every tile (32 bytes
-// and four scales each, fetched a tile ahead straight into registers), 128
-// rows a tile from wherever the chunk's tokens lie, none beside them.  At 64
-// rows a token costs a thread its unpacking (some 90 instructions for 64
-// elements of K and as many of V) and 32 exponentials; mma.sync, at an eighth
-// of the tensor rate and with every fragment unpacked again for each 32 rows,
-// took four times as long.
+// RP = 32 or 64.  The cache's 4 bits become fp16 once for all rows, K's in
+// TMEM (the first operand of its product may lie there) and V's in shared
+// memory: a thread takes half a row of K and of V of every tile (32 bytes and
+// four scales each, fetched a tile ahead straight into registers), 128 rows a
+// tile from wherever the chunk's tokens lie, none beside them.  At 64 rows a
+// token costs a thread its unpacking (some 90 instructions for 64 elements of
+// K and as many of V) and 32 exponentials; mma.sync, at an eighth of the
+// tensor rate and with every fragment unpacked again for each 32 rows, took
+// 182 us where this takes 106 (the step on a document of 32768 tokens with 64
+// branches of 64 to 8192, 32/8 heads: 36 GFLOP), 44 where 32 (32 branches of
+// 256 tokens on a prompt of 4096, 32/32 heads).
+//
+// What bounds it is the tile's chain: 2.3 us for 128 tokens of a unit, two
+// units an SM, of which the tensor products are a fifth; the rest is issue
+// slots, the stores and reads of V, P and S, and two barriers.  One CTA an SM
+// with twice the registers: 155 us for the 106; 512 threads with a quarter
+// row each: 231 (64 registers spill); fewer registers than 128, for room
+// beside the other launch: 111 to 126.
 //
 // A CTA of eight warps takes one unit, and two CTAs share an SM: one unpacks
 // and exponentiates while the other waits.  All warps do the same work.  For
@@ -23,6 +33,8 @@
 // P(t).V(t) is issued.  Both products so run while the next operand is
 // unpacked.  Sums of the weights stay with the threads until the end.  Every
 // wait is bounded.
+#include <cfloat>
+
 #include "kv4.cuh"
 #include "kv4_internal.h"
 #include "merge.cuh"
@@ -34,6 +46,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kD = 128, kTile = 128;
 constexpr float kUp = 4.f, kLift = 11.f;
+#define kNaN __int_as_float(0x7fffffff)
 constexpr unsigned kAll = 0xffffffffu;
 constexpr uint32_t kRowGroup = 2048;    // 8 tokens x 128 dims of fp16: two 1 KB swizzle atoms (d halves)
 constexpr uint32_t kTileBytes = 16 * kRowGroup;
@@ -224,22 +237,22 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
         seg_mask[s] = (uint64_t)w.x | (uint64_t)w.z << (item < ka.mma_narrow ? 16 : 32);
     }
     // The thread's piece of a row of Q, on its way while the pages are looked up.
-        constexpr int TPR = kThreads / RP, DT = kD / TPR;   // threads of a row, dims of a thread
-        const int q_row = tid / TPR, piece = tid % TPR;
-        uint32_t qw[DT / 2];
+    constexpr int TPR = kThreads / RP, DT = kD / TPR;   // threads of a row, dims of a thread
+    const int q_row = tid / TPR, piece = tid % TPR;
+    uint32_t qw[DT / 2];
 #pragma unroll
-        for (int i = 0; i < DT / 2; ++i)
-            qw[i] = 0u;
-        if (q_row < R) {
-            const int k = q_row / G;
-            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
-                                                               ((size_t)p.chunk_q[cq0 + k] * Hq + h * G + (q_row - k * G)) * kD + piece * DT);
+    for (int i = 0; i < DT / 2; ++i)
+        qw[i] = 0u;
+    if (q_row < R) {
+        const int k = q_row / G;
+        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
+                                                           ((size_t)p.chunk_q[cq0 + k] * Hq + h * G + (q_row - k * G)) * kD + piece * DT);
 #pragma unroll
-            for (int i = 0; i < DT / 8; ++i) {
-                const uint4 x = src[i];
-                qw[4 * i] = x.x, qw[4 * i + 1] = x.y, qw[4 * i + 2] = x.z, qw[4 * i + 3] = x.w;
-            }
+        for (int i = 0; i < DT / 8; ++i) {
+            const uint4 x = src[i];
+            qw[4 * i] = x.x, qw[4 * i + 1] = x.y, qw[4 * i + 2] = x.z, qw[4 * i + 3] = x.w;
         }
+    }
     __syncthreads();    // the segments
 
     // ---- rows of the chunk ----
@@ -284,11 +297,13 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
     bool uniform;
     {
         float big = 0.f;            // the row's largest finite magnitude
+        bool inf = false;
 #pragma unroll
         for (int i = 0; i < DT / 2; ++i) {
             const float2 x = bf16x2_to_float2(qw[i] & 0x7fff7fffu);
             big = x.x < INFINITY ? fmaxf(big, x.x) : big;
             big = x.y < INFINITY ? fmaxf(big, x.y) : big;
+            inf |= x.x == INFINITY || x.y == INFINITY;
         }
 #pragma unroll
         for (int o = 1; o < TPR; o <<= 1)
@@ -307,7 +322,9 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
             e = ext[0] == 1000 ? 0 : ext[0];
         // 2^e in two factors: e reaches from -113 to 147.
         const int e1 = e / 2, e2 = e - e1;
-        const float up1 = pow2(e1), up2 = pow2(e2);
+        // Infinities become NaN (with the elements beside them), so that a
+        // logit of -inf is a masked one.
+        const float up1 = inf ? kNaN : pow2(e1), up2 = pow2(e2);
 #pragma unroll
         for (int i = 0; i < DT / 8; ++i) {
             uint32_t x[4];
@@ -322,7 +339,8 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
         }
         // A column of no row has weights of 0: 2^(f * 0 - inf).
         if (piece == 0) {
-            col_f[q_row] = a.scale_log2 * pow2(-e1) * ka.k_scale * pow2(-e2);
+            // (A factor past fp32, for a row near its end, leaves logits of 0.)
+            col_f[q_row] = fminf(a.scale_log2 * pow2(-e1) * ka.k_scale * pow2(-e2), FLT_MAX);
             col_y[q_row] = q_row < R ? INFINITY : -INFINITY;
         }
     }
@@ -462,6 +480,8 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
                 const float was = col_y[tid];       // lift - maximum; -inf: no row
                 const float big = fmaxf(fmaxf(red[tid], red[RP + tid]), fmaxf(red[2 * RP + tid], red[3 * RP + tid]));
                 now = was == -INFINITY || big == -INFINITY ? was : fminf(was, kLift - big * col_f[tid]);
+                if (now == -INFINITY && was != -INFINITY)
+                    now = kNaN;         // a logit past fp32: for good, through the sums
                 alpha = now == was ? 1.f : tc::ex2(now - was);
             }
             __syncthreads();
@@ -550,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
     if (tid < RP && tid < R) {
         float sum = (red[tid] + red[RP + tid]) + (red[2 * RP + tid] + red[3 * RP + tid]);
         if (failed)
-            sum = __int_as_float(0x7fffffff);
+            sum = kNaN;
         // sum is 0 where the row attends no token, NaN where a logit was.
         const float lse2 = sum == 0.f ? -INFINITY : log2f(sum) - col_y[tid];
         const int k = tid / G;

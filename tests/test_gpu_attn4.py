@@ -318,6 +318,37 @@ def test_rows_that_are_not_finite_among_many():
     assert (out[~hit] == base[0][~hit]).all() and (lse[~hit] == base[1][~hit]).all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("queries", [1, 12, 40])
+def test_logits_at_the_end_of_fp32(queries, d):
+    """Rows of 2^100 and more: over keys of 0 every logit is 0, whatever the
+    factor; a logit above fp32's largest is NaN in its row alone; logits of
+    infinite rows the same, whatever rows are beside them."""
+    t = Tree([-1] + [0] * queries, [600] + [3] * queries, list(range(1, queries + 1)), 2, 1, d, seed=queries)
+    plan, g = t.plan(), 2.0 ** 60
+    t.g = (g, 1.0)
+    t.k4[..., :8 * d] = 0
+    t.q[:] = 0
+    t.q[..., 5] = 2.0 ** 120
+    check(t, t.run(plan, scale=1.0), scale=1.0)
+    t.g = (1.0, 1.0)
+    t.k4[..., :8 * d] = 0x22                # all 1 ...
+    x = t.k4[..., 8 * d:].reshape(-1, 2, 16, d // 16)
+    s = np.concatenate([t.slots(n) for n in range(queries + 1)])
+    x[s // 16, :, s % 16] = 0x38            # ... times 1
+    t.q[:] = 2.0 ** -9
+    base = [f64(v) for v in t.run(plan, scale=1.0)]
+    check(t, t.run(plan, scale=1.0), scale=1.0)
+    for value, at in ((2.0 ** 125, slice(None)), (np.inf, slice(3, 4)), (-np.inf, slice(3, 4)), (-np.inf, slice(None))):
+        t.q[:] = 2.0 ** -9
+        t.q[queries // 2, 1, at] = value    # (d 2^125: past fp32)
+        out, lse = (f64(v) for v in t.run(plan, scale=1.0))
+        hit = np.zeros((queries, 2), bool)
+        hit[queries // 2, 1] = True
+        assert np.isnan(out[hit]).all() and np.isnan(lse[hit]).all()
+        assert (out[~hit] == base[0][~hit]).all() and (lse[~hit] == base[1][~hit]).all()
+
+
 def test_long_path():
     """Offsets past 2^31 bytes and a path of 200000 tokens."""
     d, hkv = 128, 8
