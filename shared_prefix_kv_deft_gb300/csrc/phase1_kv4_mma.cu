@@ -61,7 +61,7 @@ struct Cfg {
     static constexpr uint32_t col = q + 2 * q_half;             // [RP] factor, [RP] lift - maximum
     static constexpr uint32_t red = col + RP * 8;               // [4 warps][RP]
     static constexpr uint32_t seg = red + 4 * RP * 4;           // [256] position, page, begin; [256] mask (8 B)
-    static constexpr uint32_t misc = seg + kMaxSegsPerChunk * 20;   // TMEM base, extremes of the rows' exponents
+    static constexpr uint32_t misc = seg + kMaxSegsPerChunk * 20;   // TMEM base, extremes of the rows' exponents, a count
     static constexpr uint32_t bars = misc + 16;                 // S, O
     static constexpr uint32_t total = bars + 16;
     static constexpr uint32_t alloc = total + 1024;
@@ -160,26 +160,53 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
                  : "memory");
 }
 
-// Column i's reduction over the warp's lanes, to lanes i and i + 16.
-template <bool kMax>
-__device__ __forceinline__ float reduce_columns(float (&v)[16], int lane)
+// Lanes 0-15 of the warp's 32, from `addr` on: lane (g, t) = (lane / 4, lane %
+// 4) gets rows g and g + 8 at columns 8 j + 2 t and + 1: v[4 j], v[4 j + 1],
+// v[4 j + 2], v[4 j + 3].  Valid after tmem_got.
+__device__ __forceinline__ void tmem_get(uint32_t addr, float (&v)[16])
 {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const float y = __shfl_xor_sync(kAll, v[i], 16);
-        v[i] = kMax ? fmaxf(v[i], y) : v[i] + y;
-    }
-#pragma unroll
-    for (int o = 8; o >= 1; o >>= 1) {
-        const bool upper = (lane & o) != 0;
-#pragma unroll
-        for (int i = 0; i < o; ++i) {
-            const float send = upper ? v[i] : v[i + o], keep = upper ? v[i + o] : v[i];
-            const float y = __shfl_xor_sync(kAll, send, o);
-            v[i] = kMax ? fmaxf(keep, y) : keep + y;
-        }
-    }
-    return v[0];
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]),
+                   "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void tmem_get(uint32_t addr, float (&v)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void tmem_got(float (&v)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]),
+                   "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_got(float (&v)[8])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7])
+                 :
+                 : "memory");
+}
+
+// Four 8x8 blocks of fp16, a pair of row lane / 4 a lane in each: lane i has
+// the address of row i of the 32 (16 bytes).
+__device__ __forceinline__ void store_rows(uint32_t addr, const uint32_t (&w)[4])
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                 : "memory");
+}
+
+// Adds one, after what the thread has seen done and before what it does next;
+// what was there.
+__device__ __forceinline__ int count_up(uint32_t addr)
+{
+    int was;
+    asm volatile("atom.acq_rel.cta.shared.add.u32 %0, [%1], 1;" : "=r"(was) : "r"(addr) : "memory");
+    return was;
 }
 
 template <int RP>
@@ -187,21 +214,22 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
 {
     using C = Cfg<RP>;
     using P = kv4::Page<kD>;
-    constexpr int NC = RP / 2;      // columns of a thread
+    constexpr int NC = RP / 2;      // columns of a warp
+    constexpr int NJ = NC / 8;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     uint8_t *smem = smem_raw + (base - raw);
     const AttnArgs &a = ka.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int half = warp >> 2, row = (warp & 3) * 32 + lane;      // tile row, half of its dims and of the columns
+    const int half = warp >> 2, row = (warp & 3) * 32 + lane, g = lane >> 2, t4 = lane & 3;    // tile row, half of its dims and of the columns
     float *col_f = reinterpret_cast<float *>(smem + C::col), *col_y = col_f + RP;
     float *red = reinterpret_cast<float *>(smem + C::red);
     int32_t *seg_pos = reinterpret_cast<int32_t *>(smem + C::seg), *seg_page = seg_pos + kMaxSegsPerChunk,
             *seg_begin = seg_page + kMaxSegsPerChunk;
     uint64_t *seg_mask = reinterpret_cast<uint64_t *>(seg_begin + kMaxSegsPerChunk);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::misc);
-    int *ext = reinterpret_cast<int *>(smem + C::misc) + 1;     // least, greatest exponent of a row
+    int *ext = reinterpret_cast<int *>(smem + C::misc) + 1;     // least, greatest exponent of a row; warps that have stored K
     const uint32_t bar_s = base + C::bars, bar_o = bar_s + 8;
 
     if (warp == 0) {
@@ -214,6 +242,7 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
         tc::fence_mbar_init();
         ext[0] = 1000;
         ext[1] = -1000;
+        ext[2] = 0;
     }
     __syncthreads();
     if (a.wait_prior)
@@ -355,10 +384,15 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
     const uint32_t row_bits = R >= RP ? 0xffffffffu >> (32 - NC)
                                       : (uint32_t)((((1ull << R) - 1) >> (half * NC)) & (0xffffffffu >> (32 - NC)));
 
-    f32x2 l[NC / 2];
+    // Of S a thread holds columns 8 j + 2 t4 and + 1 (of the warp's) for rows
+    // 16 h + 8 q + g: with a row a thread, the sums of 32 columns would take 32
+    // registers and S would have to be read twice.
+    f32x2 l[NJ], x[2][2][NJ];
 #pragma unroll
-    for (int i = 0; i < NC / 2; ++i)
-        l[i] = f2_pack(0.f, 0.f);
+    for (int j = 0; j < NJ; ++j)
+        l[j] = f2_pack(0.f, 0.f);
+    float *const my_f = col_f + half * NC + 2 * t4, *const my_y = col_y + half * NC + 2 * t4;
+    const uint32_t p_row = base + C::p + row * 128;
     bool ok = true;
     kr.to_tmem(tm_k);
     load(kr, k4, w1);
@@ -380,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
         issue_s(0);
     }
     for (int t = 0; t < ntiles; ++t) {
-        // ---- S(t) has been read from K's buffer: K(t + 1) ----
+        // ---- S(t) is there, and has been read from K's buffer: K(t + 1) ----
         if (ok)
             ok = tc::mbar_wait(bar_s, t & 1);
         tc::fence_after_sync();
@@ -388,156 +422,168 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
         if (t + 1 < ntiles) {
             kr.to_tmem(tm_k);
             load(kr, k4, w2);
+            // The last warp to have done so starts S(t + 1).
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0 && count_up(base + C::misc + 12) == (t + 1) * (kThreads / 32) - 1) {
+                tc::fence_after_sync();
+                issue_s(t + 1);
+            }
+            __syncwarp();
         }
-        // ---- exponents of the weights ----
-        // Sixteen columns at a time, read from TMEM again where they are
-        // needed again: all of them would not fit beside the sums and the rows
-        // that are on their way.
-        const uint32_t tm_st = tm_s + (t & 1) * 64;
-        f32x2 x[8];
-        auto read = [&](uint32_t from) {
-            float v[16];
-            tc::tmem_ld16(from, v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                x[i] = f2_pack(v[2 * i], v[2 * i + 1]);
-        };
-        uint32_t seen = 0;
+        uint32_t seen = 0;          // the thread's tile row's, by column
         if (t * kTile + row < T)
             seen = (uint32_t)(seg_mask[w0.meta / kPageSize] >> (half * NC)) & row_bits;
         const bool whole = __all_sync(kAll, seen == row_bits);
-        auto hide = [&](int c) {
+        const uint32_t tm_st = tm_s + (t & 1) * 64;
+        auto read = [&]() {
+            float v[2][4 * NJ];
+            tmem_get(tm_st, v[0]);
+            tmem_get(tm_st + (16u << 16), v[1]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float2 v = f2_unpack(x[i]);
-                x[i] = f2_pack((seen >> (c + 2 * i)) & 1u ? v.x : -INFINITY, (seen >> (c + 2 * i + 1)) & 1u ? v.y : -INFINITY);
+            for (int h2 = 0; h2 < 2; ++h2) {
+                tmem_got(v[h2]);
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        x[h2][q][j] = f2_pack(v[h2][4 * j + 2 * q], v[h2][4 * j + 2 * q + 1]);
             }
         };
-        auto exponents = [&](int c) {       // of columns c .. c + 15
-            read(tm_st + c);
-            const ulonglong2 *cf = reinterpret_cast<const ulonglong2 *>(col_f + half * NC + c),
-                             *cy = reinterpret_cast<const ulonglong2 *>(col_y + half * NC + c);
-            if (uniform) {
+        auto hide = [&]() {
 #pragma unroll
-                for (int i = 0; i < 8; i += 2) {
-                    const ulonglong2 y = cy[i / 2];
-                    x[i] = f2_fma(x[i], common, y.x);
-                    x[i + 1] = f2_fma(x[i + 1], common, y.y);
-                }
-            } else {
+            for (int h2 = 0; h2 < 2; ++h2)
 #pragma unroll
-                for (int i = 0; i < 8; i += 2) {
-                    const ulonglong2 f = cf[i / 2], y = cy[i / 2];
-                    x[i] = f2_fma(x[i], f.x, y.x);
-                    x[i + 1] = f2_fma(x[i + 1], f.y, y.y);
+                for (int q = 0; q < 2; ++q) {
+                    const uint32_t bits = __shfl_sync(kAll, seen, 16 * h2 + 8 * q + g) >> (2 * t4);
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j) {
+                        const float2 y = f2_unpack(x[h2][q][j]);
+                        x[h2][q][j] = f2_pack((bits >> 8 * j) & 1u ? y.x : -INFINITY, (bits >> 8 * j) & 2u ? y.y : -INFINITY);
+                    }
                 }
+        };
+        // The weights are taken with the maxima so far; where that is seen to
+        // have been too little (and for the first tile), the maxima are raised
+        // and they are taken again, before P is used.
+        f32x2 ln[NJ];
+        bool raise = t == 0;
+        for (;;) {
+            if (raise) {
+                read();
+                hide();
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) {
+                    float2 big = make_float2(-INFINITY, -INFINITY);     // (the factors are positive)
+#pragma unroll
+                    for (int h2 = 0; h2 < 2; ++h2)
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const float2 y = f2_unpack(x[h2][q][j]);
+                            big.x = fmaxf(big.x, y.x);
+                            big.y = fmaxf(big.y, y.y);
+                        }
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) {
+                        big.x = fmaxf(big.x, __shfl_xor_sync(kAll, big.x, o));
+                        big.y = fmaxf(big.y, __shfl_xor_sync(kAll, big.y, o));
+                    }
+                    if (g == 0)
+                        *reinterpret_cast<float2 *>(red + (warp & 3) * RP + half * NC + 8 * j + 2 * t4) = big;
+                }
+                __syncthreads();
+                float now = 0.f, alpha = 1.f;
+                if (tid < RP) {
+                    const float was = col_y[tid];       // lift - maximum; -inf: no row
+                    const float big = fmaxf(fmaxf(red[tid], red[RP + tid]), fmaxf(red[2 * RP + tid], red[3 * RP + tid]));
+                    now = was == -INFINITY || big == -INFINITY ? was : fminf(was, kLift - big * col_f[tid]);
+                    if (now == -INFINITY && was != -INFINITY)
+                        now = kNaN;         // a logit past fp32: for good, through the sums
+                    alpha = now == was ? 1.f : tc::ex2(now - was);
+                }
+                __syncthreads();
+                if (tid < RP) {
+                    col_y[tid] = now;
+                    red[tid] = alpha;
+                }
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+                    l[j] = f2_mul(l[j], *reinterpret_cast<const f32x2 *>(red + half * NC + 8 * j + 2 * t4));
+                if (t > 0) {
+#pragma unroll
+                    for (int c = 0; c < NC; c += 16) {
+                        float o[16];
+                        tc::tmem_ld16(tm_o + c, o);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            o[i] *= red[half * NC + c + i];
+                        tc::tmem_st16(tm_o + c, o);
+                    }
+                }
+            }
+            // ---- exponents ----
+            read();
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const f32x2 y = *reinterpret_cast<const f32x2 *>(my_y + 8 * j);
+                const f32x2 f = uniform ? common : *reinterpret_cast<const f32x2 *>(my_f + 8 * j);
+#pragma unroll
+                for (int h2 = 0; h2 < 2; ++h2)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        x[h2][q][j] = f2_fma(x[h2][q][j], f, y);
             }
             if (!whole)
-                hide(c);
-        };
-        float top = -INFINITY;
+                hide();
+            float top = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < NC; c += 16) {
-            exponents(c);
+            for (int h2 = 0; h2 < 2; ++h2)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float2 v = f2_unpack(x[i]);
-                top = fmaxf(top, fmaxf(v.x, v.y));
-            }
-        }
-        tc::fence_proxy_async();
-        tc::fence_before_sync();
-        const bool raise = __syncthreads_or(top > kLift + kUp);
-        if (tid == 0 && t + 1 < ntiles) {
-            tc::fence_after_sync();
-            issue_s(t + 1);
-        }
-        // P(t - 1).V(t - 1) is done: P, V and O are free.
-        if (t > 0 && ok)
-            ok = tc::mbar_wait(bar_o, (t - 1) & 1);
-        __syncwarp();
-        if (raise) {
-            // Maxima over the tile, from S again.
-            tc::fence_after_sync();
+                for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int c = 0; c < NC; c += 16) {
-                read(tm_st + c);
-                hide(c);
-                float v[16];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 y = f2_unpack(x[i]);
-                    v[2 * i] = y.x;
-                    v[2 * i + 1] = y.y;
-                }
-                const float big = reduce_columns<true>(v, lane);        // (factors are positive)
-                if (lane < 16)
-                    red[(warp & 3) * RP + half * NC + c + lane] = big;
-            }
-            __syncthreads();
-            float now = 0.f, alpha = 1.f;
-            if (tid < RP) {
-                const float was = col_y[tid];       // lift - maximum; -inf: no row
-                const float big = fmaxf(fmaxf(red[tid], red[RP + tid]), fmaxf(red[2 * RP + tid], red[3 * RP + tid]));
-                now = was == -INFINITY || big == -INFINITY ? was : fminf(was, kLift - big * col_f[tid]);
-                if (now == -INFINITY && was != -INFINITY)
-                    now = kNaN;         // a logit past fp32: for good, through the sums
-                alpha = now == was ? 1.f : tc::ex2(now - was);
-            }
-            __syncthreads();
-            if (tid < RP) {
-                col_y[tid] = now;
-                red[tid] = alpha;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int c = 0; c < NC; c += 16) {
-                const f32x2 *al = reinterpret_cast<const f32x2 *>(red + half * NC + c);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    l[c / 2 + i] = f2_mul(l[c / 2 + i], al[i]);
-                if (t > 0) {
-                    read(tm_o + c);
-                    float v[16];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 y = f2_unpack(f2_mul(x[i], al[i]));
-                        v[2 * i] = y.x;
-                        v[2 * i + 1] = y.y;
+                    for (int j = 0; j < NJ; ++j) {
+                        const float2 y = f2_unpack(x[h2][q][j]);
+                        top = fmaxf(top, fmaxf(y.x, y.y));
                     }
-                    tc::tmem_st16(tm_o + c, v);
-                }
-            }
-        }
-        // ---- P(t), V(t) ----
-        uint8_t *dst = smem + C::p + row * 128;
+            // ---- P(t), V(t), once P(t - 1).V(t - 1) is done ----
+            if (t > 0 && !raise && ok)
+                ok = tc::mbar_wait(bar_o, (t - 1) & 1);
+            __syncwarp();
 #pragma unroll
-        for (int c = 0; c < NC; c += 16) {
-            if (NC > 16 || raise)
-                exponents(c);
-#pragma unroll
-            for (int i = 0; i < 16; i += 8) {
+            for (int j = 0; j < NJ; ++j) {
                 uint32_t w[4];
+                ln[j] = l[j];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 y = f2_unpack(x[i / 2 + j]);
-                    const float y0 = tc::ex2(y.x), y1 = tc::ex2(y.y);
-                    l[(c + i) / 2 + j] = f2_add(l[(c + i) / 2 + j], f2_pack(y0, y1));
-                    w[j] = f16x2(y0, y1);
-                }
-                *reinterpret_cast<uint4 *>(dst + ((((half * NC + c + i) >> 3) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int h2 = 0; h2 < 2; ++h2)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const float2 y = f2_unpack(x[h2][q][j]);
+                        const float y0 = tc::ex2(y.x), y1 = tc::ex2(y.y);
+                        ln[j] = f2_add(ln[j], f2_pack(y0, y1));
+                        w[2 * h2 + q] = f16x2(y0, y1);
+                    }
+                store_rows(p_row + (((half * NJ + j) ^ (row & 7)) << 4), w);
             }
-        }
-        vr.to_smem(row_v, row & 7);
-        load(vr, v4, w1);
-        w0 = w1;
-        w1 = w2;
-        w2 = where(t + 3);
-        tc::fence_proxy_async();
-        tc::fence_before_sync();
-        __syncthreads();
-        if (tid == 0) {
+            if (t == 0 || !raise) {
+                vr.to_smem(row_v, row & 7);
+                load(vr, v4, w1);
+                w0 = w1;
+                w1 = w2;
+                w2 = where(t + 3);
+            }
+            tc::fence_proxy_async();
+            tc::fence_before_sync();
+            const bool over = __syncthreads_or(top > kLift + kUp);
             tc::fence_after_sync();
+            if (raise || !over)
+                break;
+            raise = true;
+        }
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+            l[j] = ln[j];
+        if (tid == 0) {
             const uint64_t dv = tc::smem_desc(base + C::v, 1024, kRowGroup), dp = tc::smem_desc(base + C::p, kTile * 128, 1024);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -551,17 +597,15 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
     tc::fence_after_sync();
     {
 #pragma unroll
-        for (int c = 0; c < NC; c += 16) {
-            float v[16];
+        for (int j = 0; j < NJ; ++j) {
+            float2 sum = f2_unpack(l[j]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float2 y = f2_unpack(l[c / 2 + i]);
-                v[2 * i] = y.x;
-                v[2 * i + 1] = y.y;
+            for (int o = 4; o < 32; o <<= 1) {
+                sum.x += __shfl_xor_sync(kAll, sum.x, o);
+                sum.y += __shfl_xor_sync(kAll, sum.y, o);
             }
-            const float sum = reduce_columns<false>(v, lane);
-            if (lane < 16)
-                red[(warp & 3) * RP + half * NC + c + lane] = sum;
+            if (g == 0)
+                *reinterpret_cast<float2 *>(red + (warp & 3) * RP + half * NC + 8 * j + 2 * t4) = sum;
         }
     }
     const bool failed = __syncthreads_or(!ok);
