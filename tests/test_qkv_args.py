@@ -91,3 +91,22 @@ def test_the_tests_own_format():
     # a step of the largest codes is 2 s, half of it an element's error at most;
     # s is within 2^-4 of amax / 6 (the largest code's overflow included)
     assert (np.abs(y - x) <= np.repeat(ref.E4M3[s], 16, -1) * (1 + 6 * 2.0 ** -4)).all()
+
+
+def attn4_args(of, **kw):
+    d = dict(q=A, kp=2 * A, vp=3 * A, kg=1.0, vg=1.0, off=A, ids=A, num_pages=9, hq=4, hkv=2, head_dim=64, page_size=16, scale=0.1, plan=of.handle,
+             out=4 * A, out_dtype=0, lse=5 * A, ws=6 * A, ws_bytes=1 << 30, stream=None)
+    d.update(kw)
+    return list(d.values())
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(q=None), EINVAL), (dict(kp=None), EINVAL), (dict(vp=None), EINVAL), (dict(off=None), EINVAL), (dict(ids=None), EINVAL), (dict(out=None), EINVAL),
+    (dict(lse=None), EINVAL), (dict(plan=None), EINVAL), (dict(kg=0.0), EINVAL), (dict(vg=float("nan")), EINVAL), (dict(kg=2.0 ** 61), EINVAL),
+    (dict(vg=-1.0), EINVAL), (dict(scale=0.0), EINVAL), (dict(scale=float("inf")), EINVAL), (dict(num_pages=0), EINVAL), (dict(hq=5), EINVAL), (dict(hkv=0), EINVAL),
+    (dict(q=A + 8), EINVAL), (dict(kp=A + 8), EINVAL), (dict(out=4 * A + 8), EINVAL), (dict(out_dtype=7), EINVAL), (dict(head_dim=80), EUNSUPPORTED),
+    (dict(page_size=32), EUNSUPPORTED), (dict(hq=8), -8), (dict(), -8)])
+def test_tree_attn4_argument_checks(kw, status):
+    """Of a plan that has not been uploaded: nothing reaches a GPU."""
+    plan = deft.Plan([-1, 0, 0], [100, 5, 7], [1, 2], 256, 2, naive=False)
+    assert deft.load().deft_tree_attn4(*attn4_args(plan, **kw)) == status
