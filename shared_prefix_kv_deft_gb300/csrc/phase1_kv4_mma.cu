@@ -34,7 +34,7 @@
 //
 // What bounds it is the tile's chain: 2.2 us for 128 tokens of a unit, two
 // units an SM, of which the tensor products are a fifth and the issue slots
-// half: 630 instructions a warp and tile, 256 of them the conversions and
+// half: 630 instructions a warp and tile, 128 of them the conversions and
 // products of the unpacking.  Measured and left: one CTA an SM with twice the
 // registers (155 us where two had 109), 512 threads with a quarter row each
 // (231: 64 registers spill), fewer registers than 128, for room beside the
@@ -64,12 +64,12 @@ struct Cfg {
     static constexpr uint32_t p = v + kTileBytes;               // [128 tok][128 B]
     static constexpr uint32_t q_half = RP * 128;
     static constexpr uint32_t q = p + kTile * 128;              // [d half][RP rows][128 B]
-    static constexpr uint32_t col = q + 2 * q_half;             // [RP] factor, [RP] lift - maximum
+    static constexpr uint32_t col = q + 2 * q_half;             // [RP / 2] two columns' factors, their lift - maximum
     static constexpr uint32_t red = col + RP * 8;               // [4 warps][RP]
     static constexpr uint32_t seg = red + 4 * RP * 4;           // [256] position, page, begin; [256] mask (8 B)
-    static constexpr uint32_t misc = seg + kMaxSegsPerChunk * 20;   // TMEM base, extremes of the rows' exponents, a count
-    static constexpr uint32_t bars = misc + 16;                 // S, O
-    static constexpr uint32_t total = bars + 16;
+    static constexpr uint32_t misc = seg + kMaxSegsPerChunk * 20;   // TMEM base
+    static constexpr uint32_t bars = misc + 16;                 // S, O, K
+    static constexpr uint32_t total = bars + 24;
     static constexpr uint32_t alloc = total + 1024;
     static_assert(q % 1024 == 0 && p % 1024 == 0, "128-byte-swizzle atoms");
     static_assert(2 * (alloc + 1024) <= 228 * 1024, "two CTAs an SM");
@@ -92,28 +92,27 @@ __device__ __forceinline__ float pow2(int e)   // -126 <= e <= 127
     return __int_as_float((127 + e) << 23);
 }
 
+// tc::tmem_st16 without the wait.
+__device__ __forceinline__ void tmem_put(uint32_t addr, const float (&v)[16])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+                 "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]),
+                 "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+                 : "memory");
+}
+
 // Half a token's row: 64 elements and their scales.
 struct HalfRow {
     uint4 w[2];
     uint32_t s;
-    __device__ __forceinline__ void zero()
-    {
-        w[0] = w[1] = make_uint4(0, 0, 0, 0);
-        s = 0;
-    }
-    __device__ __forceinline__ void load(const uint8_t *page, int tok, int half, bool sectors)
+    // row: the half row's place; tok: of the page.
+    __device__ __forceinline__ void load(const uint8_t *row, int tok, int half)
     {
         using P = kv4::Page<kD>;
-        const uint4 *src = reinterpret_cast<const uint4 *>(page + tok * P::kRow) + 2 * half;
-        if (sectors) {
-            asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                         : "=r"(w[0].x), "=r"(w[0].y), "=r"(w[0].z), "=r"(w[0].w), "=r"(w[1].x), "=r"(w[1].y), "=r"(w[1].z), "=r"(w[1].w)
-                         : "l"(src));
-        } else {
-            w[0] = __ldg(src);
-            w[1] = __ldg(src + 1);
-        }
-        s = __ldg(reinterpret_cast<const uint32_t *>(page + P::kScales + tok * P::kScaleRow) + half);
+        w[0] = __ldg(reinterpret_cast<const uint4 *>(row));
+        w[1] = __ldg(reinterpret_cast<const uint4 *>(row) + 1);
+        const uint8_t *sc = row + (P::kScales - tok * (P::kRow - P::kScaleRow) - half * (P::kRow - P::kScaleRow) / 2);
+        s = __ldg(reinterpret_cast<const uint32_t *>(sc));
     }
     // Words 4 b .. 4 b + 3 as fp16, eight elements each.
     template <typename F>
@@ -152,8 +151,9 @@ struct HalfRow {
                 for (int k = 0; k < 4; ++k)
                     v[4 * i + k] = __uint_as_float(h[k]);
             });
-            tc::tmem_st16(addr + 16 * b, v);
+            tmem_put(addr + 16 * b, v);
         }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
     }
 };
 
@@ -206,13 +206,12 @@ __device__ __forceinline__ void store_rows(uint32_t addr, const uint32_t (&w)[4]
                  : "memory");
 }
 
-// Adds one, after what the thread has seen done and before what it does next;
-// what was there.
-__device__ __forceinline__ int count_up(uint32_t addr)
+// The largest (a NaN counts for nothing).
+__device__ __forceinline__ float max3(float a, float b, float c)
 {
-    int was;
-    asm volatile("atom.acq_rel.cta.shared.add.u32 %0, [%1], 1;" : "=r"(was) : "r"(addr) : "memory");
-    return was;
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 template <int RP>
@@ -229,14 +228,16 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
     const AttnArgs &a = ka.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int half = warp >> 2, row = (warp & 3) * 32 + lane, g = lane >> 2, t4 = lane & 3;    // tile row, half of its dims and of the columns
-    float *col_f = reinterpret_cast<float *>(smem + C::col), *col_y = col_f + RP;
+    float *col = reinterpret_cast<float *>(smem + C::col);
+    // Column c's factor (logits in base 2 from S's numbers) and lift - maximum.
+    auto col_f = [&](int c) -> float & { return col[2 * (c & ~1) + (c & 1)]; };
+    auto col_y = [&](int c) -> float & { return col[2 * (c & ~1) + 2 + (c & 1)]; };
     float *red = reinterpret_cast<float *>(smem + C::red);
     int32_t *seg_pos = reinterpret_cast<int32_t *>(smem + C::seg), *seg_page = seg_pos + kMaxSegsPerChunk,
             *seg_begin = seg_page + kMaxSegsPerChunk;
     uint64_t *seg_mask = reinterpret_cast<uint64_t *>(seg_begin + kMaxSegsPerChunk);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::misc);
-    int *ext = reinterpret_cast<int *>(smem + C::misc) + 1;     // least, greatest exponent of a row; warps that have stored K
-    const uint32_t bar_s = base + C::bars, bar_o = bar_s + 8;
+    const uint32_t bar_s = base + C::bars, bar_o = bar_s + 8, bar_k = bar_s + 16;
 
     if (warp == 0) {
         tc::tmem_alloc(smem_u32(tmem_slot), kTmemCols);
@@ -246,9 +247,7 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
         tc::mbar_init(bar_s, 1);
         tc::mbar_init(bar_o, 1);
         tc::fence_mbar_init();
-        ext[0] = 1000;
-        ext[1] = -1000;
-        ext[2] = 0;
+        tc::mbar_init(bar_k, kThreads / 32);
     }
     __syncthreads();
     if (a.wait_prior)
@@ -292,44 +291,41 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
 
     // ---- rows of the chunk ----
     const int ntiles = (T + kTile - 1) / kTile;
-    const uint8_t *k4 = static_cast<const uint8_t *>(a.k_pages) + (size_t)h * P::kBytes;
-    const uint8_t *v4 = static_cast<const uint8_t *>(a.v_pages) + (size_t)h * P::kBytes;
-    const size_t page_step = (size_t)Hkv * P::kBytes;
+    const uint8_t *k4 = static_cast<const uint8_t *>(a.k_pages) + half * (P::kRow / 2);
+    const uint8_t *v4 = static_cast<const uint8_t *>(a.v_pages) + half * (P::kRow / 2);
+    static_assert(P::kBytes % P::kRow == 0, "rows at multiples of their length (64 bytes: 2^32 of them are 256 GB)");
     struct Where {
-        int page, meta;     // page -1: no token; segment x 16 + place in the page
+        int page;
+        int meta;           // segment x 16 + token of the page
     };
+    // Of the chunk's token at the thread's row of tile t (past the last: the
+    // last, which has no weight there).
     auto where = [&](int t) {
-        Where w{-1, 0};
-        const int x = t * kTile + row;
-        if (x < T) {
-            int seg = 0, hi = nseg;
-            while (hi - seg > 1) {
-                const int mid = (seg + hi) >> 1;
-                if (seg_pos[mid] <= x)
-                    seg = mid;
-                else
-                    hi = mid;
-            }
-            const int j = x - seg_pos[seg] + seg_begin[seg];
-            w.page = a.page_id[seg_page[seg] + j / kPageSize];
-            w.meta = seg * kPageSize + j % kPageSize;
+        const int x = min(t * kTile + row, T - 1);
+        int seg = 0, hi = nseg;
+        while (hi - seg > 1) {
+            const int mid = (seg + hi) >> 1;
+            if (seg_pos[mid] <= x)
+                seg = mid;
+            else
+                hi = mid;
         }
+        const int j = x - seg_pos[seg] + seg_begin[seg];
+        Where w;
+        w.page = a.page_id[seg_page[seg] + j / kPageSize];
+        w.meta = seg * kPageSize + j % kPageSize;
         return w;
     };
-    // (A half row is one 32-byte sector where the pools are aligned so.)
-    const bool sectors = (((uintptr_t)a.k_pages | (uintptr_t)a.v_pages) & 31u) == 0;
     auto load = [&](HalfRow &x, const uint8_t *pool, const Where &w) {
-        if (w.page >= 0)
-            x.load(pool + (size_t)w.page * page_step, w.meta % kPageSize, half, sectors);
-        else
-            x.zero();
+        const int tok = w.meta % kPageSize;
+        const uint32_t at = (uint32_t)(w.page * Hkv + h) * (P::kBytes / P::kRow) + tok;     // in rows
+        x.load(pool + (size_t)at * P::kRow, tok, half);
     };
     HalfRow kr, vr;
-    Where w0 = where(0), w1 = where(1), w2{-1, 0};      // of tiles t, t + 1, t + 2
+    Where w0 = where(0), w1 = where(1), w2;     // of tiles t, t + 1, t + 2
     load(kr, k4, w0);
     load(vr, v4, w0);
     // ---- Q^T: bf16 -> fp16 times a power of two ----
-    bool uniform;
     {
         float big = 0.f;            // the row's largest finite magnitude
         bool inf = false;
@@ -343,18 +339,7 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
 #pragma unroll
         for (int o = 1; o < TPR; o <<= 1)
             big = fmaxf(big, __shfl_xor_sync(kAll, big, o));
-        int e = big > 0.f ? 14 - ilogbf(big) : 1 << 20;        // (a row of zeros takes any)
-        // Rows within 2^8 of one another share the power of two, and with it
-        // the factor of their logits: fp16 holds the smallest one's elements
-        // down to 2^-31 of its largest.
-        if (piece == 0 && e < 1 << 20) {
-            atomicMin(ext, e);
-            atomicMax(ext + 1, e);
-        }
-        __syncthreads();
-        uniform = ext[1] - ext[0] <= 8;
-        if (uniform || e == 1 << 20)
-            e = ext[0] == 1000 ? 0 : ext[0];
+        const int e = big > 0.f ? 14 - ilogbf(big) : 0;
         // 2^e in two factors: e reaches from -113 to 147.
         const int e1 = e / 2, e2 = e - e1;
         // Infinities become NaN (with the elements beside them), so that a
@@ -375,8 +360,8 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
         // A column of no row has weights of 0: 2^(f * 0 - inf).
         if (piece == 0) {
             // (A factor past fp32, for a row near its end, leaves logits of 0.)
-            col_f[q_row] = fminf(a.scale_log2 * pow2(-e1) * ka.k_scale * pow2(-e2), FLT_MAX);
-            col_y[q_row] = q_row < R ? INFINITY : -INFINITY;
+            col_f(q_row) = fminf(a.scale_log2 * pow2(-e1) * ka.k_scale * pow2(-e2), FLT_MAX);
+            col_y(q_row) = q_row < R ? INFINITY : -INFINITY;
         }
     }
     __syncthreads();
@@ -386,18 +371,17 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
 
     uint8_t *row_v = smem + C::v + (row >> 3) * kRowGroup + half * 1024 + (row & 7) * 128;
     const uint32_t tm_k = tmem + ((uint32_t)(warp & 3) << 21) + 192 + half * 32;
-    const f32x2 common = f2_pack(col_f[0], col_f[0]);
     const uint32_t row_bits = R >= RP ? 0xffffffffu >> (32 - NC)
                                       : (uint32_t)((((1ull << R) - 1) >> (half * NC)) & (0xffffffffu >> (32 - NC)));
 
     // Of S a thread holds columns 8 j + 2 t4 and + 1 (of the warp's) for rows
     // 16 h + 8 q + g: with a row a thread, the sums of 32 columns would take 32
     // registers and S would have to be read twice.
-    f32x2 l[NJ], x[2][2][NJ];
+    float l[2 * NJ], x[2][2][2 * NJ];
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
-        l[j] = f2_pack(0.f, 0.f);
-    float *const my_f = col_f + half * NC + 2 * t4, *const my_y = col_y + half * NC + 2 * t4;
+    for (int j = 0; j < 2 * NJ; ++j)
+        l[j] = 0.f;
+    const float4 *my_col = reinterpret_cast<const float4 *>(col + half * 2 * NC + 4 * t4);
     const uint32_t p_row = base + C::p + row * 128;
     bool ok = true;
     kr.to_tmem(tm_k);
@@ -428,15 +412,12 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
         if (t + 1 < ntiles) {
             kr.to_tmem(tm_k);
             load(kr, k4, w2);
-            // The last warp to have done so starts S(t + 1).
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0 && count_up(base + C::misc + 12) == (t + 1) * (kThreads / 32) - 1) {
-                tc::fence_after_sync();
-                issue_s(t + 1);
-            }
-            __syncwarp();
+            if (lane == 0)
+                tc::mbar_arrive(bar_k);
         }
+        const Where w3 = where(t + 3);      // (its page is looked up while the tile is worked on)
         uint32_t seen = 0;          // the thread's tile row's, by column
         if (t * kTile + row < T)
             seen = (uint32_t)(seg_mask[w0.meta / kPageSize] >> (half * NC)) & row_bits;
@@ -452,8 +433,10 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
 #pragma unroll
                 for (int j = 0; j < NJ; ++j)
 #pragma unroll
-                    for (int q = 0; q < 2; ++q)
-                        x[h2][q][j] = f2_pack(v[h2][4 * j + 2 * q], v[h2][4 * j + 2 * q + 1]);
+                    for (int q = 0; q < 2; ++q) {
+                        x[h2][q][2 * j] = v[h2][4 * j + 2 * q];
+                        x[h2][q][2 * j + 1] = v[h2][4 * j + 2 * q + 1];
+                    }
             }
         };
         auto hide = [&]() {
@@ -463,16 +446,14 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
                 for (int q = 0; q < 2; ++q) {
                     const uint32_t bits = __shfl_sync(kAll, seen, 16 * h2 + 8 * q + g) >> (2 * t4);
 #pragma unroll
-                    for (int j = 0; j < NJ; ++j) {
-                        const float2 y = f2_unpack(x[h2][q][j]);
-                        x[h2][q][j] = f2_pack((bits >> 8 * j) & 1u ? y.x : -INFINITY, (bits >> 8 * j) & 2u ? y.y : -INFINITY);
-                    }
+                    for (int j = 0; j < 2 * NJ; ++j)
+                        x[h2][q][j] = (bits >> (8 * (j / 2) + (j & 1))) & 1u ? x[h2][q][j] : -INFINITY;
                 }
         };
         // The weights are taken with the maxima so far; where that is seen to
         // have been too little (and for the first tile), the maxima are raised
         // and they are taken again, before P is used.
-        f32x2 ln[NJ];
+        float ln[2 * NJ];
         bool raise = t == 0;
         for (;;) {
             if (raise) {
@@ -485,9 +466,8 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
                     for (int h2 = 0; h2 < 2; ++h2)
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
-                            const float2 y = f2_unpack(x[h2][q][j]);
-                            big.x = fmaxf(big.x, y.x);
-                            big.y = fmaxf(big.y, y.y);
+                            big.x = fmaxf(big.x, x[h2][q][2 * j]);
+                            big.y = fmaxf(big.y, x[h2][q][2 * j + 1]);
                         }
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) {
@@ -500,22 +480,22 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
                 __syncthreads();
                 float now = 0.f, alpha = 1.f;
                 if (tid < RP) {
-                    const float was = col_y[tid];       // lift - maximum; -inf: no row
+                    const float was = col_y(tid);       // lift - maximum; -inf: no row
                     const float big = fmaxf(fmaxf(red[tid], red[RP + tid]), fmaxf(red[2 * RP + tid], red[3 * RP + tid]));
-                    now = was == -INFINITY || big == -INFINITY ? was : fminf(was, kLift - big * col_f[tid]);
+                    now = was == -INFINITY || big == -INFINITY ? was : fminf(was, kLift - big * col_f(tid));
                     if (now == -INFINITY && was != -INFINITY)
                         now = kNaN;         // a logit past fp32: for good, through the sums
                     alpha = now == was ? 1.f : tc::ex2(now - was);
                 }
                 __syncthreads();
                 if (tid < RP) {
-                    col_y[tid] = now;
+                    col_y(tid) = now;
                     red[tid] = alpha;
                 }
                 __syncthreads();
 #pragma unroll
-                for (int j = 0; j < NJ; ++j)
-                    l[j] = f2_mul(l[j], *reinterpret_cast<const f32x2 *>(red + half * NC + 8 * j + 2 * t4));
+                for (int j = 0; j < 2 * NJ; ++j)
+                    l[j] *= red[half * NC + 8 * (j / 2) + 2 * t4 + (j & 1)];
                 if (t > 0) {
 #pragma unroll
                     for (int c = 0; c < NC; c += 16) {
@@ -532,13 +512,16 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
             read();
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
-                const f32x2 y = *reinterpret_cast<const f32x2 *>(my_y + 8 * j);
-                const f32x2 f = uniform ? common : *reinterpret_cast<const f32x2 *>(my_f + 8 * j);
+                const float4 z = my_col[4 * j];
+                const f32x2 f = f2_pack(z.x, z.y), y = f2_pack(z.z, z.w);
 #pragma unroll
                 for (int h2 = 0; h2 < 2; ++h2)
 #pragma unroll
-                    for (int q = 0; q < 2; ++q)
-                        x[h2][q][j] = f2_fma(x[h2][q][j], f, y);
+                    for (int q = 0; q < 2; ++q) {
+                        const float2 u = f2_unpack(f2_fma(f2_pack(x[h2][q][2 * j], x[h2][q][2 * j + 1]), f, y));
+                        x[h2][q][2 * j] = u.x;
+                        x[h2][q][2 * j + 1] = u.y;
+                    }
             }
             if (!whole)
                 hide();
@@ -548,10 +531,15 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
 #pragma unroll
-                    for (int j = 0; j < NJ; ++j) {
-                        const float2 y = f2_unpack(x[h2][q][j]);
-                        top = fmaxf(top, fmaxf(y.x, y.y));
-                    }
+                    for (int j = 0; j < 2 * NJ; j += 2)
+                        top = max3(top, x[h2][q][j], x[h2][q][j + 1]);
+            // One thread starts S(t + 1): by now the other warps' K is there.
+            if (tid == 0 && t + 1 < ntiles && (t == 0 || !raise)) {
+                if (ok)
+                    ok = tc::mbar_wait(bar_k, t & 1);
+                tc::fence_after_sync();
+                issue_s(t + 1);
+            }
             // ---- P(t), V(t), once P(t - 1).V(t - 1) is done ----
             if (t > 0 && !raise && ok)
                 ok = tc::mbar_wait(bar_o, (t - 1) & 1);
@@ -559,16 +547,18 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
                 uint32_t w[4];
-                ln[j] = l[j];
+                float l0 = l[2 * j], l1 = l[2 * j + 1];
 #pragma unroll
                 for (int h2 = 0; h2 < 2; ++h2)
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        const float2 y = f2_unpack(x[h2][q][j]);
-                        const float y0 = tc::ex2(y.x), y1 = tc::ex2(y.y);
-                        ln[j] = f2_add(ln[j], f2_pack(y0, y1));
+                        const float y0 = tc::ex2(x[h2][q][2 * j]), y1 = tc::ex2(x[h2][q][2 * j + 1]);
+                        l0 += y0;
+                        l1 += y1;
                         w[2 * h2 + q] = f16x2(y0, y1);
                     }
+                ln[2 * j] = l0;
+                ln[2 * j + 1] = l1;
                 store_rows(p_row + (((half * NJ + j) ^ (row & 7)) << 4), w);
             }
             if (t == 0 || !raise) {
@@ -576,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
                 load(vr, v4, w1);
                 w0 = w1;
                 w1 = w2;
-                w2 = where(t + 3);
+                w2 = w3;
             }
             tc::fence_proxy_async();
             tc::fence_before_sync();
@@ -587,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
             raise = true;
         }
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
+        for (int j = 0; j < 2 * NJ; ++j)
             l[j] = ln[j];
         if (tid == 0) {
             const uint64_t dv = tc::smem_desc(base + C::v, 1024, kRowGroup), dp = tc::smem_desc(base + C::p, kTile * 128, 1024);
@@ -604,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
     {
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-            float2 sum = f2_unpack(l[j]);
+            float2 sum = make_float2(l[2 * j], l[2 * j + 1]);
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) {
                 sum.x += __shfl_xor_sync(kAll, sum.x, o);
@@ -622,11 +612,11 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
         if (failed)
             sum = kNaN;
         // sum is 0 where the row attends no token, NaN where a logit was.
-        const float lse2 = sum == 0.f ? -INFINITY : log2f(sum) - col_y[tid];
+        const float lse2 = sum == 0.f ? -INFINITY : log2f(sum) - col_y(tid);
         const int k = tid / G;
         // (+inf, so that the merge's weight for it is NaN and not 0)
         a.lse_part[(size_t)(cq0 + k) * Hq + h * G + (tid - k * G)] = lse2 == lse2 ? lse2 : INFINITY;
-        col_f[tid] = sum == 0.f ? 0.f : ka.v_scale / sum;
+        col_f(tid) = sum == 0.f ? 0.f : ka.v_scale / sum;
     }
     __syncthreads();
 #pragma unroll
@@ -638,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             if (r + i < R)
-                a.o_part[((size_t)(cq0 + k) * Hq + h * G + j) * kD + row] = o[i] * col_f[r + i];
+                a.o_part[((size_t)(cq0 + k) * Hq + h * G + j) * kD + row] = o[i] * col_f(r + i);
             if (++j == G) {
                 j = 0;
                 ++k;
