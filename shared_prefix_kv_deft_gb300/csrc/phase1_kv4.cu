@@ -194,6 +194,28 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
     const int row0 = rg * NR;
     const bool idle = h >= Hkv;
 
+    // The rows of Q, on their way while the slices are looked up: lane (g, t)
+    // takes dims (D / 4) t .. of row g of eight.
+    uint32_t qw[NT][KW * 4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int r = row0 + 8 * n + g;
+#pragma unroll
+        for (int i = 0; i < KW * 4; ++i)
+            qw[n][i] = 0u;
+        if (r < R && !idle) {
+            const int k = r / G;
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
+                                                               ((size_t)p.chunk_q[cq0 + k] * Hq + h * G + (r - k * G)) * D) +
+                               t * KW;
+#pragma unroll
+            for (int i = 0; i < KW; ++i) {
+                const uint4 v = src[i];
+                qw[n][4 * i] = v.x, qw[n][4 * i + 1] = v.y, qw[n][4 * i + 2] = v.z, qw[n][4 * i + 3] = v.w;
+            }
+        }
+    }
+
     // One segment (a piece of a longer node) is the common case; the table of
     // several is made by the CTA.
     uint64_t mask0 = 0;
@@ -293,28 +315,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
     for (; issued < mine && issued < kStages; ++issued)
         issue(issued);
 
-    // ---- Q^T fragments: lane (g, t) holds dims (D / 4) t .. of row g ----
+    // ---- Q^T fragments ----
     uint32_t qa[C::kQSmem ? 1 : NT][KW * 4];
     uint4 *qs = reinterpret_cast<uint4 *>(smem + C::q) + warp * NT * KW * 32 + lane;
     float f[NT][2];                 // what rows 2t and 2t + 1 of S are multiplied by
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const int r = row0 + 8 * n + g;
-        uint32_t w[KW * 4];
-#pragma unroll
-        for (int i = 0; i < KW * 4; ++i)
-            w[i] = 0u;
-        if (r < R && !idle) {
-            const int k = r / G;
-            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
-                                                               ((size_t)p.chunk_q[cq0 + k] * Hq + h * G + (r - k * G)) * D) +
-                               t * KW;
-#pragma unroll
-            for (int i = 0; i < KW; ++i) {
-                const uint4 v = src[i];
-                w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
-            }
-        }
+        uint32_t (&w)[KW * 4] = qw[n];
         // 2^e, in two factors for rows below 2^-112 (e reaches 147).
         const int e = row_exponent<KW * 4, 4>(w), e1 = min(e, 126), e2 = e - e1;
         // (A factor past fp32, for a row near its end, leaves logits of 0.)
