@@ -33,15 +33,17 @@
 // 8 rows a step takes two pages, so that two chains of products and
 // exponentials overlap.  Every wait is bounded.
 //
-// What bounds it is the warps' latency: 64 requests of 64 to 8192 tokens,
-// 32/8 heads of 128, step of 37.4 us for 115 MB (17 us at the measured copy
-// rate).  A page costs a warp some 300 instructions, half of them on the ALU
-// pipe (unpacking, its floor, is 128: a conversion to a pair of fp16 is one
-// instruction with any byte of its operand for free, masking and shifting V's
-// nibbles together six a word), and each scheduler issues one in two cycles
-// from its four warps.  Measured and left: bytes put apart by mul.hi or the
-// pairs made by integer arithmetic (44.7, 48.4 us, then against 37.9), five
-// CTAs an SM with fewer registers (39.1).
+// What bounds it is the units' latency: 64 requests of 64 to 8192 tokens,
+// 32/8 heads of 128, a step of 36.3 us for 115 MB (17 us at the measured copy
+// rate).  Of a unit's 10 us, 4 are the chain of look-ups from its item to its
+// first page (five loads, each waiting for the one before), and in the other 6
+// each scheduler issues an instruction in two cycles from its four warps, some
+// 300 a page and warp: 64 conversions and 64 products of the unpacking, the
+// rest for V's nibbles, the softmax, the look-ups and the copies.  Leaving out
+// any one of these (in a copy for measurement) gains 5% at most.  Measured and
+// left: bytes put apart by mul.hi, pairs made by integer arithmetic (44.7, 48.4
+// us where 37.9), five CTAs an SM with fewer registers (39.1); a conversion
+// takes any byte of its operand at no cost.
 #include <cfloat>
 
 #include "kv4.cuh"

@@ -13,32 +13,35 @@
 // token costs a thread its unpacking (some 90 instructions for 64 elements of
 // K and as many of V) and 32 exponentials; mma.sync, at an eighth of the
 // tensor rate and with every fragment unpacked again for each 32 rows, took
-// 182 us where this takes 102 (the step on a document of 32768 tokens with 64
-// branches of 64 to 8192, 32/8 heads: 36 GFLOP), 44 where 31 (32 branches of
+// 182 us where this takes 99 (the step on a document of 32768 tokens with 64
+// branches of 64 to 8192, 32/8 heads: 36 GFLOP), 44 where 30 (32 branches of
 // 256 tokens on a prompt of 4096, 32/32 heads).
 //
 // A CTA of eight warps takes one unit, and two CTAs share an SM: one unpacks
 // and exponentiates while the other waits.  All warps do the same work.  For
-// tile t they unpack K(t + 1), and the last warp to have stored it starts S(t
-// + 1) into S's other buffer; they read S(t), write P(t) once P(t - 1).V(t -
-// 1) is done, unpack V(t), and vote at the tile's one barrier whether a
-// column's maximum has to be raised (when a logit passes it by more than 2^4:
-// O and the sums are then rescaled and P(t) is made again, before anything has
-// used it); P(t).V(t) is started.  Sums of the weights stay with the threads
-// until the end.  Every wait is bounded.
+// tile t they unpack K(t + 1), read S(t) and take its exponents; one thread
+// starts S(t + 1) into S's other buffer, all warps' K being there by then;
+// they write P(t) once P(t - 1).V(t - 1) is done, unpack V(t), and vote at the
+// tile's one barrier whether a column's maximum has to be raised (when a logit
+// passes it by more than 2^4: O and the sums are then rescaled and P(t) is
+// made again, before anything has used it); P(t).V(t) is started.  Sums of
+// the weights stay with the threads until the end.  Every wait is bounded.
 //
 // S is read in the fragments of an MMA's rows (16x256b): a thread has four
 // rows at RP / 8 columns, so that a column's sums, factors and maxima take a
 // fourth of the registers and reads that a row a thread would take, and S is
 // read once.
 //
-// What bounds it is the tile's chain: 2.2 us for 128 tokens of a unit, two
-// units an SM, of which the tensor products are a fifth and the issue slots
-// half: 630 instructions a warp and tile, 128 of them the conversions and
-// products of the unpacking.  Measured and left: one CTA an SM with twice the
-// registers (155 us where two had 109), 512 threads with a quarter row each
-// (231: 64 registers spill), fewer registers than 128, for room beside the
-// other launch (111 to 126).
+// What bounds it is the tile's chain: 2.1 us for 128 tokens of a unit, two
+// units an SM (hardly less for one alone), of which the tensor products are a
+// fifth and the issue slots under half: 516 instructions a warp and tile, 128
+// of them the conversions and products of the unpacking.  Measured and left:
+// one CTA an SM with twice the registers (155 us where two had 109), 512
+// threads with a quarter row each (231: 64 registers spill), fewer registers
+// than 128, for room beside the other launch (111 to 126), S's read under K's
+// unpacking (107 where 99: eight spilled words), the rows through asynchronous
+// copies in shared memory (106 to 109), the products started by other warps
+// than the first (99).
 #include <cfloat>
 
 #include "kv4.cuh"
