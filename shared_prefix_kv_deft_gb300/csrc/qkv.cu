@@ -22,9 +22,9 @@
 // sectors (with neighbouring pieces in a lane the v rows' 16-byte stores left
 // half sectors to the L2).  A warp takes one or two rounds of
 // 32 / (D / 16) heads of one kind (q, k or v) of one token, all loads ahead
-// of the arithmetic, on packed pairs; the token's cos and sin stay in
-// registers over them.  32768 tokens (32/8 heads of 128, bf16): 154 us, 5.35
-// TB/s; the 822 MB at the measured copy rate take 121.  Bound by issue slots
+// of the arithmetic; the token's cos and sin stay in registers over them.
+// 32768 tokens (32/8 heads of 128, bf16): 148 us, 5.55 TB/s; the 822 MB at
+// the measured copy rate take 121.  Bound by issue slots
 // and loads in flight together: persistent CTAs fed by a ring of bulk copies
 // in shared memory took as long as rows read straight into registers, with
 // more instructions.
@@ -42,9 +42,9 @@ constexpr int kWarps = kThreads / 32;
 constexpr unsigned kAll = 0xffffffffu;
 // Heads a group of lanes takes, and the CTAs that an SM is to hold (which sets
 // the registers): rows in flight against warps in flight.  32768 tokens of
-// bf16, 32/8 heads of 128: 2 and 4 154 us, 2 and 3 174, 2 and 5 178, 3 and 4
-// 160, 4 and 3 164, 1 and 5 194; 10007 tokens of fp32, 12/4 heads of 64: 1 and
-// 4 21.0 us, 1 and 5 20.4, 2 and 3 23.6 (18.6 since).
+// bf16, 32/8 heads of 128: 2 and 4 148 us, 2 and 3 167, 3 and 3 167, 1 and 5
+// 164, 1 and 6 208; 10007 tokens of fp32, 12/4 heads of 64: 1 and 5 18.4 us, 1
+// and 4 19.5, 1 and 6 20.0, 2 and 3 23.2.
 template <bool kF32>
 struct Shape {
     static constexpr int kHeads = kF32 ? 1 : 2, kCtas = kF32 ? 5 : 4;
@@ -85,20 +85,21 @@ struct Piece {
         if constexpr (kF32)
             v[1] = kOnce ? __ldcs(p + 1) : p[1];
     }
-    // As packed pairs of neighbours.
-    __device__ __forceinline__ void pairs(f32x2 (&x)[4]) const
+    __device__ __forceinline__ void values(float (&x)[8]) const
     {
         if constexpr (kF32) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                x[2 * i] = f2_pack(__uint_as_float(v[i].x), __uint_as_float(v[i].y));
-                x[2 * i + 1] = f2_pack(__uint_as_float(v[i].z), __uint_as_float(v[i].w));
+                x[4 * i] = __uint_as_float(v[i].x), x[4 * i + 1] = __uint_as_float(v[i].y);
+                x[4 * i + 2] = __uint_as_float(v[i].z), x[4 * i + 3] = __uint_as_float(v[i].w);
             }
         } else {
-            x[0] = bf16x2_to_f2(v[0].x);
-            x[1] = bf16x2_to_f2(v[0].y);
-            x[2] = bf16x2_to_f2(v[0].z);
-            x[3] = bf16x2_to_f2(v[0].w);
+            const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[2 * i] = __uint_as_float(w[i] << 16);
+                x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
         }
     }
 };
@@ -109,14 +110,12 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-__device__ __forceinline__ float square_sum(const f32x2 (&x)[4])
+__device__ __forceinline__ float square_sum(const float (&x)[8])
 {
     float s[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 v = f2_unpack(f2_mul(x[i], x[i]));
-        s[i] = __fadd_rn(v.x, v.y);
-    }
+    for (int i = 0; i < 4; ++i)
+        s[i] = __fadd_rn(__fmul_rn(x[2 * i], x[2 * i]), __fmul_rn(x[2 * i + 1], x[2 * i + 1]));
     return __fadd_rn(__fadd_rn(s[0], s[1]), __fadd_rn(s[2], s[3]));
 }
 
@@ -191,14 +190,13 @@ __global__ void __launch_bounds__(kThreads, Shape<kF32>::kCtas) qkv_kernel(QkvAr
     const void *src = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
     const int64_t row0 = (int64_t)tok * (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride);
     const int32_t slot = kind == 0 ? 0 : a.slot[tok];
-    // (An unsigned comparison: a negative slot is past the end too.)
-    if (kind != 0 && (uint32_t)slot >= (uint32_t)a.num_pages * kPageSize)
-        return;
     const int half = kind == 2 ? 0 : kWhole ? kLanes : a.half;
     const bool split = kWhole || a.split;
     const Place<D, kWhole> at(lane, split && half > 0 ? half : kLanes);
     const int head0 = part * (C * kRows) + sub;
 
+    // (The position first: the angles wait for it.)
+    const int32_t pos = kind == 2 || a.half == 0 ? 0 : a.position[tok];
     Piece<kF32> raw[C][2];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -211,66 +209,65 @@ __global__ void __launch_bounds__(kThreads, Shape<kF32>::kCtas) qkv_kernel(QkvAr
             raw[c][1].zero();
         }
     }
+    // (After the loads, which so do not wait for it: 148 us, before them 158.
+    // An unsigned comparison: a negative slot is past the end too.)
+    if (kind != 0 && (uint32_t)slot >= (uint32_t)a.num_pages * kPageSize)
+        return;
     // The lane's eight angles: those of its elements (both pieces' are the
     // same), or four for each piece's pairs of neighbours.
     const bool turns0 = split ? at.j < half : at.p0 < 2 * half, turns1 = split ? turns0 : at.p1 < 2 * half;
-    f32x2 cs[4], sn[4];
+    float cs[8], sn[8];
     if (turns0) {
-        const int32_t pos = a.position[tok];
         if ((uint32_t)pos < (uint32_t)a.num_positions) {
-            const ulonglong2 *t = reinterpret_cast<const ulonglong2 *>(a.cos_sin + (int64_t)pos * half * 16);
+            const float4 *t = reinterpret_cast<const float4 *>(a.cos_sin + (int64_t)pos * half * 16);
             const int i0 = split ? 2 * at.j : at.p0, i1 = split ? 2 * at.j + 1 : turns1 ? at.p1 : at.p0;
-            const ulonglong2 c0 = __ldg(t + i0), c1 = __ldg(t + i1), s0 = __ldg(t + half * 2 + i0), s1 = __ldg(t + half * 2 + i1);
-            cs[0] = c0.x, cs[1] = c0.y, cs[2] = c1.x, cs[3] = c1.y;
-            sn[0] = s0.x, sn[1] = s0.y, sn[2] = s1.x, sn[3] = s1.y;
+            const float4 c0 = __ldg(t + i0), c1 = __ldg(t + i1), s0 = __ldg(t + half * 2 + i0), s1 = __ldg(t + half * 2 + i1);
+            cs[0] = c0.x, cs[1] = c0.y, cs[2] = c0.z, cs[3] = c0.w, cs[4] = c1.x, cs[5] = c1.y, cs[6] = c1.z, cs[7] = c1.w;
+            sn[0] = s0.x, sn[1] = s0.y, sn[2] = s0.z, sn[3] = s0.w, sn[4] = s1.x, sn[5] = s1.y, sn[6] = s1.z, sn[7] = s1.w;
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                cs[i] = sn[i] = f2_pack(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
+            for (int i = 0; i < 8; ++i)
+                cs[i] = sn[i] = __int_as_float(0x7fffffff);
         }
     }
     const void *norm = kind == 0 ? a.q_norm : kind == 1 ? a.k_norm : nullptr;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int h = head0 + c * kRows;
-        f32x2 x[2][4];
-        raw[c][0].pairs(x[0]);
-        raw[c][1].pairs(x[1]);
+        float x[2][8];
+        raw[c][0].values(x[0]);
+        raw[c][1].values(x[1]);
         if (norm) {
             const float ss = at.row_sum(square_sum(x[0]), square_sum(x[1]));
             const float r = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(ss, 1.f / D), a.eps)));
-            const f32x2 r2 = f2_pack(r, r);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 Piece<kF32> wp;
                 wp.template load<false>(norm, (p == 0 ? at.p0 : at.p1) * 8);
-                f32x2 w[4];
-                wp.pairs(w);
+                float w[8];
+                wp.values(w);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    x[p][i] = f2_mul(f2_mul(x[p][i], r2), w[i]);
+                for (int i = 0; i < 8; ++i)
+                    x[p][i] = __fmul_rn(__fmul_rn(x[p][i], r), w[i]);
             }
         }
         if (turns0) {
             if (split) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // (Scalar: the assembler fuses packed products into the
-                    // packed sum behind them, whatever rounding they name.)
-                    const float2 u = f2_unpack(x[0][i]), v = f2_unpack(x[1][i]), co = f2_unpack(cs[i]), si = f2_unpack(sn[i]);
-                    const f32x2 t = f2_pack(__fsub_rn(__fmul_rn(u.x, co.x), __fmul_rn(v.x, si.x)), __fsub_rn(__fmul_rn(u.y, co.y), __fmul_rn(v.y, si.y)));
-                    x[1][i] = f2_pack(__fadd_rn(__fmul_rn(v.x, co.x), __fmul_rn(u.x, si.x)), __fadd_rn(__fmul_rn(v.y, co.y), __fmul_rn(u.y, si.y)));
-                    x[0][i] = t;
+                for (int i = 0; i < 8; ++i) {
+                    const float u = x[0][i], v = x[1][i];
+                    x[0][i] = __fsub_rn(__fmul_rn(u, cs[i]), __fmul_rn(v, sn[i]));
+                    x[1][i] = __fadd_rn(__fmul_rn(v, cs[i]), __fmul_rn(u, sn[i]));
                 }
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {       // pair i % 4 of piece i / 4, angle i
                     if (i == 4 && !turns1)
                         break;
-                    f32x2 &y = x[i / 4][i % 4];
-                    const float2 v = f2_unpack(y), c2 = f2_unpack(cs[i / 2]), s2 = f2_unpack(sn[i / 2]);
-                    const float co = i % 2 ? c2.y : c2.x, si = i % 2 ? s2.y : s2.x;
-                    y = f2_pack(__fsub_rn(__fmul_rn(v.x, co), __fmul_rn(v.y, si)), __fadd_rn(__fmul_rn(v.y, co), __fmul_rn(v.x, si)));
+                    float &u = x[i / 4][2 * (i % 4)], &v = x[i / 4][2 * (i % 4) + 1];
+                    const float t = __fsub_rn(__fmul_rn(u, cs[i]), __fmul_rn(v, sn[i]));
+                    v = __fadd_rn(__fmul_rn(v, cs[i]), __fmul_rn(u, sn[i]));
+                    u = t;
                 }
             }
         }
@@ -280,8 +277,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kF32>::kCtas) qkv_kernel(QkvAr
             uint32_t w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float2 v = f2_unpack(x[p][i]);
-                w[i] = bf16x2(v.x, v.y);
+                w[i] = bf16x2(x[p][2 * i], x[p][2 * i + 1]);
             }
             o[p] = make_uint4(w[0], w[1], w[2], w[3]);
         }
@@ -426,7 +422,7 @@ template <int D, bool k4>
 int pick_qkv(const QkvArgs &a, bool f32, cudaStream_t st)
 {
     // (With the rotation's place known: 32768 tokens 162 -> 154 us, 16384 into
-    // 4 bits and back 116 -> 106 us.)
+    // 4 bits and back 116 -> 106 us, when it was added.)
     if (a.split && a.half == D / 16)
         return f32 ? launch_qkv<D, true, k4, true>(a, st) : launch_qkv<D, false, k4, true>(a, st);
     return f32 ? launch_qkv<D, true, k4, false>(a, st) : launch_qkv<D, false, k4, false>(a, st);
