@@ -23,7 +23,7 @@
 // half sectors to the L2).  A warp takes one or two rounds of
 // 32 / (D / 16) heads of one kind (q, k or v) of one token, all loads ahead
 // of the arithmetic; the token's cos and sin stay in registers over them.
-// 32768 tokens (32/8 heads of 128, bf16): 148 us, 5.55 TB/s; the 822 MB at
+// 32768 tokens (32/8 heads of 128, bf16): 136 us, 6.0 TB/s; the 822 MB at
 // the measured copy rate take 121.  Bound by issue slots
 // and loads in flight together: persistent CTAs fed by a ring of bulk copies
 // in shared memory took as long as rows read straight into registers, with
@@ -37,17 +37,18 @@
 namespace deft {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr unsigned kAll = 0xffffffffu;
 // Heads a group of lanes takes, and the CTAs that an SM is to hold (which sets
 // the registers): rows in flight against warps in flight.  32768 tokens of
-// bf16, 32/8 heads of 128: 2 and 4 148 us, 2 and 3 167, 3 and 3 167, 1 and 5
-// 164, 1 and 6 208; 10007 tokens of fp32, 12/4 heads of 64: 1 and 5 18.4 us, 1
-// and 4 19.5, 1 and 6 20.0, 2 and 3 23.2.
+// bf16, 32/8 heads of 128: 2 and 9 136 us, though some registers spill, 2 and 8
+// 142, 2 and 7 151, 2 and 10 160, 3 and 6 162 (CTAs of 256 threads, 2 and 4:
+// 145, rows' lines marked for eviction first: 148); 10007 tokens of fp32, 12/4
+// heads of 64: 1 and 10 18.4 us, 1 and 9 20.5, 1 and 11 20.5, 2 and 7 21.0.
 template <bool kF32>
 struct Shape {
-    static constexpr int kHeads = kF32 ? 1 : 2, kCtas = kF32 ? 5 : 4;
+    static constexpr int kHeads = kF32 ? 1 : 2, kCtas = kF32 ? 10 : 9;
 };
 
 struct QkvArgs {
@@ -76,14 +77,12 @@ struct Piece {
         if constexpr (kF32)
             v[1] = v[0];
     }
-    // kOnce: read by this warp alone (a row), not by every one (a norm's weights).
-    template <bool kOnce>
     __device__ __forceinline__ void load(const void *src, int64_t elem)
     {
         const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const char *>(src) + elem * (kF32 ? 4 : 2));
-        v[0] = kOnce ? __ldcs(p) : *p;
+        v[0] = __ldg(p);
         if constexpr (kF32)
-            v[1] = kOnce ? __ldcs(p + 1) : p[1];
+            v[1] = __ldg(p + 1);
     }
     __device__ __forceinline__ void values(float (&x)[8]) const
     {
@@ -202,14 +201,14 @@ __global__ void __launch_bounds__(kThreads, Shape<kF32>::kCtas) qkv_kernel(QkvAr
     for (int c = 0; c < C; ++c) {
         const int h = head0 + c * kRows;
         if (h < heads) {
-            raw[c][0].template load<true>(src, row0 + (int64_t)h * D + at.p0 * 8);
-            raw[c][1].template load<true>(src, row0 + (int64_t)h * D + at.p1 * 8);
+            raw[c][0].load(src, row0 + (int64_t)h * D + at.p0 * 8);
+            raw[c][1].load(src, row0 + (int64_t)h * D + at.p1 * 8);
         } else {
             raw[c][0].zero();
             raw[c][1].zero();
         }
     }
-    // (After the loads, which so do not wait for it: 148 us, before them 158.
+    // (After the loads, which so do not wait for it: 148 us where 158.
     // An unsigned comparison: a negative slot is past the end too.)
     if (kind != 0 && (uint32_t)slot >= (uint32_t)a.num_pages * kPageSize)
         return;
@@ -243,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kF32>::kCtas) qkv_kernel(QkvAr
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 Piece<kF32> wp;
-                wp.template load<false>(norm, (p == 0 ? at.p0 : at.p1) * 8);
+                wp.load(norm, (p == 0 ? at.p0 : at.p1) * 8);
                 float w[8];
                 wp.values(w);
 #pragma unroll
@@ -338,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kF32>::kCtas) qkv_kernel(QkvAr
 // Blocks a thread has in flight.  6007 pages of 8 heads of 128 (504 MB, 74 us at
 // the measured copy rate): 77.9 us, at 1 block 79.9; with two 16-byte stores in
 // place of one of 32 bytes, which leaves half sectors to the L2, 88.1 and more.
-constexpr int kUnpack = 4;
+constexpr int kUnpack = 4, kUnpackThreads = 256;
 
 struct UnpackArgs {
     const uint8_t *k4, *v4;
@@ -351,7 +350,7 @@ struct UnpackArgs {
 // A thread a block of 16 elements: 8 bytes of codes and a scale in, 32 bytes
 // out; a CTA's threads go over one page's heads, K and V by blockIdx.y.
 template <int D>
-__global__ void __launch_bounds__(kThreads) unpack4_kernel(UnpackArgs a)
+__global__ void __launch_bounds__(kUnpackThreads) unpack4_kernel(UnpackArgs a)
 {
     using P = kv4::Page<D>;
     const int page = a.page_id[blockIdx.x];
@@ -362,12 +361,12 @@ __global__ void __launch_bounds__(kThreads) unpack4_kernel(UnpackArgs a)
     const uint8_t *src = (is_v ? a.v4 : a.k4) + (int64_t)page * a.num_kv_heads * P::kBytes;
     uint4 *dst = (is_v ? a.v_pages : a.k_pages) + (int64_t)blockIdx.x * a.num_kv_heads * (kPageSize * D / 8);
     const int blocks = a.num_kv_heads * D;
-    for (int b0 = threadIdx.x; b0 < blocks; b0 += kUnpack * kThreads) {
+    for (int b0 = threadIdx.x; b0 < blocks; b0 += kUnpack * kUnpackThreads) {
         uint2 w[kUnpack];
         uint32_t s[kUnpack];
 #pragma unroll
         for (int u = 0; u < kUnpack; ++u) {
-            const int b = b0 + u * kThreads;
+            const int b = b0 + u * kUnpackThreads;
             if (b < blocks) {
                 const uint8_t *head = src + (int64_t)(b / D) * P::kBytes;
                 w[u] = __ldcs(reinterpret_cast<const uint2 *>(head) + b % D);
@@ -376,7 +375,7 @@ __global__ void __launch_bounds__(kThreads) unpack4_kernel(UnpackArgs a)
         }
 #pragma unroll
         for (int u = 0; u < kUnpack; ++u) {
-            const int b = b0 + u * kThreads;
+            const int b = b0 + u * kUnpackThreads;
             if (b >= blocks)
                 break;
             const uint32_t s2 = kv4::scales2(s[u] | s[u] << 8);
@@ -397,11 +396,11 @@ __global__ void __launch_bounds__(kThreads) unpack4_kernel(UnpackArgs a)
 }
 
 template <typename Args>
-int launch(void (*kernel)(Args), dim3 grid, cudaStream_t st, const Args &a)
+int launch(void (*kernel)(Args), dim3 grid, int threads, cudaStream_t st, const Args &a)
 {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.stream = st;
     return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? DEFT_OK : DEFT_ECUDA;
 }
@@ -415,7 +414,7 @@ int launch_qkv(QkvArgs a, cudaStream_t st)
     const int64_t tasks = (int64_t)a.num_tokens * (a.q_tasks + 2 * a.kv_tasks);
     if (tasks > INT32_MAX)
         return DEFT_EUNSUPPORTED;
-    return launch(qkv_kernel<D, kF32, k4, kWhole>, dim3((unsigned)((tasks + kWarps - 1) / kWarps)), st, a);
+    return launch(qkv_kernel<D, kF32, k4, kWhole>, dim3((unsigned)((tasks + kWarps - 1) / kWarps)), kThreads, st, a);
 }
 
 template <int D, bool k4>
@@ -554,7 +553,7 @@ int deft_kv_unpack4(const void *k4_pages, const void *v4_pages, float k_scale, f
                  num_listed, num_pages, num_kv_heads};
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const dim3 grid((unsigned)num_listed, 2);
-    return head_dim == 128 ? launch(unpack4_kernel<128>, grid, st, a) : launch(unpack4_kernel<64>, grid, st, a);
+    return head_dim == 128 ? launch(unpack4_kernel<128>, grid, kUnpackThreads, st, a) : launch(unpack4_kernel<64>, grid, kUnpackThreads, st, a);
 }
 
 }  // extern "C"
