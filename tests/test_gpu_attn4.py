@@ -226,6 +226,24 @@ def test_growing_logits_and_one_that_leads_all(d):
     check(t, t.run(t.plan(8192)), scale=None)
 
 
+@pytest.mark.parametrize("queries", [4, 12, 20, 50])
+@pytest.mark.parametrize("rising", [True, False])
+def test_logits_that_rise_or_fall_over_a_chunk(queries, rising):
+    """Every width: the maxima raised tile after tile (by 2^4 and more each),
+    or once and then far above everything; branches that see half of it."""
+    n = 1500
+    t = Tree([-1] + [0] * queries, [n] + [1 + i % 40 for i in range(queries)], list(range(1, queries + 1)), 1, 1, 128, seed=queries)
+    t.q[:] = np.abs(t.q) + 0.25
+    t.q = f64(torch.from_numpy(t.q.astype(np.float32)).bfloat16())
+    s = t.slots(0)
+    codes, scales = t.k4[..., :8 * 128].reshape(-1, 1, 16, 64), t.k4[..., 8 * 128:].reshape(-1, 1, 16, 8)
+    codes[s // 16, :, s % 16] &= 0x77           # keys of no negative element: logits follow the scales
+    at = np.arange(n) if rising else np.arange(n)[::-1]
+    scales[s // 16, :, s % 16] = (0x20 + at * 40 // n)[:, None, None]    # 2^-3 to 2^2
+    for chunk in (256, 2048):
+        check(t, t.run(t.plan(chunk)))
+
+
 @pytest.mark.parametrize("scale", [1e-30, 1.0, 40.0])
 def test_scales(scale):
     t = Tree([-1, 0, 0], [100, 9, 30], [1, 2, 0], 2, 3, 128)
