@@ -587,7 +587,7 @@ typedef struct deft_qk_turn {
     int32_t interleaved;       /* 1: pairs of neighbours, 0: of halves               */
     int32_t num_positions;
     const float *cos_sin;      /* [num_positions][rot_dim]                           */
-    const int32_t *position;   /* [num_tokens]                                       */
+    const int32_t *position;   /* [num_tokens] (may be NULL where that is 0)         */
 } deft_qk_turn;
 int deft_qkv_write(const void *q, const void *k, const void *v, int32_t in_dtype, int64_t q_stride, int64_t k_stride,
                    int64_t v_stride, const int32_t *slot, int32_t num_tokens, const deft_qk_turn *turn, void *q_out,

@@ -441,7 +441,7 @@ int check_qkv(const void *q, const void *k, const void *v, int32_t in_dtype, int
         return DEFT_EINVAL;
     const deft_qk_turn none{};
     const deft_qk_turn &t = turn ? *turn : none;
-    if (t.rot_dim < 0 || t.rot_dim > head_dim || (t.rot_dim > 0 && (!t.cos_sin || !t.position || t.num_positions < 1)) ||
+    if (t.rot_dim < 0 || t.rot_dim > head_dim || (t.rot_dim > 0 && (!t.cos_sin || t.num_positions < 1)) ||
         (t.interleaved != 0 && t.interleaved != 1) || ((t.q_norm || t.k_norm) && !(t.eps >= 0.f && t.eps <= 1e30f)))
         return DEFT_EINVAL;
     if ((head_dim != 64 && head_dim != 128) || page_size != kPageSize || num_pages > INT32_MAX / kPageSize ||
@@ -453,7 +453,7 @@ int check_qkv(const void *q, const void *k, const void *v, int32_t in_dtype, int
         return DEFT_EINVAL;
     if ((int64_t)num_tokens * (num_q_heads + 2 * (int64_t)num_kv_heads) > INT32_MAX)
         return DEFT_EUNSUPPORTED;
-    if (num_tokens > 0 && (!k || !v || !slot || (num_q_heads > 0 && (!q || !q_out))))
+    if (num_tokens > 0 && (!k || !v || !slot || (t.rot_dim > 0 && !t.position) || (num_q_heads > 0 && (!q || !q_out))))
         return DEFT_EINVAL;
     uintptr_t all = (uintptr_t)k | (uintptr_t)v | (uintptr_t)k_pool | (uintptr_t)v_pool | (uintptr_t)t.q_norm |
                     (uintptr_t)t.k_norm | (uintptr_t)t.cos_sin;
