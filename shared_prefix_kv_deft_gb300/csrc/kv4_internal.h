@@ -4,7 +4,33 @@
 
 #include "deft_internal.h"
 
+#ifdef __CUDACC__
+#define DEFT_HOST_DEVICE __host__ __device__
+#else
+#define DEFT_HOST_DEVICE
+#endif
+
 namespace deft {
+
+// A ring of barriers, one copy a phase: copy j completes phase j / stages of
+// barrier j % stages.
+template <typename Wait>
+DEFT_HOST_DEVICE inline bool ring_wait(int j, int stages, Wait &&wait)
+{
+    return wait(j % stages, (uint32_t)(j / stages) & 1u);
+}
+
+// The copies that may still be on their way when the wait for copy `first`
+// has run out and `issued` copies went out in all: the ones from `first` on.
+// (Earlier ones have been waited for.  A barrier answers for the parity of the
+// phase before the one it is in: another parity than the copy's would be
+// answered at once with the copy in flight, and a stage without a copy never.)
+template <typename Wait>
+DEFT_HOST_DEVICE inline void ring_drain(int first, int issued, int stages, Wait &&wait)
+{
+    for (int j = first; j < issued; ++j)
+        ring_wait(j, stages, wait);
+}
 
 // A phase-1 launch over a 4-bit cache: items [first, first + n) of one of
 // the partition's two lists.

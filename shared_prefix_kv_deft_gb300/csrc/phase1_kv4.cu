@@ -371,7 +371,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
     // shared memory a page, not 40).
     const int kg = g ^ (g >> 1 & 1);
     const int vx = 2 * t + (t & 1), vy = 2 * t + 1 - (t & 1);
-    bool ok = true;
+    auto landed = [&](int stage, uint32_t parity) { return tc::mbar_wait(bars + stage * 8, parity); };
+    int failed = -1;                // the step whose copy did not land in time
     for (int i = 0; i < mine; ++i) {
         if (i > 0 && i % kBatch == 0)
             cur = next;      // (issue() is at most kStages ahead: it has filled this batch)
@@ -382,8 +383,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
             desc[p2] = __shfl_sync(kAll, cur, i % kBatch * PP + p2);
             whole &= desc[p2] >> 31 != 0;
         }
-        if (!__all_sync(kAll, tc::mbar_wait(bars + (i % kStages) * 8, (i / kStages) & 1))) {
-            ok = false;
+        if (!__all_sync(kAll, ring_wait(i, kStages, landed))) {
+            failed = i;
             break;
         }
         uint8_t *stage = smem + (warp * kStages + i % kStages) * C::kStage;
@@ -577,10 +578,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
             ++issued;
         }
     }
-    if (!ok) {
-        // A copy that never landed: give the others their time, and say so.
-        for (int i = 0; i < kStages; ++i)
-            tc::mbar_wait(bars + i * 8, 0);
+    if (failed >= 0) {
+        // A copy that did not land: time for it and for those behind it, before
+        // the ring is used for the states or freed, and say so.
+        ring_drain(failed, issued, kStages, landed);
         if (lane == 0)
             report_failure(p.status, 401);
 #pragma unroll

@@ -1,6 +1,7 @@
 """The calls around the 4-bit cache at their edges, as far as no GPU is needed:
 empty batches, argument ranges, the arithmetic of the format."""
 import ctypes
+import subprocess
 
 import pytest
 
@@ -26,3 +27,77 @@ def test_no_tokens_need_no_positions(tokens, status, four):
     tail = [4, 4, 2, 64, 16, None]
     lib = deft.load()
     assert (lib.deft_qkv_write4(*args, 1.0, 1.0, *tail) if four else lib.deft_qkv_write(*args, *tail)) == status
+
+
+RING = r"""
+#include <cstdio>
+#include <vector>
+
+#include "kv4_internal.h"
+
+// Barriers as the GPU's: one arrival a phase, and a wait for a parity is
+// answered when the phase before the present one had it.
+struct Ring {
+    std::vector<int> phase;                 // completed, by stage
+    std::vector<std::vector<int>> flying;   // copies on their way, by stage
+    int asked = 0, vain = 0;
+    explicit Ring(int stages) : phase(stages), flying(stages) {}
+    void issue(int j) { flying[j % phase.size()].push_back(j); }
+    void land(int s)
+    {
+        phase[s]++;
+        flying[s].clear();
+    }
+    // A wait that lets the stage's copy land, if the parity asked for is that copy's.
+    bool operator()(int s, unsigned parity)
+    {
+        asked++;
+        if (((phase[s] & 1) ^ 1) == (int)parity && phase[s] > 0)
+            return true;
+        if (flying[s].empty() || (phase[s] & 1) != (int)parity) {
+            vain++;
+            return false;
+        }
+        land(s);
+        return true;
+    }
+};
+
+int main()
+{
+    int bad = 0, runs = 0;
+    for (int stages = 1; stages <= 4; ++stages)
+        for (int mine = 1; mine <= 13; ++mine)
+            for (int failed = 0; failed < mine; ++failed) {
+                Ring r(stages);
+                auto wait = [&](int s, unsigned p) { return r(s, p); };
+                int issued = 0;
+                while (issued < mine && issued < stages)
+                    r.issue(issued++);
+                for (int i = 0; i < failed; ++i) {
+                    bad += !deft::ring_wait(i, stages, wait);
+                    if (issued < mine)
+                        r.issue(issued++);
+                }
+                r.asked = 0;
+                deft::ring_drain(failed, issued, stages, wait);
+                for (auto &f : r.flying)
+                    bad += !f.empty();
+                bad += r.vain != 0 || r.asked != issued - failed;
+                ++runs;
+            }
+    std::printf("%d %d\n", runs, bad);
+    return bad != 0;
+}
+"""
+
+
+def test_a_failed_wait_leaves_no_copy_behind(tmp_path):
+    """Whichever copy of whichever ring does not land in time: the drain waits
+    for every copy that is still on its way, and for nothing else."""
+    src = tmp_path / "ring.cpp"
+    src.write_text(RING)
+    exe = tmp_path / "ring"
+    subprocess.run(["g++", "-std=c++17", "-O1", f"-I{deft_build.CSRC}", f"-I{deft_build.INCLUDE}", str(src), "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.split() == [str(4 * 13 * 14 // 2), "0"]
