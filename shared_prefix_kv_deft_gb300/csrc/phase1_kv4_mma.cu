@@ -71,8 +71,8 @@ struct Cfg {
     static constexpr uint32_t red = col + RP * 8;               // [4 warps][RP]
     static constexpr uint32_t seg = red + 4 * RP * 4;           // [256] position, page, begin; [256] mask (8 B)
     static constexpr uint32_t misc = seg + kMaxSegsPerChunk * 20;   // TMEM base
-    static constexpr uint32_t bars = misc + 16;                 // S, O, K
-    static constexpr uint32_t total = bars + 24;
+    static constexpr uint32_t bars = misc + 16;                 // S, O, K, end
+    static constexpr uint32_t total = bars + 32;
     static constexpr uint32_t alloc = total + 1024;
     static_assert(q % 1024 == 0 && p % 1024 == 0, "128-byte-swizzle atoms");
     static_assert(2 * (alloc + 1024) <= 228 * 1024, "two CTAs an SM");
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
             *seg_begin = seg_page + kMaxSegsPerChunk;
     uint64_t *seg_mask = reinterpret_cast<uint64_t *>(seg_begin + kMaxSegsPerChunk);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::misc);
-    const uint32_t bar_s = base + C::bars, bar_o = bar_s + 8, bar_k = bar_s + 16;
+    const uint32_t bar_s = base + C::bars, bar_o = bar_s + 8, bar_k = bar_s + 16, bar_end = bar_s + 24;
 
     if (warp == 0) {
         tc::tmem_alloc(smem_u32(tmem_slot), kTmemCols);
@@ -249,8 +249,9 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
     if (tid == 0) {
         tc::mbar_init(bar_s, 1);
         tc::mbar_init(bar_o, 1);
-        tc::fence_mbar_init();
         tc::mbar_init(bar_k, kThreads / 32);
+        tc::mbar_init(bar_end, 1);
+        tc::fence_mbar_init();
     }
     __syncthreads();
     if (a.wait_prior)
@@ -608,8 +609,14 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
         }
     }
     const bool failed = __syncthreads_or(!ok);
-    if (failed && tid == 0)
+    if (failed && tid == 0) {
         report_failure(p.status, 402);
+        // The products still under way end before their operands' places and
+        // TMEM are given back: a barrier of their own, whose first phase ends
+        // with the last of them (S's and O's may be some phases behind).
+        tc::mma_commit(bar_end);
+        tc::mbar_wait(bar_end, 0);
+    }
     if (tid < RP && tid < R) {
         float sum = (red[tid] + red[RP + tid]) + (red[2 * RP + tid] + red[3 * RP + tid]);
         if (failed)
