@@ -663,6 +663,7 @@ int deft_kv_unpack4(const void *k4_pages, const void *v4_pages, float k_scale, f
  *     fp32's largest, has NaN in out and lse (a logit below fp32's least may
  *     give NaN too); no other row is affected.  page_id and node_page_off are trusted, as in
  *     deft_tree_attn (page_id may be NULL where no path has a token).
+ *   - At most 2^32 heads' pages, num_pages * num_kv_heads (DEFT_EUNSUPPORTED).
  * out 16-byte aligned (DEFT_EINVAL).  Several steps of one plan may run at
  * the same time, each with its own outputs and workspace (this call does not use the plan's work queues).  A
  * kernel wait that runs out is reported by deft_step_status.  k_scale and

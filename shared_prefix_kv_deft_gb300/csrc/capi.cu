@@ -589,6 +589,9 @@ int deft_tree_attn4(const void *q, const void *k4_pages, const void *v4_pages, f
         return DEFT_EINVAL;
     if ((uintptr_t)out & 15u)
         return DEFT_EINVAL;
+    // The kernels number a pool's pages of one head in 32 bits.
+    if (num_pages > 0 && num_kv_heads > 0 && (uint64_t)num_pages * (uint64_t)num_kv_heads > (1ull << 32))
+        return DEFT_EUNSUPPORTED;
     // No page is read where no query's path has a token.
     if (!page_id && plan && plan->tree.fma_items.empty() && plan->tree.mma_items.empty())
         page_id = node_page_off;

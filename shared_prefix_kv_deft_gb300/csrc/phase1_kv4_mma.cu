@@ -297,7 +297,6 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
     const int ntiles = (T + kTile - 1) / kTile;
     const uint8_t *k4 = static_cast<const uint8_t *>(a.k_pages) + half * (P::kRow / 2);
     const uint8_t *v4 = static_cast<const uint8_t *>(a.v_pages) + half * (P::kRow / 2);
-    static_assert(P::kBytes % P::kRow == 0, "rows at multiples of their length (64 bytes: 2^32 of them are 256 GB)");
     struct Where {
         int page;
         int meta;           // segment x 16 + token of the page
@@ -322,8 +321,8 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
     };
     auto load = [&](HalfRow &x, const uint8_t *pool, const Where &w) {
         const int tok = w.meta % kPageSize;
-        const uint32_t at = (uint32_t)(w.page * Hkv + h) * (P::kBytes / P::kRow) + tok;     // in rows
-        x.load(pool + (size_t)at * P::kRow, tok, half);
+        const uint32_t at = (uint32_t)w.page * (uint32_t)Hkv + h;   // (the step is refused where this could pass 32 bits)
+        x.load(pool + ((size_t)at * P::kBytes + tok * P::kRow), tok, half);
     };
     HalfRow kr, vr;
     Where w0 = where(0), w1 = where(1), w2;     // of tiles t, t + 1, t + 2

@@ -27,3 +27,26 @@ def test_no_tokens_with_a_rotation(interleaved):
         before = [p.clone() for p in pools]
         assert call(r.q[:0], r.k[:0], r.v[:0], cu([]), *pools, **kw).shape == (0, 2, 64)
         assert all(torch.equal(a, b) for a, b in zip(pools, before))
+
+
+@pytest.mark.parametrize("first", [(1 << 32) // (8 * 18) - 7, 1 << 27])
+@pytest.mark.parametrize("d", [64, 128])
+def test_pages_far_from_the_pools_start(d, first):
+    """Pages whose rows, counted from the pool's start, pass 2^32 (and 256 GB):
+    a pool that begins so far before the pages which the step names, all of
+    which are there.  Units of 2, 12, 20 and 40 rows."""
+    import ctypes
+    for queries in (2, 12, 20, 40):
+        t = Tree([-1] + [0] * queries, [300] + [1 + i % 33 for i in range(queries)], list(range(1, queries + 1)), 8, 1, d, seed=queries)
+        plan = t.plan()
+        q, k4, v4, off, ids = t.tensors()
+        want = t.run(plan)
+        ids = ids + first
+        bufs = deft.alloc_buffers(plan, queries, 8, d, out_dtype=deft.DEFT_OUT_F32)
+        start = first * 8 * 9 * d
+        rc = deft.load().deft_tree_attn4(q.data_ptr(), k4.data_ptr() - start, v4.data_ptr() - start, 1.0, 1.0, off.data_ptr(), ids.data_ptr(),
+                                         first + k4.shape[0], 8, 8, d, 16, 1 / d ** 0.5, plan.handle, bufs.out.data_ptr(), deft.DEFT_OUT_F32,
+                                         bufs.lse.data_ptr(), bufs.workspace.data_ptr(), ctypes.c_size_t(bufs.workspace.numel()),
+                                         torch.cuda.current_stream().cuda_stream)
+        assert rc == 0 and plan.step_status() == 0
+        assert torch.equal(bufs.out, want[0]) and torch.equal(bufs.lse, want[1])

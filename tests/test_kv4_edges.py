@@ -101,3 +101,12 @@ def test_a_failed_wait_leaves_no_copy_behind(tmp_path):
     subprocess.run(["g++", "-std=c++17", "-O1", f"-I{deft_build.CSRC}", f"-I{deft_build.INCLUDE}", str(src), "-o", str(exe)], check=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True)
     assert r.returncode == 0 and r.stdout.split() == [str(4 * 13 * 14 // 2), "0"]
+
+
+@pytest.mark.parametrize("pages,heads,status", [((1 << 31) - 1, 2, ESTATE), (1 << 28, 16, ESTATE), ((1 << 28) + 1, 16, EUNSUPPORTED),
+                                                ((1 << 31) - 1, 4, EUNSUPPORTED), ((1 << 31) - 1, 1 << 20, EUNSUPPORTED)])
+def test_pages_of_heads_are_numbered_in_32_bits(pages, heads, status):
+    """Of a plan that has not been uploaded: nothing reaches a GPU."""
+    plan = deft.Plan([-1, 0, 0], [100, 5, 7], [1, 2], 256, 2, naive=False)
+    rc = deft.load().deft_tree_attn4(A, 2 * A, 3 * A, 1.0, 1.0, A, A, pages, 2 * heads, heads, 128, 16, 0.1, plan.handle, 4 * A, 0, 5 * A, 6 * A, 1 << 30, None)
+    assert rc == status
