@@ -75,12 +75,15 @@ struct Piece {
         if constexpr (kF32)
             v[1] = v[0];
     }
+    // kKept: of memory that nothing writes while the kernel runs (the rows may
+    // be queries in place).
+    template <bool kKept = false>
     __device__ __forceinline__ void load(const void *src, int64_t elem)
     {
         const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const char *>(src) + elem * (kF32 ? 4 : 2));
-        v[0] = __ldg(p);
+        v[0] = kKept ? __ldg(p) : p[0];
         if constexpr (kF32)
-            v[1] = __ldg(p + 1);
+            v[1] = kKept ? __ldg(p + 1) : p[1];
     }
     __device__ __forceinline__ void values(float (&x)[8]) const
     {
@@ -240,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kF32>::kCtas) qkv_kernel(QkvAr
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 Piece<kF32> wp;
-                wp.load(norm, (p == 0 ? at.p0 : at.p1) * 8);
+                wp.template load<true>(norm, (p == 0 ? at.p0 : at.p1) * 8);
                 float w[8];
                 wp.values(w);
 #pragma unroll

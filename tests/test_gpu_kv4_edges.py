@@ -50,3 +50,16 @@ def test_pages_far_from_the_pools_start(d, first):
                                          torch.cuda.current_stream().cuda_stream)
         assert rc == 0 and plan.step_status() == 0
         assert torch.equal(bufs.out, want[0]) and torch.equal(bufs.lse, want[1])
+
+
+@pytest.mark.parametrize("d,hq,rot", [(64, 3, 64), (64, 5, 16), (128, 32, 128), (128, 1, 48)])
+def test_queries_in_place(d, hq, rot):
+    """q_out on q itself, from a start in the middle of a sector on (so that
+    neighbouring rows share sectors), is q_out elsewhere, bit for bit."""
+    r = Rows(T=3000, hq=hq, hkv=1, d=d, rot=rot)
+    want = deft.deft_qkv_write(r.q, r.k, r.v, cu(r.slot), *r.pools(), **r.kw)
+    for call, pools in ((deft.deft_qkv_write, r.pools()), (deft.deft_qkv_write4, r.pools4())):
+        q = torch.empty(r.q.numel() + 8, dtype=torch.bfloat16, device="cuda")[8:].view(r.q.shape)
+        q.copy_(r.q)
+        assert q.data_ptr() % 32 == 16
+        assert call(q, r.k, r.v, cu(r.slot), *pools, q_out=q, **r.kw) is q and torch.equal(q, want)
