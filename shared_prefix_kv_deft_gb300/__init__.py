@@ -675,6 +675,8 @@ def alloc_kv4_pages(num_pages: int, num_kv_heads: int, head_dim: int, device="cu
     """(k4_pages, v4_pages) of a 4-bit cache, uint8 [pages, heads, kv4_page_bytes(head_dim)]."""
     import torch
     shape = (int(num_pages), int(num_kv_heads), kv4_page_bytes(head_dim))
+    if shape[2] == 0:
+        raise ValueError("a 4-bit cache has a head_dim of 64 or 128")
     return tuple(torch.empty(shape, dtype=torch.uint8, device=device) for _ in "kv")
 
 

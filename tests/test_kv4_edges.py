@@ -110,3 +110,10 @@ def test_pages_of_heads_are_numbered_in_32_bits(pages, heads, status):
     plan = deft.Plan([-1, 0, 0], [100, 5, 7], [1, 2], 256, 2, naive=False)
     rc = deft.load().deft_tree_attn4(A, 2 * A, 3 * A, 1.0, 1.0, A, A, pages, 2 * heads, heads, 128, 16, 0.1, plan.handle, 4 * A, 0, 5 * A, 6 * A, 1 << 30, None)
     assert rc == status
+
+
+def test_alloc_kv4_pages_refuses_other_heads():
+    assert [p.shape for p in deft.alloc_kv4_pages(3, 2, 64, "cpu")] == [(3, 2, 576)] * 2
+    for d in (0, -64, 32, 96, 256):
+        with pytest.raises(ValueError):
+            deft.alloc_kv4_pages(3, 2, d, "cpu")
