@@ -84,9 +84,12 @@ __device__ __forceinline__ uint32_t scale_of(float amax, float six_g)
 
 // Eight elements as codes: x / sg (sg: the block's scale times g), rounded
 // to the nearest, halfway to the even code, at most 6 in magnitude.  The
-// quotient is the correctly rounded one, by one residual step on x * (1 /
-// sg): a bf16 x over an 8-bit scale often lies exactly between two codes,
-// where x * (1 / sg) alone is an ulp to either side.
+// codes are those of the correctly rounded quotient (tested for every bf16 x
+// next to every border), by Markstein's division (IBM Journal of Research and
+// Development 34, 1990): the product y0 = x * (1 / sg), its residual y0 * sg -
+// x, which one fused multiply-add gives exactly, and one more that takes the
+// residual over sg from y0.  A bf16 x over an 8-bit scale often lies exactly
+// between two codes, where y0 alone is an ulp to either side.
 __device__ __forceinline__ uint32_t pack8(const float (&x)[8], float amax, float sg)
 {
     const float r = sg > 0.f ? __frcp_rn(sg) : 0.f;

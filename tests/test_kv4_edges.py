@@ -2,6 +2,7 @@
 empty batches, argument ranges, the arithmetic of the format."""
 import ctypes
 import subprocess
+from fractions import Fraction
 
 import pytest
 
@@ -117,3 +118,44 @@ def test_alloc_kv4_pages_refuses_other_heads():
     for d in (0, -64, 32, 96, 256):
         with pytest.raises(ValueError):
             deft.alloc_kv4_pages(3, 2, d, "cpu")
+
+
+def rounded(x: Fraction) -> Fraction:
+    """x > 0 to 24 significant bits, halfway to even."""
+    e = x.numerator.bit_length() - x.denominator.bit_length() - 24
+    unit = Fraction(2) ** (e + (x / Fraction(2) ** e >= 1 << 24))
+    return round(x / unit) * unit       # (Fraction's round is to even)
+
+
+def test_quotients_are_the_correctly_rounded_ones():
+    """The append's quotient (the product with the reciprocal, and one step on
+    the exact residual) gives the code of the correctly rounded x / sg for
+    every bf16 x and every fp32 sg.  Both are within two units in the last
+    place of x / sg, so they can only lie on two sides of a border t (or one
+    on it) where sg is within a few units of x / t: all of those are tried,
+    for all 128 significands of x and all seven borders.  Powers of two change
+    nothing (the residual is far from fp32's least numbers)."""
+    borders = [Fraction(b) / 4 for b in (1, 3, 5, 7, 10, 14, 20)]
+
+    def code(y):        # halfway to the even code
+        return sum(y > t if i % 2 == 0 else y >= t for i, t in enumerate(borders))
+
+    assert [code(t) for t in borders] == [0, 2, 2, 4, 4, 6, 6]
+    off = changed = 0
+    for m in range(128):
+        x = 1 + Fraction(m, 128)
+        for t in borders:
+            near = rounded(x / t)
+            unit = Fraction(2) ** (near.numerator.bit_length() - near.denominator.bit_length() - 25)
+            for u in range(-24, 25):
+                sg = rounded(near + u * unit)
+                r = rounded(1 / sg)
+                y0 = rounded(x * r)
+                left = y0 * sg - x
+                step = rounded(abs(left)) * r if left else Fraction(0)
+                y = rounded(y0 - step if left > 0 else y0 + step)
+                want = rounded(x / sg)
+                off += code(y) != code(want)
+                changed += code(y0) != code(want)
+    assert off == 0
+    assert changed > 0      # (the product alone would not do)
