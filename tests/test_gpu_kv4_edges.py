@@ -63,3 +63,21 @@ def test_queries_in_place(d, hq, rot):
         q.copy_(r.q)
         assert q.data_ptr() % 32 == 16
         assert call(q, r.k, r.v, cu(r.slot), *pools, q_out=q, **r.kw) is q and torch.equal(q, want)
+
+
+@pytest.mark.parametrize("place", [0, 20, -1])
+def test_the_smoke_check_sees_one_wrong_page_of_v(monkeypatch, place):
+    """Expected outputs with a page of V an eighth too small: of the prefix (16
+    of more than 740 tokens), or of a branch."""
+    import __graft_entry__ as entry
+    entry.smoke_kv4(deft, torch)
+    unpack = deft.deft_kv_unpack4
+
+    def other(*a, **kw):
+        kp, vp = unpack(*a, **kw)
+        vp[place] *= 0.875
+        return kp, vp
+
+    monkeypatch.setattr(deft, "deft_kv_unpack4", other)
+    with pytest.raises(RuntimeError):
+        entry.smoke_kv4(deft, torch)
