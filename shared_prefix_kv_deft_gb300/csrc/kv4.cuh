@@ -87,8 +87,8 @@ __device__ __forceinline__ uint32_t scale_of(float amax, float six_g)
 // codes are those of the correctly rounded quotient (tested for every bf16 x
 // next to every border), by Markstein's division (IBM Journal of Research and
 // Development 34, 1990): the product y0 = x * (1 / sg), its residual y0 * sg -
-// x, which one fused multiply-add gives exactly, and one more that takes the
-// residual over sg from y0.  A bf16 x over an 8-bit scale often lies exactly
+// x by one fused multiply-add, and one more that takes the residual over sg
+// from y0.  A bf16 x over an 8-bit scale often lies exactly
 // between two codes, where y0 alone is an ulp to either side.
 __device__ __forceinline__ uint32_t pack8(const float (&x)[8], float amax, float sg)
 {
