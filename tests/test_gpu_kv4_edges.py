@@ -81,3 +81,70 @@ def test_the_smoke_check_sees_one_wrong_page_of_v(monkeypatch, place):
     monkeypatch.setattr(deft, "deft_kv_unpack4", other)
     with pytest.raises(RuntimeError):
         entry.smoke_kv4(deft, torch)
+
+
+def traced(call):
+    """What the call returns, and (kernel, bucket, items) of its launches."""
+    deft.trace_enable(True)
+    try:
+        got = call()
+        return got, [(r["kernel"], r["bucket"], r["items"]) for r in deft.trace_read()]
+    finally:
+        deft.trace_enable(False)
+
+
+# KV heads, group, head_dim; units' rows, CTAs an SM of that width, KV heads a
+# CTA takes at most.
+WIDTHS = [(8, 4, 128, 8, 4, 4), (8, 4, 64, 8, 4, 4), (32, 1, 128, 8, 4, 4), (6, 3, 64, 8, 4, 2), (8, 12, 128, 16, 3, 4), (4, 15, 64, 16, 3, 4),
+          (6, 9, 128, 16, 3, 2), (8, 16, 64, 64, 2, 2), (8, 40, 64, 64, 2, 2), (5, 33, 64, 64, 2, 1)]
+
+
+@pytest.mark.parametrize("beside,pieces", [("one less", 1), ("whole", 1), ("one more", 1), ("a quarter more", 1), ("a quarter more", 2), ("half more", 2),
+                                           ("twice", 1)])
+@pytest.mark.parametrize("width", WIDTHS)
+def test_rounds_of_ctas(width, beside, pieces):
+    """So many requests that CTAs which take several KV heads of an item fill
+    the device (a unit a warp, no joining of warps), exactly, with one CTA
+    less, with some more in a second launch, whose CTAs take fewer heads, and
+    twice over; each request one unit a head, or two and a merge
+    (as after all units of the tensor-core list)."""
+    hkv, group, d, rows, per_sm, most = width
+    slots = per_sm * torch.cuda.get_device_properties(0).multi_processor_count
+    groups = hkv // most
+    one, two = (-(-x * slots // groups) for x in (1, 2))    # items that fill one round, and two
+    items = {"one less": one - 1, "whole": one, "one more": one + 1, "a quarter more": one + one // 4, "half more": one + one // 2, "twice": two}[beside]
+    n = round(items / pieces)
+    unit = max(64, 16 * group)      # (a chunk is at least 16 tokens a row long)
+    length = [unit * (pieces - 1) + unit // 2 + 1 + (7 * i) % (unit // 2) for i in range(n)]
+    t = Tree([-1] * n, length, list(range(n)), hkv, group, d, seed=n)
+    plan = t.plan(unit)
+    total = n * pieces
+    assert plan.stats["num_fma_items"] + plan.stats["num_mma_items"] == total
+    got, launches = traced(lambda: t.run(plan))
+    bulk = total * groups // slots * slots // groups
+    want = [("phase1_kv4", rows, x) for x in (bulk, total - bulk) if x] + ([("phase2_merge", 0, n)] if pieces > 1 or rows == 64 else [])
+    assert launches == want
+    if pieces == 1:
+        assert (bulk > 0) == (beside != "one less") and (total > bulk or beside in ("whole", "twice"))
+    check(t, got)
+
+
+@pytest.mark.parametrize("hkv,group,d", [(8, 1, 128), (8, 3, 64), (4, 2, 128)])
+def test_many_widths_at_once(hkv, group, d):
+    """Prefixes under 3 to 40 branches each: one, two and more rows a unit in
+    one list, wide units beside them, every launch of a width and its rest."""
+    parent, length, query = [], [], []
+    for i in range(60):
+        root = len(parent)
+        parent.append(-1)
+        length.append(300 + 37 * (i % 11))
+        for j in range([3, 6, 8, 5, 20, 40][i % 6]):
+            query.append(len(parent))
+            parent.append(root)
+            length.append(1 + (13 * i + 29 * j) % 100)
+    t = Tree(parent, length, query, hkv, group, d, seed=hkv)
+    plan = t.plan(128)
+    got, launches = traced(lambda: t.run(plan))
+    kinds = [b for k, b, _ in launches if k == "phase1_kv4"]
+    assert kinds.count(8) == 2 and max(kinds) == 64 and launches[-1][0] == "phase2_merge"
+    check(t, got)
