@@ -148,3 +148,73 @@ def test_many_widths_at_once(hkv, group, d):
     kinds = [b for k, b, _ in launches if k == "phase1_kv4"]
     assert kinds.count(8) == 2 and max(kinds) == 64 and launches[-1][0] == "phase2_merge"
     check(t, got)
+
+
+@pytest.mark.parametrize("chunk", [2048, 64])
+@pytest.mark.parametrize("shape", [(1, 4, 64), (1, 4, 128), (1, 12, 64), (1, 12, 128), (9, 2, 64), (20, 2, 128)])
+def test_rows_that_are_not_finite_have_a_lse_of_nan(shape, chunk):
+    """Never an infinity, which would say that a row attended nothing: rows
+    of one partial, written by their unit, and of several, by the merge; at
+    every width.  Queries with a NaN or an infinity of their own, then a NaN
+    key.  The other rows are as near to 64 bits as ever (check's bounds), not
+    the same bits: a unit's rows raise their maxima together, and a row that is
+    not finite calls for none.  A weight is 2^11 times a power of two times
+    itself when it is rounded, 2^15 at most, whichever time that was: the bounds
+    hold for each."""
+    queries, group, d = shape
+    if queries == 1:
+        t = Tree([-1], [200], [0], 2, group, d)
+    else:
+        t = Tree([-1] + [0] * queries, [200] + [9] * queries, list(range(1, queries + 1)), 2, group, d)
+    plan = t.plan(chunk)
+    base = t.run(plan)
+    q = t.q.copy()
+
+    def others(out, lse):
+        t.q = q
+        check(t, (torch.where(lse.isnan()[..., None], base[0], out), torch.where(lse.isnan(), base[1], lse)))
+
+    hit = np.zeros(base[1].shape, bool)
+    for i, (value, row) in enumerate([(np.nan, 0), (np.inf, 2), (-np.inf, group), (np.nan, 2 * group - 1)]):
+        t.q[i % queries, row, 5 * i] = value
+        hit[i % queries, row] = True
+    got = t.run(plan)
+    assert (np.isnan(f64(got[1])) == hit).all() and np.isnan(f64(got[0])[hit]).all()
+    others(*got)
+    s = t.slots(0)[77]          # a key of KV head 1 that all queries attend
+    scale = t.k4[..., 8 * d:].reshape(-1, 2, 16, d // 16)[s // 16, 1, s % 16, 1:2]
+    was = scale.copy()
+    scale[:] = 0x7F
+    got = t.run(plan)
+    hit[:], hit[:, group:] = False, True
+    assert (np.isnan(f64(got[1])) == hit).all() and np.isnan(f64(got[0])[hit]).all()
+    scale[:] = was
+    others(*got)
+
+
+@pytest.mark.parametrize("hkv,group,d", [(2, 2, 128), (2, 3, 64), (8, 1, 128)])
+def test_plans_that_are_updated_and_rebuilt(hkv, group, d):
+    """One plan through Plan.update (tokens appended, a branch pruned) and
+    Plan.rebuild (other trees, larger and smaller), uploaded and used again
+    each time."""
+    rng = np.random.default_rng(d + group)
+    parent, length = [-1] + [0] * 20, [500] + [int(x) for x in rng.integers(1, 60, 20)]
+    t = Tree(parent, length, list(range(1, 21)), hkv, group, d, seed=1)
+    plan = t.plan(128)
+    steps = [(t, t.run(plan))]
+    for step in range(4):
+        length = [length[0]] + [n + int(rng.integers(0, 20)) for n in length[1:]]
+        if step == 2:
+            length[5] = 0
+        t = Tree(parent, length, list(range(1, 21)), hkv, group, d, seed=step + 2)
+        plan.update(length)
+        plan.upload()
+        steps.append((t, t.run(plan)))
+    for n, m in ((3, 1200), (40, 90), (1, 5), (17, 400)):
+        parent, length = [-1] + [0] * n, [m] + [1 + 7 * i % 50 for i in range(n)]
+        t = Tree(parent, length, list(range(1, n + 1)), hkv, group, d, seed=m)
+        plan.rebuild(parent, length, list(range(1, n + 1)), 128, group, naive=False)
+        plan.upload()
+        steps.append((t, t.run(plan)))
+    for t, got in steps:
+        check(t, got)

@@ -1,10 +1,12 @@
 """The calls around the 4-bit cache at their edges, as far as no GPU is needed:
 empty batches, argument ranges, the arithmetic of the format."""
+import contextlib
 import ctypes
 import subprocess
 from fractions import Fraction
 
 import pytest
+import torch
 
 import shared_prefix_kv_deft_gb300 as deft
 from shared_prefix_kv_deft_gb300 import build as deft_build
@@ -159,3 +161,34 @@ def test_quotients_are_the_correctly_rounded_ones():
                 changed += code(y0) != code(want)
     assert off == 0
     assert changed > 0      # (the product alone would not do)
+
+
+@pytest.mark.parametrize("call", ["deft_qkv_write", "deft_qkv_write4", "deft_kv_unpack4", "deft_tree_attn4"])
+@pytest.mark.parametrize("stream", [0, 0x77])
+def test_outputs_come_from_the_launch_streams_memory(monkeypatch, call, stream):
+    """Every call that allocates its outputs does so inside
+    _allocating_for(its stream)."""
+    class Allocated(Exception):
+        pass
+
+    inside = []
+
+    @contextlib.contextmanager
+    def allocating_for(st):
+        inside.append(st)
+        yield
+        inside.pop()
+
+    def empty(*a, **kw):
+        raise Allocated(list(inside))
+
+    rows, pages = torch.zeros((2, 1, 64), dtype=torch.bfloat16), torch.zeros((1, 1, 16, 64), dtype=torch.bfloat16)
+    four, index = torch.zeros((1, 1, 576), dtype=torch.uint8), torch.zeros(2, dtype=torch.int32)
+    plan = deft.Plan([-1], [5], [0, 0], 256, 1, naive=False)
+    args = {"deft_qkv_write": (rows, rows, rows, index, pages, pages), "deft_qkv_write4": (rows, rows, rows, index, four, four),
+            "deft_kv_unpack4": (four, four, index), "deft_tree_attn4": (rows, four, four, index, index, plan)}[call]
+    monkeypatch.setattr(deft, "_allocating_for", allocating_for)
+    monkeypatch.setattr(torch, "empty", empty)
+    with pytest.raises(Allocated) as e:
+        getattr(deft, call)(*args, stream=stream)
+    assert e.value.args[0] == [stream]
