@@ -194,7 +194,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
     const int TS = kWarps / (ka.heads * groups);
     const int ts = warp % TS, rg = warp / TS % groups, h = hg * ka.heads + warp / (TS * groups);
     const int row0 = rg * NR;
-    const bool idle = h >= Hkv;
 
     // The rows of Q, on their way while the slices are looked up: lane (g, t)
     // takes dims (D / 4) t .. of row g of eight.
@@ -205,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
 #pragma unroll
         for (int i = 0; i < KW * 4; ++i)
             qw[n][i] = 0u;
-        if (r < R && !idle) {
+        if (r < R) {
             const int k = r / G;
             const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
                                                                ((size_t)p.chunk_q[cq0 + k] * Hq + h * G + (r - k * G)) * D) +
@@ -260,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
         __syncthreads();
         total = seg_first[nseg];
     }
-    const int steps = (total + PP - 1) / PP, mine = !idle && steps > ts ? (steps - ts + TS - 1) / TS : 0;
+    const int steps = (total + PP - 1) / PP, mine = steps > ts ? (steps - ts + TS - 1) / TS : 0;
     const uint64_t row_bits = R >= 64 ? ~0ull : (1ull << R) - 1;
     const uint32_t my_rows = (uint32_t)(row_bits >> row0) & (uint32_t)((1ull << NR) - 1);
 
@@ -635,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
     }
 
     // ---- out: lane (g, t) holds dims (D / 8) g .. of rows 2t and 2t + 1 ----
-    if (ts == 0 && !idle) {
+    if (ts == 0) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -688,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
 template <int D, int NT>
 int launch(Kv4Args ka, const DevPartition &p, cudaStream_t st)
 {
-    ka.head_groups = (ka.a.num_kv_heads + ka.heads - 1) / ka.heads;
+    ka.head_groups = ka.a.num_kv_heads / ka.heads;      // (heads divides them: every warp has a unit)
     const int64_t ctas = (int64_t)ka.n * ka.head_groups;
     if (ctas > INT32_MAX)
         return (int)cudaErrorInvalidConfiguration;
