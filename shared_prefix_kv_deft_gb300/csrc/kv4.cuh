@@ -119,5 +119,23 @@ __device__ __forceinline__ uint32_t pack8(const float (&x)[8], float amax, float
     return b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24;
 }
 
+// ---- of the steps ----
+// A weight is held as 2^kLift * 2^(s - m), m a maximum that is raised when a
+// logit passes it by more than kUp (both in base 2).
+constexpr float kUp = 4.f, kLift = 11.f;
+
+__device__ __forceinline__ float nan() { return __int_as_float(0x7fffffff); }
+
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi)
+{
+    const __half2 r = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+__device__ __forceinline__ float pow2(int e)   // -126 <= e <= 127
+{
+    return __int_as_float((127 + e) << 23);
+}
+
 }  // namespace kv4
 }  // namespace deft

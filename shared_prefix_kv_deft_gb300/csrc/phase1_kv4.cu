@@ -55,8 +55,6 @@ namespace deft {
 namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr float kUp = 4.f, kLift = 11.f;
-#define kNaN __int_as_float(0x7fffffff)
 constexpr unsigned kAll = 0xffffffffu;
 
 template <int D, int NT>
@@ -93,17 +91,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x)
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
-}
-
-__device__ __forceinline__ uint32_t f16x2(float lo, float hi)
-{
-    const __half2 r = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
-
-__device__ __forceinline__ float pow2(int e)   // -126 <= e <= 127
-{
-    return __int_as_float((127 + e) << 23);
 }
 
 // The exponent of the power of two that puts a row's largest finite
@@ -326,21 +313,21 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
         // 2^e, in two factors for rows below 2^-112 (e reaches 147).
         const int e = row_exponent<KW * 4, 4>(w), e1 = min(e, 126), e2 = e - e1;
         // (A factor past fp32, for a row near its end, leaves logits of 0.)
-        const float up = pow2(e1), fr = fminf(a.scale_log2 * pow2(-e1) * ka.k_scale * pow2(-e2), FLT_MAX);
+        const float up = kv4::pow2(e1), fr = fminf(a.scale_log2 * kv4::pow2(-e1) * ka.k_scale * kv4::pow2(-e2), FLT_MAX);
         f[n][0] = __shfl_sync(kAll, fr, 8 * t);
         f[n][1] = __shfl_sync(kAll, fr, 8 * t + 4);
         if (e2 == 0) {
 #pragma unroll
             for (int i = 0; i < KW * 4; ++i) {
                 const float2 v = bf16x2_to_float2(w[i]);
-                w[i] = f16x2(v.x * up, v.y * up);
+                w[i] = kv4::f16x2(v.x * up, v.y * up);
             }
         } else {
-            const float up2 = pow2(e2);
+            const float up2 = kv4::pow2(e2);
 #pragma unroll
             for (int i = 0; i < KW * 4; ++i) {
                 const float2 v = bf16x2_to_float2(w[i]);
-                w[i] = f16x2(v.x * up * up2, v.y * up * up2);
+                w[i] = kv4::f16x2(v.x * up * up2, v.y * up * up2);
             }
         }
         if constexpr (C::kQSmem) {
@@ -482,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    grow |= x[p2][n][j] > kLift + kUp;
+                    grow |= x[p2][n][j] > kv4::kLift + kv4::kUp;
         if (__any_sync(kAll, grow)) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -495,8 +482,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
                     y = fmaxf(y, __shfl_xor_sync(kAll, y, 4));
                     y = fmaxf(y, __shfl_xor_sync(kAll, y, 8));
                     y = fmaxf(y, __shfl_xor_sync(kAll, y, 16));
-                    y = fmaxf(m[n][j], y - kLift);
-                    y = y == INFINITY ? kNaN : y;       // a logit past fp32: for good, through l
+                    y = fmaxf(m[n][j], y - kv4::kLift);
+                    y = y == INFINITY ? kv4::nan() : y;       // a logit past fp32: for good, through l
                     const float alpha = y == m[n][j] ? 1.f : tc::ex2(m[n][j] - y);
                     m[n][j] = y;
                     l[n][j] *= alpha;
@@ -526,8 +513,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
                 const float p3 = tc::ex2(x[p2][n][3]), q0 = tc::ex2(x[p2][n][2]);
                 l[n][0] += p0 + q0;
                 l[n][1] += p1 + p3;
-                pb[p2][n][0] = transpose8(f16x2(p0, p1));
-                pb[p2][n][1] = transpose8(f16x2(q0, p3));
+                pb[p2][n][0] = transpose8(kv4::f16x2(p0, p1));
+                pb[p2][n][1] = transpose8(kv4::f16x2(q0, p3));
             }
         // ---- O^T ----
 #pragma unroll
@@ -585,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kCtas) phase1_kv4_kernel
             report_failure(p.status, 401);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-            l[n][0] = l[n][1] = kNaN;
+            l[n][0] = l[n][1] = kv4::nan();
     }
 
     // ---- the states of the warps that shared the slices, joined by halves:

@@ -54,8 +54,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kD = 128, kTile = 128;
-constexpr float kUp = 4.f, kLift = 11.f;
-#define kNaN __int_as_float(0x7fffffff)
 constexpr unsigned kAll = 0xffffffffu;
 constexpr uint32_t kRowGroup = 2048;    // 8 tokens x 128 dims of fp16: two 1 KB swizzle atoms (d halves)
 constexpr uint32_t kTileBytes = 16 * kRowGroup;
@@ -82,17 +80,6 @@ struct Cfg {
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_mn)
 {
     return tc::idesc_bf16(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
-}
-
-__device__ __forceinline__ uint32_t f16x2(float lo, float hi)
-{
-    const __half2 r = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
-
-__device__ __forceinline__ float pow2(int e)   // -126 <= e <= 127
-{
-    return __int_as_float((127 + e) << 23);
 }
 
 // tc::tmem_st16 without the wait.
@@ -347,14 +334,14 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
         const int e1 = e / 2, e2 = e - e1;
         // Infinities become NaN (with the elements beside them), so that a
         // logit of -inf is a masked one.
-        const float up1 = inf ? kNaN : pow2(e1), up2 = pow2(e2);
+        const float up1 = inf ? kv4::nan() : kv4::pow2(e1), up2 = kv4::pow2(e2);
 #pragma unroll
         for (int i = 0; i < DT / 8; ++i) {
             uint32_t x[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float2 y = bf16x2_to_float2(qw[4 * i + j]);
-                x[j] = f16x2(y.x * up1 * up2, y.y * up1 * up2);
+                x[j] = kv4::f16x2(y.x * up1 * up2, y.y * up1 * up2);
             }
             const int chunk = piece * (DT / 8) + i;         // of the row's sixteen
             *reinterpret_cast<uint4 *>(smem + C::q + (chunk >> 3) * C::q_half + q_row * 128 + (((chunk & 7) ^ (q_row & 7)) << 4)) =
@@ -363,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
         // A column of no row has weights of 0: 2^(f * 0 - inf).
         if (piece == 0) {
             // (A factor past fp32, for a row near its end, leaves logits of 0.)
-            col_f(q_row) = fminf(a.scale_log2 * pow2(-e1) * ka.k_scale * pow2(-e2), FLT_MAX);
+            col_f(q_row) = fminf(a.scale_log2 * kv4::pow2(-e1) * ka.k_scale * kv4::pow2(-e2), FLT_MAX);
             col_y(q_row) = q_row < R ? INFINITY : -INFINITY;
         }
     }
@@ -485,9 +472,9 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
                 if (tid < RP) {
                     const float was = col_y(tid);       // lift - maximum; -inf: no row
                     const float big = fmaxf(fmaxf(red[tid], red[RP + tid]), fmaxf(red[2 * RP + tid], red[3 * RP + tid]));
-                    now = was == -INFINITY || big == -INFINITY ? was : fminf(was, kLift - big * col_f(tid));
+                    now = was == -INFINITY || big == -INFINITY ? was : fminf(was, kv4::kLift - big * col_f(tid));
                     if (now == -INFINITY && was != -INFINITY)
-                        now = kNaN;         // a logit past fp32: for good, through the sums
+                        now = kv4::nan();         // a logit past fp32: for good, through the sums
                     alpha = now == was ? 1.f : tc::ex2(now - was);
                 }
                 __syncthreads();
@@ -558,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
                         const float y0 = tc::ex2(x[h2][q][2 * j]), y1 = tc::ex2(x[h2][q][2 * j + 1]);
                         l0 += y0;
                         l1 += y1;
-                        w[2 * h2 + q] = f16x2(y0, y1);
+                        w[2 * h2 + q] = kv4::f16x2(y0, y1);
                     }
                 ln[2 * j] = l0;
                 ln[2 * j + 1] = l1;
@@ -573,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
             }
             tc::fence_proxy_async();
             tc::fence_before_sync();
-            const bool over = __syncthreads_or(top > kLift + kUp);
+            const bool over = __syncthreads_or(top > kv4::kLift + kv4::kUp);
             tc::fence_after_sync();
             if (raise || !over)
                 break;
@@ -619,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 2) phase1_kv4_mma_kernel(Kv4Args ka,
     if (tid < RP && tid < R) {
         float sum = (red[tid] + red[RP + tid]) + (red[2 * RP + tid] + red[3 * RP + tid]);
         if (failed)
-            sum = kNaN;
+            sum = kv4::nan();
         // sum is 0 where the row attends no token, NaN where a logit was.
         const float lse2 = sum == 0.f ? -INFINITY : log2f(sum) - col_y(tid);
         const int k = tid / G;
