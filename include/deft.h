@@ -425,8 +425,8 @@ int deft_tree_attn_noalloc(const void *q, const void *k_pages, const void *v_pag
 /*
  * Per-launch kernel timing, for measurement tools (no counterpart on the
  * pages).  While enabled, every kernel launch made by deft_tree_attn,
- * deft_naive_attn and deft_tree_attn4 is bracketed by two CUDA events recorded on the launch
- * stream.  deft_trace_read waits for those events, writes up to `cap`
+ * deft_naive_attn and deft_tree_attn4 is bracketed by two CUDA events recorded
+ * on the launch stream.  deft_trace_read waits for those events, writes up to `cap`
  * records (in launch order) to `out`, sets *count to the number written and
  * forgets all pending records.  Events are created on first use and reused;
  * the library is not thread-safe while tracing is on.
@@ -434,9 +434,11 @@ int deft_tree_attn_noalloc(const void *q, const void *k_pages, const void *v_pag
 typedef struct deft_trace_record {
     int32_t kernel;   /* DEFT_K_* */
     int32_t family;   /* 0 tree partition, 1 naive partition                  */
-    int32_t bucket;   /* row bucket b (rows <= 2^b) of a CUDA-core launch     */
+    int32_t bucket;   /* row bucket b (rows <= 2^b) of a CUDA-core launch;
+                         the most rows (8, 16, 32, 64) of a 4-bit one         */
     int32_t fallback; /* 1 if the launch ran >= 16-row chunks on CUDA cores   */
-    int32_t items;    /* work items (grid = items * num_kv_heads for phase 1) */
+    int32_t items;    /* work items (grid = items * num_kv_heads for phase 1;
+                         a 4-bit launch may take several heads a CTA)         */
     float ms;         /* event-measured duration                              */
 } deft_trace_record;
 
@@ -627,8 +629,9 @@ int deft_qkv_write(const void *q, const void *k, const void *v, int32_t in_dtype
  * whole, the bf16 pages' table is node_page_off with page_id[i] = i.  An entry
  * outside [0, num_pages) leaves its page as it was; an entry may repeat.
  * The 4-bit pools 16-byte aligned, the bf16 ones 32-byte aligned and
- * overlapping no input (DEFT_EINVAL where they start at one); head_dim in {64, 128}, page_size 16
- * (DEFT_EUNSUPPORTED), at most 2^18 heads.  Never allocates, never
+ * overlapping no input (DEFT_EINVAL where they start at one); head_dim in
+ * {64, 128}, page_size 16 (DEFT_EUNSUPPORTED), at most 2^18 heads
+ * (DEFT_EINVAL).  Never allocates, never
  * synchronises; stream-ordered on `stream`; may be captured into a CUDA
  * graph.
  */
@@ -646,27 +649,31 @@ int deft_kv_unpack4(const void *k4_pages, const void *v4_pages, float k_scale, f
  * (deft_plan_at's positions and deft_plan_ex's flags included), page tables,
  * q, out, lse, workspace and rules, with k4_pages and v4_pages as above and
  * the k_scale and v_scale they were written with.
- *   - Every product and sum is taken from the cache's exact values: fp16
- *     products of q and c * s (both exact) summed in fp32, weights rounded
- *     to fp16 (2^-11), the sums and lse in fp32.
- *   - Any gqa_group a plan takes (1..64), head_dim in {64, 128}; a launch
- *     for each width of work items that the plan has (up to 8, to 15, to 32
- *     and to 64 rows), then the merge of the queries that need it.  A
- *     chunk of 256 tokens is 36 KB a head here: a larger chunk_target (512,
- *     1024) leaves fewer partials to merge where there are requests or
- *     branches enough to fill the device.
+ *   - Every product and sum is taken from the cache's exact values, c * s in
+ *     fp16, and q in fp16 after a power of two that its row is multiplied by:
+ *     elements of at least 2^-31 of the row's largest exactly, smaller ones
+ *     to within 2^-39 of it.  Products are exact and summed in fp32, weights
+ *     are rounded to fp16 (2^-11; under 2^-25 of the row's largest weight to
+ *     within 2^-36 of it), the sums and lse are fp32.
+ *   - Any gqa_group a plan takes (1..64), head_dim in {64, 128}; one or
+ *     two launches for each width of work items that the plan has (up to 8,
+ *     to 15, to 32 and to 64 rows), then the merge of the queries that need
+ *     it.  A chunk_target of 256, 512 or 1024 gives much the same time (the
+ *     fastest and the slowest of the three are within 30% of one another on a
+ *     tree of short nodes, within 10% elsewhere, 256 never far from the best).
  *   - Cache slots past a node's last token never affect a result, whatever
  *     they hold.  A block whose scale is NaN (written from a NaN) counts as
  *     NaN: in K for the rows that attend its token, in V for every row of the
  *     work item that reads its page.  q may hold anything: a row with an
  *     infinity or NaN of its own, and one with a logit that is NaN or above
  *     fp32's largest, has NaN in out and lse (a logit below fp32's least may
- *     give NaN too); no other row is affected.  page_id and node_page_off are trusted, as in
+ *     give NaN too); no other row has, and others differ by no more
+ *     than their weights' rounding.  page_id and node_page_off are trusted, as in
  *     deft_tree_attn (page_id may be NULL where no path has a token).
  *   - At most 2^32 heads' pages, num_pages * num_kv_heads (DEFT_EUNSUPPORTED).
  * out 16-byte aligned (DEFT_EINVAL).  Several steps of one plan may run at
- * the same time, each with its own outputs and workspace (this call does not use the plan's work queues).  A
- * kernel wait that runs out is reported by deft_step_status.  k_scale and
+ * the same time, each with its own outputs and workspace (this call does not
+ * use the plan's work queues).  A kernel wait that runs out is reported by deft_step_status.  k_scale and
  * v_scale in [2^-60, 2^60] (DEFT_EINVAL).  Never allocates, never
  * synchronises; stream-ordered on `stream`; may be captured into a CUDA
  * graph.

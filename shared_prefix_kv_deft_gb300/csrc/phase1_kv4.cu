@@ -19,8 +19,8 @@
 // two tokens' nibbles put side by side first, so that one conversion makes a
 // pair along the tokens.  c * s is exact in fp16, and so is Q once each row
 // is multiplied by a power of two that puts its largest element in [2^14,
-// 2^15) (what falls below fp16 there is 2^-39 of the row's largest).  S^T's
-// layout becomes P^T's by a transposition of 8x8 blocks between lanes.
+// 2^15) (elements under 2^-31 of the row's largest are off by at most 2^-39 of
+// it).  S^T's layout becomes P^T's by a transposition of 8x8 blocks between lanes.
 //
 // P is held as 2^11 * 2^(s - m), m a maximum that is raised only when a logit
 // passes it by more than 2^4: at most 2^15, and weights down to 2^-35 of the
@@ -34,7 +34,7 @@
 // exponentials overlap.  Every wait is bounded.
 //
 // What bounds it is the units' latency: 64 requests of 64 to 8192 tokens,
-// 32/8 heads of 128, a step of 36.3 us for 115 MB (17 us at the measured copy
+// 32/8 heads of 128, a step of 36.1 us for 115 MB (17 us at the measured copy
 // rate).  Of a unit's 10 us, 4 are the chain of look-ups from its item to its
 // first page (five loads, each waiting for the one before), and in the other 6
 // each scheduler issues an instruction in two cycles from its four warps, some
@@ -42,7 +42,7 @@
 // rest for V's nibbles, the softmax, the look-ups and the copies.  Leaving out
 // any one of these (in a copy for measurement) gains 5% at most.  Measured and
 // left: bytes put apart by mul.hi, pairs made by integer arithmetic (44.7, 48.4
-// us where 37.9), five CTAs an SM with fewer registers (39.1); a conversion
+// us where 37.9), five CTAs an SM with fewer registers (39.1 where 37.9); a conversion
 // takes any byte of its operand at no cost.
 #include <cfloat>
 
@@ -839,8 +839,9 @@ int dispatch_step4(const AttnArgs &a, const DevPartition &dp, const Partition &h
     ka.a = a;
     ka.k_scale = k_scale, ka.v_scale = v_scale;
     ka.mma_narrow = hp.mma_bucket_off[1];
-    // One launch for each width, the widest first: 33 to 64 and 16 to 32 rows
-    // (the tensor-core list; on mma.sync at head_dim 64), 9 to 15, up to 8.
+    // One or two launches for each width, the widest first: 33 to 64 and 16 to
+    // 32 rows (the tensor-core list; on mma.sync at head_dim 64), 9 to 15, up
+    // to 8.
     struct Part {
         int32_t wide, first, n, rows;
     };
@@ -851,10 +852,13 @@ int dispatch_step4(const AttnArgs &a, const DevPartition &dp, const Partition &h
         if (x.n == 0)
             continue;
         ka.wide = x.wide;
-        // Items are sorted by length: whole rounds of CTAs with as many heads
-        // as they take, and the rest, the shorter ones, over more CTAs (64
-        // requests: 830 CTAs of four heads are one round of 760 and 70 that
-        // would keep the device waiting for their whole length).
+        // Whole rounds of CTAs with as many heads as they take, and the rest
+        // over more CTAs (64 requests: 830 CTAs of four heads are one round
+        // of 608 and 222 that would keep the device waiting for their whole
+        // length).  The items of one width are sorted by length, so that the
+        // rest are the shorter ones; of several widths joined here (1, 2, 4
+        // and 8 rows; at head_dim 64 32 and 64) they are sorted by width
+        // first, and the rest come from the widest.
         const bool tcgen = x.wide && tc;
         const int64_t slots = (int64_t)(x.rows > 16 ? 2 : x.rows > 8 ? 3 : 4) * num_sms();
         int most = x.rows > 16 ? 2 : 4;
